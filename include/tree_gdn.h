@@ -1,6 +1,7 @@
 /*
  * tree_gdn.h -- C ABI of the tree conv + tree Gated DeltaNet library (forward and
- * backward), with a tree Mamba2 (SSD) forward beside it,
+ * backward), with a tree Mamba2 (SSD) forward, tree attention and token log
+ * probabilities (each forward and backward) beside it,
  * for AMD Instinct MI355X (gfx950).
  *
  * The library runs the forward pass of a recurrent mixer over a prefix trie
@@ -446,6 +447,170 @@ int tree_ssd_scan(const void* x, const float* dt, const float* A, const void* B,
                   void* y, const float* init_states, float* states, int64_t n_tokens, int32_t n_groups,
                   int32_t n_heads, int32_t d_state, int32_t head_dim, int32_t dtype, const tree_plan_t* plan,
                   const void* dplan, size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * tree_attention_plan -- host tables of the tree attention over the trie of
+ * `plan` (host only, no device work; built once per plan and shared by every
+ * attention layer): for every 128 packed rows, the runs of packed rows their
+ * tokens see, those all of them see first; for every 128 keys, the runs of
+ * rows that see them, cut into parts of at most 2048; and every token's place
+ * in a depth-first walk with the end of its segment's subtree, which decide
+ * single pairs.  Any numbering with parents before children is accepted.  The
+ * tables are copies: the plan may be freed before them.
+ * Errors: INVALID_ARG (also: out of host memory), UNSUPPORTED (a trie whose
+ * run lists exceed 2^26 entries: very deep and branched all along).
+ */
+typedef struct tree_attention_plan tree_attention_plan_t; /* opaque, host memory, immutable once built */
+int tree_attention_plan(const tree_plan_t* plan, tree_attention_plan_t** out);
+void tree_attention_plan_free(tree_attention_plan_t* aplan);
+
+/* Bytes of device memory tree_attention_plan_upload writes. */
+size_t tree_attention_plan_device_bytes(const tree_attention_plan_t* aplan);
+
+/*
+ * tree_attention_plan_upload -- the tables' device copy, as tree_plan_upload
+ * is the plan's: asynchronous on `stream`, from pageable memory of `aplan`;
+ * (dplan, dplan_bytes) is recorded, and the attention entry points take no
+ * other buffer.
+ * Errors: INVALID_ARG, WORKSPACE (dplan_bytes too small), HIP.
+ */
+int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, size_t dplan_bytes, void* stream);
+
+/*
+ * tree_attention -- softmax attention in which token i sees exactly the tokens
+ * of its own root-to-token path, itself included ("Tree Training" section 3.1
+ * Eq. 6 and the tree attention mask of section 3.2):
+ *
+ *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i),
+ *   lse_i = log sum_j exp(scale q_i . k_j),
+ *
+ * j over that path.  Query head h uses key/value head h / (h_q / h_kv).
+ * A token that is not on the path has no influence, whatever it holds
+ * (infinities and NaN included).
+ *
+ * q      device, [n_tokens, h_q, d], dtype, ldq elements between token rows
+ * k, v   device, [n_tokens, h_kv, d], dtype, ldk, ldv     (read)
+ * o      device, [n_tokens, h_q, d], dtype, contiguous    (written; no alias)
+ * lse    device, [n_tokens, h_q] fp32, or NULL            (written)
+ * Heads of a token row are contiguous; ldq >= h_q d and ldk, ldv >= h_kv d
+ * (slices of one projection's output need no copy).  Pointers and row
+ * distances are multiples of 16 bytes.
+ * scale  > 0 and finite (1 / sqrt(d) as a rule).
+ * dtype  TREE_DTYPE_BF16 (bf16 MFMA; scores, maxima, sums and the output's
+ *        accumulation in fp32, probabilities rounded to bf16 for their
+ *        product with v) or TREE_DTYPE_F32 (fp32 MFMA throughout).
+ * d in {32, 64, 128}.  No workspace; results do not depend on the schedule.
+ * dplan, dplan_bytes  device copy of `aplan` (tree_attention_plan_upload).
+ * Errors: INVALID_ARG, SIZE (n_tokens != plan N), UNSUPPORTED (d, or h_q not a
+ * multiple of h_kv), WORKSPACE (dplan_bytes too small), HIP.
+ */
+int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, int64_t ldq, int64_t ldk,
+                   int64_t ldv, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
+                   const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* stream);
+
+/*
+ * tree_attention_backward_workspace_bytes -- device workspace of
+ * tree_attention_backward: dO . o of every row and head, and the partial dk,
+ * dv of key tiles whose work is split.  0 for a NULL or unsupported argument.
+ */
+size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
+                                               int32_t d);
+
+/*
+ * tree_attention_backward -- gradients of tree_attention, the probabilities
+ * recomputed from the forward's lse.  With delta_i = dO_i . o_i:
+ *   ds_ij = p_ij (dO_i . v_j - delta_i),
+ *   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i,
+ *   dv_j = sum_i p_ij dO_i,
+ * i over every token whose path holds j (all branches below it) and every
+ * query head of j's group.  Sums run in a fixed order: the result is
+ * deterministic.
+ *
+ * q, k, v, o, lse  the forward's inputs and outputs; o and dout with ldo, lddo
+ *            elements between token rows                 (read)
+ * dout       device, [n_tokens, h_q, d], dtype           (read)
+ * dq         device, [n_tokens, h_q, d], dtype, contiguous  (written)
+ * dk, dv     device, [n_tokens, h_kv, d], dtype, contiguous (written)
+ * ws         device workspace, ws_bytes >= tree_attention_backward_workspace_bytes.
+ * Everything else as for tree_attention; ds and p are rounded to bf16 for
+ * their products under TREE_DTYPE_BF16.
+ * Errors: as tree_attention.
+ */
+int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                            const void* dout, void* dq, void* dk, void* dv, int64_t ldq, int64_t ldk, int64_t ldv,
+                            int64_t ldo, int64_t lddo, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d,
+                            float scale, int32_t dtype, const tree_attention_plan_t* aplan, const void* dplan,
+                            size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/* Most alternatives tree_logprobs returns per row. */
+#define TREE_MAX_TOP_K 64
+
+/*
+ * tree_logprobs_workspace_bytes -- device workspace of tree_logprobs: 0 from
+ * 512 rows on, else the partial sums and lists of rows that are spread over
+ * several work-groups.
+ */
+size_t tree_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_k);
+
+/*
+ * tree_logprobs -- log probabilities of the trie's tokens, each under the
+ * logits of the token in front of it on its path ("Tree Training" section 3.1
+ * Eq. 6: token t's loss term is that of its own root-to-leaf path), from one
+ * pass over the logits.  With z = logits / temperature of a row:
+ *   lse = log sum_i exp(z_i),  entropy = -sum_i p_i log p_i, p_i = exp(z_i - lse),
+ *   logp[t] = z_{tokens[t]} - lse   for every token t behind the row:
+ * the next token of its segment or, for a segment's last row, the first token
+ * of every child.  Called on all rows it writes all of logp; a root's first
+ * token has no row in front and gets 0 from the call that holds its own row.
+ *
+ * logits   device, [n_rows, vocab], dtype, ld elements between rows: those of
+ *          packed rows first_row .. first_row + n_rows - 1 (a part of the
+ *          trie at a time is fine)                       (read)
+ * tokens   device, [n_tokens] int32 or int64 (token_bytes 4 or 8); one outside
+ *          [0, vocab) is not asked for: its logp is 0    (read)
+ * logp     device, [n_tokens] fp32: the entries of tokens behind these rows
+ *                                                        (written)
+ * entropy, lse  device, [n_rows] fp32                    (written)
+ * top_logp, top_id  device, [n_rows, top_k] fp32 and int32 (NULL if top_k =
+ *          0): the top_k most likely tokens, best first, the lowest index
+ *          first among equal logits                      (written)
+ * temperature  > 0 and finite.   0 <= top_k <= min(vocab, TREE_MAX_TOP_K).
+ * A row of nothing but -inf has lse -inf, entropy 0 and log probabilities
+ * -inf.  A NaN or +inf makes its row's sums NaN; a NaN logit is never among
+ * the top_k (missing entries have id -1).
+ * Arithmetic in fp32, relative to a reference value near the row's maximum.
+ * dplan, dplan_bytes  device copy of `plan`, as for tree_conv.
+ * Errors: INVALID_ARG, SIZE, WORKSPACE, HIP.
+ */
+int tree_logprobs(const void* logits, const void* tokens, float* logp, float* entropy, float* lse, float* top_logp,
+                  int32_t* top_id, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab,
+                  int32_t token_bytes, float temperature, int32_t top_k, int32_t dtype, const tree_plan_t* plan,
+                  const void* dplan, size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * tree_logprobs_backward -- the gradient of the logits for gradients dlogp of
+ * the log probabilities and dentropy of the entropies, from one pass over the
+ * logits.  With G = sum of dlogp[t] over the tokens t behind the row:
+ *   dlogits_i = (1 / temperature) (sum_t dlogp[t] [tokens[t] = i] - G p_i
+ *               - dentropy p_i (log p_i + entropy)),
+ * the children's first tokens adding up in their common row, in index order.
+ *
+ * logits, tokens, ld, first_row, n_rows ..  as for tree_logprobs.
+ * lse, entropy  device, [n_rows] fp32: tree_logprobs' results  (read)
+ * dlogp      device, [n_tokens] fp32 (entries of tokens outside the vocabulary
+ *            are not read)                               (read)
+ * dentropy   device, [n_rows] fp32, or NULL (zeros; entropy may then be NULL)
+ * dlogits    device, [n_rows, vocab], dtype, ldd elements between rows; may be
+ *            `logits` itself (with ldd = ld)             (written)
+ * A row of nothing but -inf gets a zero gradient.  p is recomputed from the
+ * fp32 lse, to a relative error of about 2^-24 (|lse| + |log p|).
+ * Errors: INVALID_ARG, SIZE, WORKSPACE, HIP.
+ */
+int tree_logprobs_backward(const void* logits, const void* tokens, const float* lse, const float* entropy,
+                           const float* dlogp, const float* dentropy, void* dlogits, int64_t ld, int64_t ldd,
+                           int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab, int32_t token_bytes,
+                           float temperature, int32_t dtype, const tree_plan_t* plan, const void* dplan,
+                           size_t dplan_bytes, void* stream);
 
 /* Message for the last failed call on this thread ("" if none). */
 const char* tree_last_error(void);

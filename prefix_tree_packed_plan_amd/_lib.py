@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -76,6 +76,20 @@ SIGNATURES = {
                                               _I32, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P, _SZ, _P]),
     "tree_ssd_scan": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32,
                                      _P, _P, _SZ, _P, _SZ, _P]),
+    "tree_attention_plan": (ctypes.c_int, [_P, ctypes.POINTER(_P)]),
+    "tree_attention_plan_free": (None, [_P]),
+    "tree_attention_plan_device_bytes": (_SZ, [_P]),
+    "tree_attention_plan_upload": (ctypes.c_int, [_P, _P, _SZ, _P]),
+    "tree_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _I32, _I32, _F, _I32,
+                                      _P, _P, _SZ, _P]),
+    "tree_attention_backward_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
+    "tree_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64,
+                                               _I64, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P, _SZ, _P]),
+    "tree_logprobs_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "tree_logprobs": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _F, _I32, _I32,
+                                     _P, _P, _SZ, _P, _SZ, _P]),
+    "tree_logprobs_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32,
+                                              _F, _I32, _P, _P, _SZ, _P]),
     "tree_last_error": (ctypes.c_char_p, []),
 }
 
@@ -133,6 +147,7 @@ class TreePlan:
         _check(lib.tree_plan_query(self._h, ctypes.byref(st)))
         self.stats = {f: getattr(st, f) for f, _ in PlanStats._fields_}
         self._dev = {}
+        self._attn = None
 
     @property
     def handle(self):
@@ -200,10 +215,53 @@ class TreePlan:
             self._dev[key] = buf
         return self._dev[key]
 
+    def attention(self) -> "AttentionPlan":
+        """The attention tables of this trie (built once, at the first use)."""
+        if self._attn is None:
+            self._attn = AttentionPlan(self)
+        return self._attn
+
     def __del__(self):
         h = getattr(self, "_h", None)
         if h and _lib is not None:
             _lib.tree_plan_free(h)
+            self._h = None
+
+
+class AttentionPlan:
+    """Host tables of the tree attention (tree_attention_plan), plus their
+    device copies."""
+
+    def __init__(self, plan: TreePlan):
+        h = _P()
+        _check(load().tree_attention_plan(plan.handle, ctypes.byref(h)))
+        self._h = h
+        self._dev = {}
+
+    @property
+    def handle(self):
+        return self._h
+
+    def device_bytes(self) -> int:
+        return int(load().tree_attention_plan_device_bytes(self._h))
+
+    def on_device(self, device):
+        """The tables' device copy on `device` (uploaded once, stream-ordered)."""
+        import torch
+        dev = torch.device(device)
+        key = dev.index if dev.index is not None else torch.cuda.current_device()
+        if key not in self._dev:
+            buf = torch.empty(self.device_bytes(), dtype=torch.uint8, device=dev)
+            stream = torch.cuda.current_stream(buf.device).cuda_stream
+            _check(load().tree_attention_plan_upload(self._h, buf.data_ptr(), buf.numel(), stream))
+            torch.cuda.current_stream(buf.device).synchronize()
+            self._dev[key] = buf
+        return self._dev[key]
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h and _lib is not None:
+            _lib.tree_attention_plan_free(h)
             self._h = None
 
 
@@ -505,3 +563,202 @@ def tree_ssd_scan(x, dt, A, B, C, plan: TreePlan, D=None, return_states: bool = 
     if return_states:
         return y, states
     return y
+
+
+def _need_rows(t, name, dtype=None, device=None):
+    """A [N, H, d] device tensor whose heads are contiguous within a token
+    row; returns the elements between rows."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N, H, d]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}'s heads must be contiguous within a token row")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _attention_shapes(q, k, v, plan):
+    if k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("shapes must be q [N, H_q, d] and k, v [N, H_kv, d]")
+    if q.shape[0] != plan.n_tokens:
+        raise ValueError(f"q has {q.shape[0]} tokens, the plan {plan.n_tokens}")
+
+
+def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, return_lse: bool = False, out=None,
+                   lse=None):
+    """Tree attention: o [N, H_q, d] (and lse [N, H_q] fp32).  Every token
+    attends to the tokens of its own root-to-token path, itself included.
+
+    q [N, H_q, d]; k, v [N, H_kv, d] (H_q a multiple of H_kv; bf16 or fp32; d
+    32, 64 or 128).  They may be slices of one projection's output: only the
+    heads within a token row have to be contiguous.  scale: default
+    1 / sqrt(d)."""
+    import torch
+    ldq = _need_rows(q, "q")
+    dev = q.device
+    ldk = _need_rows(k, "k", q.dtype, dev)
+    ldv = _need_rows(v, "v", q.dtype, dev)
+    _attention_shapes(q, k, v, plan)
+    n, h_q, d = q.shape
+    o = torch.empty((n, h_q, d), dtype=q.dtype, device=dev) if out is None else out
+    _need(o, "out", q.dtype, dev)
+    _need_shape(o, "out", (n, h_q, d))
+    if return_lse and lse is None:
+        lse = torch.empty((n, h_q), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev)
+        _need_shape(lse, "lse", (n, h_q))
+    aplan = plan.attention()
+    dplan = aplan.on_device(dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    _check(load().tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                 lse.data_ptr() if lse is not None else None, ldq, ldk, ldv, n, h_q, k.shape[1], d,
+                                 d ** -0.5 if scale is None else float(scale), _dtype_code(q), aplan.handle,
+                                 dplan.data_ptr(), dplan.numel(), stream))
+    if return_lse:
+        return o, lse
+    return o
+
+
+def tree_attention_backward(q, k, v, o, lse, do, plan: TreePlan, scale: Optional[float] = None, workspace=None):
+    """Gradients (dq, dk, dv) of tree_attention in the inputs' dtype, given the
+    upstream gradient do [N, H_q, d] and the forward's o and lse
+    (tree_attention(..., return_lse=True)).  Deterministic."""
+    import torch
+    ldq = _need_rows(q, "q")
+    dev = q.device
+    ldk = _need_rows(k, "k", q.dtype, dev)
+    ldv = _need_rows(v, "v", q.dtype, dev)
+    ldo = _need_rows(o, "o", q.dtype, dev)
+    lddo = _need_rows(do, "do", q.dtype, dev)
+    _attention_shapes(q, k, v, plan)
+    n, h_q, d = q.shape
+    _need_shape(o, "o", (n, h_q, d))
+    _need_shape(do, "do", (n, h_q, d))
+    _need(lse, "lse", torch.float32, dev)
+    _need_shape(lse, "lse", (n, h_q))
+    dq = torch.empty((n, h_q, d), dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    lib = load()
+    aplan = plan.attention()
+    need = int(lib.tree_attention_backward_workspace_bytes(aplan.handle, h_q, k.shape[1], d))
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    dplan = aplan.on_device(dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    _check(lib.tree_attention_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                       do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ldq, ldk, ldv, ldo,
+                                       lddo, n, h_q, k.shape[1], d, d ** -0.5 if scale is None else float(scale),
+                                       _dtype_code(q), aplan.handle, dplan.data_ptr(), dplan.numel(),
+                                       workspace.data_ptr() if workspace is not None else None, ws_bytes, stream))
+    return dq, dk, dv
+
+
+class TokenLogprobs(NamedTuple):
+    logp: "torch.Tensor"      # [N] fp32: log probability of every token on its own path  # noqa: F821
+    entropy: "torch.Tensor"   # [n_rows] fp32, of every row of logits  # noqa: F821
+    lse: "torch.Tensor"       # [n_rows] fp32  # noqa: F821
+    top_logp: "torch.Tensor"  # [n_rows, top_k] fp32, best first (None without top_k)  # noqa: F821
+    top_ids: "torch.Tensor"   # [n_rows, top_k] int32  # noqa: F821
+
+
+def _logprob_args(logits, tokens, plan, first_row):
+    """Checks the logits of packed rows first_row ..; returns (elements between
+    rows, bytes of a token id)."""
+    import torch
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [n_rows, vocab] with contiguous rows")
+    _need(tokens, "tokens", device=logits.device)
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"tokens must be int32 or int64, got {tokens.dtype}")
+    _need_shape(tokens, "tokens", (plan.n_tokens,))
+    if first_row < 0 or logits.shape[0] < 1 or first_row + logits.shape[0] > plan.n_tokens:
+        raise ValueError(f"rows {first_row} .. {first_row + logits.shape[0]} are not rows of the plan's "
+                         f"{plan.n_tokens} tokens")
+    ld = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    return ld, tokens.element_size()
+
+
+def tree_logprobs(logits, tokens, plan: TreePlan, temperature: float = 1.0, top_k: int = 0, first_row: int = 0,
+                  logp=None, workspace=None) -> TokenLogprobs:
+    """Log probabilities of the trie's tokens under logits / temperature, each
+    from the row in front of it on its own path (a segment's last row serves
+    the first token of every child); with them the entropy, log-sum-exp and
+    top_k most likely tokens of every row.
+
+    logits [n_rows, vocab] (bf16 or fp32; rows may be further apart than
+    vocab) belong to packed rows first_row, first_row + 1, ...; tokens [N]
+    int32 or int64, one outside the vocabulary gets 0.  logp [N] fp32 (a new
+    one of zeros by default) receives the entries of tokens behind these rows:
+    pass the same tensor to the calls that cover a trie part by part."""
+    import torch
+    ld, token_bytes = _logprob_args(logits, tokens, plan, first_row)
+    dev, f32 = logits.device, torch.float32
+    rows, vocab = logits.shape
+    if logp is None:
+        whole = rows == plan.n_tokens
+        logp = (torch.empty if whole else torch.zeros)((plan.n_tokens,), dtype=f32, device=dev)
+    _need(logp, "logp", f32, dev)
+    _need_shape(logp, "logp", (plan.n_tokens,))
+    entropy = torch.empty(rows, dtype=f32, device=dev)
+    lse = torch.empty(rows, dtype=f32, device=dev)
+    top_logp = torch.empty((rows, top_k), dtype=f32, device=dev) if top_k > 0 else None
+    top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+    lib = load()
+    workspace, ws_bytes = _workspace(workspace, int(lib.tree_logprobs_workspace_bytes(rows, vocab, top_k)), dev)
+    dplan = plan.on_device(dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    _check(lib.tree_logprobs(logits.data_ptr(), tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+                             p(top_logp), p(top_ids), ld, plan.n_tokens, int(first_row), rows, vocab, token_bytes,
+                             float(temperature), int(top_k), _dtype_code(logits), plan.handle, dplan.data_ptr(),
+                             dplan.numel(), p(workspace), ws_bytes, stream))
+    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
+
+
+def tree_logprobs_backward(logits, tokens, lse, entropy, dlogp, plan: TreePlan, dentropy=None,
+                           temperature: float = 1.0, first_row: int = 0, out=None):
+    """The gradient of the logits (their shape and dtype) for gradients dlogp
+    [N] fp32 of tree_logprobs' logp and dentropy [n_rows] fp32 of its entropy
+    (default zero; entropy may then be None).  lse and entropy are that call's
+    results.  out may be `logits` itself, which is then overwritten."""
+    import torch
+    ld, token_bytes = _logprob_args(logits, tokens, plan, first_row)
+    dev, f32 = logits.device, torch.float32
+    rows, vocab = logits.shape
+    _need(lse, "lse", f32, dev)
+    _need_shape(lse, "lse", (rows,))
+    _need(dlogp, "dlogp", f32, dev)
+    _need_shape(dlogp, "dlogp", (plan.n_tokens,))
+    if dentropy is not None:
+        _need(dentropy, "dentropy", f32, dev)
+        _need_shape(dentropy, "dentropy", (rows,))
+        _need(entropy, "entropy", f32, dev)
+        _need_shape(entropy, "entropy", (rows,))
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+    elif out is not logits:
+        _need(out, "out", logits.dtype, dev)
+        _need_shape(out, "out", (rows, vocab))
+    ldd = ld if out is logits else vocab
+    dplan = plan.on_device(dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    _check(load().tree_logprobs_backward(logits.data_ptr(), tokens.data_ptr(), lse.data_ptr(),
+                                         p(entropy) if dentropy is not None else None, dlogp.data_ptr(), p(dentropy),
+                                         out.data_ptr(), ld, ldd, plan.n_tokens, int(first_row), rows, vocab,
+                                         token_bytes, float(temperature), _dtype_code(logits), plan.handle,
+                                         dplan.data_ptr(), dplan.numel(), stream))
+    return out

@@ -2,14 +2,18 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <string>
 #include <vector>
 
 #include "../../include/tree_gdn.h"
+#include "attn_plan.hpp"
 #include "launch.hpp"
 #include "plan.hpp"
 
@@ -20,6 +24,13 @@ struct tree_plan {
   // stale, short or foreign buffer is rejected on the host before any launch.
   // The plan is otherwise immutable; the list has its own lock so that the
   // plan can be shared across threads.
+  mutable std::mutex mu;
+  mutable std::vector<std::pair<const void*, size_t>> uploads;
+};
+
+// The attention tables and, as for the plan, the buffers they were uploaded into.
+struct tree_attention_plan {
+  tg::AttnPlan p;
   mutable std::mutex mu;
   mutable std::vector<std::pair<const void*, size_t>> uploads;
 };
@@ -59,6 +70,101 @@ int check_dplan(const tree_plan_t* plan, const void* dplan, size_t dplan_bytes, 
       return TREE_OK;
     }
   return fail(TREE_ERR_INVALID_ARG, "%s: dplan %p is not an upload of this plan (tree_plan_upload)", fn, dplan);
+}
+
+// The same for the attention tables.
+int check_dplan(const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, const char* fn) {
+  const size_t need = aplan->p.device_bytes();
+  if (dplan_bytes < need)
+    return fail(TREE_ERR_WORKSPACE, "%s: dplan has %zu bytes, the attention plan needs %zu", fn, dplan_bytes, need);
+  std::lock_guard<std::mutex> lock(aplan->mu);
+  for (const auto& u : aplan->uploads)
+    if (u.first == dplan) {
+      if (dplan_bytes > u.second)
+        return fail(TREE_ERR_INVALID_ARG, "%s: dplan_bytes %zu exceeds the %zu bytes it was uploaded with", fn,
+                    dplan_bytes, u.second);
+      return TREE_OK;
+    }
+  return fail(TREE_ERR_INVALID_ARG, "%s: dplan %p is not an upload of this attention plan (tree_attention_plan_upload)",
+              fn, dplan);
+}
+
+bool positive(float x) { return std::isfinite(x) && x > 0.f; }
+
+// Sizes, head layout and scale of an attention call.
+int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale,
+                    int32_t dtype, const char* fn) {
+  if (n_tokens != p.n_tokens)
+    return fail(TREE_ERR_SIZE, "%s: n_tokens %lld != plan tokens %lld", fn, static_cast<long long>(n_tokens),
+                static_cast<long long>(p.n_tokens));
+  if (h_q <= 0 || h_kv <= 0 || d <= 0) return fail(TREE_ERR_INVALID_ARG, "%s: head counts and sizes must be > 0", fn);
+  if (!dtype_ok(dtype)) return fail(TREE_ERR_INVALID_ARG, "%s: bad dtype %d", fn, dtype);
+  if (h_q % h_kv != 0)
+    return fail(TREE_ERR_UNSUPPORTED, "%s: h_q %d is not a multiple of h_kv %d", fn, h_q, h_kv);
+  if (!tg::attention_supported(d, dtype))
+    return fail(TREE_ERR_UNSUPPORTED, "%s: d=%d dtype=%d not compiled in", fn, d, dtype);
+  if (!positive(scale)) return fail(TREE_ERR_INVALID_ARG, "%s: scale must be > 0 and finite", fn);
+  if (static_cast<int64_t>(std::max(p.n_qtiles, p.n_kitems)) * h_q >= (int64_t(1) << 31))
+    return fail(TREE_ERR_UNSUPPORTED, "%s: too many tiles (%d) for %d heads", fn, std::max(p.n_qtiles, p.n_kitems),
+                h_q);
+  return TREE_OK;
+}
+// A tensor of token rows `ld` elements apart, read and written 16 bytes at a time.
+int check_rows(const void* ptr, int64_t ld, int64_t least, int32_t dtype, const char* name, const char* fn) {
+  const int64_t size = dtype == TREE_DTYPE_F32 ? 4 : 2;
+  if (ld < least || ld > (int64_t(1) << 40))
+    return fail(TREE_ERR_INVALID_ARG, "%s: %s has rows %lld elements apart, a row holds %lld", fn, name,
+                static_cast<long long>(ld), static_cast<long long>(least));
+  if (reinterpret_cast<uintptr_t>(ptr) % 16 != 0 || ld * size % 16 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: %s is not aligned to 16 bytes in every row", fn, name);
+  return TREE_OK;
+}
+
+// Work-groups a group's query heads are spread over in the gradients of k and
+// v: at least 2 a CU where the key tiles alone are fewer.
+int32_t attention_split(const tg::AttnPlan& p, int32_t h_q, int32_t h_kv) {
+  const int64_t work = static_cast<int64_t>(p.n_kitems) * h_kv;
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(h_q / h_kv, (511 + work) / work)));
+}
+size_t attention_delta_bytes(const tg::AttnPlan& p, int32_t h_q) {
+  return (static_cast<size_t>(p.n_tokens) * h_q * sizeof(float) + 255) / 256 * 256;
+}
+
+// A row is spread over several work-groups only where the rows alone leave
+// CUs idle; a slice has at least 2048 columns and starts on 128 bytes.
+struct Spread {
+  int32_t split, slice;
+};
+Spread spread(int32_t n_rows, int32_t vocab, int32_t least) {
+  const int64_t most = (static_cast<int64_t>(vocab) + 2047) / 2048;
+  int64_t s = n_rows >= 512 ? 1 : std::min<int64_t>((1023 + n_rows) / n_rows, most);
+  s = std::max<int64_t>({s, least, 1});
+  const int64_t slice = ((vocab + s - 1) / s + 63) / 64 * 64;
+  return {static_cast<int32_t>((vocab + slice - 1) / slice), static_cast<int32_t>(slice)};
+}
+Spread logprob_spread(int32_t n_rows, int32_t vocab) { return spread(n_rows, vocab, 1); }
+Spread logprob_backward_spread(int32_t n_rows, int32_t vocab) {
+  return spread(n_rows, vocab, static_cast<int32_t>((static_cast<int64_t>(vocab) + tg::kMaxSlice - 1) / tg::kMaxSlice));
+}
+
+int check_logprobs(const tg::Plan& p, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab,
+                   int32_t token_bytes, float temperature, int32_t dtype, const char* fn) {
+  if (n_tokens != p.n_tokens)
+    return fail(TREE_ERR_SIZE, "%s: n_tokens %lld != plan tokens %lld", fn, static_cast<long long>(n_tokens),
+                static_cast<long long>(p.n_tokens));
+  if (first_row < 0 || n_rows <= 0 || static_cast<int64_t>(first_row) + n_rows > p.n_tokens)
+    return fail(TREE_ERR_INVALID_ARG, "%s: rows %d .. +%d are not rows of the plan's %lld tokens", fn, first_row, n_rows,
+                static_cast<long long>(p.n_tokens));
+  if (vocab <= 0 || vocab > (1 << 30)) return fail(TREE_ERR_INVALID_ARG, "%s: vocab %d must be in 1..2^30", fn, vocab);
+  if (ld < vocab || ld > (int64_t(1) << 40))
+    return fail(TREE_ERR_INVALID_ARG, "%s: rows %lld elements apart hold %d", fn, static_cast<long long>(ld), vocab);
+  if (token_bytes != 4 && token_bytes != 8)
+    return fail(TREE_ERR_INVALID_ARG, "%s: token_bytes must be 4 or 8 (got %d)", fn, token_bytes);
+  if (!positive(temperature)) return fail(TREE_ERR_INVALID_ARG, "%s: temperature must be > 0 and finite", fn);
+  if (!positive(1.f / temperature))
+    return fail(TREE_ERR_INVALID_ARG, "%s: 1 / temperature must be > 0 and finite", fn);
+  if (!dtype_ok(dtype)) return fail(TREE_ERR_INVALID_ARG, "%s: bad dtype %d", fn, dtype);
+  return TREE_OK;
 }
 
 // Blocks along the tokens of the conv backward (each walks every n-th tile).
@@ -638,6 +744,276 @@ int tree_ssd_scan(const void* x, const float* dt, const float* A, const void* B,
     const hipError_t e = tg::launch_ssd_scan(a, d_state, head_dim, dtype, st);
     if (e != hipSuccess) return hip_fail("tree_ssd_scan: launch", e);
   }
+  return TREE_OK;
+}
+
+int tree_attention_plan(const tree_plan_t* plan, tree_attention_plan_t** out) {
+  if (!plan || !out) return fail(TREE_ERR_INVALID_ARG, "tree_attention_plan: null argument");
+  *out = nullptr;
+  try {
+    std::unique_ptr<tree_attention_plan_t> a(new tree_attention_plan_t);
+    std::string err;
+    const int rc = tg::build_attn_plan(plan->p, &a->p, &err);
+    if (rc != TREE_OK) {
+      g_err = err;
+      return rc;
+    }
+    *out = a.release();
+    return TREE_OK;
+  } catch (const std::exception&) {
+    return fail(TREE_ERR_INVALID_ARG, "tree_attention_plan: out of host memory");
+  }
+}
+
+void tree_attention_plan_free(tree_attention_plan_t* aplan) { delete aplan; }
+
+size_t tree_attention_plan_device_bytes(const tree_attention_plan_t* aplan) {
+  return aplan ? aplan->p.device_bytes() : 0;
+}
+
+int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, size_t dplan_bytes, void* stream) {
+  if (!aplan || !dplan) return fail(TREE_ERR_INVALID_ARG, "tree_attention_plan_upload: null argument");
+  const size_t need = aplan->p.device_bytes();
+  if (dplan_bytes < need)
+    return fail(TREE_ERR_WORKSPACE, "tree_attention_plan_upload: dplan has %zu bytes, needs %zu", dplan_bytes, need);
+  if (reinterpret_cast<uintptr_t>(dplan) % 32 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "tree_attention_plan_upload: dplan is not aligned to 32 bytes");
+  const hipError_t e = hipMemcpyAsync(dplan, aplan->p.mirror.data(), need, hipMemcpyHostToDevice,
+                                      static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_attention_plan_upload: hipMemcpyAsync", e);
+  try {
+    std::lock_guard<std::mutex> lock(aplan->mu);
+    for (auto& u : aplan->uploads)
+      if (u.first == dplan) {
+        u.second = dplan_bytes;
+        return TREE_OK;
+      }
+    aplan->uploads.emplace_back(dplan, dplan_bytes);
+  } catch (const std::exception&) {
+    return fail(TREE_ERR_INVALID_ARG, "tree_attention_plan_upload: out of host memory");
+  }
+  return TREE_OK;
+}
+
+int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, int64_t ldq, int64_t ldk,
+                   int64_t ldv, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
+                   const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* stream) {
+  const char* fn = "tree_attention";
+  if (!aplan || !q || !k || !v || !o || !dplan) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  const tg::AttnPlan& p = aplan->p;
+  if (const int rc = check_attention(p, n_tokens, h_q, h_kv, d, scale, dtype, fn)) return rc;
+  const int64_t rq = static_cast<int64_t>(h_q) * d, rk = static_cast<int64_t>(h_kv) * d;
+  if (const int rc = check_rows(q, ldq, rq, dtype, "q", fn)) return rc;
+  if (const int rc = check_rows(k, ldk, rk, dtype, "k", fn)) return rc;
+  if (const int rc = check_rows(v, ldv, rk, dtype, "v", fn)) return rc;
+  if (const int rc = check_rows(o, rq, rq, dtype, "o", fn)) return rc;
+  if (o == q || o == k || o == v) return fail(TREE_ERR_INVALID_ARG, "%s: o must not alias q, k or v", fn);
+  if (const int rc = check_dplan(aplan, dplan, dplan_bytes, fn)) return rc;
+  const int32_t* base = static_cast<const int32_t*>(dplan);
+  tg::AttnArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = o;
+  a.lse = lse;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.tok_d = base + p.m_d;
+  a.tok_e = base + p.m_e;
+  a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_q);
+  a.runs = reinterpret_cast<const tg::AttnRun*>(base + p.m_runs);
+  a.n_items = p.n_qtiles;
+  a.n_tok = p.n_tokens;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.scale = scale;
+  const hipError_t e = tg::launch_attention(a, d, dtype, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_attention: launch", e);
+  return TREE_OK;
+}
+
+size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
+                                               int32_t d) {
+  if (!aplan || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0) return 0;
+  const tg::AttnPlan& p = aplan->p;
+  const int32_t split = attention_split(p, h_q, h_kv);
+  const size_t slots = split > 1 ? static_cast<size_t>(p.n_kitems) * split : p.n_multi_parts;
+  return attention_delta_bytes(p, h_q) + slots * h_kv * 2 * tg::kKTile * d * sizeof(float);
+}
+
+int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                            const void* dout, void* dq, void* dk, void* dv, int64_t ldq, int64_t ldk, int64_t ldv,
+                            int64_t ldo, int64_t lddo, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d,
+                            float scale, int32_t dtype, const tree_attention_plan_t* aplan, const void* dplan,
+                            size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "tree_attention_backward";
+  if (!aplan || !q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !dplan)
+    return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  const tg::AttnPlan& p = aplan->p;
+  if (const int rc = check_attention(p, n_tokens, h_q, h_kv, d, scale, dtype, fn)) return rc;
+  const int64_t rq = static_cast<int64_t>(h_q) * d, rk = static_cast<int64_t>(h_kv) * d;
+  if (const int rc = check_rows(q, ldq, rq, dtype, "q", fn)) return rc;
+  if (const int rc = check_rows(k, ldk, rk, dtype, "k", fn)) return rc;
+  if (const int rc = check_rows(v, ldv, rk, dtype, "v", fn)) return rc;
+  if (const int rc = check_rows(o, ldo, rq, dtype, "o", fn)) return rc;
+  if (const int rc = check_rows(dout, lddo, rq, dtype, "dout", fn)) return rc;
+  if (const int rc = check_rows(dq, rq, rq, dtype, "dq", fn)) return rc;
+  if (const int rc = check_rows(dk, rk, rk, dtype, "dk", fn)) return rc;
+  if (const int rc = check_rows(dv, rk, rk, dtype, "dv", fn)) return rc;
+  const void* outs[3] = {dq, dk, dv};
+  const void* ins[5] = {q, k, v, o, dout};
+  for (const void* x : outs)
+    for (const void* y : ins)
+      if (x == y) return fail(TREE_ERR_INVALID_ARG, "%s: gradients must not alias the inputs", fn);
+  if (dq == dk || dq == dv || dk == dv) return fail(TREE_ERR_INVALID_ARG, "%s: gradients must not alias", fn);
+  const size_t need = tree_attention_backward_workspace_bytes(aplan, h_q, h_kv, d);
+  if (!ws || ws_bytes < need)
+    return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, need);
+  if (reinterpret_cast<uintptr_t>(ws) % 16 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: the workspace is not aligned to 16 bytes", fn);
+  if (const int rc = check_dplan(aplan, dplan, dplan_bytes, fn)) return rc;
+  const int32_t* base = static_cast<const int32_t*>(dplan);
+  tg::AttnArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.dout = dout;
+  a.out = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.lse = const_cast<float*>(lse);
+  a.delta = static_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + attention_delta_bytes(p, h_q));
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldo = ldo;
+  a.lddo = lddo;
+  a.tok_d = base + p.m_d;
+  a.tok_e = base + p.m_e;
+  a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_q);
+  a.runs = reinterpret_cast<const tg::AttnRun*>(base + p.m_runs);
+  a.parts = reinterpret_cast<const tg::AttnParts*>(base + p.m_parts);
+  a.n_items = p.n_qtiles;
+  a.n_multi_parts = p.n_multi_parts;
+  a.n_tok = p.n_tokens;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.split = attention_split(p, h_q, h_kv);
+  a.n_parts = a.split > 1 ? p.n_ktiles : p.n_multi;
+  a.scale = scale;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = tg::launch_attention_dq(a, d, dtype, st);  // also delta
+  if (e == hipSuccess) {
+    a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_k);
+    a.n_items = p.n_kitems;
+    e = tg::launch_attention_dkv(a, d, dtype, st);
+  }
+  if (e != hipSuccess) return hip_fail("tree_attention_backward: launch", e);
+  return TREE_OK;
+}
+
+size_t tree_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_k) {
+  if (n_rows <= 0 || vocab <= 0 || vocab > (1 << 30) || top_k < 0 || top_k > TREE_MAX_TOP_K) return 0;
+  const Spread s = logprob_spread(n_rows, vocab);
+  return s.split == 1 ? 0 : static_cast<size_t>(n_rows) * s.split * (16 + 8 * top_k);
+}
+
+int tree_logprobs(const void* logits, const void* tokens, float* logp, float* entropy, float* lse, float* top_logp,
+                  int32_t* top_id, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab,
+                  int32_t token_bytes, float temperature, int32_t top_k, int32_t dtype, const tree_plan_t* plan,
+                  const void* dplan, size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "tree_logprobs";
+  if (!plan || !logits || !tokens || !logp || !entropy || !lse || !dplan)
+    return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  const tg::Plan& p = plan->p;
+  if (const int rc = check_logprobs(p, ld, n_tokens, first_row, n_rows, vocab, token_bytes, temperature, dtype, fn))
+    return rc;
+  if (top_k < 0 || top_k > TREE_MAX_TOP_K || top_k > vocab)
+    return fail(TREE_ERR_INVALID_ARG, "%s: top_k %d must be in 0..min(%d, vocab)", fn, top_k, TREE_MAX_TOP_K);
+  if (top_k > 0 && (!top_logp || !top_id)) return fail(TREE_ERR_INVALID_ARG, "%s: top_logp or top_id is null", fn);
+  const size_t need = tree_logprobs_workspace_bytes(n_rows, vocab, top_k);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, need);
+  if (need > 0 && reinterpret_cast<uintptr_t>(ws) % 16 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: the workspace is not aligned to 16 bytes", fn);
+  if (const int rc = check_dplan(plan, dplan, dplan_bytes, fn)) return rc;
+  const int32_t* base = static_cast<const int32_t*>(dplan);
+  const Spread s = logprob_spread(n_rows, vocab);
+  tg::LogprobArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.token64 = token_bytes == 8;
+  a.first_row = first_row;
+  a.n_rows = n_rows;
+  a.vocab = vocab;
+  a.inv_t = 1.f / temperature;
+  a.top_k = top_k;
+  a.split = s.split;
+  a.slice = s.slice;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_logp = top_logp;
+  a.top_id = top_id;
+  a.part = static_cast<float*>(ws);
+  a.seg_off = base + p.m_seg_off;
+  a.parent = base + p.m_parent;
+  a.kid_off = base + p.m_kid_off;
+  a.kid = base + p.m_kid;
+  a.n_seg = p.n_seg;
+  const hipError_t e = tg::launch_logprobs(a, dtype, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_logprobs: launch", e);
+  return TREE_OK;
+}
+
+int tree_logprobs_backward(const void* logits, const void* tokens, const float* lse, const float* entropy,
+                           const float* dlogp, const float* dentropy, void* dlogits, int64_t ld, int64_t ldd,
+                           int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab, int32_t token_bytes,
+                           float temperature, int32_t dtype, const tree_plan_t* plan, const void* dplan,
+                           size_t dplan_bytes, void* stream) {
+  const char* fn = "tree_logprobs_backward";
+  if (!plan || !logits || !tokens || !lse || !dlogp || !dlogits || !dplan || (dentropy && !entropy))
+    return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  const tg::Plan& p = plan->p;
+  if (const int rc = check_logprobs(p, ld, n_tokens, first_row, n_rows, vocab, token_bytes, temperature, dtype, fn))
+    return rc;
+  if (const int rc = check_logprobs(p, ldd, n_tokens, first_row, n_rows, vocab, token_bytes, temperature, dtype, fn))
+    return rc;
+  if (dlogits == logits && ldd != ld)
+    return fail(TREE_ERR_INVALID_ARG, "%s: dlogits over logits needs ldd = ld", fn);
+  if (const int rc = check_dplan(plan, dplan, dplan_bytes, fn)) return rc;
+  const int32_t* base = static_cast<const int32_t*>(dplan);
+  const Spread s = logprob_backward_spread(n_rows, vocab);
+  if (static_cast<int64_t>(n_rows) * s.split >= (int64_t(1) << 31))
+    return fail(TREE_ERR_INVALID_ARG, "%s: %d rows of %d columns are too many for one call", fn, n_rows, vocab);
+  tg::LogprobArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.token64 = token_bytes == 8;
+  a.first_row = first_row;
+  a.n_rows = n_rows;
+  a.vocab = vocab;
+  a.inv_t = 1.f / temperature;
+  a.split = s.split;
+  a.slice = s.slice;
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  a.lse_in = lse;
+  a.entropy_in = entropy;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  a.seg_off = base + p.m_seg_off;
+  a.parent = base + p.m_parent;
+  a.kid_off = base + p.m_kid_off;
+  a.kid = base + p.m_kid;
+  a.n_seg = p.n_seg;
+  const hipError_t e = tg::launch_logprobs_backward(a, dtype, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_logprobs_backward: launch", e);
   return TREE_OK;
 }
 

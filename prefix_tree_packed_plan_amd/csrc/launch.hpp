@@ -201,4 +201,81 @@ struct SsdArgs {
 hipError_t launch_ssd_scan(const SsdArgs& a, int d_state, int head_dim, int dtype, hipStream_t stream);
 bool ssd_supported(int d_state, int head_dim, int dtype);
 
+struct AttnItem;
+struct AttnRun;
+struct AttnParts;
+
+// Tree attention (tree_attn.hip).  ld*: elements between a tensor's token
+// rows; heads are d elements apart.  o, dq, dk, dv are contiguous.
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* o;     // backward: the forward's output
+  const void* dout;  // backward
+  void* out;         // forward's o, or dq
+  void* dk;
+  void* dv;
+  float* lse;        // [N, h_q] natural log; written by the forward, read by the backward
+  float* delta;      // backward workspace [N, h_q]: sum over d of dout * o
+  float* part;       // backward workspace: partial dk, dv [slot, h_kv, 2, kKTile, d]
+  int64_t ldq, ldk, ldv, ldo, lddo;
+  const int32_t* tok_d;  // [N + 1]
+  const int32_t* tok_e;  // [N + 1]
+  const AttnItem* items;
+  const AttnRun* runs;
+  const AttnParts* parts;
+  int32_t n_items;
+  int32_t n_parts;       // key tiles whose partial sums are added (reduce launch)
+  int32_t n_multi_parts; // parts numbered below this belong to tiles with several
+  int32_t n_tok;
+  int32_t h_q, h_kv;
+  int32_t split;         // dk, dv: work-groups a group's query heads are spread over
+  float scale;
+};
+
+bool attention_supported(int d, int dtype);
+hipError_t launch_attention(const AttnArgs& a, int d, int dtype, hipStream_t stream);
+hipError_t launch_attention_dq(const AttnArgs& a, int d, int dtype, hipStream_t stream);
+hipError_t launch_attention_dkv(const AttnArgs& a, int d, int dtype, hipStream_t stream);
+
+// Token log probabilities over the trie (tree_logprobs.hip).  Rows are
+// packed token rows first_row .. first_row + n_rows - 1; `logits` holds just
+// those.  Token t's logits are the row in front of it on its path.
+struct LogprobArgs {
+  const void* logits;   // [n_rows, vocab], ld elements between rows
+  int64_t ld;
+  const void* tokens;   // [N], int32 or int64
+  int32_t token64;
+  int32_t first_row, n_rows, vocab;
+  float inv_t;          // 1 / temperature
+  int32_t top_k;
+  int32_t split;        // work-groups a row is spread over
+  int32_t slice;        // columns of one of them
+  float* logp;          // [N]
+  float* entropy;       // [n_rows]
+  float* lse;           // [n_rows]
+  float* top_logp;      // [n_rows, top_k] or null
+  int32_t* top_id;      // [n_rows, top_k] or null
+  float* part;          // workspace [n_rows, split, 4] and the lists (split > 1)
+  // backward
+  const float* dlogp;     // [N]
+  const float* dentropy;  // [n_rows] or null
+  const float* lse_in;
+  const float* entropy_in;
+  void* dlogits;          // [n_rows, vocab], ldd elements between rows
+  int64_t ldd;
+  const int32_t* seg_off;
+  const int32_t* parent;
+  const int32_t* kid_off;
+  const int32_t* kid;
+  int32_t n_seg;
+};
+
+constexpr int kMaxTopK = 64;          // one list entry per lane
+constexpr int kMaxSlice = 1 << 17;    // columns a work-group takes at most
+
+hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_logprobs_backward(const LogprobArgs& a, int dtype, hipStream_t stream);
+
 }  // namespace tg

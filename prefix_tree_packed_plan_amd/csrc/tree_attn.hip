@@ -1,0 +1,821 @@
+// Tree attention, forward and backward (gfx950).  Per query head and token i,
+// over the tokens j on i's root-to-token path (attn_plan.hpp):
+//     s_ij = scale q_i . k_j,  p_ij = exp(s_ij) / sum_j exp(s_ij),
+//     o_i = sum_j p_ij v_j,    lse_i = log sum_j exp(s_ij),
+// and, for given dO, with delta_i = dO_i . o_i and p recomputed from lse:
+//     dv_j = sum_i p_ij dO_i,  ds_ij = p_ij (dO_i . v_j - delta_i),
+//     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i.
+//
+// All products run on 32x32 MFMA tiles whose accumulator keeps one row of
+// the softmax in one lane column: the scores are computed transposed
+// (keys x queries), lane l holds 16 keys of query l % 32, and row sums and
+// maxima need one exchange between lanes l and l ^ 32.  The accumulator is
+// then the B operand of the next product as it stands, because an MFMA's
+// contraction index may be permuted if both operands agree: contraction slot
+// (h = l / 32, e) is row 4h + e % 4 + 8 (e / 4) of the block, which is where
+// the accumulator has its rows, and the A operand (V, K, Q or dO transposed)
+// is read from LDS in that order by the transposing read.
+//
+// fp32 inputs run the same code on fp32 MFMA (32x32x2), four per 16-byte
+// fragment, with exact products.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/tree_gdn.h"
+#include "attn_plan.hpp"
+#include "chunk_mfma.hpp"
+#include "launch.hpp"
+
+namespace tg {
+
+namespace {
+
+using chunk::bf16x8;
+using chunk::ex2;
+using chunk::kLog2e;
+using chunk::lds_void;
+using chunk::pk2;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(1))) const void glb_void;
+typedef __attribute__((address_space(3))) const chunk::u32x4 lds_u4;
+
+// 16 bytes from LDS.
+__device__ __forceinline__ uint4 lds16(const char* p) {
+  const chunk::u32x4 w = *(lds_u4*)p;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRows = 64;  // rows of a staged tile
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// ---- LDS tiles --------------------------------------------------------------
+// Rows of RB bytes; the 16-byte chunk c of row r sits at slot c ^ swz(r), so
+// that operand reads (32 rows, one chunk each) and transposing reads (4 rows
+// x 64 bytes) touch every bank once per half wave.
+template <int RB>
+__device__ __forceinline__ constexpr int swz(int r) {
+  return RB >= 256 ? 4 * (r & 3) + ((r >> 2) & 3) : RB == 128 ? 4 * ((r >> 1) & 1) + ((r >> 2) & 3) : (r >> 2) & 3;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x16 mm(const uint4 a, const uint4 b, const f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mm<uint16_t>(const uint4 a, const uint4 b, const f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mm<float>(const uint4 a, const uint4 b, f32x16 c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+}
+
+// Compile-time sizes of element type T and head size D.  A fragment is 16
+// bytes a lane: contraction depth KD (16 in bf16, 8 in fp32).
+template <typename T, int D>
+struct Cfg {
+  static constexpr int RB = D * int(sizeof(T));  // bytes of a row
+  static constexpr int NC = RB / 16;             // 16-byte chunks of a row
+  static constexpr int NK = RB / 32;             // fragments along a row
+  static constexpr int NDB = D / 32;             // 32-wide blocks of a row
+  static constexpr int KD = 32 / int(sizeof(T));
+  static constexpr int NS = 32 / KD;             // fragments along 32 rows
+  static constexpr int TILE = kRows * RB;        // bytes of a staged tile
+  static constexpr int NI = TILE / 1024 / 4;     // DMA instructions of each of 4 waves
+};
+
+// Fragment s of 32 accumulator rows as the B operand of the next product
+// (bf16: rounded to nearest even, at most 2^-9 of the value).
+template <typename T>
+__device__ __forceinline__ uint4 frag(const f32x16& p, int s);
+template <>
+__device__ __forceinline__ uint4 frag<uint16_t>(const f32x16& p, int s) {
+  return make_uint4(pk2(p[8 * s], p[8 * s + 1]), pk2(p[8 * s + 2], p[8 * s + 3]), pk2(p[8 * s + 4], p[8 * s + 5]),
+                    pk2(p[8 * s + 6], p[8 * s + 7]));
+}
+template <>
+__device__ __forceinline__ uint4 frag<float>(const f32x16& p, int s) {
+  return make_uint4(__float_as_uint(p[4 * s]), __float_as_uint(p[4 * s + 1]), __float_as_uint(p[4 * s + 2]),
+                    __float_as_uint(p[4 * s + 3]));
+}
+
+// Byte offsets of this lane's operand reads in a tile.
+template <typename T, int D>
+struct Reader {
+  using C = Cfg<T, D>;
+  int row;  // operand reads: row lane % 32, chunk lane / 32
+  int tr;   // transposing reads
+  __device__ __forceinline__ explicit Reader(int lane) {
+    const int r = lane & 31, h = lane >> 5, i = lane & 15;
+    row = r * C::RB + 16 * (h ^ swz<C::RB>(r));
+    if (sizeof(T) == 2) {
+      const int k = 4 * h + (i >> 2);
+      tr = k * C::RB + 16 * ((2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) ^ swz<C::RB>(k)) + 8 * (i & 1);
+    } else {
+      tr = 4 * h * C::RB + 16 * ((r >> 2) ^ h) + 4 * (r & 3);
+    }
+  }
+  // Rows 32 kb + lane % 32, fragment ks of the row.
+  __device__ __forceinline__ uint4 rows(const char* t, int kb, int ks) const {
+    return lds16(t + ((row ^ (32 * ks)) + kb * 32 * C::RB));
+  }
+  // Fragment s of rows 32 kb .. 32 kb + 31 of the transposed tile: column 32
+  // db + lane % 32.
+  __device__ __forceinline__ uint4 cols(const char* t, int kb, int s, int db) const;
+};
+template <typename T, int D>
+__device__ __forceinline__ uint4 Reader<T, D>::cols(const char* t, int kb, int s, int db) const {
+  if constexpr (sizeof(T) == 2) {
+    const int o = (tr ^ (64 * db)) + (32 * kb + 16 * s) * C::RB;
+    const int o8 = (tr ^ (64 * db) ^ 32) + (32 * kb + 16 * s + 8) * C::RB;
+    return chunk::cat(chunk::tile_tr(t, o), chunk::tile_tr(t, o8));
+  } else {
+    uint4 r;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int sj = (C::RB >= 256 ? 4 * j : 4 * (j >> 1)) ^ (2 * (s & 1));
+      const int o = (tr ^ (16 * sj) ^ (128 * db)) + (32 * kb + 8 * s + j) * C::RB;
+      w[j] = *(__attribute__((address_space(3))) const uint32_t*)(t + o);
+    }
+    return r;
+  }
+}
+
+// ---- values that are not finite ----------------------------------------------
+// A masked pair's probability is 0, but 0 times an infinity or a NaN of a row
+// the token does not see would still reach it through the MFMA.  In tiles
+// with masked pairs such elements are therefore left out of the product and
+// added, one row at a time, where the probability is not 0.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) {  // nonzero iff one of the word's elements is not finite
+  if (sizeof(T) == 4) return (w & 0x7F800000u) == 0x7F800000u;
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t finite(uint32_t w) {  // elements that are not finite replaced by 0
+  if (sizeof(T) == 4) return nonfinite<T>(w) ? 0u : w;
+  const uint32_t f = nonfinite<T>(w) >> 15;  // bit 0, bit 16
+  return w & ~(f * 0xFFFFu);
+}
+template <typename T>
+__device__ __forceinline__ uint4 finite(const uint4 w) {
+  return make_uint4(finite<T>(w.x), finite<T>(w.y), finite<T>(w.z), finite<T>(w.w));
+}
+// Whether this thread's share (a quarter of a wave's tile) has one.
+template <typename T, int D>
+__device__ __forceinline__ bool any_nonfinite(const char* t, int tid) {
+  using C = Cfg<T, D>;
+  uint32_t f = 0;
+#pragma unroll
+  for (int i = 0; i < C::TILE / 4096; ++i) {
+    const uint4 w = lds16(t + 16 * (tid + 256 * i));
+    f |= nonfinite<T>(w.x) | nonfinite<T>(w.y) | nonfinite<T>(w.z) | nonfinite<T>(w.w);
+  }
+  return f != 0;
+}
+template <typename T>
+__device__ __forceinline__ float element(const char* p);
+template <>
+__device__ __forceinline__ float element<uint16_t>(const char* p) {
+  return __uint_as_float(uint32_t(*(__attribute__((address_space(3))) const uint16_t*)p) << 16);
+}
+template <>
+__device__ __forceinline__ float element<float>(const char* p) {
+  return *(__attribute__((address_space(3))) const float*)p;
+}
+// acc[db] (columns 32 db + accumulator row, of the tile's rows weighted by w)
+// += the elements the sanitised product left out.
+template <typename T, int D>
+__device__ __attribute__((noinline)) void add_nonfinite(f32x16* acc, const f32x16* w, const char* t, int lane) {
+  using C = Cfg<T, D>;
+  bool bad = false;  // this lane's row (= lane) has one
+#pragma unroll 1
+  for (int c = 0; c < C::NC; ++c) {
+    const uint4 x = lds16(t + lane * C::RB + 16 * c);
+    bad = bad || (nonfinite<T>(x.x) | nonfinite<T>(x.y) | nonfinite<T>(x.z) | nonfinite<T>(x.w));
+  }
+  const int h = lane >> 5;
+  for (uint64_t m = __ballot(bad); m; m &= m - 1) {
+    const int c = __builtin_ctzll(m), kb = c >> 5, cc = c & 31;
+    const int reg = 4 * (cc >> 3) + (cc & 3), half = (cc >> 2) & 1;
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x = kb == 0 && i == reg ? w[0][i] : x;
+      x = kb == 1 && i == reg ? w[1][i] : x;
+    }
+    const float y = __shfl_xor(x, 32, 64);
+    x = h == half ? x : y;
+#pragma unroll
+    for (int db = 0; db < C::NDB; ++db)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int d = 32 * db + 8 * (i >> 2) + 4 * h + (i & 3);
+        const int by = d * int(sizeof(T));
+        const float e = element<T>(t + c * C::RB + 16 * ((by >> 4) ^ swz<C::RB>(c)) + (by & 15));
+        const bool lost = (__float_as_uint(e) & 0x7F800000u) == 0x7F800000u;
+        if (lost && x != 0.f) acc[db][i] += x * e;
+      }
+  }
+}
+
+// acc[db] += (rows of the tile, transposed) times w: the tile's 64 rows are
+// contracted with the 64 accumulator rows of w[0], w[1].
+template <typename T, int D, bool SAFE>
+__device__ __forceinline__ void contract(f32x16* acc, const f32x16* w, const char* t, const Reader<T, D>& rd) {
+  using C = Cfg<T, D>;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int s = 0; s < C::NS; ++s) {
+      const uint4 b = frag<T>(w[kb], s);
+#pragma unroll
+      for (int db = 0; db < C::NDB; ++db) {
+        uint4 a = rd.cols(t, kb, s, db);
+        if (SAFE) a = finite<T>(a);
+        acc[db] = mm<T>(a, b, acc[db]);
+      }
+    }
+}
+
+// ---- run lists ----------------------------------------------------------------
+// The packed row of virtual position v, for tiles of kRows positions taken in
+// order (uniform over the wave but for `row`'s argument).
+struct Cursor {
+  const AttnRun* runs;
+  int n, end;  // runs; positions of this item end here
+  int cur, virt, row0, next;
+  __device__ __forceinline__ Cursor(const AttnRun* r, const AttnItem& it) : runs(r + it.run_off), n(it.n_runs), end(it.v1) {
+    cur = 0;
+    load();
+    seek(it.v0);
+  }
+  __device__ __forceinline__ void load() {
+    virt = runs[cur].virt;
+    row0 = runs[cur].row;
+    next = cur + 1 < n ? runs[cur + 1].virt : 0x7FFFFFFF;
+  }
+  __device__ __forceinline__ void seek(int v) {
+    while (next <= v) {
+      ++cur;
+      load();
+    }
+  }
+  // v0 lies in run `cur`; x < kRows.  Positions past the end repeat the last.
+  __device__ __forceinline__ int row(int v0, int x) const {
+    const int v = min(v0 + x, end - 1);
+    if (min(v0 + kRows, end) <= next) return row0 + (v - virt);
+    int c = cur, lo = virt, r = row0;
+    while (c + 1 < n) {
+      const int nv = runs[c + 1].virt;
+      if (nv > v) break;
+      ++c;
+      lo = nv;
+      r = runs[c].row;
+    }
+    return r + (v - lo);
+  }
+};
+
+__device__ __forceinline__ void dma16(const void* src, char* lds) {
+  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(const void* src, char* lds) {
+  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)lds, 4, 0, 0);
+}
+__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// The 64 rows at virtual position v0 of two tensors into LDS tiles ta, tb, by
+// 4 waves (wave w: every fourth group of 1024 bytes).
+template <typename T, int D>
+__device__ __forceinline__ void stage(const Cursor& cs, int v0, const char* a, int64_t lda, char* ta, const char* b,
+                                      int64_t ldb, char* tb, int wave, int lane) {
+  using C = Cfg<T, D>;
+#pragma unroll
+  for (int i = 0; i < C::NI; ++i) {
+    const int g = 4 * i + wave, r = g * (1024 / C::RB) + lane / C::NC;
+    const int64_t row = cs.row(v0, r);
+    const int c = 16 * ((lane % C::NC) ^ swz<C::RB>(r));
+    dma16(a + row * lda + c, ta + 1024 * g);
+    dma16(b + row * ldb + c, tb + 1024 * g);
+  }
+}
+
+// The sum or maximum of a lane and the lane 32 away.
+__device__ __forceinline__ float half_swap(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// Fragments of row `p` (D elements): the B operand whose column is this lane.
+template <typename T, int D>
+__device__ __forceinline__ void load_frags(uint4* f, const char* p, int half) {
+#pragma unroll
+  for (int ks = 0; ks < Cfg<T, D>::NK; ++ks) f[ks] = *reinterpret_cast<const uint4*>(p + 32 * ks + 16 * half);
+}
+
+// Stores the accumulator's column (this lane's row of the result, D values
+// times f) in 16-byte pieces: lanes l and l ^ 32 hold 4 columns each of every
+// 8, and exchange so that each writes 8 (bf16).
+template <typename T, int D>
+__device__ __forceinline__ void store_row(T* p, const f32x16* acc, float f, int half, bool on) {
+#pragma unroll
+  for (int db = 0; db < D / 32; ++db) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (on)
+          *reinterpret_cast<float4*>(p + 32 * db + 8 * c + 4 * half) =
+              make_float4(acc[db][4 * c] * f, acc[db][4 * c + 1] * f, acc[db][4 * c + 2] * f, acc[db][4 * c + 3] * f);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        const uint32_t x0 = pk2(acc[db][4 * c] * f, acc[db][4 * c + 1] * f);
+        const uint32_t x1 = pk2(acc[db][4 * c + 2] * f, acc[db][4 * c + 3] * f);
+        const uint32_t y0 = pk2(acc[db][4 * c + 4] * f, acc[db][4 * c + 5] * f);
+        const uint32_t y1 = pk2(acc[db][4 * c + 6] * f, acc[db][4 * c + 7] * f);
+        const auto r0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+        const auto r1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+        if (on) *reinterpret_cast<uint4*>(p + 32 * db + 8 * (c + half)) = make_uint4(r0[0], r1[0], r0[1], r1[1]);
+      }
+    }
+  }
+}
+
+// ---- forward --------------------------------------------------------------------
+template <typename T, int D>
+struct FwdSmem {
+  alignas(16) char k[2][Cfg<T, D>::TILE];
+  alignas(16) char v[2][Cfg<T, D>::TILE];
+  alignas(16) int d[2][kRows];
+  alignas(16) int e[2][kRows];
+};
+
+// Visibility of one staged tile of keys to the queries of one lane column
+// (position dq): bit i of the result, accumulator row i of block kb.
+__device__ __forceinline__ uint32_t visible(const int* d, const int* e, int kb, int half, int dq) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int4 x = *reinterpret_cast<const int4*>(d + 32 * kb + 8 * c + 4 * half);
+    const int4 y = *reinterpret_cast<const int4*>(e + 32 * kb + 8 * c + 4 * half);
+    m |= (x.x <= dq && dq < y.x ? 1u : 0u) << (4 * c);
+    m |= (x.y <= dq && dq < y.y ? 1u : 0u) << (4 * c + 1);
+    m |= (x.z <= dq && dq < y.z ? 1u : 0u) << (4 * c + 2);
+    m |= (x.w <= dq && dq < y.w ? 1u : 0u) << (4 * c + 3);
+  }
+  return m;
+}
+
+// Least and greatest position of the wave's rows (lane l: row l % 32).
+__device__ __forceinline__ void span(int dq, int& lo, int& hi) {
+  lo = hi = dq;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    lo = min(lo, __shfl_xor(lo, o, 64));
+    hi = max(hi, __shfl_xor(hi, o, 64));
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+}
+
+// One work-group of four waves: kQTile rows of one query head, 32 a wave.
+template <typename T, int D>
+__global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
+  using C = Cfg<T, D>;
+  __shared__ FwdSmem<T, D> sm;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.x % a.h_q, hk = h / (a.h_q / a.h_kv);
+  const AttnItem it = a.items[blockIdx.x / a.h_q];
+  const int64_t row = int64_t(it.tile) * kQTile + 32 * wave + (lane & 31);
+  const bool on = row < a.n_tok;
+  const int64_t r = on ? row : a.n_tok - 1;
+  const char* kp = static_cast<const char*>(a.k) + int64_t(hk) * C::RB;
+  const char* vp = static_cast<const char*>(a.v) + int64_t(hk) * C::RB;
+  const int64_t ldk = a.ldk * int64_t(sizeof(T)), ldv = a.ldv * int64_t(sizeof(T));
+
+  Cursor cs(a.runs, it);
+  auto fetch = [&](int v0, int buf) {
+    cs.seek(v0);
+    stage<T, D>(cs, v0, kp, ldk, sm.k[buf], vp, ldv, sm.v[buf], wave, lane);
+    if (v0 + kRows > it.n_full && wave < 2) {
+      const int x = v0 + lane < cs.end ? cs.row(v0, lane) : a.n_tok;
+      if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
+      else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
+    }
+  };
+  fetch(0, 0);
+
+  uint4 q[C::NK];
+  load_frags<T, D>(q, static_cast<const char*>(a.q) + (r * a.ldq + int64_t(h) * D) * int64_t(sizeof(T)), half);
+  const int dq = a.tok_d[r];
+  int dlo, dhi;
+  span(dq, dlo, dhi);
+
+  const Reader<T, D> rd(lane);
+  const float c = a.scale * kLog2e;
+  f32x16 acc[C::NDB];
+#pragma unroll
+  for (int db = 0; db < C::NDB; ++db) acc[db] = zero16();
+  float m = kNegInf, l = 0.f;  // running maximum of q.k (both halves of the wave agree), this lane's part of the sum
+
+  int buf = 0;
+  for (int v0 = 0; v0 < it.n_total; v0 += kRows, buf ^= 1) {
+    wait_dma();
+    __syncthreads();
+    if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
+    const char* kt = sm.k[buf];
+    const char* vt = sm.v[buf];
+    bool masked = v0 + kRows > it.n_full, bad = false;
+    if (masked) {
+      bad = __syncthreads_or(any_nonfinite<T, D>(vt, threadIdx.x));
+      const int kd = sm.d[buf][lane], ke = sm.e[buf][lane];
+      if (__ballot(kd <= dhi && dlo < ke) == 0) continue;  // no row of this wave sees a key of this tile
+      masked = __ballot(kd <= dlo && dhi < ke) != ~0ull;   // every row sees every key
+    }
+    f32x16 p[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      p[kb] = zero16();
+#pragma unroll
+      for (int ks = 0; ks < C::NK; ++ks) p[kb] = mm<T>(rd.rows(kt, kb, ks), q[ks], p[kb]);
+    }
+    if (masked) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : kNegInf;
+      }
+    }
+    float mt = p[0][0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, p[0][i]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mt = fmaxf(mt, p[1][i]);
+    mt = fmaxf(mt, half_swap(mt));
+    // A row's accumulators follow its maximum only when that has grown by more
+    // than 2^8: until then the probabilities stay below 2^8, harmless in fp32
+    // and no less exact in bf16.
+    const bool grown = (mt - m) * c > 8.f;
+    if (__any(grown)) {
+      const float mn = grown ? mt : m;
+      const float al = m == kNegInf ? 0.f : ex2((m - mn) * c);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int db = 0; db < C::NDB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[db][i] *= al;
+    }
+    const float mc = m == kNegInf ? 0.f : m * c;  // -inf: this row has seen no key yet
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[kb][i] = ex2(fmaf(p[kb][i], c, -mc));
+        l += p[kb][i];
+      }
+    if (masked && bad) {
+      contract<T, D, true>(acc, p, vt, rd);
+      add_nonfinite<T, D>(acc, p, vt, lane);
+    } else {
+      contract<T, D, false>(acc, p, vt, rd);
+    }
+  }
+  l += half_swap(l);
+  const float inv = 1.f / l;
+  store_row<T, D>(static_cast<T*>(a.out) + (r * a.h_q + h) * D, acc, inv, half, on);
+  if (a.lse && on && half == 0) a.lse[r * a.h_q + h] = (m * c + __log2f(l)) * kLn2;
+}
+
+// ---- gradient of q -----------------------------------------------------------------
+// Same tiles as the forward; also leaves delta for the other gradients.
+template <typename T, int D>
+__global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_kernel(AttnArgs a) {
+  using C = Cfg<T, D>;
+  __shared__ FwdSmem<T, D> sm;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.x % a.h_q, hk = h / (a.h_q / a.h_kv);
+  const AttnItem it = a.items[blockIdx.x / a.h_q];
+  const int64_t row = int64_t(it.tile) * kQTile + 32 * wave + (lane & 31);
+  const bool on = row < a.n_tok;
+  const int64_t r = on ? row : a.n_tok - 1;
+  const char* kp = static_cast<const char*>(a.k) + int64_t(hk) * C::RB;
+  const char* vp = static_cast<const char*>(a.v) + int64_t(hk) * C::RB;
+  const int64_t ldk = a.ldk * int64_t(sizeof(T)), ldv = a.ldv * int64_t(sizeof(T));
+
+  Cursor cs(a.runs, it);
+  auto fetch = [&](int v0, int buf) {
+    cs.seek(v0);
+    stage<T, D>(cs, v0, kp, ldk, sm.k[buf], vp, ldv, sm.v[buf], wave, lane);
+    if (v0 + kRows > it.n_full && wave < 2) {
+      const int x = v0 + lane < cs.end ? cs.row(v0, lane) : a.n_tok;
+      if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
+      else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
+    }
+  };
+  fetch(0, 0);
+
+  uint4 q[C::NK], g[C::NK];
+  load_frags<T, D>(q, static_cast<const char*>(a.q) + (r * a.ldq + int64_t(h) * D) * int64_t(sizeof(T)), half);
+  load_frags<T, D>(g, static_cast<const char*>(a.dout) + (r * a.lddo + int64_t(h) * D) * int64_t(sizeof(T)), half);
+  float delta = 0.f;
+  {
+    const char* op = static_cast<const char*>(a.o) + (r * a.ldo + int64_t(h) * D) * int64_t(sizeof(T));
+#pragma unroll
+    for (int ks = 0; ks < C::NK; ++ks) {
+      const uint4 o = *reinterpret_cast<const uint4*>(op + 32 * ks + 16 * half);
+      const uint32_t x[4] = {o.x, o.y, o.z, o.w}, y[4] = {g[ks].x, g[ks].y, g[ks].z, g[ks].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (sizeof(T) == 4) {
+          delta = fmaf(__uint_as_float(x[j]), __uint_as_float(y[j]), delta);
+        } else {
+          delta = fmaf(chunk::lo_f(x[j]), chunk::lo_f(y[j]), delta);
+          delta = fmaf(chunk::hi_f(x[j]), chunk::hi_f(y[j]), delta);
+        }
+      }
+    }
+    delta += half_swap(delta);
+    if (on && half == 0) a.delta[r * a.h_q + h] = delta;
+  }
+  const float lse2 = a.lse[r * a.h_q + h] * kLog2e;
+  const int dq = a.tok_d[r];
+  int dlo, dhi;
+  span(dq, dlo, dhi);
+
+  const Reader<T, D> rd(lane);
+  const float c = a.scale * kLog2e;
+  f32x16 acc[C::NDB];
+#pragma unroll
+  for (int db = 0; db < C::NDB; ++db) acc[db] = zero16();
+
+  int buf = 0;
+  for (int v0 = 0; v0 < it.n_total; v0 += kRows, buf ^= 1) {
+    wait_dma();
+    __syncthreads();
+    if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
+    const char* kt = sm.k[buf];
+    const char* vt = sm.v[buf];
+    bool masked = v0 + kRows > it.n_full, bad = false;
+    if (masked) {
+      bad = __syncthreads_or(any_nonfinite<T, D>(kt, threadIdx.x));
+      const int kd = sm.d[buf][lane], ke = sm.e[buf][lane];
+      if (__ballot(kd <= dhi && dlo < ke) == 0) continue;
+      masked = __ballot(kd <= dlo && dhi < ke) != ~0ull;
+    }
+    f32x16 p[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int ks = 0; ks < C::NK; ++ks) {
+        s = mm<T>(rd.rows(kt, kb, ks), q[ks], s);
+        dp = mm<T>(rd.rows(vt, kb, ks), g[ks], dp);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[kb][i] = ex2(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+      if (masked) {
+        const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : 0.f;
+      }
+    }
+    if (masked && bad) {
+      contract<T, D, true>(acc, p, kt, rd);
+      add_nonfinite<T, D>(acc, p, kt, lane);
+    } else {
+      contract<T, D, false>(acc, p, kt, rd);
+    }
+  }
+  store_row<T, D>(static_cast<T*>(a.out) + (r * a.h_q + h) * D, acc, a.scale, half, on);
+}
+
+// ---- gradients of k and v ------------------------------------------------------------
+template <typename T, int D>
+struct BwdSmem {
+  alignas(16) char q[2][Cfg<T, D>::TILE];
+  alignas(16) char g[2][Cfg<T, D>::TILE];
+  alignas(16) float lse[2][kRows];
+  alignas(16) float delta[2][kRows];
+  alignas(16) int d[2][kRows];
+};
+
+// One work-group of four waves: kKTile keys of one key/value head, 32 a wave,
+// over this item's part of the rows that see them and every split-th query
+// head of the group.
+template <typename T, int D>
+__global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
+  using C = Cfg<T, D>;
+  __shared__ BwdSmem<T, D> sm;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = blockIdx.x % a.split, hk = (blockIdx.x / a.split) % a.h_kv;
+  const AttnItem it = a.items[blockIdx.x / (a.split * a.h_kv)];
+  const int group = a.h_q / a.h_kv;
+  const int key = 32 * wave + (lane & 31);
+  const int64_t row = int64_t(it.tile) * kKTile + key;
+  const bool on = row < a.n_tok;
+  const int64_t r = on ? row : a.n_tok - 1;
+  const int64_t ldq = a.ldq * int64_t(sizeof(T)), ldg = a.lddo * int64_t(sizeof(T));
+
+  Cursor cs(a.runs, it);
+  auto fetch = [&](int v0, int h, int buf) {
+    cs.seek(v0);
+    stage<T, D>(cs, v0, static_cast<const char*>(a.q) + int64_t(h) * C::RB, ldq, sm.q[buf],
+                static_cast<const char*>(a.dout) + int64_t(h) * C::RB, ldg, sm.g[buf], wave, lane);
+    if (wave < 3) {
+      const int64_t x = cs.row(v0, lane);
+      if (wave == 0) dma4(a.lse + x * a.h_q + h, reinterpret_cast<char*>(sm.lse[buf]));
+      else if (wave == 1) dma4(a.delta + x * a.h_q + h, reinterpret_cast<char*>(sm.delta[buf]));
+      else dma4(a.tok_d + (v0 + lane < cs.end ? x : a.n_tok), reinterpret_cast<char*>(sm.d[buf]));
+    }
+  };
+  int h = hk * group + sub;
+  fetch(it.v0, h, 0);
+
+  uint4 kf[C::NK], vf[C::NK];
+  load_frags<T, D>(kf, static_cast<const char*>(a.k) + (r * a.ldk + int64_t(hk) * D) * int64_t(sizeof(T)), half);
+  load_frags<T, D>(vf, static_cast<const char*>(a.v) + (r * a.ldv + int64_t(hk) * D) * int64_t(sizeof(T)), half);
+  const int kd = a.tok_d[r], ke = a.tok_e[r];
+  int kdlo, kdhi, kelo, kehi;
+  span(kd, kdlo, kdhi);
+  span(ke, kelo, kehi);
+
+  const Reader<T, D> rd(lane);
+  const float c = a.scale * kLog2e;
+  f32x16 dk[C::NDB], dv[C::NDB];
+#pragma unroll
+  for (int db = 0; db < C::NDB; ++db) dk[db] = dv[db] = zero16();
+
+  int buf = 0;
+  for (int v0 = it.v0; h < (hk + 1) * group; buf ^= 1) {
+    wait_dma();
+    __syncthreads();
+    int nv = v0 + kRows, nh = h;
+    if (nv >= it.v1) {
+      nv = it.v0;
+      nh += a.split;
+      cs.cur = 0;
+      cs.load();
+    }
+    if (nh < (hk + 1) * group) fetch(nv, nh, buf ^ 1);
+    const char* qt = sm.q[buf];
+    const char* gt = sm.g[buf];
+    bool masked = min(v0 + kRows, it.v1) > it.n_full || v0 + kRows > it.v1, bad_q = false, bad_g = false, skip = false;
+    v0 = nv;
+    h = nh;
+    if (masked) {
+      bad_q = __syncthreads_or(any_nonfinite<T, D>(qt, threadIdx.x));
+      bad_g = __syncthreads_or(any_nonfinite<T, D>(gt, threadIdx.x));
+      const int qd = sm.d[buf][lane];
+      skip = __ballot(kdlo <= qd && qd < kehi) == 0;
+      masked = __ballot(kdhi <= qd && qd < kelo) != ~0ull;
+    }
+    if (skip) continue;
+    f32x16 p[2], ds[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int ks = 0; ks < C::NK; ++ks) {
+        s = mm<T>(rd.rows(qt, kb, ks), kf[ks], s);
+        dp = mm<T>(rd.rows(gt, kb, ks), vf[ks], dp);
+      }
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const int o = 32 * kb + 8 * i4 + 4 * half;
+        const float4 ls = *reinterpret_cast<const float4*>(&sm.lse[buf][o]);
+        const float4 de = *reinterpret_cast<const float4*>(&sm.delta[buf][o]);
+        const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 4 * i4 + j;
+          p[kb][i] = ex2(fmaf(s[i], c, -l4[j] * kLog2e));
+          ds[kb][i] = p[kb][i] * (dp[i] - d4[j]);
+        }
+        if (masked) {
+          const int4 dd = *reinterpret_cast<const int4*>(&sm.d[buf][o]);
+          const int x4[4] = {dd.x, dd.y, dd.z, dd.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool see = kd <= x4[j] && x4[j] < ke;
+            p[kb][4 * i4 + j] = see ? p[kb][4 * i4 + j] : 0.f;
+            ds[kb][4 * i4 + j] = see ? ds[kb][4 * i4 + j] : 0.f;
+          }
+        }
+      }
+    }
+    if (masked && bad_g) {
+      contract<T, D, true>(dv, p, gt, rd);
+      add_nonfinite<T, D>(dv, p, gt, lane);
+    } else {
+      contract<T, D, false>(dv, p, gt, rd);
+    }
+    if (masked && bad_q) {
+      contract<T, D, true>(dk, ds, qt, rd);
+      add_nonfinite<T, D>(dk, ds, qt, lane);
+    } else {
+      contract<T, D, false>(dk, ds, qt, rd);
+    }
+  }
+  if (a.split == 1 && it.part >= a.n_multi_parts) {
+    store_row<T, D>(static_cast<T*>(a.dk) + (r * a.h_kv + hk) * D, dk, a.scale, half, on);
+    store_row<T, D>(static_cast<T*>(a.dv) + (r * a.h_kv + hk) * D, dv, 1.f, half, on);
+  } else {
+    const int64_t slot = (int64_t(it.part) * a.split + sub) * a.h_kv + hk;
+    float* w = a.part + slot * (2 * kKTile * D) + key * D;
+    store_row<float, D>(w, dk, a.scale, half, true);
+    store_row<float, D>(w + kKTile * D, dv, 1.f, half, true);
+  }
+}
+
+// dk, dv of a key tile from its parts, in their order.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  const int hk = blockIdx.y, which = blockIdx.z;
+  const AttnParts pt = a.parts[blockIdx.x];
+  const int64_t slots = int64_t(pt.n_parts) * a.split, slot0 = int64_t(pt.part0) * a.split;
+  T* out = static_cast<T*>(which ? a.dv : a.dk);
+  for (int i = threadIdx.x; i < kKTile * D / 4; i += 256) {
+    const int64_t row = int64_t(pt.tile) * kKTile + i / (D / 4);
+    if (row >= a.n_tok) break;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t j = 0; j < slots; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(
+          a.part + ((slot0 + j) * a.h_kv + hk) * (2 * kKTile * D) + which * kKTile * D)[i];
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    T* p = out + (row * a.h_kv + hk) * D + 4 * (i % (D / 4));
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = s;
+    else *reinterpret_cast<uint2*>(p) = make_uint2(pk2(s.x, s.y), pk2(s.z, s.w));
+  }
+}
+
+template <typename F>
+hipError_t dispatch(int d, int dtype, F f) {
+  if (dtype == TREE_DTYPE_BF16) {
+    if (d == 32) return f(uint16_t{}, std::integral_constant<int, 32>{});
+    if (d == 64) return f(uint16_t{}, std::integral_constant<int, 64>{});
+    if (d == 128) return f(uint16_t{}, std::integral_constant<int, 128>{});
+  } else if (dtype == TREE_DTYPE_F32) {
+    if (d == 32) return f(float{}, std::integral_constant<int, 32>{});
+    if (d == 64) return f(float{}, std::integral_constant<int, 64>{});
+    if (d == 128) return f(float{}, std::integral_constant<int, 128>{});
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+bool attention_supported(int d, int dtype) {
+  return (d == 32 || d == 64 || d == 128) && (dtype == TREE_DTYPE_BF16 || dtype == TREE_DTYPE_F32);
+}
+
+hipError_t launch_attention(const AttnArgs& a, int d, int dtype, hipStream_t stream) {
+  return dispatch(d, dtype, [&](auto t, auto dd) {
+    attn_fwd_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_attention_dq(const AttnArgs& a, int d, int dtype, hipStream_t stream) {
+  return dispatch(d, dtype, [&](auto t, auto dd) {
+    attn_dq_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_attention_dkv(const AttnArgs& a, int d, int dtype, hipStream_t stream) {
+  return dispatch(d, dtype, [&](auto t, auto dd) {
+    attn_dkv_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_items * a.h_kv * a.split), 256, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.n_parts > 0) {
+      attn_join_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_parts, a.h_kv, 2), 256, 0, stream>>>(a);
+      e = hipGetLastError();
+    }
+    return e;
+  });
+}
+
+}  // namespace tg

@@ -1,0 +1,486 @@
+// Log probabilities of a trie's tokens, and their gradient (gfx950).
+//
+// With z = logits / T of one row, lse = log sum_i exp(z_i), p_i = exp(z_i -
+// lse) and H = -sum_i p_i log p_i = lse - sum_i p_i z_i:
+//   token t behind the row:  logp_t = z_{tok t} - lse,
+//   dz_i = sum_t g_t ([i = tok t] - p_i) - h p_i (log p_i + H)
+// for gradients g_t of logp_t and h of H.  A row in the middle of a segment
+// has one token behind it; the last row of a segment has the first token of
+// every child ("Tree Training" section 3.1 Eq. 6: each token's value is the
+// one of its own root-to-leaf path), whose gradients add up in that row.
+//
+// Both kernels read the logits once.  The forward keeps, per lane, a reference
+// value m (raised only when a value passes it by a factor 2^10, so nearly
+// never) and s = sum exp2(c (x - m)), t = sum exp2(c (x - m)) (x - m) with c =
+// log2(e) / T; then H = log s - t / (T s).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tree_gdn.h"
+#include "chunk_mfma.hpp"
+#include "launch.hpp"
+
+namespace tg {
+
+namespace {
+
+using chunk::ex2;
+using chunk::kLog2e;
+using chunk::pk2;
+
+constexpr int kThreads = 256;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kNoId = 0x7FFFFFFF;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const u32x4 w, float* x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = chunk::lo_f(w[j]);
+      x[2 * j + 1] = chunk::hi_f(w[j]);
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float* x) {
+    return u32x4{pk2(x[0], x[1]), pk2(x[2], x[3]), pk2(x[4], x[5]), pk2(x[6], x[7])};
+  }
+  static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
+  static __device__ __forceinline__ void put(uint16_t* p, float x) { *p = static_cast<uint16_t>(pk2(x, x)); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const u32x4 w, float* x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(w[j]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float* x) {
+    return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+  }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ void put(float* p, float x) { *p = x; }
+};
+
+// A slice of a row: columns [0, head) and [tail, n) element by element (they
+// are not part of an aligned 16-byte piece), the rest in `vecs` pieces.
+template <typename T>
+struct Slice {
+  const T* p;
+  int n, head, vecs, tail;
+  __device__ __forceinline__ Slice(const T* base, int count) : p(base), n(count) {
+    constexpr int N = Vec<T>::N;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    head = min(n, off ? N - off : 0);
+    vecs = (n - head) / N;
+    tail = head + vecs * N;
+  }
+  // Element-wise column of thread i (i < ends()).
+  __device__ __forceinline__ int ends() const { return head + n - tail; }
+  __device__ __forceinline__ int end_col(int i) const { return i < head ? i : tail + i - head; }
+};
+
+// The segment of packed row r: a 64-way search by the whole wave.
+__device__ __forceinline__ int seg_of(const int32_t* seg_off, int n_seg, int r, int lane) {
+  int lo = 0, hi = n_seg;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) >> 6, at = lo + lane * step;
+    const bool le = at < hi && seg_off[at] <= r;
+    lo += (__popcll(__ballot(le)) - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// The tokens behind packed row r.
+struct Behind {
+  int n, row;         // how many; the only one's row (middle of a segment)
+  const int32_t *kid, *seg_off;
+  bool root_start;    // r is a root's first token (it has no row in front)
+  __device__ __forceinline__ Behind(const LogprobArgs& a, int r, int lane) : seg_off(a.seg_off) {
+    const int s = seg_of(a.seg_off, a.n_seg, r, lane);
+    const bool last = r + 1 == a.seg_off[s + 1];
+    kid = last ? a.kid + a.kid_off[s] : nullptr;
+    n = last ? a.kid_off[s + 1] - a.kid_off[s] : 1;
+    row = r + 1;
+    root_start = a.parent[s] < 0 && r == a.seg_off[s];
+  }
+  __device__ __forceinline__ int at(int j) const { return kid ? seg_off[kid[j]] : row; }
+};
+
+// Token id of row t, or -1 where it is outside the vocabulary.
+__device__ __forceinline__ int token(const LogprobArgs& a, int t) {
+  if (a.token64) {
+    const int64_t x = static_cast<const int64_t*>(a.tokens)[t];
+    return x >= 0 && x < a.vocab ? static_cast<int>(x) : -1;
+  }
+  const int32_t x = static_cast<const int32_t*>(a.tokens)[t];
+  return x >= 0 && x < a.vocab ? x : -1;
+}
+
+// ---- the largest values of a row ------------------------------------------------
+// A wave's list, best first: lane j < k holds entry j.  Ties go to the lowest
+// index.  (tv, ti) is the last entry, which a new one has to beat.
+struct TopList {
+  float v = kNegInf, tv = kNegInf;
+  int id = kNoId, ti = kNoId, k;
+  __device__ __forceinline__ explicit TopList(int k_) : k(k_) {}
+  static __device__ __forceinline__ bool better(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
+  // One candidate per lane (index kNoId: none).
+  __device__ __forceinline__ void offer(float x, int i, int lane) {
+    uint64_t m = __ballot(better(x, i, tv, ti));
+    while (m) {
+      const int src = __builtin_ctzll(m);
+      const float nx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), src));
+      const int ni = __builtin_amdgcn_readlane(i, src);
+      const int pos = __popcll(__ballot(lane < k && better(v, id, nx, ni)));
+      const float up = __shfl_up(v, 1, 64);
+      const int upi = __shfl_up(id, 1, 64);
+      if (lane > pos) {
+        v = up;
+        id = upi;
+      }
+      if (lane == pos) {
+        v = nx;
+        id = ni;
+      }
+      tv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), k - 1));
+      ti = __builtin_amdgcn_readlane(id, k - 1);
+      m &= m - 1;
+      m &= __ballot(better(x, i, tv, ti));
+    }
+  }
+};
+
+// ---- forward --------------------------------------------------------------------
+struct Sums {
+  float m, s, t;  // reference value, sum of e = exp2(c (x - m)), sum of e (x - m)
+};
+// The sums of both, over the larger reference.
+__device__ __forceinline__ Sums join(const Sums a, const Sums b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == kNegInf) return Sums{m, a.s + b.s, a.t + b.t};
+  Sums r{m, 0.f, 0.f};
+  // A factor of 0 (that side is empty, or far below) drops t, whose shift may
+  // overflow; a NaN stays in s.
+  const float da = a.m - m, db = b.m - m;
+  const float fa = ex2(da * c), fb = ex2(db * c);
+  r.s = a.s * fa + b.s * fb;
+  r.t = (fa == 0.f ? 0.f : fmaf(da, a.s, a.t) * fa) + (fb == 0.f ? 0.f : fmaf(db, b.s, b.t) * fb);
+  return r;
+}
+
+template <typename T>
+struct Scan {
+  static constexpr int N = Vec<T>::N;
+  float c, slack;  // slack: how far a value may pass m (10 / c)
+  float m = kNegInf, mr = 0.f, s = 0.f, t = 0.f;
+  __device__ __forceinline__ explicit Scan(float c_) : c(c_), slack(10.f / c_) {}
+  // n values (the others -inf).
+  template <int n>
+  __device__ __forceinline__ float add(const float* x) {
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < n; ++j) top = fmaxf(top, x[j]);
+    if (__any(top > m + slack)) {
+      const float mn = fmaxf(m, top);
+      const float d = m == kNegInf ? 0.f : m - mn, f = ex2(d * c);
+      t = f == 0.f ? 0.f : fmaf(d, s, t) * f;
+      s *= f;
+      m = mn;
+      mr = m == kNegInf ? 0.f : m;
+    }
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float y = x[j] - mr, e = ex2(y * c);
+      s += e;
+      t = fmaf(e, fmaxf(y, -3.4e38f), t);  // e = 0 where y = -inf
+    }
+    return top;
+  }
+};
+
+// Everything a row's sums decide, by the threads tid, tid + nt, ...
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, int lr, const Sums z, const Behind& b, int tid, int nt) {
+  const T* x = static_cast<const T*>(a.logits) + int64_t(lr) * a.ld;
+  const bool empty = z.m == kNegInf && z.s == 0.f;  // every logit is -inf
+  const float ls = __log2f(z.s) * kLn2;             // log s
+  if (tid == 0) {
+    a.lse[lr] = empty ? kNegInf : z.m * a.inv_t + ls;
+    a.entropy[lr] = empty ? 0.f : ls - a.inv_t * (z.t / z.s);
+    if (b.root_start) a.logp[a.first_row + lr] = 0.f;
+  }
+  for (int j = tid; j < b.n; j += nt) {
+    const int t = b.at(j), id = token(a, t);
+    a.logp[t] = id < 0 ? 0.f : empty ? kNegInf : (Vec<T>::one(x + id) - z.m) * a.inv_t - ls;
+  }
+}
+__device__ __forceinline__ void put_top(const LogprobArgs& a, int lr, const Sums z, const TopList& l, int lane) {
+  if (lane >= a.top_k) return;
+  const bool empty = z.m == kNegInf && z.s == 0.f;
+  const int64_t o = int64_t(lr) * a.top_k + lane;
+  a.top_id[o] = l.id == kNoId ? -1 : l.id;
+  a.top_logp[o] = empty ? kNegInf : (l.v - z.m) * a.inv_t - __log2f(z.s) * kLn2;
+}
+__device__ __forceinline__ float* part_lists(const LogprobArgs& a) {
+  return a.part + int64_t(a.n_rows) * a.split * 4;
+}
+
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
+  constexpr int N = Vec<T>::N, U = 4;
+  __shared__ Sums sums[kThreads / 64];
+  __shared__ float tv[TOP ? kThreads : 1];
+  __shared__ int ti[TOP ? kThreads : 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = blockIdx.x / a.split, part = blockIdx.x % a.split;
+  const int c0 = part * a.slice;
+  const Slice<T> sl(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld + c0, min(a.slice, a.vocab - c0));
+  Scan<T> sc(a.inv_t * kLog2e);
+  TopList top(a.top_k);
+
+  const auto* pv = reinterpret_cast<const u32x4*>(sl.p + sl.head);
+  auto one = [&](const u32x4 w, int v) {
+    float x[N];
+    Vec<T>::unpack(w, x);
+    const float big = sc.template add<N>(x);
+    if constexpr (TOP) {
+      if (__any(big >= top.tv)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) top.offer(x[j], c0 + sl.head + v * N + j, lane);
+      }
+    }
+  };
+  int v = tid;
+  for (int i = 0; i < sl.vecs / (U * kThreads); ++i, v += U * kThreads) {
+    u32x4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) one(w[u], v + u * kThreads);
+  }
+  // The last pieces, and the columns outside of them; lanes without one add
+  // -inf, which changes nothing.
+  const int turns = (sl.vecs - (v - tid) + kThreads - 1) / kThreads;
+  for (int i = 0; i < turns; ++i, v += kThreads) {
+    float x[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = kNegInf;
+    if (v < sl.vecs) Vec<T>::unpack(__builtin_nontemporal_load(pv + v), x);
+    const float big = sc.template add<N>(x);
+    if constexpr (TOP) {
+      if (__any(big >= top.tv)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) top.offer(x[j], v < sl.vecs ? c0 + sl.head + v * N + j : kNoId, lane);
+      }
+    }
+  }
+  if (wave == 0) {
+    const int i = lane;
+    const bool has = i < sl.ends();
+    const float x = has ? Vec<T>::one(sl.p + sl.end_col(i)) : kNegInf;
+    sc.template add<1>(&x);
+    if constexpr (TOP) top.offer(x, has ? c0 + sl.end_col(i) : kNoId, lane);
+  }
+
+  Sums z{sc.m, sc.s, sc.t};
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const Sums y{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)};
+    z = join(z, y, sc.c);
+  }
+  if (lane == 0) sums[wave] = z;
+  if constexpr (TOP) {
+    tv[tid] = top.v;
+    ti[tid] = top.id;
+  }
+  __syncthreads();
+  z = sums[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) z = join(z, sums[w], sc.c);
+  if constexpr (TOP) {
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 1; w < kThreads / 64; ++w) {
+        const bool has = lane < a.top_k;
+        top.offer(has ? tv[64 * w + lane] : kNegInf, has ? ti[64 * w + lane] : kNoId, lane);
+      }
+    }
+  }
+  if (a.split == 1) {
+    const Behind b(a, a.first_row + lr, lane);
+    finish_row<T>(a, lr, z, b, tid, kThreads);
+    if (TOP && wave == 0) put_top(a, lr, z, top, lane);
+  } else {
+    if (tid == 0) *reinterpret_cast<float4*>(a.part + int64_t(blockIdx.x) * 4) = make_float4(z.m, z.s, z.t, 0.f);
+    if (TOP && wave == 0 && lane < a.top_k)
+      *reinterpret_cast<float2*>(part_lists(a) + (int64_t(blockIdx.x) * a.top_k + lane) * 2) =
+          make_float2(top.v, __int_as_float(top.id));
+  }
+}
+
+// A row spread over several work-groups: its sums and lists joined by one wave.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
+  const int lane = threadIdx.x, lr = blockIdx.x;
+  const float c = a.inv_t * kLog2e;
+  const Behind b(a, a.first_row + lr, lane);
+  Sums z{kNegInf, 0.f, 0.f};
+  for (int i = lane; i < a.split; i += 64) {
+    const float4 y = *reinterpret_cast<const float4*>(a.part + (int64_t(lr) * a.split + i) * 4);
+    z = join(z, Sums{y.x, y.y, y.z}, c);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const Sums y{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)};
+    z = join(z, y, c);
+  }
+  finish_row<T>(a, lr, z, b, lane, 64);
+  if constexpr (TOP) {
+    TopList top(a.top_k);
+    const float2* l = reinterpret_cast<const float2*>(part_lists(a)) + int64_t(lr) * a.split * a.top_k;
+    const int n = a.split * a.top_k;
+    for (int i = lane; i < n + lane; i += 64) {
+      const float2 y = i < n ? l[i] : make_float2(kNegInf, __int_as_float(kNoId));
+      top.offer(y.x, __float_as_int(y.y), lane);
+    }
+    put_top(a, lr, z, top, lane);
+  }
+}
+
+// ---- backward ---------------------------------------------------------------------
+constexpr int kListed = 512;  // tokens behind a row that are kept in LDS
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a) {
+  constexpr int N = Vec<T>::N, U = 4;
+  __shared__ uint32_t flag[kMaxSlice / N / 32];  // pieces of the slice with a token behind the row
+  __shared__ int ids[kListed];
+  __shared__ float gs[kListed];
+  __shared__ float wsum[kThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = blockIdx.x / a.split, part = blockIdx.x % a.split;
+  const int c0 = part * a.slice;
+  const Slice<T> sl(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld + c0, min(a.slice, a.vocab - c0));
+  T* out = static_cast<T*>(a.dlogits) + int64_t(lr) * a.ldd + c0;
+  const Behind b(a, a.first_row + lr, lane);
+  for (int i = tid; i < (sl.vecs + 31) / 32; i += kThreads) flag[i] = 0;
+  __syncthreads();
+  // The gradients behind the row: their sum, and which pieces they touch.
+  float g = 0.f;
+  for (int j = tid; j < b.n; j += kThreads) {
+    const int t = b.at(j), id = token(a, t);
+    const float gj = id < 0 ? 0.f : a.dlogp[t];
+    g += gj;
+    if (j < kListed) {
+      ids[j] = id;
+      gs[j] = gj;
+    }
+    const int at = id - c0 - sl.head;
+    if (id >= 0 && at >= 0 && at < sl.vecs * N) atomicOr(&flag[at / N >> 5], 1u << (at / N & 31));
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) g += __shfl_xor(g, o, 64);
+  if (lane == 0) wsum[wave] = g;
+  __syncthreads();
+  g = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) g += wsum[w];
+
+  const float lse = a.lse_in[lr], dh = a.dentropy ? a.dentropy[lr] : 0.f;
+  const bool empty = lse == kNegInf;
+  const float ca = empty ? 0.f : -(g + dh * (a.dentropy ? a.entropy_in[lr] : 0.f)) * a.inv_t, cb = empty ? 0.f : -dh * a.inv_t;
+  // The gradient of a value whose token is not behind the row.
+  auto grad = [&](float x) {
+    const float lp = fmaf(x, a.inv_t, -lse);
+    return ex2(lp * kLog2e) * fmaf(cb, fmaxf(lp, -1e4f), ca);  // exp is 0 below -104
+  };
+  // What the tokens behind the row that equal `id` add, in their order.
+  auto direct = [&](int id) {
+    float s = 0.f;
+    for (int j = 0; j < b.n; ++j) {
+      if (j < kListed) {
+        s += ids[j] == id ? gs[j] : 0.f;
+      } else {
+        const int t = b.at(j);
+        if (token(a, t) == id) s += a.dlogp[t];
+      }
+    }
+    return s * a.inv_t;
+  };
+  const auto* pv = reinterpret_cast<const u32x4*>(sl.p + sl.head);
+  const bool aligned = (reinterpret_cast<uintptr_t>(out + sl.head) & 15) == 0;
+  auto one = [&](const u32x4 w, int v) {
+    float x[N];
+    Vec<T>::unpack(w, x);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = empty ? 0.f : grad(x[j]);
+    if ((flag[v >> 5] >> (v & 31)) & 1 && !empty) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] += direct(c0 + sl.head + v * N + j);
+    }
+    T* o = out + sl.head + v * N;
+    if (aligned) {
+      __builtin_nontemporal_store(Vec<T>::pack(x), reinterpret_cast<u32x4*>(o));
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) Vec<T>::put(o + j, x[j]);
+    }
+  };
+  int v = tid;
+  for (int i = 0; i < sl.vecs / (U * kThreads); ++i, v += U * kThreads) {
+    u32x4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) one(w[u], v + u * kThreads);
+  }
+  for (; v < sl.vecs; v += kThreads) one(__builtin_nontemporal_load(pv + v), v);
+  if (tid < sl.ends()) {
+    const int col = sl.end_col(tid);
+    const float x = Vec<T>::one(sl.p + col);
+    Vec<T>::put(out + col, empty ? 0.f : grad(x) + direct(c0 + col));
+  }
+}
+
+}  // namespace
+
+hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
+  const bool top = a.top_k > 0;
+  if (dtype == TREE_DTYPE_BF16) {
+    if (top) logprobs_kernel<uint16_t, true><<<grid, block, 0, stream>>>(a);
+    else logprobs_kernel<uint16_t, false><<<grid, block, 0, stream>>>(a);
+  } else {
+    if (top) logprobs_kernel<float, true><<<grid, block, 0, stream>>>(a);
+    else logprobs_kernel<float, false><<<grid, block, 0, stream>>>(a);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.split == 1) return e;
+  const dim3 rows(a.n_rows);
+  if (dtype == TREE_DTYPE_BF16) {
+    if (top) logprobs_join_kernel<uint16_t, true><<<rows, 64, 0, stream>>>(a);
+    else logprobs_join_kernel<uint16_t, false><<<rows, 64, 0, stream>>>(a);
+  } else {
+    if (top) logprobs_join_kernel<float, true><<<rows, 64, 0, stream>>>(a);
+    else logprobs_join_kernel<float, false><<<rows, 64, 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_logprobs_backward(const LogprobArgs& a, int dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
+  if (dtype == TREE_DTYPE_BF16) logprobs_backward_kernel<uint16_t><<<grid, block, 0, stream>>>(a);
+  else logprobs_backward_kernel<float><<<grid, block, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace tg
