@@ -488,13 +488,14 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
  * A token that is not on the path has no influence, whatever it holds
  * (infinities and NaN included).
  *
- * q      device, [n_tokens, h_q, d], dtype, ldq elements between token rows
- * k, v   device, [n_tokens, h_kv, d], dtype, ldk, ldv     (read)
+ * q      device, [n_tokens, h_q, d], dtype                (read)
+ * k, v   device, [n_tokens, h_kv, d], dtype               (read)
  * o      device, [n_tokens, h_q, d], dtype, contiguous    (written; no alias)
- * lse    device, [n_tokens, h_q] fp32, or NULL            (written)
- * Heads of a token row are contiguous; ldq >= h_q d and ldk, ldv >= h_kv d
- * (slices of one projection's output need no copy).  Pointers and row
- * distances are multiples of 16 bytes.
+ * lse    device, [n_tokens, h_q] fp32, contiguous, or NULL (written)
+ * strides host, [3][2]: elements between token rows and between heads of q,
+ *        k and v, >= 0 (a head's d elements are contiguous; slices of one
+ *        projection's output and head-major tensors need no copy), or NULL:
+ *        all contiguous.  Pointers, rows and heads start on 16 bytes.
  * scale  > 0 and finite (1 / sqrt(d) as a rule).
  * dtype  TREE_DTYPE_BF16 (bf16 MFMA; scores, maxima, sums and the output's
  *        accumulation in fp32, probabilities rounded to bf16 for their
@@ -504,8 +505,8 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
  * Errors: INVALID_ARG, SIZE (n_tokens != plan N), UNSUPPORTED (d, or h_q not a
  * multiple of h_kv), WORKSPACE (dplan_bytes too small), HIP.
  */
-int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, int64_t ldq, int64_t ldk,
-                   int64_t ldv, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
+int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
+                   int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
                    const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* stream);
 
 /*
@@ -526,19 +527,19 @@ size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* apla
  * query head of j's group.  Sums run in a fixed order: the result is
  * deterministic.
  *
- * q, k, v, o, lse  the forward's inputs and outputs; o and dout with ldo, lddo
- *            elements between token rows                 (read)
+ * q, k, v, o, lse  the forward's inputs and outputs    (read)
  * dout       device, [n_tokens, h_q, d], dtype           (read)
  * dq         device, [n_tokens, h_q, d], dtype, contiguous  (written)
  * dk, dv     device, [n_tokens, h_kv, d], dtype, contiguous (written)
+ * strides    host, [5][2], of q, k, v, o and dout, or NULL, as above
  * ws         device workspace, ws_bytes >= tree_attention_backward_workspace_bytes.
  * Everything else as for tree_attention; ds and p are rounded to bf16 for
  * their products under TREE_DTYPE_BF16.
  * Errors: as tree_attention.
  */
 int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                            const void* dout, void* dq, void* dk, void* dv, int64_t ldq, int64_t ldk, int64_t ldv,
-                            int64_t ldo, int64_t lddo, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d,
+                            const void* dout, void* dq, void* dk, void* dv, const int64_t* strides,
+                            int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d,
                             float scale, int32_t dtype, const tree_attention_plan_t* aplan, const void* dplan,
                             size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream);
 

@@ -80,11 +80,10 @@ SIGNATURES = {
     "tree_attention_plan_free": (None, [_P]),
     "tree_attention_plan_device_bytes": (_SZ, [_P]),
     "tree_attention_plan_upload": (ctypes.c_int, [_P, _P, _SZ, _P]),
-    "tree_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _I32, _I32, _F, _I32,
-                                      _P, _P, _SZ, _P]),
+    "tree_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P]),
     "tree_attention_backward_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
-    "tree_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64,
-                                               _I64, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P, _SZ, _P]),
+    "tree_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F,
+                                               _I32, _P, _P, _SZ, _P, _SZ, _P]),
     "tree_logprobs_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "tree_logprobs": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _F, _I32, _I32,
                                      _P, _P, _SZ, _P, _SZ, _P]),
@@ -565,9 +564,9 @@ def tree_ssd_scan(x, dt, A, B, C, plan: TreePlan, D=None, return_states: bool = 
     return y
 
 
-def _need_rows(t, name, dtype=None, device=None):
-    """A [N, H, d] device tensor whose heads are contiguous within a token
-    row; returns the elements between rows."""
+def _need_heads(t, name, dtype=None, device=None):
+    """A [N, H, d] device tensor whose heads' d elements are contiguous; returns
+    the elements between token rows and between heads."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -580,9 +579,9 @@ def _need_rows(t, name, dtype=None, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}'s heads must be contiguous within a token row")
-    return t.stride(0) if n > 1 else h * d
+    if d > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s heads must be contiguous")
+    return (t.stride(0) if n > 1 else 0, t.stride(1) if h > 1 else 0)
 
 
 def _attention_shapes(q, k, v, plan):
@@ -598,14 +597,13 @@ def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, retur
     attends to the tokens of its own root-to-token path, itself included.
 
     q [N, H_q, d]; k, v [N, H_kv, d] (H_q a multiple of H_kv; bf16 or fp32; d
-    32, 64 or 128).  They may be slices of one projection's output: only the
-    heads within a token row have to be contiguous.  scale: default
-    1 / sqrt(d)."""
+    32, 64 or 128).  They may be slices of one projection's output or
+    head-major: only a head's d elements have to be contiguous.  scale:
+    default 1 / sqrt(d)."""
     import torch
-    ldq = _need_rows(q, "q")
+    st = _need_heads(q, "q")
     dev = q.device
-    ldk = _need_rows(k, "k", q.dtype, dev)
-    ldv = _need_rows(v, "v", q.dtype, dev)
+    st += _need_heads(k, "k", q.dtype, dev) + _need_heads(v, "v", q.dtype, dev)
     _attention_shapes(q, k, v, plan)
     n, h_q, d = q.shape
     o = torch.empty((n, h_q, d), dtype=q.dtype, device=dev) if out is None else out
@@ -620,7 +618,7 @@ def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, retur
     dplan = aplan.on_device(dev)
     stream = torch.cuda.current_stream(dev).cuda_stream
     _check(load().tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                 lse.data_ptr() if lse is not None else None, ldq, ldk, ldv, n, h_q, k.shape[1], d,
+                                 lse.data_ptr() if lse is not None else None, (_I64 * 6)(*st), n, h_q, k.shape[1], d,
                                  d ** -0.5 if scale is None else float(scale), _dtype_code(q), aplan.handle,
                                  dplan.data_ptr(), dplan.numel(), stream))
     if return_lse:
@@ -633,12 +631,10 @@ def tree_attention_backward(q, k, v, o, lse, do, plan: TreePlan, scale: Optional
     upstream gradient do [N, H_q, d] and the forward's o and lse
     (tree_attention(..., return_lse=True)).  Deterministic."""
     import torch
-    ldq = _need_rows(q, "q")
+    st = _need_heads(q, "q")
     dev = q.device
-    ldk = _need_rows(k, "k", q.dtype, dev)
-    ldv = _need_rows(v, "v", q.dtype, dev)
-    ldo = _need_rows(o, "o", q.dtype, dev)
-    lddo = _need_rows(do, "do", q.dtype, dev)
+    st += _need_heads(k, "k", q.dtype, dev) + _need_heads(v, "v", q.dtype, dev)
+    st += _need_heads(o, "o", q.dtype, dev) + _need_heads(do, "do", q.dtype, dev)
     _attention_shapes(q, k, v, plan)
     n, h_q, d = q.shape
     _need_shape(o, "o", (n, h_q, d))
@@ -655,8 +651,7 @@ def tree_attention_backward(q, k, v, o, lse, do, plan: TreePlan, scale: Optional
     dplan = aplan.on_device(dev)
     stream = torch.cuda.current_stream(dev).cuda_stream
     _check(lib.tree_attention_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                       do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ldq, ldk, ldv, ldo,
-                                       lddo, n, h_q, k.shape[1], d, d ** -0.5 if scale is None else float(scale),
+                                       do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), (_I64 * 10)(*st), n, h_q, k.shape[1], d, d ** -0.5 if scale is None else float(scale),
                                        _dtype_code(q), aplan.handle, dplan.data_ptr(), dplan.numel(),
                                        workspace.data_ptr() if workspace is not None else None, ws_bytes, stream))
     return dq, dk, dv

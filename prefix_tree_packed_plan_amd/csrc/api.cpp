@@ -109,14 +109,25 @@ int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_
                 h_q);
   return TREE_OK;
 }
-// A tensor of token rows `ld` elements apart, read and written 16 bytes at a time.
-int check_rows(const void* ptr, int64_t ld, int64_t least, int32_t dtype, const char* name, const char* fn) {
+// A [n_tokens, heads, d] tensor read 16 bytes at a time: `strides` holds the
+// elements between token rows and between heads, or is null for a contiguous
+// tensor.
+int make_heads(const void* ptr, const int64_t* strides, int32_t heads, int32_t d, int32_t dtype, const char* name,
+               const char* fn, tg::Heads* out) {
   const int64_t size = dtype == TREE_DTYPE_F32 ? 4 : 2;
-  if (ld < least || ld > (int64_t(1) << 40))
-    return fail(TREE_ERR_INVALID_ARG, "%s: %s has rows %lld elements apart, a row holds %lld", fn, name,
-                static_cast<long long>(ld), static_cast<long long>(least));
-  if (reinterpret_cast<uintptr_t>(ptr) % 16 != 0 || ld * size % 16 != 0)
-    return fail(TREE_ERR_INVALID_ARG, "%s: %s is not aligned to 16 bytes in every row", fn, name);
+  const int64_t row = (strides ? strides[0] : static_cast<int64_t>(heads) * d) * size;
+  const int64_t head = (strides ? strides[1] : d) * size;
+  const int64_t most = int64_t(1) << 40;
+  if (row < 0 || head < 0 || row > most || head > most)
+    return fail(TREE_ERR_INVALID_ARG, "%s: bad strides of %s", fn, name);
+  if (reinterpret_cast<uintptr_t>(ptr) % 16 != 0 || row % 16 != 0 || head % 16 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: %s is not aligned to 16 bytes in every row and head", fn, name);
+  *out = tg::Heads{static_cast<const char*>(ptr), row, head};
+  return TREE_OK;
+}
+int check_aligned(const void* ptr, const char* name, const char* fn) {
+  if (reinterpret_cast<uintptr_t>(ptr) % 16 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: %s is not aligned to 16 bytes", fn, name);
   return TREE_OK;
 }
 
@@ -795,30 +806,24 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
   return TREE_OK;
 }
 
-int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, int64_t ldq, int64_t ldk,
-                   int64_t ldv, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
+int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
+                   int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
                    const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* stream) {
   const char* fn = "tree_attention";
   if (!aplan || !q || !k || !v || !o || !dplan) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
   const tg::AttnPlan& p = aplan->p;
   if (const int rc = check_attention(p, n_tokens, h_q, h_kv, d, scale, dtype, fn)) return rc;
-  const int64_t rq = static_cast<int64_t>(h_q) * d, rk = static_cast<int64_t>(h_kv) * d;
-  if (const int rc = check_rows(q, ldq, rq, dtype, "q", fn)) return rc;
-  if (const int rc = check_rows(k, ldk, rk, dtype, "k", fn)) return rc;
-  if (const int rc = check_rows(v, ldv, rk, dtype, "v", fn)) return rc;
-  if (const int rc = check_rows(o, rq, rq, dtype, "o", fn)) return rc;
+  tg::AttnArgs a{};
+  const auto st_of = [&](int i) { return strides ? strides + 2 * i : nullptr; };
+  if (const int rc = make_heads(q, st_of(0), h_q, d, dtype, "q", fn, &a.q)) return rc;
+  if (const int rc = make_heads(k, st_of(1), h_kv, d, dtype, "k", fn, &a.k)) return rc;
+  if (const int rc = make_heads(v, st_of(2), h_kv, d, dtype, "v", fn, &a.v)) return rc;
+  if (const int rc = check_aligned(o, "o", fn)) return rc;
   if (o == q || o == k || o == v) return fail(TREE_ERR_INVALID_ARG, "%s: o must not alias q, k or v", fn);
   if (const int rc = check_dplan(aplan, dplan, dplan_bytes, fn)) return rc;
   const int32_t* base = static_cast<const int32_t*>(dplan);
-  tg::AttnArgs a{};
-  a.q = q;
-  a.k = k;
-  a.v = v;
   a.out = o;
   a.lse = lse;
-  a.ldq = ldq;
-  a.ldk = ldk;
-  a.ldv = ldv;
   a.tok_d = base + p.m_d;
   a.tok_e = base + p.m_e;
   a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_q);
@@ -843,8 +848,8 @@ size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* apla
 }
 
 int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                            const void* dout, void* dq, void* dk, void* dv, int64_t ldq, int64_t ldk, int64_t ldv,
-                            int64_t ldo, int64_t lddo, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d,
+                            const void* dout, void* dq, void* dk, void* dv, const int64_t* strides,
+                            int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d,
                             float scale, int32_t dtype, const tree_attention_plan_t* aplan, const void* dplan,
                             size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "tree_attention_backward";
@@ -852,15 +857,16 @@ int tree_attention_backward(const void* q, const void* k, const void* v, const v
     return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
   const tg::AttnPlan& p = aplan->p;
   if (const int rc = check_attention(p, n_tokens, h_q, h_kv, d, scale, dtype, fn)) return rc;
-  const int64_t rq = static_cast<int64_t>(h_q) * d, rk = static_cast<int64_t>(h_kv) * d;
-  if (const int rc = check_rows(q, ldq, rq, dtype, "q", fn)) return rc;
-  if (const int rc = check_rows(k, ldk, rk, dtype, "k", fn)) return rc;
-  if (const int rc = check_rows(v, ldv, rk, dtype, "v", fn)) return rc;
-  if (const int rc = check_rows(o, ldo, rq, dtype, "o", fn)) return rc;
-  if (const int rc = check_rows(dout, lddo, rq, dtype, "dout", fn)) return rc;
-  if (const int rc = check_rows(dq, rq, rq, dtype, "dq", fn)) return rc;
-  if (const int rc = check_rows(dk, rk, rk, dtype, "dk", fn)) return rc;
-  if (const int rc = check_rows(dv, rk, rk, dtype, "dv", fn)) return rc;
+  tg::AttnArgs a{};
+  const auto st_of = [&](int i) { return strides ? strides + 2 * i : nullptr; };
+  if (const int rc = make_heads(q, st_of(0), h_q, d, dtype, "q", fn, &a.q)) return rc;
+  if (const int rc = make_heads(k, st_of(1), h_kv, d, dtype, "k", fn, &a.k)) return rc;
+  if (const int rc = make_heads(v, st_of(2), h_kv, d, dtype, "v", fn, &a.v)) return rc;
+  if (const int rc = make_heads(o, st_of(3), h_q, d, dtype, "o", fn, &a.o)) return rc;
+  if (const int rc = make_heads(dout, st_of(4), h_q, d, dtype, "dout", fn, &a.dout)) return rc;
+  if (const int rc = check_aligned(dq, "dq", fn)) return rc;
+  if (const int rc = check_aligned(dk, "dk", fn)) return rc;
+  if (const int rc = check_aligned(dv, "dv", fn)) return rc;
   const void* outs[3] = {dq, dk, dv};
   const void* ins[5] = {q, k, v, o, dout};
   for (const void* x : outs)
@@ -874,23 +880,12 @@ int tree_attention_backward(const void* q, const void* k, const void* v, const v
     return fail(TREE_ERR_INVALID_ARG, "%s: the workspace is not aligned to 16 bytes", fn);
   if (const int rc = check_dplan(aplan, dplan, dplan_bytes, fn)) return rc;
   const int32_t* base = static_cast<const int32_t*>(dplan);
-  tg::AttnArgs a{};
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.o = o;
-  a.dout = dout;
   a.out = dq;
   a.dk = dk;
   a.dv = dv;
   a.lse = const_cast<float*>(lse);
   a.delta = static_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + attention_delta_bytes(p, h_q));
-  a.ldq = ldq;
-  a.ldk = ldk;
-  a.ldv = ldv;
-  a.ldo = ldo;
-  a.lddo = lddo;
   a.tok_d = base + p.m_d;
   a.tok_e = base + p.m_e;
   a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_q);

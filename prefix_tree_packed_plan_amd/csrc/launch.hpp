@@ -205,21 +205,25 @@ struct AttnItem;
 struct AttnRun;
 struct AttnParts;
 
-// Tree attention (tree_attn.hip).  ld*: elements between a tensor's token
-// rows; heads are d elements apart.  o, dq, dk, dv are contiguous.
+// A [N, H, d] tensor: bytes between its token rows and between its heads (the
+// d elements of a head are contiguous).
+struct Heads {
+  const char* p;
+  int64_t row, head;
+  __host__ __device__ const char* at(int64_t r, int64_t h) const { return p + r * row + h * head; }
+};
+
+// Tree attention (tree_attn.hip).  out, dk, dv are contiguous.
 struct AttnArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const void* o;     // backward: the forward's output
-  const void* dout;  // backward
+  Heads q, k, v;
+  Heads o;           // backward: the forward's output
+  Heads dout;        // backward
   void* out;         // forward's o, or dq
   void* dk;
   void* dv;
   float* lse;        // [N, h_q] natural log; written by the forward, read by the backward
   float* delta;      // backward workspace [N, h_q]: sum over d of dout * o
   float* part;       // backward workspace: partial dk, dv [slot, h_kv, 2, kKTile, d]
-  int64_t ldq, ldk, ldv, ldo, lddo;
   const int32_t* tok_d;  // [N + 1]
   const int32_t* tok_e;  // [N + 1]
   const AttnItem* items;

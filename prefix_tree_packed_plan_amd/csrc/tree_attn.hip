@@ -39,7 +39,6 @@ using chunk::lds_void;
 using chunk::pk2;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(1))) const void glb_void;
 typedef __attribute__((address_space(3))) const chunk::u32x4 lds_u4;
 
 // 16 bytes from LDS.
@@ -150,9 +149,12 @@ __device__ __forceinline__ uint4 Reader<T, D>::cols(const char* t, int kb, int s
 
 // ---- values that are not finite ----------------------------------------------
 // A masked pair's probability is 0, but 0 times an infinity or a NaN of a row
-// the token does not see would still reach it through the MFMA.  In tiles
-// with masked pairs such elements are therefore left out of the product and
-// added, one row at a time, where the probability is not 0.
+// the token does not see would still reach it through the MFMA.  A tile with
+// masked pairs that holds such elements therefore adds them first, one row at
+// a time and only where the probability is not 0, and then clears them in LDS
+// for the product.  In the gradients of k and v the rows are queries: one with
+// such a value in q, dO or o has a delta that is not finite; it is cleared, and
+// the gradients of every key it sees become NaN.
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {  // nonzero iff one of the word's elements is not finite
   if (sizeof(T) == 4) return (w & 0x7F800000u) == 0x7F800000u;
@@ -163,10 +165,6 @@ __device__ __forceinline__ uint32_t finite(uint32_t w) {  // elements that are n
   if (sizeof(T) == 4) return nonfinite<T>(w) ? 0u : w;
   const uint32_t f = nonfinite<T>(w) >> 15;  // bit 0, bit 16
   return w & ~(f * 0xFFFFu);
-}
-template <typename T>
-__device__ __forceinline__ uint4 finite(const uint4 w) {
-  return make_uint4(finite<T>(w.x), finite<T>(w.y), finite<T>(w.z), finite<T>(w.w));
 }
 // Whether this thread's share (a quarter of a wave's tile) has one.
 template <typename T, int D>
@@ -180,20 +178,20 @@ __device__ __forceinline__ bool any_nonfinite(const char* t, int tid) {
   }
   return f != 0;
 }
-template <typename T>
-__device__ __forceinline__ float element(const char* p);
-template <>
-__device__ __forceinline__ float element<uint16_t>(const char* p) {
-  return __uint_as_float(uint32_t(*(__attribute__((address_space(3))) const uint16_t*)p) << 16);
-}
-template <>
-__device__ __forceinline__ float element<float>(const char* p) {
-  return *(__attribute__((address_space(3))) const float*)p;
+// Clears this thread's share.
+template <typename T, int D>
+__device__ __forceinline__ void clear_nonfinite(char* t, int tid) {
+#pragma unroll 1
+  for (int i = 0; i < Cfg<T, D>::TILE / 4096; ++i) {
+    const uint4 w = lds16(t + 16 * (tid + 256 * i));
+    *(__attribute__((address_space(3))) chunk::u32x4*)(t + 16 * (tid + 256 * i)) =
+        chunk::u32x4{finite<T>(w.x), finite<T>(w.y), finite<T>(w.z), finite<T>(w.w)};
+  }
 }
 // acc[db] (columns 32 db + accumulator row, of the tile's rows weighted by w)
-// += the elements the sanitised product left out.
+// += the elements that are not finite.
 template <typename T, int D>
-__device__ __attribute__((noinline)) void add_nonfinite(f32x16* acc, const f32x16* w, const char* t, int lane) {
+__device__ __forceinline__ void add_nonfinite(f32x16 (&acc)[D / 32], const f32x16 (&w)[2], const char* t, int lane) {
   using C = Cfg<T, D>;
   bool bad = false;  // this lane's row (= lane) has one
 #pragma unroll 1
@@ -202,6 +200,7 @@ __device__ __attribute__((noinline)) void add_nonfinite(f32x16* acc, const f32x1
     bad = bad || (nonfinite<T>(x.x) | nonfinite<T>(x.y) | nonfinite<T>(x.z) | nonfinite<T>(x.w));
   }
   const int h = lane >> 5;
+#pragma unroll 1
   for (uint64_t m = __ballot(bad); m; m &= m - 1) {
     const int c = __builtin_ctzll(m), kb = c >> 5, cc = c & 31;
     const int reg = 4 * (cc >> 3) + (cc & 3), half = (cc >> 2) & 1;
@@ -216,33 +215,41 @@ __device__ __attribute__((noinline)) void add_nonfinite(f32x16* acc, const f32x1
 #pragma unroll
     for (int db = 0; db < C::NDB; ++db)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int d = 32 * db + 8 * (i >> 2) + 4 * h + (i & 3);
-        const int by = d * int(sizeof(T));
-        const float e = element<T>(t + c * C::RB + 16 * ((by >> 4) ^ swz<C::RB>(c)) + (by & 15));
-        const bool lost = (__float_as_uint(e) & 0x7F800000u) == 0x7F800000u;
-        if (lost && x != 0.f) acc[db][i] += x * e;
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const int by = (32 * db + 8 * i4 + 4 * h) * int(sizeof(T));
+        const char* p = t + c * C::RB + 16 * ((by >> 4) ^ swz<C::RB>(c)) + (by & 15);
+        float e[4];
+        if (sizeof(T) == 4) {
+          const uint4 z = lds16(p);
+          e[0] = __uint_as_float(z.x), e[1] = __uint_as_float(z.y);
+          e[2] = __uint_as_float(z.z), e[3] = __uint_as_float(z.w);
+        } else {
+          const chunk::u32x2 z = *(chunk::lds_cu2*)p;
+          e[0] = chunk::lo_f(z[0]), e[1] = chunk::hi_f(z[0]);
+          e[2] = chunk::lo_f(z[1]), e[3] = chunk::hi_f(z[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool lost = (__float_as_uint(e[j]) & 0x7F800000u) == 0x7F800000u;
+          acc[db][4 * i4 + j] += lost && x != 0.f ? x * e[j] : 0.f;
+        }
+        asm volatile("" ::: "memory");  // one read at a time: this path must not cost the others registers
       }
   }
 }
 
-// acc[db] += (rows of the tile, transposed) times w: the tile's 64 rows are
-// contracted with the 64 accumulator rows of w[0], w[1].
-template <typename T, int D, bool SAFE>
-__device__ __forceinline__ void contract(f32x16* acc, const f32x16* w, const char* t, const Reader<T, D>& rd) {
+// acc[db] += (rows 32 kb .. 32 kb + 31 of the tile, transposed) times w: they
+// are contracted with w's accumulator rows.
+template <typename T, int D>
+__device__ __forceinline__ void contract(f32x16 (&acc)[D / 32], const f32x16& w, const char* t, int kb,
+                                         const Reader<T, D>& rd) {
   using C = Cfg<T, D>;
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
+  for (int s = 0; s < C::NS; ++s) {
+    const uint4 b = frag<T>(w, s);
 #pragma unroll
-    for (int s = 0; s < C::NS; ++s) {
-      const uint4 b = frag<T>(w[kb], s);
-#pragma unroll
-      for (int db = 0; db < C::NDB; ++db) {
-        uint4 a = rd.cols(t, kb, s, db);
-        if (SAFE) a = finite<T>(a);
-        acc[db] = mm<T>(a, b, acc[db]);
-      }
-    }
+    for (int db = 0; db < C::NDB; ++db) acc[db] = mm<T>(rd.cols(t, kb, s, db), b, acc[db]);
+  }
 }
 
 // ---- run lists ----------------------------------------------------------------
@@ -268,7 +275,8 @@ struct Cursor {
       load();
     }
   }
-  // v0 lies in run `cur`; x < kRows.  Positions past the end repeat the last.
+  // The row of position v0 + x (x < kRows, v0 in run `cur`); positions past
+  // the end repeat the last.
   __device__ __forceinline__ int row(int v0, int x) const {
     const int v = min(v0 + x, end - 1);
     if (min(v0 + kRows, end) <= next) return row0 + (v - virt);
@@ -284,27 +292,47 @@ struct Cursor {
   }
 };
 
+// 16 (4) bytes a lane from `src` to LDS at lds + 16 (4) * lane.  In inline asm,
+// because the compiler would otherwise wait for all DMA in flight before any
+// read of LDS; it has no output registers, and wait_dma() is the wait.
+__device__ __forceinline__ uint32_t lds_at(const char* lds) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)lds)));
+}
 __device__ __forceinline__ void dma16(const void* src, char* lds) {
-  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)lds, 16, 0, 0);
+  int m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(lds_at(lds)), "v"(src)
+               : "memory");
 }
 __device__ __forceinline__ void dma4(const void* src, char* lds) {
-  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)lds, 4, 0, 0);
+  int m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(lds_at(lds)), "v"(src)
+               : "memory");
 }
-__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All of this wave's loads and DMA have landed: vmcnt(0), the other counters
+// as they are.  The builtin, unlike inline asm, lets the compiler know that its
+// own loads have, so that it adds no wait behind the next tile's DMA.
+__device__ __forceinline__ void wait_dma() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  asm volatile("" ::: "memory");
+}
 
-// The 64 rows at virtual position v0 of two tensors into LDS tiles ta, tb, by
-// 4 waves (wave w: every fourth group of 1024 bytes).
+// 64 rows of two tensors into LDS tiles ta, tb, by 4 waves (wave w: every
+// fourth group of 1024 bytes); lane l names the row of tile row l.
 template <typename T, int D>
-__device__ __forceinline__ void stage(const Cursor& cs, int v0, const char* a, int64_t lda, char* ta, const char* b,
-                                      int64_t ldb, char* tb, int wave, int lane) {
+__device__ __forceinline__ void stage(int row, const char* a, int64_t lda, char* ta, const char* b, int64_t ldb,
+                                      char* tb, int wave, int lane) {
   using C = Cfg<T, D>;
 #pragma unroll
   for (int i = 0; i < C::NI; ++i) {
     const int g = 4 * i + wave, r = g * (1024 / C::RB) + lane / C::NC;
-    const int64_t row = cs.row(v0, r);
+    const int64_t from = __shfl(row, r, 64);
     const int c = 16 * ((lane % C::NC) ^ swz<C::RB>(r));
-    dma16(a + row * lda + c, ta + 1024 * g);
-    dma16(b + row * ldb + c, tb + 1024 * g);
+    dma16(a + from * lda + c, ta + 1024 * g);
+    dma16(b + from * ldb + c, tb + 1024 * g);
   }
 }
 
@@ -405,16 +433,16 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
   const int64_t row = int64_t(it.tile) * kQTile + 32 * wave + (lane & 31);
   const bool on = row < a.n_tok;
   const int64_t r = on ? row : a.n_tok - 1;
-  const char* kp = static_cast<const char*>(a.k) + int64_t(hk) * C::RB;
-  const char* vp = static_cast<const char*>(a.v) + int64_t(hk) * C::RB;
-  const int64_t ldk = a.ldk * int64_t(sizeof(T)), ldv = a.ldv * int64_t(sizeof(T));
+  const char* kp = a.k.at(0, hk);
+  const char* vp = a.v.at(0, hk);
 
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int buf) {
     cs.seek(v0);
-    stage<T, D>(cs, v0, kp, ldk, sm.k[buf], vp, ldv, sm.v[buf], wave, lane);
+    const int row = cs.row(v0, lane);
+    stage<T, D>(row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
     if (v0 + kRows > it.n_full && wave < 2) {
-      const int x = v0 + lane < cs.end ? cs.row(v0, lane) : a.n_tok;
+      const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
       else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
     }
@@ -422,7 +450,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
   fetch(0, 0);
 
   uint4 q[C::NK];
-  load_frags<T, D>(q, static_cast<const char*>(a.q) + (r * a.ldq + int64_t(h) * D) * int64_t(sizeof(T)), half);
+  load_frags<T, D>(q, a.q.at(r, h), half);
   const int dq = a.tok_d[r];
   int dlo, dhi;
   span(dq, dlo, dhi);
@@ -440,62 +468,68 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     __syncthreads();
     if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
     const char* kt = sm.k[buf];
-    const char* vt = sm.v[buf];
-    bool masked = v0 + kRows > it.n_full, bad = false;
+    char* vt = sm.v[buf];
+    bool masked = v0 + kRows > it.n_full, bad = false, skip = false;
     if (masked) {
       bad = __syncthreads_or(any_nonfinite<T, D>(vt, threadIdx.x));
       const int kd = sm.d[buf][lane], ke = sm.e[buf][lane];
-      if (__ballot(kd <= dhi && dlo < ke) == 0) continue;  // no row of this wave sees a key of this tile
-      masked = __ballot(kd <= dlo && dhi < ke) != ~0ull;   // every row sees every key
+      skip = __ballot(kd <= dhi && dlo < ke) == 0;        // no row of this wave sees a key of this tile
+      masked = __ballot(kd <= dlo && dhi < ke) != ~0ull;  // every row sees every key
     }
     f32x16 p[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      p[kb] = zero16();
-#pragma unroll
-      for (int ks = 0; ks < C::NK; ++ks) p[kb] = mm<T>(rd.rows(kt, kb, ks), q[ks], p[kb]);
-    }
-    if (masked) {
+    if (!skip) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
+        p[kb] = zero16();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : kNegInf;
+        for (int ks = 0; ks < C::NK; ++ks) p[kb] = mm<T>(rd.rows(kt, kb, ks), q[ks], p[kb]);
       }
-    }
-    float mt = p[0][0];
+      if (masked) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, p[0][i]);
+        for (int kb = 0; kb < 2; ++kb) {
+          const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mt = fmaxf(mt, p[1][i]);
-    mt = fmaxf(mt, half_swap(mt));
-    // A row's accumulators follow its maximum only when that has grown by more
-    // than 2^8: until then the probabilities stay below 2^8, harmless in fp32
-    // and no less exact in bf16.
-    const bool grown = (mt - m) * c > 8.f;
-    if (__any(grown)) {
-      const float mn = grown ? mt : m;
-      const float al = m == kNegInf ? 0.f : ex2((m - mn) * c);
-      m = mn;
-      l *= al;
-#pragma unroll
-      for (int db = 0; db < C::NDB; ++db)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[db][i] *= al;
-    }
-    const float mc = m == kNegInf ? 0.f : m * c;  // -inf: this row has seen no key yet
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[kb][i] = ex2(fmaf(p[kb][i], c, -mc));
-        l += p[kb][i];
+          for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : kNegInf;
+        }
       }
-    if (masked && bad) {
-      contract<T, D, true>(acc, p, vt, rd);
-      add_nonfinite<T, D>(acc, p, vt, lane);
-    } else {
-      contract<T, D, false>(acc, p, vt, rd);
+      float mt = p[0][0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) mt = fmaxf(mt, p[0][i]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mt = fmaxf(mt, p[1][i]);
+      mt = fmaxf(mt, half_swap(mt));
+      // A row's accumulators follow its maximum only when that has grown by
+      // more than 2^8: until then the probabilities stay below 2^8, harmless
+      // in fp32 and no less exact in bf16.
+      const bool grown = (mt - m) * c > 8.f;
+      if (__any(grown)) {
+        const float mn = grown ? mt : m;
+        const float al = m == kNegInf ? 0.f : ex2((m - mn) * c);
+        m = mn;
+        l *= al;
+#pragma unroll
+        for (int db = 0; db < C::NDB; ++db)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[db][i] *= al;
+      }
+      const float mc = m == kNegInf ? 0.f : m * c;  // -inf: this row has seen no key yet
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[kb][i] = ex2(fmaf(p[kb][i], c, -mc));
+          l += p[kb][i];
+        }
+    }
+    if (bad) {
+      if (!skip) add_nonfinite<T, D>(acc, p, vt, lane);
+      __syncthreads();
+      clear_nonfinite<T, D>(vt, threadIdx.x);
+      __syncthreads();
+    }
+    if (!skip) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], vt, kb, rd);
     }
   }
   l += half_swap(l);
@@ -517,16 +551,16 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
   const int64_t row = int64_t(it.tile) * kQTile + 32 * wave + (lane & 31);
   const bool on = row < a.n_tok;
   const int64_t r = on ? row : a.n_tok - 1;
-  const char* kp = static_cast<const char*>(a.k) + int64_t(hk) * C::RB;
-  const char* vp = static_cast<const char*>(a.v) + int64_t(hk) * C::RB;
-  const int64_t ldk = a.ldk * int64_t(sizeof(T)), ldv = a.ldv * int64_t(sizeof(T));
+  const char* kp = a.k.at(0, hk);
+  const char* vp = a.v.at(0, hk);
 
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int buf) {
     cs.seek(v0);
-    stage<T, D>(cs, v0, kp, ldk, sm.k[buf], vp, ldv, sm.v[buf], wave, lane);
+    const int row = cs.row(v0, lane);
+    stage<T, D>(row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
     if (v0 + kRows > it.n_full && wave < 2) {
-      const int x = v0 + lane < cs.end ? cs.row(v0, lane) : a.n_tok;
+      const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
       else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
     }
@@ -534,11 +568,11 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
   fetch(0, 0);
 
   uint4 q[C::NK], g[C::NK];
-  load_frags<T, D>(q, static_cast<const char*>(a.q) + (r * a.ldq + int64_t(h) * D) * int64_t(sizeof(T)), half);
-  load_frags<T, D>(g, static_cast<const char*>(a.dout) + (r * a.lddo + int64_t(h) * D) * int64_t(sizeof(T)), half);
+  load_frags<T, D>(q, a.q.at(r, h), half);
+  load_frags<T, D>(g, a.dout.at(r, h), half);
   float delta = 0.f;
   {
-    const char* op = static_cast<const char*>(a.o) + (r * a.ldo + int64_t(h) * D) * int64_t(sizeof(T));
+    const char* op = a.o.at(r, h);
 #pragma unroll
     for (int ks = 0; ks < C::NK; ++ks) {
       const uint4 o = *reinterpret_cast<const uint4*>(op + 32 * ks + 16 * half);
@@ -572,37 +606,43 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
     wait_dma();
     __syncthreads();
     if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
-    const char* kt = sm.k[buf];
+    char* kt = sm.k[buf];
     const char* vt = sm.v[buf];
-    bool masked = v0 + kRows > it.n_full, bad = false;
+    bool masked = v0 + kRows > it.n_full, bad = false, skip = false;
     if (masked) {
       bad = __syncthreads_or(any_nonfinite<T, D>(kt, threadIdx.x));
       const int kd = sm.d[buf][lane], ke = sm.e[buf][lane];
-      if (__ballot(kd <= dhi && dlo < ke) == 0) continue;
+      skip = __ballot(kd <= dhi && dlo < ke) == 0;
       masked = __ballot(kd <= dlo && dhi < ke) != ~0ull;
     }
     f32x16 p[2];
+    if (!skip) {
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      f32x16 s = zero16(), dp = zero16();
+      for (int kb = 0; kb < 2; ++kb) {
+        f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-      for (int ks = 0; ks < C::NK; ++ks) {
-        s = mm<T>(rd.rows(kt, kb, ks), q[ks], s);
-        dp = mm<T>(rd.rows(vt, kb, ks), g[ks], dp);
-      }
+        for (int ks = 0; ks < C::NK; ++ks) {
+          s = mm<T>(rd.rows(kt, kb, ks), q[ks], s);
+          dp = mm<T>(rd.rows(vt, kb, ks), g[ks], dp);
+        }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[kb][i] = ex2(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
-      if (masked) {
-        const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
+        for (int i = 0; i < 16; ++i) p[kb][i] = ex2(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+        if (masked) {
+          const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : 0.f;
+          for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : 0.f;
+        }
       }
     }
-    if (masked && bad) {
-      contract<T, D, true>(acc, p, kt, rd);
-      add_nonfinite<T, D>(acc, p, kt, lane);
-    } else {
-      contract<T, D, false>(acc, p, kt, rd);
+    if (bad) {
+      if (!skip) add_nonfinite<T, D>(acc, p, kt, lane);
+      __syncthreads();
+      clear_nonfinite<T, D>(kt, threadIdx.x);
+      __syncthreads();
+    }
+    if (!skip) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], kt, kb, rd);
     }
   }
   store_row<T, D>(static_cast<T*>(a.out) + (r * a.h_q + h) * D, acc, a.scale, half, on);
@@ -634,26 +674,23 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
   const int64_t row = int64_t(it.tile) * kKTile + key;
   const bool on = row < a.n_tok;
   const int64_t r = on ? row : a.n_tok - 1;
-  const int64_t ldq = a.ldq * int64_t(sizeof(T)), ldg = a.lddo * int64_t(sizeof(T));
 
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int h, int buf) {
     cs.seek(v0);
-    stage<T, D>(cs, v0, static_cast<const char*>(a.q) + int64_t(h) * C::RB, ldq, sm.q[buf],
-                static_cast<const char*>(a.dout) + int64_t(h) * C::RB, ldg, sm.g[buf], wave, lane);
-    if (wave < 3) {
-      const int64_t x = cs.row(v0, lane);
-      if (wave == 0) dma4(a.lse + x * a.h_q + h, reinterpret_cast<char*>(sm.lse[buf]));
-      else if (wave == 1) dma4(a.delta + x * a.h_q + h, reinterpret_cast<char*>(sm.delta[buf]));
-      else dma4(a.tok_d + (v0 + lane < cs.end ? x : a.n_tok), reinterpret_cast<char*>(sm.d[buf]));
-    }
+    const int row = cs.row(v0, lane);
+    stage<T, D>(row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave, lane);
+    const int64_t x = int64_t(row) * a.h_q + h;
+    if (wave == 0) dma4(a.lse + x, reinterpret_cast<char*>(sm.lse[buf]));
+    else if (wave == 1) dma4(a.delta + x, reinterpret_cast<char*>(sm.delta[buf]));
+    else if (wave == 2) dma4(a.tok_d + (v0 + lane < cs.end ? row : a.n_tok), reinterpret_cast<char*>(sm.d[buf]));
   };
   int h = hk * group + sub;
   fetch(it.v0, h, 0);
 
   uint4 kf[C::NK], vf[C::NK];
-  load_frags<T, D>(kf, static_cast<const char*>(a.k) + (r * a.ldk + int64_t(hk) * D) * int64_t(sizeof(T)), half);
-  load_frags<T, D>(vf, static_cast<const char*>(a.v) + (r * a.ldv + int64_t(hk) * D) * int64_t(sizeof(T)), half);
+  load_frags<T, D>(kf, a.k.at(r, hk), half);
+  load_frags<T, D>(vf, a.v.at(r, hk), half);
   const int kd = a.tok_d[r], ke = a.tok_e[r];
   int kdlo, kdhi, kelo, kehi;
   span(kd, kdlo, kdhi);
@@ -677,27 +714,51 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
       cs.load();
     }
     if (nh < (hk + 1) * group) fetch(nv, nh, buf ^ 1);
-    const char* qt = sm.q[buf];
-    const char* gt = sm.g[buf];
-    bool masked = min(v0 + kRows, it.v1) > it.n_full || v0 + kRows > it.v1, bad_q = false, bad_g = false, skip = false;
+    char* qt = sm.q[buf];
+    char* gt = sm.g[buf];
+    bool masked = min(v0 + kRows, it.v1) > it.n_full || v0 + kRows > it.v1, skip = false;
+    uint64_t bad = 0;  // rows of a tile with masked pairs whose delta is not finite
     v0 = nv;
     h = nh;
     if (masked) {
-      bad_q = __syncthreads_or(any_nonfinite<T, D>(qt, threadIdx.x));
-      bad_g = __syncthreads_or(any_nonfinite<T, D>(gt, threadIdx.x));
+      bad = __ballot(nonfinite<float>(__float_as_uint(sm.delta[buf][lane])));
       const int qd = sm.d[buf][lane];
       skip = __ballot(kdlo <= qd && qd < kehi) == 0;
       masked = __ballot(kdhi <= qd && qd < kelo) != ~0ull;
     }
+    if (bad) {  // uniform over the work-group
+      float x = 0.f;
+      for (uint64_t m = bad; m; m &= m - 1) {
+        const int rd = sm.d[buf][__builtin_ctzll(m)];
+        x = kd <= rd && rd < ke ? __builtin_nanf("") : x;
+      }
+#pragma unroll
+      for (int db = 0; db < C::NDB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          dk[db][i] += x;
+          dv[db][i] += x;
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < kRows * C::NC; i += 256)
+        if ((bad >> (i / C::NC)) & 1) {
+          *(__attribute__((address_space(3))) chunk::u32x4*)(qt + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
+          *(__attribute__((address_space(3))) chunk::u32x4*)(gt + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
+        }
+      if (threadIdx.x < kRows && (bad >> threadIdx.x) & 1) {
+        sm.lse[buf][threadIdx.x] = -kNegInf;  // p = 0
+        sm.delta[buf][threadIdx.x] = 0.f;
+      }
+      __syncthreads();
+    }
     if (skip) continue;
-    f32x16 p[2], ds[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      f32x16 s = zero16(), dp = zero16();
+      f32x16 p = zero16(), ds = zero16();
 #pragma unroll
       for (int ks = 0; ks < C::NK; ++ks) {
-        s = mm<T>(rd.rows(qt, kb, ks), kf[ks], s);
-        dp = mm<T>(rd.rows(gt, kb, ks), vf[ks], dp);
+        p = mm<T>(rd.rows(qt, kb, ks), kf[ks], p);
+        ds = mm<T>(rd.rows(gt, kb, ks), vf[ks], ds);
       }
 #pragma unroll
       for (int i4 = 0; i4 < 4; ++i4) {
@@ -708,8 +769,8 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = 4 * i4 + j;
-          p[kb][i] = ex2(fmaf(s[i], c, -l4[j] * kLog2e));
-          ds[kb][i] = p[kb][i] * (dp[i] - d4[j]);
+          p[i] = ex2(fmaf(p[i], c, -l4[j] * kLog2e));
+          ds[i] = p[i] * (ds[i] - d4[j]);
         }
         if (masked) {
           const int4 dd = *reinterpret_cast<const int4*>(&sm.d[buf][o]);
@@ -717,23 +778,13 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const bool see = kd <= x4[j] && x4[j] < ke;
-            p[kb][4 * i4 + j] = see ? p[kb][4 * i4 + j] : 0.f;
-            ds[kb][4 * i4 + j] = see ? ds[kb][4 * i4 + j] : 0.f;
+            p[4 * i4 + j] = see ? p[4 * i4 + j] : 0.f;
+            ds[4 * i4 + j] = see ? ds[4 * i4 + j] : 0.f;
           }
         }
       }
-    }
-    if (masked && bad_g) {
-      contract<T, D, true>(dv, p, gt, rd);
-      add_nonfinite<T, D>(dv, p, gt, lane);
-    } else {
-      contract<T, D, false>(dv, p, gt, rd);
-    }
-    if (masked && bad_q) {
-      contract<T, D, true>(dk, ds, qt, rd);
-      add_nonfinite<T, D>(dk, ds, qt, lane);
-    } else {
-      contract<T, D, false>(dk, ds, qt, rd);
+      contract<T, D>(dv, p, gt, kb, rd);
+      contract<T, D>(dk, ds, qt, kb, rd);
     }
   }
   if (a.split == 1 && it.part >= a.n_multi_parts) {

@@ -12,6 +12,10 @@ BIG = 1 << 40
 NAN, INF = float("nan"), float("inf")
 
 
+def strides(x):
+    return ctypes.cast((ctypes.c_int64 * len(x))(*x), ctypes.c_void_p)
+
+
 def plan_of(parents=(-1, 0, 0), lens=(100, 60, 70)):
     return _lib.TreePlan(np.array(parents, np.int32), np.array(lens, np.int32), 4)
 
@@ -35,7 +39,7 @@ def test_attention_plan_is_built_on_the_host():
 def test_attention_refusals_need_no_device():
     a = plan_of().attention()
     lib = _lib.load()
-    good = dict(q=P, k=P, v=P, o=P2, lse=None, ldq=512, ldk=256, ldv=256, n=230, hq=4, hkv=2, d=128, scale=0.1,
+    good = dict(q=P, k=P, v=P, o=P2, lse=None, st=None, n=230, hq=4, hkv=2, d=128, scale=0.1,
                 dtype=1, aplan=a.handle, dplan=P, bytes=BIG, stream=None)
 
     def call(**kw):
@@ -50,8 +54,14 @@ def test_attention_refusals_need_no_device():
     assert call(hq=3) == -4 and call(d=48) == -4 and call(d=256) == -4
     for scale in (0.0, -0.1, NAN, INF):
         assert call(scale=scale) == -1
-    assert call(ldq=511) == -1 and call(ldk=255) == -1 and call(ldv=0) == -1 and call(ldq=-512) == -1
-    assert call(ldq=516) == -1 and call(q=ctypes.c_void_p(0x1008)) == -1  # 16-byte rows
+    ok = [512, 128, 256, 128, 256, 128]
+    assert call(st=strides(ok)) == -1 and b"not an upload" in lib.tree_last_error()
+    for i in range(6):  # negative, not on 16 bytes, absurd
+        for x in (-512, ok[i] + 4, 1 << 50):
+            assert call(st=strides(ok[:i] + [x] + ok[i + 1:])) == -1
+            assert b"of q" in lib.tree_last_error() or b"not aligned" in lib.tree_last_error() or \
+                b"bad strides" in lib.tree_last_error()
+    assert call(q=ctypes.c_void_p(0x1008)) == -1 and call(o=ctypes.c_void_p(0x2004)) == -1
     assert call(o=P) == -1
 
 
@@ -62,8 +72,7 @@ def test_attention_backward_refusals_need_no_device():
     assert need >= 230 * 4 * 4
     assert lib.tree_attention_backward_workspace_bytes(None, 4, 2, 128) == 0
     assert lib.tree_attention_backward_workspace_bytes(a.handle, 3, 2, 128) == 0
-    good = dict(q=P, k=P, v=P, o=P, lse=P, do=P, dq=P2, dk=P3, dv=P4, ldq=512, ldk=256, ldv=256, ldo=512, lddo=512,
-                n=230, hq=4, hkv=2, d=128, scale=0.1, dtype=1, aplan=a.handle, dplan=P, bytes=BIG, ws=P, ws_bytes=need,
+    good = dict(q=P, k=P, v=P, o=P, lse=P, do=P, dq=P2, dk=P3, dv=P4, st=None, n=230, hq=4, hkv=2, d=128, scale=0.1, dtype=1, aplan=a.handle, dplan=P, bytes=BIG, ws=P, ws_bytes=need,
                 stream=None)
 
     def call(**kw):
@@ -74,7 +83,11 @@ def test_attention_backward_refusals_need_no_device():
         assert call(**{name: None}) == -1
     assert call(ws=None) == -5 and call(ws_bytes=need - 1) == -5
     assert call(n=231) == -3 and call(hq=5) == -4 and call(d=96) == -4 and call(scale=0.0) == -1
-    assert call(ldo=508) == -1 and call(lddo=514) == -1
+    ok = [512, 128, 256, 128, 256, 128, 512, 128, 128, 230 * 128]
+    assert call(st=strides(ok)) == -1 and b"not an upload" in lib.tree_last_error()
+    for i in range(10):
+        assert call(st=strides(ok[:i] + [ok[i] + 1] + ok[i + 1:])) == -1 and b"not aligned" in lib.tree_last_error()
+    assert call(dk=ctypes.c_void_p(0x3008)) == -1 and call(ws=ctypes.c_void_p(0x1008)) == -1
     assert call(dq=P) == -1 and call(dk=P2) == -1 and call(dv=P3) == -1
 
 

@@ -140,6 +140,27 @@ def test_attention_slices_of_one_projection(dtype):
     assert all(torch.equal(x, y) for x, y in zip(grads, a[7:]))
 
 
+def test_attention_head_major_and_repeated_tensors():
+    """Head-major storage, and k, v repeated over tokens' storage (stride 0):
+    the bits of the contiguous tensors."""
+    parents, lens = dfs_trie(9, 7, [20, 61])
+    n = int(lens.sum())
+    say("attention strides")
+    q, k, v, do = tensors(n, 4, 2, 64, torch.bfloat16)
+    plan = ptp.tree_plan(parents, lens, 4)
+    o, lse = ptp.tree_attention(q, k, v, plan, return_lse=True)
+    grads = ptp.tree_attention_backward(q, k, v, o, lse, do, plan)
+    q2, k2, v2, o2, do2 = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v, o, do))
+    assert not q2.is_contiguous()
+    o3, lse3 = ptp.tree_attention(q2, k2, v2, plan, return_lse=True)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+    assert all(torch.equal(x, y) for x, y in zip(grads, ptp.tree_attention_backward(q2, k2, v2, o2, lse, do2, plan)))
+    one = k[:1].expand(n, 2, 64)
+    same = ptp.tree_attention(q, one, one, plan)
+    assert torch.equal(same, ptp.tree_attention(q, one.contiguous(), one.contiguous(), plan))
+    assert torch.equal(same.view(n, 2, 2, 64), one[:, :, None].expand(n, 2, 2, 64))
+
+
 def test_attention_scale_and_large_scores():
     """Scores of several hundred: the running maximum moves far and often."""
     parents, lens = dfs_trie(8, 8, [50, 130, 70])
@@ -280,7 +301,7 @@ def test_attention_refusals():
     with pytest.raises(ValueError):
         ptp.tree_attention(q, k, v[:, :1], plan)
     with pytest.raises(ValueError):
-        ptp.tree_attention(q.transpose(1, 2).contiguous().transpose(1, 2), k, v, plan)
+        ptp.tree_attention(q.transpose(1, 2).contiguous().transpose(1, 2), k, v, plan)  # a head's elements apart
     with pytest.raises(TypeError):
         ptp.tree_attention(q, k.float(), v, plan)
     with pytest.raises(TypeError):
@@ -309,6 +330,6 @@ def test_attention_refusals():
     out = torch.empty_like(q)
     big = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
     for buf in (big, stale):
-        rc = lib.tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None, 256, 128, 128, 32, 4, 2,
+        rc = lib.tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None, None, 32, 4, 2,
                                 64, 0.125, 1, a.handle, buf.data_ptr(), max(buf.numel(), a.device_bytes()), None)
         assert rc == -1 and b"not an upload" in lib.tree_last_error()
