@@ -511,8 +511,8 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
 
 /*
  * tree_attention_backward_workspace_bytes -- device workspace of
- * tree_attention_backward: dO . o of every row and head, and the partial dk,
- * dv of key tiles whose work is split.  0 for a NULL or unsupported argument.
+ * tree_attention_backward: dO . o and the lse of every row and head, and the
+ * partial dk, dv of key tiles whose work is split.  0 for a NULL or unsupported argument.
  */
 size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
                                                int32_t d);

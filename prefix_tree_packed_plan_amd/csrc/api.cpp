@@ -138,7 +138,7 @@ int32_t attention_split(const tg::AttnPlan& p, int32_t h_q, int32_t h_kv) {
   return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(h_q / h_kv, (511 + work) / work)));
 }
 size_t attention_delta_bytes(const tg::AttnPlan& p, int32_t h_q) {
-  return (static_cast<size_t>(p.n_tokens) * h_q * sizeof(float) + 255) / 256 * 256;
+  return (2 * static_cast<size_t>(p.n_tokens) * h_q * sizeof(float) + 255) / 256 * 256;
 }
 
 // A row is spread over several work-groups only where the rows alone leave

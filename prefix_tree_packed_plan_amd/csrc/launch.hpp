@@ -222,7 +222,7 @@ struct AttnArgs {
   void* dk;
   void* dv;
   float* lse;        // [N, h_q] natural log; written by the forward, read by the backward
-  float* delta;      // backward workspace [N, h_q]: sum over d of dout * o
+  float* delta;      // backward workspace [2, N, h_q]: -(sum over d of dout * o), -lse / scale
   float* part;       // backward workspace: partial dk, dv [slot, h_kv, 2, kKTile, d]
   const int32_t* tok_d;  // [N + 1]
   const int32_t* tok_e;  // [N + 1]

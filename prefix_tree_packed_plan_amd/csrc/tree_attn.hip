@@ -41,6 +41,20 @@ using chunk::pk2;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) const chunk::u32x4 lds_u4;
 
+// A copy of x the compiler knows nothing of: what is computed from it is
+// computed where it stands, and not kept in registers across a loop.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// This lane's number, made anew at every use.
+__device__ __forceinline__ int lane_id() {
+  int x;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+  return x;
+}
+
 // 16 bytes from LDS.
 __device__ __forceinline__ uint4 lds16(const char* p) {
   const chunk::u32x4 w = *(lds_u4*)p;
@@ -252,6 +266,35 @@ __device__ __forceinline__ void contract(f32x16 (&acc)[D / 32], const f32x16& w,
   }
 }
 
+// use(i, load(i)) for i < N with the next three loads in flight, in exactly
+// this order: left to itself the compiler takes either one operand at a time
+// or more than the registers hold.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+template <int N, typename Load, typename Use>
+__device__ __forceinline__ void pipe(Load load, Use use) {
+  constexpr int P = N < 3 ? N : 3;
+  uint4 x[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) x[i] = load(i);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    use(i, x[i % P]);
+    if (i + P < N) x[i % P] = load(i + P);
+    fence();
+  }
+}
+// Accumulator rows 8 (i / 4) + i % 4 of 32 values (p already points at the
+// lane's half).
+__device__ __forceinline__ f32x16 rows16(const float* p) {
+  f32x16 r;
+#pragma unroll
+  for (int i4 = 0; i4 < 4; ++i4) {
+    const float4 x = *reinterpret_cast<const float4*>(p + 8 * i4);
+    r[4 * i4] = x.x, r[4 * i4 + 1] = x.y, r[4 * i4 + 2] = x.z, r[4 * i4 + 3] = x.w;
+  }
+  return r;
+}
+
 // ---- run lists ----------------------------------------------------------------
 // The packed row of virtual position v, for tiles of kRows positions taken in
 // order (uniform over the wave but for `row`'s argument).
@@ -326,6 +369,7 @@ template <typename T, int D>
 __device__ __forceinline__ void stage(int row, const char* a, int64_t lda, char* ta, const char* b, int64_t ldb,
                                       char* tb, int wave, int lane) {
   using C = Cfg<T, D>;
+  lane = opaque(lane);
 #pragma unroll
   for (int i = 0; i < C::NI; ++i) {
     const int g = 4 * i + wave, r = g * (1024 / C::RB) + lane / C::NC;
@@ -539,7 +583,8 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
 }
 
 // ---- gradient of q -----------------------------------------------------------------
-// Same tiles as the forward; also leaves delta for the other gradients.
+// Same tiles as the forward; also leaves -delta and -lse / scale, which the
+// other gradients' sums start from.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -588,9 +633,12 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
       }
     }
     delta += half_swap(delta);
-    if (on && half == 0) a.delta[r * a.h_q + h] = delta;
   }
-  const float lse2 = a.lse[r * a.h_q + h] * kLog2e;
+  const float lse = a.lse[r * a.h_q + h], lse2 = lse * kLog2e;
+  if (on && half == 0) {
+    a.delta[r * a.h_q + h] = -delta;
+    a.delta[(int64_t(a.n_tok) + r) * a.h_q + h] = -lse / a.scale;
+  }
   const int dq = a.tok_d[r];
   int dlo, dhi;
   span(dq, dlo, dhi);
@@ -653,8 +701,8 @@ template <typename T, int D>
 struct BwdSmem {
   alignas(16) char q[2][Cfg<T, D>::TILE];
   alignas(16) char g[2][Cfg<T, D>::TILE];
-  alignas(16) float lse[2][kRows];
-  alignas(16) float delta[2][kRows];
+  alignas(16) float lse[2][kRows];    // -lse / scale
+  alignas(16) float delta[2][kRows];  // -delta
   alignas(16) int d[2][kRows];
 };
 
@@ -678,10 +726,11 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int h, int buf) {
     cs.seek(v0);
+    const int lane = lane_id();
     const int row = cs.row(v0, lane);
     stage<T, D>(row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave, lane);
     const int64_t x = int64_t(row) * a.h_q + h;
-    if (wave == 0) dma4(a.lse + x, reinterpret_cast<char*>(sm.lse[buf]));
+    if (wave == 0) dma4(a.delta + int64_t(a.n_tok) * a.h_q + x, reinterpret_cast<char*>(sm.lse[buf]));
     else if (wave == 1) dma4(a.delta + x, reinterpret_cast<char*>(sm.delta[buf]));
     else if (wave == 2) dma4(a.tok_d + (v0 + lane < cs.end ? row : a.n_tok), reinterpret_cast<char*>(sm.d[buf]));
   };
@@ -696,7 +745,6 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
   span(kd, kdlo, kdhi);
   span(ke, kelo, kehi);
 
-  const Reader<T, D> rd(lane);
   const float c = a.scale * kLog2e;
   f32x16 dk[C::NDB], dv[C::NDB];
 #pragma unroll
@@ -721,6 +769,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
     v0 = nv;
     h = nh;
     if (masked) {
+      const int lane = lane_id();
       bad = __ballot(nonfinite<float>(__float_as_uint(sm.delta[buf][lane])));
       const int qd = sm.d[buf][lane];
       skip = __ballot(kdlo <= qd && qd < kehi) == 0;
@@ -740,40 +789,40 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
           dv[db][i] += x;
         }
       __syncthreads();
-      for (int i = threadIdx.x; i < kRows * C::NC; i += 256)
+      for (int i = 64 * wave + lane_id(); i < kRows * C::NC; i += 256)
         if ((bad >> (i / C::NC)) & 1) {
           *(__attribute__((address_space(3))) chunk::u32x4*)(qt + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
           *(__attribute__((address_space(3))) chunk::u32x4*)(gt + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
         }
-      if (threadIdx.x < kRows && (bad >> threadIdx.x) & 1) {
-        sm.lse[buf][threadIdx.x] = -kNegInf;  // p = 0
-        sm.delta[buf][threadIdx.x] = 0.f;
+      const int r = lane_id();
+      if (wave == 0 && (bad >> r) & 1) {
+        sm.lse[buf][r] = kNegInf;  // p = 0
+        sm.delta[buf][r] = 0.f;
       }
       __syncthreads();
     }
     if (skip) continue;
-#pragma unroll
+    const int ln = lane_id(), half = ln >> 5;
+    Reader<T, D> rd(ln);
+#pragma unroll 1
     for (int kb = 0; kb < 2; ++kb) {
-      f32x16 p = zero16(), ds = zero16();
+      rd.row = opaque(rd.row);
+      rd.tr = opaque(rd.tr);
+      // The sums start at -lse / scale and -delta: p = exp2(c s), ds = p dp.
+      f32x16 p = rows16(sm.lse[buf] + 32 * kb + 4 * half);
+      pipe<C::NK>([&](int ks) { return rd.rows(qt, kb, ks); },
+                  [&](int ks, const uint4 x) { p = mm<T>(x, kf[ks], p); });
+      f32x16 ds = rows16(sm.delta[buf] + 32 * kb + 4 * half);
+      pipe<C::NK>([&](int ks) { return rd.rows(gt, kb, ks); },
+                  [&](int ks, const uint4 x) {
+                    ds = mm<T>(x, vf[ks], ds);
 #pragma unroll
-      for (int ks = 0; ks < C::NK; ++ks) {
-        p = mm<T>(rd.rows(qt, kb, ks), kf[ks], p);
-        ds = mm<T>(rd.rows(gt, kb, ks), vf[ks], ds);
-      }
+                    for (int i = 16 * ks / C::NK; i < 16 * (ks + 1) / C::NK; ++i) p[i] = ex2(p[i] * c);
+                  });
+      if (masked) {  // an unseen row's dO . v may be anything
 #pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const int o = 32 * kb + 8 * i4 + 4 * half;
-        const float4 ls = *reinterpret_cast<const float4*>(&sm.lse[buf][o]);
-        const float4 de = *reinterpret_cast<const float4*>(&sm.delta[buf][o]);
-        const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 4 * i4 + j;
-          p[i] = ex2(fmaf(p[i], c, -l4[j] * kLog2e));
-          ds[i] = p[i] * (ds[i] - d4[j]);
-        }
-        if (masked) {
-          const int4 dd = *reinterpret_cast<const int4*>(&sm.d[buf][o]);
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const int4 dd = *reinterpret_cast<const int4*>(&sm.d[buf][32 * kb + 8 * i4 + 4 * half]);
           const int x4[4] = {dd.x, dd.y, dd.z, dd.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -783,8 +832,18 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
           }
         }
       }
-      contract<T, D>(dv, p, gt, kb, rd);
-      contract<T, D>(dk, ds, qt, kb, rd);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ds[i] *= p[i];
+      uint4 pb[C::NS], db[C::NS];
+#pragma unroll
+      for (int s = 0; s < C::NS; ++s) {
+        pb[s] = frag<T>(p, s);
+        db[s] = frag<T>(ds, s);
+      }
+      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(gt, kb, i / C::NDB, i % C::NDB); },
+                           [&](int i, const uint4 x) { dv[i % C::NDB] = mm<T>(x, pb[i / C::NDB], dv[i % C::NDB]); });
+      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(qt, kb, i / C::NDB, i % C::NDB); },
+                           [&](int i, const uint4 x) { dk[i % C::NDB] = mm<T>(x, db[i / C::NDB], dk[i % C::NDB]); });
     }
   }
   if (a.split == 1 && it.part >= a.n_multi_parts) {

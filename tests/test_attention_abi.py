@@ -97,11 +97,11 @@ def test_attention_workspace_counts_split_work():
     partial sums for its parts."""
     lib = _lib.load()
     many = plan_of([-1] * 600, [128] * 600).attention()
-    assert lib.tree_attention_backward_workspace_bytes(many.handle, 2, 1, 64) == 600 * 128 * 2 * 4
+    assert lib.tree_attention_backward_workspace_bytes(many.handle, 2, 1, 64) == 2 * 600 * 128 * 2 * 4
     few = plan_of([-1], [128]).attention()
-    assert lib.tree_attention_backward_workspace_bytes(few.handle, 4, 1, 64) == 128 * 4 * 4 + 4 * 2 * 128 * 64 * 4
+    assert lib.tree_attention_backward_workspace_bytes(few.handle, 4, 1, 64) == 2 * 128 * 4 * 4 + 4 * 2 * 128 * 64 * 4
     part = plan_of([-1] + [-1] * 600, [4096] + [128] * 600).attention()  # tiles 0..15 have two parts
-    delta = (4096 + 600 * 128) * 4
+    delta = 2 * (4096 + 600 * 128) * 4
     assert lib.tree_attention_backward_workspace_bytes(part.handle, 1, 1, 64) == delta + 32 * 2 * 128 * 64 * 4
 
 
