@@ -138,6 +138,14 @@ struct Reader {
   __device__ __forceinline__ uint4 rows(const char* t, int kb, int ks) const {
     return lds16(t + ((row ^ (32 * ks)) + kb * 32 * C::RB));
   }
+  // The same lane's reads 32 rows further on (the offsets' low bits, which
+  // the reads change, are not touched).
+  __device__ __forceinline__ Reader block(int kb) const {
+    Reader r = *this;
+    r.row = opaque(row + kb * 32 * C::RB);
+    r.tr = opaque(tr + kb * 32 * C::RB);
+    return r;
+  }
   // Fragment s of rows 32 kb .. 32 kb + 31 of the transposed tile: column 32
   // db + lane % 32.
   __device__ __forceinline__ uint4 cols(const char* t, int kb, int s, int db) const;
@@ -308,9 +316,9 @@ struct Cursor {
     seek(it.v0);
   }
   __device__ __forceinline__ void load() {
-    virt = runs[cur].virt;
-    row0 = runs[cur].row;
-    next = cur + 1 < n ? runs[cur + 1].virt : 0x7FFFFFFF;
+    virt = __builtin_amdgcn_readfirstlane(runs[cur].virt);
+    row0 = __builtin_amdgcn_readfirstlane(runs[cur].row);
+    next = cur + 1 < n ? __builtin_amdgcn_readfirstlane(runs[cur + 1].virt) : 0x7FFFFFFF;
   }
   __device__ __forceinline__ void seek(int v) {
     while (next <= v) {
@@ -318,6 +326,8 @@ struct Cursor {
       load();
     }
   }
+  // Whether the tile at v0 (in run `cur`) is kRows rows of one run.
+  __device__ __forceinline__ bool whole(int v0) const { return v0 + kRows <= min(next, end); }
   // The row of position v0 + x (x < kRows, v0 in run `cur`); positions past
   // the end repeat the last.
   __device__ __forceinline__ int row(int v0, int x) const {
@@ -348,6 +358,17 @@ __device__ __forceinline__ void dma16(const void* src, char* lds) {
                : "s"(lds_at(lds)), "v"(src)
                : "memory");
 }
+// From src + off, src the same for all lanes.
+__device__ __forceinline__ void dma16(const char* src, int off, char* lds) {
+  const uint64_t p = reinterpret_cast<uint64_t>(src);
+  const uint64_t u = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p)))) |
+                     uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p >> 32)))) << 32;
+  int m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(lds_at(lds)), "v"(off), "s"(u)
+               : "memory");
+}
 __device__ __forceinline__ void dma4(const void* src, char* lds) {
   int m0;
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, off\n\ts_mov_b32 m0, %0"
@@ -363,20 +384,34 @@ __device__ __forceinline__ void wait_dma() {
   asm volatile("" ::: "memory");
 }
 
-// 64 rows of two tensors into LDS tiles ta, tb, by 4 waves (wave w: every
-// fourth group of 1024 bytes); lane l names the row of tile row l.
+// The 64 rows at virtual position v0 of two tensors (a head's first row at a,
+// b; bytes lda, ldb between rows) into LDS tiles ta, tb, by 4 waves (wave w:
+// every fourth group of 1024 bytes).  Rows of one run need no address
+// arithmetic in the vector unit: all lanes share a base.  `row` is this lane's
+// row of the tile (lane l: row l), used otherwise.
 template <typename T, int D>
-__device__ __forceinline__ void stage(int row, const char* a, int64_t lda, char* ta, const char* b, int64_t ldb,
-                                      char* tb, int wave, int lane) {
+__device__ __forceinline__ void stage(const Cursor& cs, int v0, int row, const char* a, int64_t lda, char* ta,
+                                      const char* b, int64_t ldb, char* tb, int wave) {
   using C = Cfg<T, D>;
-  lane = opaque(lane);
+  constexpr int PER = 1024 / C::RB;  // rows of a group
+  const int lane = lane_id();
+  if (cs.whole(v0) && lda < (1 << 24) && ldb < (1 << 24)) {
+    const int64_t first = cs.row0 + (v0 - cs.virt);
 #pragma unroll
-  for (int i = 0; i < C::NI; ++i) {
-    const int g = 4 * i + wave, r = g * (1024 / C::RB) + lane / C::NC;
-    const int64_t from = __shfl(row, r, 64);
-    const int c = 16 * ((lane % C::NC) ^ swz<C::RB>(r));
-    dma16(a + from * lda + c, ta + 1024 * g);
-    dma16(b + from * ldb + c, tb + 1024 * g);
+    for (int i = 0; i < C::NI; ++i) {
+      const int g = 4 * i + wave, c = 16 * ((lane % C::NC) ^ swz<C::RB>(g * PER + lane / C::NC));
+      dma16(a + (first + g * PER) * lda, (lane / C::NC) * int(lda) + c, ta + 1024 * g);
+      dma16(b + (first + g * PER) * ldb, (lane / C::NC) * int(ldb) + c, tb + 1024 * g);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < C::NI; ++i) {
+      const int g = 4 * i + wave, r = g * PER + lane / C::NC;
+      const int64_t from = __shfl(row, r, 64);
+      const int c = 16 * ((lane % C::NC) ^ swz<C::RB>(r));
+      dma16(a + from * lda + c, ta + 1024 * g);
+      dma16(b + from * ldb + c, tb + 1024 * g);
+    }
   }
 }
 
@@ -483,9 +518,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int buf) {
     cs.seek(v0);
-    const int row = cs.row(v0, lane);
-    stage<T, D>(row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
-    if (v0 + kRows > it.n_full && wave < 2) {
+    const bool part = v0 + kRows > it.n_full;
+    const int row = part || !cs.whole(v0) ? cs.row(v0, lane) : 0;
+    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave);
+    if (part && wave < 2) {
       const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
       else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
@@ -506,8 +542,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
   for (int db = 0; db < C::NDB; ++db) acc[db] = zero16();
   float m = kNegInf, l = 0.f;  // running maximum of q.k (both halves of the wave agree), this lane's part of the sum
 
-  int buf = 0;
-  for (int v0 = 0; v0 < it.n_total; v0 += kRows, buf ^= 1) {
+  // The tile at v0 is in buffer `buf`, a constant: LDS addresses then are a
+  // lane's offset plus an immediate.
+  const auto tile = [&](int v0, auto buffer) {
+    constexpr int buf = decltype(buffer)::value;
     wait_dma();
     __syncthreads();
     if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
@@ -575,6 +613,12 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], vt, kb, rd);
     }
+  };
+  for (int v0 = 0;;) {
+    tile(v0, std::integral_constant<int, 0>{});
+    if ((v0 += kRows) >= it.n_total) break;
+    tile(v0, std::integral_constant<int, 1>{});
+    if ((v0 += kRows) >= it.n_total) break;
   }
   l += half_swap(l);
   const float inv = 1.f / l;
@@ -602,9 +646,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int buf) {
     cs.seek(v0);
-    const int row = cs.row(v0, lane);
-    stage<T, D>(row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
-    if (v0 + kRows > it.n_full && wave < 2) {
+    const bool part = v0 + kRows > it.n_full;
+    const int row = part || !cs.whole(v0) ? cs.row(v0, lane) : 0;
+    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave);
+    if (part && wave < 2) {
       const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
       else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
@@ -649,8 +694,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
 #pragma unroll
   for (int db = 0; db < C::NDB; ++db) acc[db] = zero16();
 
-  int buf = 0;
-  for (int v0 = 0; v0 < it.n_total; v0 += kRows, buf ^= 1) {
+  // The tile at v0 is in buffer `buf`, a constant: LDS addresses then are a
+  // lane's offset plus an immediate.
+  const auto tile = [&](int v0, auto buffer) {
+    constexpr int buf = decltype(buffer)::value;
     wait_dma();
     __syncthreads();
     if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
@@ -692,6 +739,12 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], kt, kb, rd);
     }
+  };
+  for (int v0 = 0;;) {
+    tile(v0, std::integral_constant<int, 0>{});
+    if ((v0 += kRows) >= it.n_total) break;
+    tile(v0, std::integral_constant<int, 1>{});
+    if ((v0 += kRows) >= it.n_total) break;
   }
   store_row<T, D>(static_cast<T*>(a.out) + (r * a.h_q + h) * D, acc, a.scale, half, on);
 }
@@ -728,7 +781,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
     cs.seek(v0);
     const int lane = lane_id();
     const int row = cs.row(v0, lane);
-    stage<T, D>(row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave, lane);
+    stage<T, D>(cs, v0, row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave);
     const int64_t x = int64_t(row) * a.h_q + h;
     if (wave == 0) dma4(a.delta + int64_t(a.n_tok) * a.h_q + x, reinterpret_cast<char*>(sm.lse[buf]));
     else if (wave == 1) dma4(a.delta + x, reinterpret_cast<char*>(sm.delta[buf]));
@@ -750,8 +803,9 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
 #pragma unroll
   for (int db = 0; db < C::NDB; ++db) dk[db] = dv[db] = zero16();
 
-  int buf = 0;
-  for (int v0 = it.v0; h < (hk + 1) * group; buf ^= 1) {
+  int v0 = it.v0;
+  const auto tile = [&](auto buffer) {
+    constexpr int buf = decltype(buffer)::value;
     wait_dma();
     __syncthreads();
     int nv = v0 + kRows, nh = h;
@@ -801,19 +855,18 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
       }
       __syncthreads();
     }
-    if (skip) continue;
+    if (skip) return;
     const int ln = lane_id(), half = ln >> 5;
-    Reader<T, D> rd(ln);
+    const Reader<T, D> all(ln);
 #pragma unroll 1
     for (int kb = 0; kb < 2; ++kb) {
-      rd.row = opaque(rd.row);
-      rd.tr = opaque(rd.tr);
+      const Reader<T, D> rd = all.block(kb);
       // The sums start at -lse / scale and -delta: p = exp2(c s), ds = p dp.
       f32x16 p = rows16(sm.lse[buf] + 32 * kb + 4 * half);
-      pipe<C::NK>([&](int ks) { return rd.rows(qt, kb, ks); },
+      pipe<C::NK>([&](int ks) { return rd.rows(qt, 0, ks); },
                   [&](int ks, const uint4 x) { p = mm<T>(x, kf[ks], p); });
       f32x16 ds = rows16(sm.delta[buf] + 32 * kb + 4 * half);
-      pipe<C::NK>([&](int ks) { return rd.rows(gt, kb, ks); },
+      pipe<C::NK>([&](int ks) { return rd.rows(gt, 0, ks); },
                   [&](int ks, const uint4 x) {
                     ds = mm<T>(x, vf[ks], ds);
 #pragma unroll
@@ -840,11 +893,17 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
         pb[s] = frag<T>(p, s);
         db[s] = frag<T>(ds, s);
       }
-      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(gt, kb, i / C::NDB, i % C::NDB); },
+      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(gt, 0, i / C::NDB, i % C::NDB); },
                            [&](int i, const uint4 x) { dv[i % C::NDB] = mm<T>(x, pb[i / C::NDB], dv[i % C::NDB]); });
-      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(qt, kb, i / C::NDB, i % C::NDB); },
+      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(qt, 0, i / C::NDB, i % C::NDB); },
                            [&](int i, const uint4 x) { dk[i % C::NDB] = mm<T>(x, db[i / C::NDB], dk[i % C::NDB]); });
     }
+  };
+  while (true) {
+    tile(std::integral_constant<int, 0>{});
+    if (h >= (hk + 1) * group) break;
+    tile(std::integral_constant<int, 1>{});
+    if (h >= (hk + 1) * group) break;
   }
   if (a.split == 1 && it.part >= a.n_multi_parts) {
     store_row<T, D>(static_cast<T*>(a.dk) + (r * a.h_kv + hk) * D, dk, a.scale, half, on);
