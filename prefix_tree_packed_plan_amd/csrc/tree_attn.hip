@@ -421,6 +421,14 @@ __device__ __forceinline__ float half_swap(float x) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// A wave in its matrix products goes before one in its exponentials: the two
+// waves of a SIMD then take turns, and the matrix unit waits less (chain of
+// 16383 tokens, 8 heads of 128: 609 -> 567 us).
+__device__ __forceinline__ void matrix_first(bool on) {
+  if (on) __builtin_amdgcn_s_setprio(1);
+  else __builtin_amdgcn_s_setprio(0);
+}
+
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;
 #pragma unroll
@@ -560,12 +568,14 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     }
     f32x16 p[2];
     if (!skip) {
+      matrix_first(true);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         p[kb] = zero16();
 #pragma unroll
         for (int ks = 0; ks < C::NK; ++ks) p[kb] = mm<T>(rd.rows(kt, kb, ks), q[ks], p[kb]);
       }
+      matrix_first(false);
       if (masked) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -610,8 +620,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
       __syncthreads();
     }
     if (!skip) {
+      matrix_first(true);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], vt, kb, rd);
+      matrix_first(false);
     }
   };
   for (int v0 = 0;;) {
@@ -715,11 +727,13 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         f32x16 s = zero16(), dp = zero16();
+        matrix_first(true);
 #pragma unroll
         for (int ks = 0; ks < C::NK; ++ks) {
           s = mm<T>(rd.rows(kt, kb, ks), q[ks], s);
           dp = mm<T>(rd.rows(vt, kb, ks), g[ks], dp);
         }
+        matrix_first(false);
 #pragma unroll
         for (int i = 0; i < 16; ++i) p[kb][i] = ex2(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
         if (masked) {
@@ -736,8 +750,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
       __syncthreads();
     }
     if (!skip) {
+      matrix_first(true);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], kt, kb, rd);
+      matrix_first(false);
     }
   };
   for (int v0 = 0;;) {
@@ -863,6 +879,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
       const Reader<T, D> rd = all.block(kb);
       // The sums start at -lse / scale and -delta: p = exp2(c s), ds = p dp.
       f32x16 p = rows16(sm.lse[buf] + 32 * kb + 4 * half);
+      matrix_first(true);
       pipe<C::NK>([&](int ks) { return rd.rows(qt, 0, ks); },
                   [&](int ks, const uint4 x) { p = mm<T>(x, kf[ks], p); });
       f32x16 ds = rows16(sm.delta[buf] + 32 * kb + 4 * half);
@@ -872,6 +889,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
 #pragma unroll
                     for (int i = 16 * ks / C::NK; i < 16 * (ks + 1) / C::NK; ++i) p[i] = ex2(p[i] * c);
                   });
+      matrix_first(false);
       if (masked) {  // an unseen row's dO . v may be anything
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
@@ -893,10 +911,12 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
         pb[s] = frag<T>(p, s);
         db[s] = frag<T>(ds, s);
       }
+      matrix_first(true);
       pipe<C::NS * C::NDB>([&](int i) { return rd.cols(gt, 0, i / C::NDB, i % C::NDB); },
                            [&](int i, const uint4 x) { dv[i % C::NDB] = mm<T>(x, pb[i / C::NDB], dv[i % C::NDB]); });
       pipe<C::NS * C::NDB>([&](int i) { return rd.cols(qt, 0, i / C::NDB, i % C::NDB); },
                            [&](int i, const uint4 x) { dk[i % C::NDB] = mm<T>(x, db[i / C::NDB], dk[i % C::NDB]); });
+      matrix_first(false);
     }
   };
   while (true) {
