@@ -453,9 +453,9 @@ int tree_ssd_scan(const void* x, const float* dt, const float* A, const void* B,
  * `plan` (host only, no device work; built once per plan and shared by every
  * attention layer): for every 128 packed rows, the runs of packed rows their
  * tokens see, those all of them see first; for every 128 keys, the runs of
- * rows that see them, cut into parts of at most 2048; and every token's place
- * in a depth-first walk with the end of its segment's subtree, which decide
- * single pairs.  Any numbering with parents before children is accepted.  The
+ * rows that see them; both whole and cut into parts, for calls with few tiles
+ * or lists of very different lengths; and every token's place in a depth-first
+ * walk with the end of its segment's subtree, which decide single pairs.  Any numbering with parents before children is accepted.  The
  * tables are copies: the plan may be freed before them.
  * Errors: INVALID_ARG (also: out of host memory), UNSUPPORTED (a trie whose
  * run lists exceed 2^26 entries: very deep and branched all along).
@@ -475,6 +475,14 @@ size_t tree_attention_plan_device_bytes(const tree_attention_plan_t* aplan);
  * Errors: INVALID_ARG, WORKSPACE (dplan_bytes too small), HIP.
  */
 int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, size_t dplan_bytes, void* stream);
+
+/*
+ * tree_attention_workspace_bytes -- device workspace of tree_attention: the
+ * results of parts of a tile's keys, where those are spread over several
+ * work-groups (few tiles and heads, or very different path lengths); 0
+ * otherwise and for a NULL or bad argument.
+ */
+size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d);
 
 /*
  * tree_attention -- softmax attention in which token i sees exactly the tokens
@@ -500,19 +508,22 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
  * dtype  TREE_DTYPE_BF16 (bf16 MFMA; scores, maxima, sums and the output's
  *        accumulation in fp32, probabilities rounded to bf16 for their
  *        product with v) or TREE_DTYPE_F32 (fp32 MFMA throughout).
- * d in {32, 64, 128}.  No workspace; results do not depend on the schedule.
+ * d in {32, 64, 128}.
  * dplan, dplan_bytes  device copy of `aplan` (tree_attention_plan_upload).
+ * ws     device workspace, ws_bytes >= tree_attention_workspace_bytes (may be
+ *        NULL if that is 0).
  * Errors: INVALID_ARG, SIZE (n_tokens != plan N), UNSUPPORTED (d, or h_q not a
  * multiple of h_kv), WORKSPACE (dplan_bytes too small), HIP.
  */
 int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
                    int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
-                   const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* stream);
+                   const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* ws,
+                   size_t ws_bytes, void* stream);
 
 /*
  * tree_attention_backward_workspace_bytes -- device workspace of
  * tree_attention_backward: dO . o and the lse of every row and head, and the
- * partial dk, dv of key tiles whose work is split.  0 for a NULL or unsupported argument.
+ * results of parts of a tile's work.  0 for a NULL or unsupported argument.
  */
 size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
                                                int32_t d);

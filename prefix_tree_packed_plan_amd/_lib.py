@@ -80,7 +80,9 @@ SIGNATURES = {
     "tree_attention_plan_free": (None, [_P]),
     "tree_attention_plan_device_bytes": (_SZ, [_P]),
     "tree_attention_plan_upload": (ctypes.c_int, [_P, _P, _SZ, _P]),
-    "tree_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P]),
+    "tree_attention_workspace_bytes": (_SZ, [_P, _I32, _I32]),
+    "tree_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P, _SZ,
+                                      _P]),
     "tree_attention_backward_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
     "tree_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F,
                                                _I32, _P, _P, _SZ, _P, _SZ, _P]),
@@ -592,7 +594,7 @@ def _attention_shapes(q, k, v, plan):
 
 
 def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, return_lse: bool = False, out=None,
-                   lse=None):
+                   lse=None, workspace=None):
     """Tree attention: o [N, H_q, d] (and lse [N, H_q] fp32).  Every token
     attends to the tokens of its own root-to-token path, itself included.
 
@@ -614,13 +616,15 @@ def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, retur
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
         _need_shape(lse, "lse", (n, h_q))
+    lib = load()
     aplan = plan.attention()
+    workspace, ws_bytes = _workspace(workspace, int(lib.tree_attention_workspace_bytes(aplan.handle, h_q, d)), dev)
     dplan = aplan.on_device(dev)
     stream = torch.cuda.current_stream(dev).cuda_stream
-    _check(load().tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                 lse.data_ptr() if lse is not None else None, (_I64 * 6)(*st), n, h_q, k.shape[1], d,
-                                 d ** -0.5 if scale is None else float(scale), _dtype_code(q), aplan.handle,
-                                 dplan.data_ptr(), dplan.numel(), stream))
+    p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    _check(lib.tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), p(lse), (_I64 * 6)(*st), n, h_q,
+                              k.shape[1], d, d ** -0.5 if scale is None else float(scale), _dtype_code(q),
+                              aplan.handle, dplan.data_ptr(), dplan.numel(), p(workspace), ws_bytes, stream))
     if return_lse:
         return o, lse
     return o

@@ -104,9 +104,9 @@ int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_
   if (!tg::attention_supported(d, dtype))
     return fail(TREE_ERR_UNSUPPORTED, "%s: d=%d dtype=%d not compiled in", fn, d, dtype);
   if (!positive(scale)) return fail(TREE_ERR_INVALID_ARG, "%s: scale must be > 0 and finite", fn);
-  if (static_cast<int64_t>(std::max(p.n_qtiles, p.n_kitems)) * h_q >= (int64_t(1) << 31))
-    return fail(TREE_ERR_UNSUPPORTED, "%s: too many tiles (%d) for %d heads", fn, std::max(p.n_qtiles, p.n_kitems),
-                h_q);
+  // Grids: parts x heads; and heads along the join launches' second axis.
+  if (h_q > 65535 || (static_cast<int64_t>(p.q.n_tiles) + tg::AttnPlan::kMaxParts) * h_q >= (int64_t(1) << 31))
+    return fail(TREE_ERR_UNSUPPORTED, "%s: too many heads (%d) for %d tiles", fn, h_q, p.q.n_tiles);
   return TREE_OK;
 }
 // A [n_tokens, heads, d] tensor read 16 bytes at a time: `strides` holds the
@@ -131,11 +131,26 @@ int check_aligned(const void* ptr, const char* name, const char* fn) {
   return TREE_OK;
 }
 
-// Work-groups a group's query heads are spread over in the gradients of k and
-// v: at least 2 a CU where the key tiles alone are fewer.
-int32_t attention_split(const tg::AttnPlan& p, int32_t h_q, int32_t h_kv) {
-  const int64_t work = static_cast<int64_t>(p.n_kitems) * h_kv;
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(h_q / h_kv, (511 + work) / work)));
+// How a call's lists are cut, and the parts whose results go to the workspace.
+struct Work {
+  const tg::AttnCut* cut;
+  int32_t split, n_join, n_parts;
+};
+Work attention_work(const tg::AttnLists& l, int32_t heads, int32_t steps) {
+  Work w{};
+  w.cut = &tg::choose_cut(l, heads, steps, steps > 1 ? &w.split : nullptr);
+  if (w.split < 1) w.split = 1;
+  w.n_join = w.split > 1 ? l.n_tiles : w.cut->n_multi;
+  w.n_parts = w.split > 1 ? w.cut->n_items : w.cut->n_multi_parts;
+  return w;
+}
+void set_work(const Work& w, const int32_t* base, tg::AttnArgs* a) {
+  a->items = reinterpret_cast<const tg::AttnItem*>(base + w.cut->m_items);
+  a->parts = reinterpret_cast<const tg::AttnParts*>(base + w.cut->m_parts);
+  a->n_items = w.cut->n_items;
+  a->n_join = w.n_join;
+  a->n_parts = w.n_parts;
+  a->split = w.split;
 }
 size_t attention_delta_bytes(const tg::AttnPlan& p, int32_t h_q) {
   return (2 * static_cast<size_t>(p.n_tokens) * h_q * sizeof(float) + 255) / 256 * 256;
@@ -806,9 +821,16 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
   return TREE_OK;
 }
 
+size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d) {
+  if (!aplan || h_q <= 0 || d <= 0) return 0;
+  const Work w = attention_work(aplan->p.q, h_q, 1);
+  return static_cast<size_t>(w.n_parts) * h_q * tg::attention_part_floats(d) * sizeof(float);
+}
+
 int tree_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
                    int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale, int32_t dtype,
-                   const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* stream) {
+                   const tree_attention_plan_t* aplan, const void* dplan, size_t dplan_bytes, void* ws,
+                   size_t ws_bytes, void* stream) {
   const char* fn = "tree_attention";
   if (!aplan || !q || !k || !v || !o || !dplan) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
   const tg::AttnPlan& p = aplan->p;
@@ -820,15 +842,20 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
   if (const int rc = make_heads(v, st_of(2), h_kv, d, dtype, "v", fn, &a.v)) return rc;
   if (const int rc = check_aligned(o, "o", fn)) return rc;
   if (o == q || o == k || o == v) return fail(TREE_ERR_INVALID_ARG, "%s: o must not alias q, k or v", fn);
+  const size_t need = tree_attention_workspace_bytes(aplan, h_q, d);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, need);
+  if (need > 0)
+    if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;
   if (const int rc = check_dplan(aplan, dplan, dplan_bytes, fn)) return rc;
   const int32_t* base = static_cast<const int32_t*>(dplan);
   a.out = o;
   a.lse = lse;
+  a.part = static_cast<float*>(ws);
   a.tok_d = base + p.m_d;
   a.tok_e = base + p.m_e;
-  a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_q);
   a.runs = reinterpret_cast<const tg::AttnRun*>(base + p.m_runs);
-  a.n_items = p.n_qtiles;
+  set_work(attention_work(p.q, h_q, 1), base, &a);
   a.n_tok = p.n_tokens;
   a.h_q = h_q;
   a.h_kv = h_kv;
@@ -842,9 +869,10 @@ size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* apla
                                                int32_t d) {
   if (!aplan || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0) return 0;
   const tg::AttnPlan& p = aplan->p;
-  const int32_t split = attention_split(p, h_q, h_kv);
-  const size_t slots = split > 1 ? static_cast<size_t>(p.n_kitems) * split : p.n_multi_parts;
-  return attention_delta_bytes(p, h_q) + slots * h_kv * 2 * tg::kKTile * d * sizeof(float);
+  const Work wq = attention_work(p.q, h_q, 1), wk = attention_work(p.k, h_kv, h_q / h_kv);
+  const size_t dq = static_cast<size_t>(wq.n_parts) * h_q * tg::attention_dq_part_floats(d);
+  const size_t dkv = static_cast<size_t>(wk.n_parts) * wk.split * h_kv * tg::attention_dkv_part_floats(d);
+  return attention_delta_bytes(p, h_q) + std::max(dq, dkv) * sizeof(float);
 }
 
 int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -876,8 +904,7 @@ int tree_attention_backward(const void* q, const void* k, const void* v, const v
   const size_t need = tree_attention_backward_workspace_bytes(aplan, h_q, h_kv, d);
   if (!ws || ws_bytes < need)
     return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, need);
-  if (reinterpret_cast<uintptr_t>(ws) % 16 != 0)
-    return fail(TREE_ERR_INVALID_ARG, "%s: the workspace is not aligned to 16 bytes", fn);
+  if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;
   if (const int rc = check_dplan(aplan, dplan, dplan_bytes, fn)) return rc;
   const int32_t* base = static_cast<const int32_t*>(dplan);
   a.out = dq;
@@ -888,23 +915,17 @@ int tree_attention_backward(const void* q, const void* k, const void* v, const v
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + attention_delta_bytes(p, h_q));
   a.tok_d = base + p.m_d;
   a.tok_e = base + p.m_e;
-  a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_q);
   a.runs = reinterpret_cast<const tg::AttnRun*>(base + p.m_runs);
-  a.parts = reinterpret_cast<const tg::AttnParts*>(base + p.m_parts);
-  a.n_items = p.n_qtiles;
-  a.n_multi_parts = p.n_multi_parts;
   a.n_tok = p.n_tokens;
   a.h_q = h_q;
   a.h_kv = h_kv;
-  a.split = attention_split(p, h_q, h_kv);
-  a.n_parts = a.split > 1 ? p.n_ktiles : p.n_multi;
   a.scale = scale;
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  set_work(attention_work(p.q, h_q, 1), base, &a);
   hipError_t e = tg::launch_attention_dq(a, d, dtype, st);  // also delta
   if (e == hipSuccess) {
-    a.items = reinterpret_cast<const tg::AttnItem*>(base + p.m_k);
-    a.n_items = p.n_kitems;
-    e = tg::launch_attention_dkv(a, d, dtype, st);
+    set_work(attention_work(p.k, h_kv, h_q / h_kv), base, &a);
+    e = tg::launch_attention_dkv(a, d, dtype, st);  // its parts take dq's place in the workspace
   }
   if (e != hipSuccess) return hip_fail("tree_attention_backward: launch", e);
   return TREE_OK;

@@ -27,7 +27,96 @@ int32_t emit(std::vector<Range>* r, int32_t v, std::vector<AttnRun>* runs) {
   return v;
 }
 
+// Cuts every list into equal parts of at most `most` positions, each a whole
+// number of 64; the parts of tiles with several are numbered first.
+AttnCut cut_lists(const std::vector<AttnItem>& lists, int64_t most, std::vector<AttnItem>* items,
+                  std::vector<AttnParts>* parts) {
+  AttnCut c;
+  c.most = static_cast<int32_t>(most);
+  std::vector<AttnParts> all;
+  items->clear();
+  parts->clear();
+  for (AttnItem it : lists) {
+    const int64_t n_parts = (it.n_total + most - 1) / most;
+    const int64_t each = n_parts == 1 ? it.n_total : ((it.n_total + n_parts - 1) / n_parts + 63) / 64 * 64;
+    all.push_back({it.tile, static_cast<int32_t>(items->size()), 0, 0});
+    for (int64_t v = 0; v < it.n_total; v += each) {
+      it.v0 = static_cast<int32_t>(v);
+      it.v1 = static_cast<int32_t>(std::min<int64_t>(it.n_total, v + each));
+      c.longest = std::max(c.longest, it.v1 - it.v0);
+      items->push_back(it);
+      all.back().n_parts += 1;
+    }
+  }
+  int32_t next = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (AttnParts x : all) {
+      if ((x.n_parts > 1) != (pass == 0)) continue;
+      for (int32_t i = 0; i < x.n_parts; ++i) (*items)[x.part0 + i].part = next + i;
+      x.part0 = next;
+      next += x.n_parts;
+      parts->push_back(x);
+    }
+    if (pass == 0) {
+      c.n_multi = static_cast<int32_t>(parts->size());
+      c.n_multi_parts = next;
+    }
+  }
+  c.n_items = next;
+  std::stable_sort(items->begin(), items->end(),
+                   [](const AttnItem& x, const AttnItem& y) { return x.v1 - x.v0 > y.v1 - y.v0; });
+  return c;
+}
+
+// All cuts of one kind of lists, appended to the device copy.
+AttnLists cut_all(const std::vector<AttnItem>& lists, std::vector<int32_t>* mirror) {
+  AttnLists l;
+  l.n_tiles = static_cast<int32_t>(lists.size());
+  int64_t longest = 0;
+  for (const AttnItem& it : lists) {
+    l.total += it.n_total;
+    longest = std::max<int64_t>(longest, it.n_total);
+  }
+  std::vector<AttnItem> items;
+  std::vector<AttnParts> parts;
+  const auto append = [&](const void* p, size_t ints) {
+    const size_t at = (mirror->size() + 7) / 8 * 8;
+    mirror->resize(at + ints, 0);
+    std::memcpy(mirror->data() + at, p, ints * sizeof(int32_t));
+    return at;
+  };
+  static_assert(sizeof(AttnItem) == 32 && sizeof(AttnRun) == 8 && sizeof(AttnParts) == 16, "device layout");
+  for (int64_t most = int64_t(1) << 31; most >= 256; most = most > 8192 ? 8192 : most / 2) {
+    const bool whole = most > 8192;
+    if (!whole && longest <= most) continue;  // the whole lists again
+    if (!whole && l.total / most + l.n_tiles > AttnPlan::kMaxParts) break;
+    AttnCut c = cut_lists(lists, whole ? std::max<int64_t>(longest, 1) : most, &items, &parts);
+    c.m_items = append(items.data(), items.size() * 8);
+    c.m_parts = append(parts.data(), parts.size() * 4);
+    l.cuts.push_back(c);
+  }
+  return l;
+}
+
 }  // namespace
+
+const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t* split) {
+  if (split) *split = 1;
+  const AttnCut& whole = l.cuts.front();
+  const int64_t room = l.total * heads * steps;  // of kSlots slots
+  const auto fits = [&](int64_t len) { return 4 * len * kSlots <= 3 * room; };
+  for (const AttnCut& c : l.cuts) {
+    if (!fits(int64_t(c.longest) * steps) && &c != &l.cuts.back()) continue;
+    int32_t s = 1;
+    if (split)
+      while (s < steps && !fits(int64_t(c.longest) * ((steps + s - 1) / s))) ++s;
+    const int64_t saved = int64_t(whole.longest) * steps - int64_t(c.longest) * ((steps + s - 1) / s);
+    if (saved < kWorth) return whole;
+    if (split) *split = s;
+    return c;
+  }
+  return whole;
+}
 
 int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
   const int32_t n_seg = p.n_seg;
@@ -73,7 +162,7 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
   for (int32_t s = 0; s < n_seg; ++s) top[s] = s > 0 && p.parents[s] == s - 1 ? top[s - 1] : s;
 
   std::vector<AttnRun> runs;
-  std::vector<AttnItem> qitems, kitems;
+  std::vector<AttnItem> qlists, klists;
   const auto too_large = [&] {
     *err = "tree_attention_plan: the tiles' run lists exceed 2^26 entries";
     return TREE_ERR_UNSUPPORTED;
@@ -123,15 +212,14 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
     }
     AttnItem it{t, static_cast<int32_t>(runs.size()), 0, 0, 0, 0, 0, 0};
     it.n_full = emit(&full, 0, &runs);
-    it.n_total = it.v1 = emit(&part, it.n_full, &runs);
+    it.n_total = emit(&part, it.n_full, &runs);
     it.n_runs = static_cast<int32_t>(runs.size()) - it.run_off;
-    qitems.push_back(it);
+    qlists.push_back(it);
     if (static_cast<int64_t>(runs.size()) > AttnPlan::kMaxRuns || steps > (int64_t(1) << 31)) return too_large();
   }
 
   // Key tiles: the subtrees of the tile's segments.
   const int32_t n_kt = (n + kKTile - 1) / kKTile;
-  std::vector<AttnParts> parts;
   std::vector<Range> pres;
   for (int32_t t = 0, s1 = 0; t < n_kt; ++t) {
     const int32_t lo = t * kKTile, hi = std::min<int64_t>(n, int64_t(lo) + kKTile);
@@ -177,49 +265,13 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
     it.n_full = emit(&full, 0, &runs);
     it.n_total = emit(&part, it.n_full, &runs);
     it.n_runs = static_cast<int32_t>(runs.size()) - it.run_off;
-    // Equal parts, each a whole number of 64 virtual rows.
-    const int32_t n_parts = static_cast<int32_t>((int64_t(it.n_total) + kPart - 1) / kPart);
-    const int32_t each = ((it.n_total + n_parts - 1) / n_parts + 63) / 64 * 64;
-    parts.push_back({t, static_cast<int32_t>(kitems.size()), 0, 0});
-    for (int64_t v = 0; v < it.n_total; v += each) {
-      it.v0 = static_cast<int32_t>(v);
-      it.v1 = static_cast<int32_t>(std::min<int64_t>(it.n_total, v + each));
-      kitems.push_back(it);
-      parts.back().n_parts += 1;
-    }
+    klists.push_back(it);
     if (static_cast<int64_t>(runs.size()) > AttnPlan::kMaxRuns || steps > (int64_t(1) << 31)) return too_large();
   }
-  // Part numbers: key tiles with several parts first.
-  std::vector<AttnParts> ordered;
-  int32_t next = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (AttnParts x : parts) {
-      if ((x.n_parts > 1) != (pass == 0)) continue;
-      for (int32_t i = 0; i < x.n_parts; ++i) kitems[x.part0 + i].part = next + i;
-      x.part0 = next;
-      next += x.n_parts;
-      ordered.push_back(x);
-    }
-    if (pass == 0) {
-      a.n_multi = static_cast<int32_t>(ordered.size());
-      a.n_multi_parts = next;
-    }
-  }
-  // Longest work first.
-  const auto longer = [](const AttnItem& x, const AttnItem& y) { return x.v1 - x.v0 > y.v1 - y.v0; };
-  std::stable_sort(qitems.begin(), qitems.end(), longer);
-  std::stable_sort(kitems.begin(), kitems.end(), longer);
-
-  a.n_qtiles = n_qt;
-  a.n_ktiles = n_kt;
-  a.n_kitems = static_cast<int32_t>(kitems.size());
   const auto up = [](size_t x) { return (x + 7) / 8 * 8; };
   a.m_d = 0;
   a.m_e = up(size_t(n) + 1);
-  a.m_q = a.m_e + up(size_t(n) + 1);
-  a.m_k = a.m_q + qitems.size() * 8;
-  a.m_parts = a.m_k + kitems.size() * 8;
-  a.m_runs = up(a.m_parts + ordered.size() * 4);
+  a.m_runs = a.m_e + up(size_t(n) + 1);
   a.mirror.assign(a.m_runs + runs.size() * 2, 0);
   for (int32_t s = 0; s < n_seg; ++s)
     for (int32_t j = 0; j < p.lens[s]; ++j) {
@@ -228,11 +280,9 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
     }
   a.mirror[a.m_d + n] = -1;  // the position of no token: sees nothing,
   a.mirror[a.m_e + n] = 0;   // and nothing sees it
-  static_assert(sizeof(AttnItem) == 32 && sizeof(AttnRun) == 8 && sizeof(AttnParts) == 16, "device layout");
-  std::memcpy(a.mirror.data() + a.m_q, qitems.data(), qitems.size() * sizeof(AttnItem));
-  std::memcpy(a.mirror.data() + a.m_k, kitems.data(), kitems.size() * sizeof(AttnItem));
-  std::memcpy(a.mirror.data() + a.m_parts, ordered.data(), ordered.size() * sizeof(AttnParts));
   std::memcpy(a.mirror.data() + a.m_runs, runs.data(), runs.size() * sizeof(AttnRun));
+  a.q = cut_all(qlists, &a.mirror);
+  a.k = cut_all(klists, &a.mirror);
   *out = std::move(a);
   return TREE_OK;
 }

@@ -14,8 +14,12 @@
 // one run), laid end to end as virtual key positions: first the runs every
 // row sees (no test needed), then the others.  A key tile (kKTile rows) has
 // the rows that see any of its keys in the same form, for the gradients of k
-// and v; a long list is cut into parts of at most kPart virtual rows, whose
-// partial sums are added in the order of the parts.
+// and v.
+//
+// A list may be cut into parts, worked on by different work-groups, whose
+// results are added in the order of the parts.  The tables hold every list
+// whole and cut into parts of at most 8192, 4096, .. 256 positions; a call
+// takes the coarsest cut that balances its work-groups (choose_cut).
 #pragma once
 
 #include <cstddef>
@@ -29,7 +33,6 @@ namespace tg {
 
 constexpr int32_t kQTile = 128;
 constexpr int32_t kKTile = 128;
-constexpr int32_t kPart = 2048;
 
 // One tile's list of runs.  Virtual positions [v0, v1) of it are this item's
 // work; [0, n_full) need no visibility test; n_total is the list's length.
@@ -40,29 +43,54 @@ struct AttnItem {
   int32_t n_full;
   int32_t n_total;
   int32_t v0, v1;
-  int32_t part;      // key tiles: number of this part among all parts
+  int32_t part;      // number of this part among all parts of the cut
 };
 struct AttnRun {
   int32_t virt;  // virtual position of the run's first row
   int32_t row;   // its packed row
 };
-// A key tile's parts: part0 .. part0 + n_parts - 1.
+// A tile's parts: part0 .. part0 + n_parts - 1.
 struct AttnParts {
   int32_t tile, part0, n_parts, pad;
 };
 
+// All lists of one kind, each cut into parts of at most `most` positions.
+struct AttnCut {
+  int32_t most = 0;
+  int32_t n_items = 0;
+  int32_t n_multi = 0;        // tiles with more than one part (first in the parts table)
+  int32_t n_multi_parts = 0;  // their parts (numbered first)
+  int32_t longest = 0;        // positions of the longest part
+  size_t m_items = 0, m_parts = 0;  // in the device copy: AttnItem (longest first), AttnParts
+};
+struct AttnLists {
+  int32_t n_tiles = 0;
+  int64_t total = 0;          // positions of all lists
+  std::vector<AttnCut> cuts;  // whole lists first, then finer and finer
+};
+
 struct AttnPlan {
   int32_t n_tokens = 0;
-  int32_t n_qtiles = 0, n_kitems = 0, n_ktiles = 0;
-  int32_t n_multi = 0;        // key tiles with more than one part (first in `parts`)
-  int32_t n_multi_parts = 0;  // their parts (numbered first)
+  AttnLists q, k;
   // Entries a trie may need at most: the run lists of all tiles together.
   static constexpr int64_t kMaxRuns = int64_t(1) << 26;
+  // A cut of more parts is not made (the coarser ones have parts enough).
+  static constexpr int64_t kMaxParts = 1 << 16;
 
   std::vector<int32_t> mirror;  // device copy
-  size_t m_d = 0, m_e = 0, m_q = 0, m_k = 0, m_runs = 0, m_parts = 0;
+  size_t m_d = 0, m_e = 0, m_runs = 0;
   size_t device_bytes() const { return mirror.size() * sizeof(int32_t); }
 };
+
+// The cut for `heads` work items per part, each `steps` times as long as the
+// part, on a device that runs kSlots work-groups at a time: the coarsest whose
+// longest item is at most 3/4 of what a slot gets on average, else the finest
+// -- and whole lists where cutting would shorten the longest item by less than
+// kWorth positions, about what the joining costs.  *split (1..steps, may be
+// null) spreads the steps of the finest cut over further work-groups.
+constexpr int32_t kSlots = 512;
+constexpr int32_t kWorth = 768;
+const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t* split);
 
 // Returns 0 or a negative TREE_ERR_* code; on failure *err holds a message.
 int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err);

@@ -223,21 +223,26 @@ struct AttnArgs {
   void* dv;
   float* lse;        // [N, h_q] natural log; written by the forward, read by the backward
   float* delta;      // backward workspace [2, N, h_q]: -(sum over d of dout * o), -lse / scale
-  float* part;       // backward workspace: partial dk, dv [slot, h_kv, 2, kKTile, d]
+  float* part;       // workspace: results of parts of a list (tree_attn.hip)
   const int32_t* tok_d;  // [N + 1]
   const int32_t* tok_e;  // [N + 1]
   const AttnItem* items;
   const AttnRun* runs;
   const AttnParts* parts;
   int32_t n_items;
-  int32_t n_parts;       // key tiles whose partial sums are added (reduce launch)
-  int32_t n_multi_parts; // parts numbered below this belong to tiles with several
+  int32_t n_join;        // tiles whose parts are added (join launch)
+  int32_t n_parts;       // parts numbered below this write to `part`
   int32_t n_tok;
   int32_t h_q, h_kv;
   int32_t split;         // dk, dv: work-groups a group's query heads are spread over
   float scale;
 };
 
+// Floats of one part's results: the forward's sums with each row's maximum and
+// sum of exponentials; dq; dk and dv.
+int64_t attention_part_floats(int d);
+int64_t attention_dq_part_floats(int d);
+int64_t attention_dkv_part_floats(int d);
 bool attention_supported(int d, int dtype);
 hipError_t launch_attention(const AttnArgs& a, int d, int dtype, hipStream_t stream);
 hipError_t launch_attention_dq(const AttnArgs& a, int d, int dtype, hipStream_t stream);

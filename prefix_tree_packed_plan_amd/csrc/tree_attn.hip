@@ -20,7 +20,6 @@
 // fragment, with exact products.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
 #include <cstdint>
 
 #include "../../include/tree_gdn.h"
@@ -40,6 +39,7 @@ using chunk::pk2;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) const chunk::u32x4 lds_u4;
+typedef __attribute__((address_space(3))) chunk::u32x4 lds_mu4;
 
 // A copy of x the compiler knows nothing of: what is computed from it is
 // computed where it stands, and not kept in registers across a loop.
@@ -171,12 +171,13 @@ __device__ __forceinline__ uint4 Reader<T, D>::cols(const char* t, int kb, int s
 
 // ---- values that are not finite ----------------------------------------------
 // A masked pair's probability is 0, but 0 times an infinity or a NaN of a row
-// the token does not see would still reach it through the MFMA.  A tile with
-// masked pairs that holds such elements therefore adds them first, one row at
-// a time and only where the probability is not 0, and then clears them in LDS
-// for the product.  In the gradients of k and v the rows are queries: one with
-// such a value in q, dO or o has a delta that is not finite; it is cleared, and
-// the gradients of every key it sees become NaN.
+// the token does not see would still reach it through the MFMA.  Tiles with
+// masked pairs that hold such elements therefore take them out first.  In the
+// forward (rows of v) they are added one row at a time, where the probability
+// is not 0, and cleared in LDS.  In the backward the whole row is cleared, and
+// the gradients of every token that sees it (of dq) or that it sees (dk, dv)
+// become NaN; a row with such a value in q, dO or o has a delta that is not
+// finite.
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {  // nonzero iff one of the word's elements is not finite
   if (sizeof(T) == 4) return (w & 0x7F800000u) == 0x7F800000u;
@@ -206,24 +207,38 @@ __device__ __forceinline__ void clear_nonfinite(char* t, int tid) {
 #pragma unroll 1
   for (int i = 0; i < Cfg<T, D>::TILE / 4096; ++i) {
     const uint4 w = lds16(t + 16 * (tid + 256 * i));
-    *(__attribute__((address_space(3))) chunk::u32x4*)(t + 16 * (tid + 256 * i)) =
+    *(lds_mu4*)(t + 16 * (tid + 256 * i)) =
         chunk::u32x4{finite<T>(w.x), finite<T>(w.y), finite<T>(w.z), finite<T>(w.w)};
   }
+}
+// Which of the tile's rows hold one (bit r: row r).
+template <typename T, int D>
+__device__ __forceinline__ uint64_t nonfinite_rows(const char* t, int lane) {
+  using C = Cfg<T, D>;
+  uint32_t f = 0;
+#pragma unroll 1
+  for (int c = 0; c < C::NC; ++c) {
+    const uint4 x = lds16(t + lane * C::RB + 16 * c);
+    f |= nonfinite<T>(x.x) | nonfinite<T>(x.y) | nonfinite<T>(x.z) | nonfinite<T>(x.w);
+  }
+  return __ballot(f != 0);
+}
+// Clears this thread's share of the rows of set `rows`.
+template <typename T, int D>
+__device__ __forceinline__ void clear_rows(char* t, uint64_t rows, int tid) {
+  using C = Cfg<T, D>;
+#pragma unroll 1
+  for (int i = tid; i < kRows * C::NC; i += 256)
+    if ((rows >> (i / C::NC)) & 1) *(lds_mu4*)(t + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
 }
 // acc[db] (columns 32 db + accumulator row, of the tile's rows weighted by w)
 // += the elements that are not finite.
 template <typename T, int D>
 __device__ __forceinline__ void add_nonfinite(f32x16 (&acc)[D / 32], const f32x16 (&w)[2], const char* t, int lane) {
   using C = Cfg<T, D>;
-  bool bad = false;  // this lane's row (= lane) has one
-#pragma unroll 1
-  for (int c = 0; c < C::NC; ++c) {
-    const uint4 x = lds16(t + lane * C::RB + 16 * c);
-    bad = bad || (nonfinite<T>(x.x) | nonfinite<T>(x.y) | nonfinite<T>(x.z) | nonfinite<T>(x.w));
-  }
   const int h = lane >> 5;
 #pragma unroll 1
-  for (uint64_t m = __ballot(bad); m; m &= m - 1) {
+  for (uint64_t m = nonfinite_rows<T, D>(t, lane); m; m &= m - 1) {
     const int c = __builtin_ctzll(m), kb = c >> 5, cc = c & 31;
     const int reg = 4 * (cc >> 3) + (cc & 3), half = (cc >> 2) & 1;
     float x = 0.f;
@@ -274,13 +289,13 @@ __device__ __forceinline__ void contract(f32x16 (&acc)[D / 32], const f32x16& w,
   }
 }
 
-// use(i, load(i)) for i < N with the next three loads in flight, in exactly
-// this order: left to itself the compiler takes either one operand at a time
+// use(i, load(i)) for i < N with the next F loads in flight, in exactly this
+// order: left to itself the compiler takes either one operand at a time
 // or more than the registers hold.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
-template <int N, typename Load, typename Use>
+template <int N, int F, typename Load, typename Use>
 __device__ __forceinline__ void pipe(Load load, Use use) {
-  constexpr int P = N < 3 ? N : 3;
+  constexpr int P = N < F ? N : F;
   uint4 x[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) x[i] = load(i);
@@ -471,6 +486,15 @@ __device__ __forceinline__ void store_row(T* p, const f32x16* acc, float f, int 
   }
 }
 
+// ---- parts of a list --------------------------------------------------------------
+// What a work-group leaves of its part (floats): the forward's unnormalised
+// output rows, then every row's maximum and sum; rows of dq; rows of dk, then
+// of dv.
+__host__ __device__ constexpr int64_t fwd_part(int d) { return int64_t(kQTile) * (d + 2); }
+__host__ __device__ constexpr int64_t dq_part(int d) { return int64_t(kQTile) * d; }
+__host__ __device__ constexpr int64_t dkv_part(int d) { return int64_t(kKTile) * d * 2; }
+constexpr int kJoinRows = 16;
+
 // ---- forward --------------------------------------------------------------------
 template <typename T, int D>
 struct FwdSmem {
@@ -535,7 +559,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
       else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
     }
   };
-  fetch(0, 0);
+  fetch(it.v0, 0);
 
   uint4 q[C::NK];
   load_frags<T, D>(q, a.q.at(r, h), half);
@@ -556,7 +580,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     constexpr int buf = decltype(buffer)::value;
     wait_dma();
     __syncthreads();
-    if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
+    if (v0 + kRows < it.v1) fetch(v0 + kRows, buf ^ 1);
     const char* kt = sm.k[buf];
     char* vt = sm.v[buf];
     bool masked = v0 + kRows > it.n_full, bad = false, skip = false;
@@ -626,16 +650,58 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
       matrix_first(false);
     }
   };
-  for (int v0 = 0;;) {
+  for (int v0 = it.v0;;) {
     tile(v0, std::integral_constant<int, 0>{});
-    if ((v0 += kRows) >= it.n_total) break;
+    if ((v0 += kRows) >= it.v1) break;
     tile(v0, std::integral_constant<int, 1>{});
-    if ((v0 += kRows) >= it.n_total) break;
+    if ((v0 += kRows) >= it.v1) break;
   }
   l += half_swap(l);
+  if (it.part < a.n_parts) {
+    // Part of the list: the sums as they are, with the maximum (in powers of
+    // 2) and the sum of exponentials they go by.
+    float* w = a.part + (int64_t(it.part) * a.h_q + h) * fwd_part(D);
+    const int key = 32 * wave + (lane & 31);
+    store_row<float, D>(w + key * D, acc, 1.f, half, true);
+    if (half == 0) *reinterpret_cast<float2*>(w + kQTile * D + 2 * key) = make_float2(m * c, l);
+    return;
+  }
   const float inv = 1.f / l;
   store_row<T, D>(static_cast<T*>(a.out) + (r * a.h_q + h) * D, acc, inv, half, on);
   if (a.lse && on && half == 0) a.lse[r * a.h_q + h] = (m * c + __log2f(l)) * kLn2;
+}
+
+// The output of a query tile from its parts, in their order: 16 rows a
+// work-group.
+template <typename T, int D>
+__global__ __launch_bounds__(kJoinRows * D / 4) void attn_fwd_join_kernel(AttnArgs a) {
+  const int h = blockIdx.y, key = kJoinRows * blockIdx.z + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
+  const AttnParts pt = a.parts[blockIdx.x];
+  const int64_t row = int64_t(pt.tile) * kQTile + key;
+  if (row >= a.n_tok) return;
+  const int64_t step = int64_t(a.h_q) * fwd_part(D);
+  const float* w = a.part + (int64_t(pt.part0) * a.h_q + h) * fwd_part(D);
+  const float* st = w + kQTile * D + 2 * key;
+  float m = kNegInf;
+  for (int j = 0; j < pt.n_parts; ++j) m = fmaxf(m, st[j * step]);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 2
+  for (int j = 0; j < pt.n_parts; ++j) {
+    const float2 x = *reinterpret_cast<const float2*>(st + j * step);
+    const float4 y = *reinterpret_cast<const float4*>(w + j * step + key * D + col);
+    const float f = x.x == kNegInf ? 0.f : ex2(x.x - m);  // -inf: the row sees nothing of this part
+    l = fmaf(f, x.y, l);
+    s.x = fmaf(f, y.x, s.x);
+    s.y = fmaf(f, y.y, s.y);
+    s.z = fmaf(f, y.z, s.z);
+    s.w = fmaf(f, y.w, s.w);
+  }
+  const float inv = 1.f / l;
+  T* out = static_cast<T*>(a.out) + (row * a.h_q + h) * D + col;
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(out) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+  else *reinterpret_cast<uint2*>(out) = make_uint2(pk2(s.x * inv, s.y * inv), pk2(s.z * inv, s.w * inv));
+  if (a.lse && col == 0) a.lse[row * a.h_q + h] = (m + __log2f(l)) * kLn2;
 }
 
 // ---- gradient of q -----------------------------------------------------------------
@@ -667,7 +733,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
       else dma4(a.tok_e + x, reinterpret_cast<char*>(sm.e[buf]));
     }
   };
-  fetch(0, 0);
+  fetch(it.v0, 0);
 
   uint4 q[C::NK], g[C::NK];
   load_frags<T, D>(q, a.q.at(r, h), half);
@@ -712,57 +778,77 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
     constexpr int buf = decltype(buffer)::value;
     wait_dma();
     __syncthreads();
-    if (v0 + kRows < it.n_total) fetch(v0 + kRows, buf ^ 1);
+    if (v0 + kRows < it.v1) fetch(v0 + kRows, buf ^ 1);
     char* kt = sm.k[buf];
     const char* vt = sm.v[buf];
-    bool masked = v0 + kRows > it.n_full, bad = false, skip = false;
+    bool masked = v0 + kRows > it.n_full, skip = false;
     if (masked) {
-      bad = __syncthreads_or(any_nonfinite<T, D>(kt, threadIdx.x));
+      const bool bad = __syncthreads_or(any_nonfinite<T, D>(kt, threadIdx.x));
       const int kd = sm.d[buf][lane], ke = sm.e[buf][lane];
       skip = __ballot(kd <= dhi && dlo < ke) == 0;
       masked = __ballot(kd <= dlo && dhi < ke) != ~0ull;
-    }
-    f32x16 p[2];
-    if (!skip) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        f32x16 s = zero16(), dp = zero16();
-        matrix_first(true);
-#pragma unroll
-        for (int ks = 0; ks < C::NK; ++ks) {
-          s = mm<T>(rd.rows(kt, kb, ks), q[ks], s);
-          dp = mm<T>(rd.rows(vt, kb, ks), g[ks], dp);
+      if (bad) {
+        const uint64_t rows = nonfinite_rows<T, D>(kt, lane);
+        float x = 0.f;
+        for (uint64_t m = rows; m; m &= m - 1) {
+          const int r = __builtin_ctzll(m);
+          x = sm.d[buf][r] <= dq && dq < sm.e[buf][r] ? __builtin_nanf("") : x;
         }
-        matrix_first(false);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[kb][i] = ex2(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
-        if (masked) {
-          const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
+        for (int db = 0; db < C::NDB; ++db)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[kb][i] = (see >> i) & 1 ? p[kb][i] : 0.f;
-        }
+          for (int i = 0; i < 16; ++i) acc[db][i] += x;
+        __syncthreads();
+        clear_rows<T, D>(kt, rows, threadIdx.x);
+        __syncthreads();
       }
     }
-    if (bad) {
-      if (!skip) add_nonfinite<T, D>(acc, p, kt, lane);
-      __syncthreads();
-      clear_nonfinite<T, D>(kt, threadIdx.x);
-      __syncthreads();
-    }
-    if (!skip) {
-      matrix_first(true);
+    if (skip) return;
+    f32x16 ds[2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) contract<T, D>(acc, p[kb], kt, kb, rd);
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16 s = zero16(), dp = zero16();
+      matrix_first(true);
+      pipe<C::NK, 2>([&](int ks) { return rd.rows(kt, kb, ks); },
+                  [&](int ks, const uint4 x) { s = mm<T>(x, q[ks], s); });
+      pipe<C::NK, 2>([&](int ks) { return rd.rows(vt, kb, ks); },
+                  [&](int ks, const uint4 x) {
+                    dp = mm<T>(x, g[ks], dp);
+#pragma unroll
+                    for (int i = 16 * ks / C::NK; i < 16 * (ks + 1) / C::NK; ++i) s[i] = ex2(fmaf(s[i], c, -lse2));
+                  });
       matrix_first(false);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ds[kb][i] = s[i] * (dp[i] - delta);
+      if (masked) {
+        const uint32_t see = visible(sm.d[buf], sm.e[buf], kb, half, dq);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ds[kb][i] = (see >> i) & 1 ? ds[kb][i] : 0.f;
+      }
     }
+    matrix_first(true);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+      pipe<C::NS * C::NDB, 2>([&](int i) { return rd.cols(kt, kb, i / C::NDB, i % C::NDB); },
+                           [&](int i, const uint4 x) {
+                             acc[i % C::NDB] = mm<T>(x, frag<T>(ds[kb], i / C::NDB), acc[i % C::NDB]);
+                           });
+    matrix_first(false);
   };
-  for (int v0 = 0;;) {
+  for (int v0 = it.v0;;) {
     tile(v0, std::integral_constant<int, 0>{});
-    if ((v0 += kRows) >= it.n_total) break;
+    if ((v0 += kRows) >= it.v1) break;
     tile(v0, std::integral_constant<int, 1>{});
-    if ((v0 += kRows) >= it.n_total) break;
+    if ((v0 += kRows) >= it.v1) break;
   }
-  store_row<T, D>(static_cast<T*>(a.out) + (r * a.h_q + h) * D, acc, a.scale, half, on);
+  {
+    const int lane = lane_id(), key = 32 * wave + (lane & 31);
+    const int64_t row = int64_t(it.tile) * kQTile + key;
+    if (it.part < a.n_parts)
+      store_row<float, D>(a.part + (int64_t(it.part) * a.h_q + h) * dq_part(D) + key * D, acc, a.scale, lane >> 5, true);
+    else
+      store_row<T, D>(static_cast<T*>(a.out) + (row * a.h_q + h) * D, acc, a.scale, lane >> 5, row < a.n_tok);
+  }
 }
 
 // ---- gradients of k and v ------------------------------------------------------------
@@ -787,10 +873,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
   const int sub = blockIdx.x % a.split, hk = (blockIdx.x / a.split) % a.h_kv;
   const AttnItem it = a.items[blockIdx.x / (a.split * a.h_kv)];
   const int group = a.h_q / a.h_kv;
-  const int key = 32 * wave + (lane & 31);
-  const int64_t row = int64_t(it.tile) * kKTile + key;
-  const bool on = row < a.n_tok;
-  const int64_t r = on ? row : a.n_tok - 1;
+  const int64_t r = min(int64_t(it.tile) * kKTile + 32 * wave + (lane & 31), int64_t(a.n_tok) - 1);
 
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int h, int buf) {
@@ -859,12 +942,9 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
           dv[db][i] += x;
         }
       __syncthreads();
-      for (int i = 64 * wave + lane_id(); i < kRows * C::NC; i += 256)
-        if ((bad >> (i / C::NC)) & 1) {
-          *(__attribute__((address_space(3))) chunk::u32x4*)(qt + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
-          *(__attribute__((address_space(3))) chunk::u32x4*)(gt + 16 * i) = chunk::u32x4{0u, 0u, 0u, 0u};
-        }
       const int r = lane_id();
+      clear_rows<T, D>(qt, bad, 64 * wave + r);
+      clear_rows<T, D>(gt, bad, 64 * wave + r);
       if (wave == 0 && (bad >> r) & 1) {
         sm.lse[buf][r] = kNegInf;  // p = 0
         sm.delta[buf][r] = 0.f;
@@ -880,10 +960,10 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
       // The sums start at -lse / scale and -delta: p = exp2(c s), ds = p dp.
       f32x16 p = rows16(sm.lse[buf] + 32 * kb + 4 * half);
       matrix_first(true);
-      pipe<C::NK>([&](int ks) { return rd.rows(qt, 0, ks); },
+      pipe<C::NK, 3>([&](int ks) { return rd.rows(qt, 0, ks); },
                   [&](int ks, const uint4 x) { p = mm<T>(x, kf[ks], p); });
       f32x16 ds = rows16(sm.delta[buf] + 32 * kb + 4 * half);
-      pipe<C::NK>([&](int ks) { return rd.rows(gt, 0, ks); },
+      pipe<C::NK, 3>([&](int ks) { return rd.rows(gt, 0, ks); },
                   [&](int ks, const uint4 x) {
                     ds = mm<T>(x, vf[ks], ds);
 #pragma unroll
@@ -912,9 +992,9 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
         db[s] = frag<T>(ds, s);
       }
       matrix_first(true);
-      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(gt, 0, i / C::NDB, i % C::NDB); },
+      pipe<C::NS * C::NDB, 3>([&](int i) { return rd.cols(gt, 0, i / C::NDB, i % C::NDB); },
                            [&](int i, const uint4 x) { dv[i % C::NDB] = mm<T>(x, pb[i / C::NDB], dv[i % C::NDB]); });
-      pipe<C::NS * C::NDB>([&](int i) { return rd.cols(qt, 0, i / C::NDB, i % C::NDB); },
+      pipe<C::NS * C::NDB, 3>([&](int i) { return rd.cols(qt, 0, i / C::NDB, i % C::NDB); },
                            [&](int i, const uint4 x) { dk[i % C::NDB] = mm<T>(x, db[i / C::NDB], dk[i % C::NDB]); });
       matrix_first(false);
     }
@@ -925,40 +1005,45 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
     tile(std::integral_constant<int, 1>{});
     if (h >= (hk + 1) * group) break;
   }
-  if (a.split == 1 && it.part >= a.n_multi_parts) {
-    store_row<T, D>(static_cast<T*>(a.dk) + (r * a.h_kv + hk) * D, dk, a.scale, half, on);
-    store_row<T, D>(static_cast<T*>(a.dv) + (r * a.h_kv + hk) * D, dv, 1.f, half, on);
+  const int ln = lane_id(), hl = ln >> 5, key = 32 * wave + (ln & 31);
+  if (it.part >= a.n_parts) {
+    const int64_t row = int64_t(it.tile) * kKTile + key;
+    store_row<T, D>(static_cast<T*>(a.dk) + (row * a.h_kv + hk) * D, dk, a.scale, hl, row < a.n_tok);
+    store_row<T, D>(static_cast<T*>(a.dv) + (row * a.h_kv + hk) * D, dv, 1.f, hl, row < a.n_tok);
   } else {
-    const int64_t slot = (int64_t(it.part) * a.split + sub) * a.h_kv + hk;
-    float* w = a.part + slot * (2 * kKTile * D) + key * D;
-    store_row<float, D>(w, dk, a.scale, half, true);
-    store_row<float, D>(w + kKTile * D, dv, 1.f, half, true);
+    float* w = a.part + ((int64_t(it.part) * a.split + sub) * a.h_kv + hk) * dkv_part(D) + key * D;
+    store_row<float, D>(w, dk, a.scale, hl, true);
+    store_row<float, D>(w + kKTile * D, dv, 1.f, hl, true);
   }
 }
 
-// dk, dv of a key tile from its parts, in their order.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int hk = blockIdx.y, which = blockIdx.z;
+// A tile's gradients (dq, or dk and dv) from its parts, in their order: 16 rows
+// a work-group.
+template <typename T, int D, bool DQ>
+__global__ __launch_bounds__(kJoinRows * D / 4) void attn_grad_join_kernel(AttnArgs a) {
+  const int heads = DQ ? a.h_q : a.h_kv, h = blockIdx.y;
+  const int which = DQ ? 0 : blockIdx.z & 1, row0 = kJoinRows * (DQ ? blockIdx.z : blockIdx.z >> 1);
   const AttnParts pt = a.parts[blockIdx.x];
-  const int64_t slots = int64_t(pt.n_parts) * a.split, slot0 = int64_t(pt.part0) * a.split;
-  T* out = static_cast<T*>(which ? a.dv : a.dk);
-  for (int i = threadIdx.x; i < kKTile * D / 4; i += 256) {
-    const int64_t row = int64_t(pt.tile) * kKTile + i / (D / 4);
-    if (row >= a.n_tok) break;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t j = 0; j < slots; ++j) {
-      const float4 x = reinterpret_cast<const float4*>(
-          a.part + ((slot0 + j) * a.h_kv + hk) * (2 * kKTile * D) + which * kKTile * D)[i];
-      s.x += x.x;
-      s.y += x.y;
-      s.z += x.z;
-      s.w += x.w;
-    }
-    T* p = out + (row * a.h_kv + hk) * D + 4 * (i % (D / 4));
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = s;
-    else *reinterpret_cast<uint2*>(p) = make_uint2(pk2(s.x, s.y), pk2(s.z, s.w));
+  const int64_t split = DQ ? 1 : a.split, slots = pt.n_parts * split;
+  const int64_t floats = DQ ? dq_part(D) : dkv_part(D), step = heads * floats / 4;
+  const int key = row0 + threadIdx.x / (D / 4);
+  const int64_t row = int64_t(pt.tile) * kKTile + key;
+  if (row >= a.n_tok) return;
+  const float4* p = reinterpret_cast<const float4*>(a.part + (pt.part0 * split * heads + h) * floats +
+                                                    which * kKTile * D) +
+                    key * (D / 4) + threadIdx.x % (D / 4);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int64_t j = 0; j < slots; ++j) {
+    const float4 x = p[j * step];
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
   }
+  T* out = static_cast<T*>(DQ ? a.out : which ? a.dv : a.dk) + (row * heads + h) * D + 4 * (threadIdx.x % (D / 4));
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(out) = s;
+  else *reinterpret_cast<uint2*>(out) = make_uint2(pk2(s.x, s.y), pk2(s.z, s.w));
 }
 
 template <typename F>
@@ -981,26 +1066,48 @@ bool attention_supported(int d, int dtype) {
   return (d == 32 || d == 64 || d == 128) && (dtype == TREE_DTYPE_BF16 || dtype == TREE_DTYPE_F32);
 }
 
+int64_t attention_part_floats(int d) { return fwd_part(d); }
+int64_t attention_dq_part_floats(int d) { return dq_part(d); }
+int64_t attention_dkv_part_floats(int d) { return dkv_part(d); }
+
 hipError_t launch_attention(const AttnArgs& a, int d, int dtype, hipStream_t stream) {
   return dispatch(d, dtype, [&](auto t, auto dd) {
-    attn_fwd_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
-    return hipGetLastError();
+    using T = decltype(t);
+    constexpr int D = decltype(dd)::value;
+    attn_fwd_kernel<T, D><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.n_join > 0) {
+      attn_fwd_join_kernel<T, D><<<dim3(a.n_join, a.h_q, kQTile / kJoinRows), kJoinRows * D / 4, 0, stream>>>(a);
+      e = hipGetLastError();
+    }
+    return e;
   });
 }
 
 hipError_t launch_attention_dq(const AttnArgs& a, int d, int dtype, hipStream_t stream) {
   return dispatch(d, dtype, [&](auto t, auto dd) {
-    attn_dq_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
-    return hipGetLastError();
+    using T = decltype(t);
+    constexpr int D = decltype(dd)::value;
+    attn_dq_kernel<T, D><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.n_join > 0) {
+      attn_grad_join_kernel<T, D, true>
+          <<<dim3(a.n_join, a.h_q, kQTile / kJoinRows), kJoinRows * D / 4, 0, stream>>>(a);
+      e = hipGetLastError();
+    }
+    return e;
   });
 }
 
 hipError_t launch_attention_dkv(const AttnArgs& a, int d, int dtype, hipStream_t stream) {
   return dispatch(d, dtype, [&](auto t, auto dd) {
-    attn_dkv_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_items * a.h_kv * a.split), 256, 0, stream>>>(a);
+    using T = decltype(t);
+    constexpr int D = decltype(dd)::value;
+    attn_dkv_kernel<T, D><<<dim3(a.n_items * a.h_kv * a.split), 256, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.n_parts > 0) {
-      attn_join_kernel<decltype(t), decltype(dd)::value><<<dim3(a.n_parts, a.h_kv, 2), 256, 0, stream>>>(a);
+    if (e == hipSuccess && a.n_join > 0) {
+      attn_grad_join_kernel<T, D, false>
+          <<<dim3(a.n_join, a.h_kv, 2 * kKTile / kJoinRows), kJoinRows * D / 4, 0, stream>>>(a);
       e = hipGetLastError();
     }
     return e;

@@ -65,80 +65,91 @@ static void check(const std::vector<int32_t>& parents, const std::vector<int32_t
     CHECK(!(d[n] <= d[i] && d[i] < e[n]) && !(d[i] <= d[n] && d[n] < e[i]), "token %d and no token", i);
     for (int j = 0; j < n; ++j) CHECK((d[j] <= d[i] && d[i] < e[j]) == sees(i, j), "tokens %d, %d", i, j);
   }
-  const AttnItem* q = reinterpret_cast<const AttnItem*>(a.mirror.data() + a.m_q);
-  const AttnItem* k = reinterpret_cast<const AttnItem*>(a.mirror.data() + a.m_k);
   const AttnRun* runs = reinterpret_cast<const AttnRun*>(a.mirror.data() + a.m_runs);
-  const AttnParts* parts = reinterpret_cast<const AttnParts*>(a.mirror.data() + a.m_parts);
-  CHECK(a.m_q % 8 == 0 && a.m_k % 8 == 0 && a.m_parts % 4 == 0 && a.m_runs % 2 == 0, "alignment");
-  CHECK(a.n_qtiles == (n + tg::kQTile - 1) / tg::kQTile && a.n_ktiles == (n + tg::kKTile - 1) / tg::kKTile, "tiles");
-  std::vector<char> had(a.n_qtiles, 0);
-  for (int t = 0; t < a.n_qtiles; ++t) {
-    const AttnItem& it = q[t];
-    CHECK(it.tile >= 0 && it.tile < a.n_qtiles && !had[it.tile], "query tile %d", it.tile);
-    had[it.tile] = 1;
-    CHECK(it.v0 == 0 && it.v1 == it.n_total && it.n_runs > 0, "query tile %d", it.tile);
-    int bad = 0;
-    std::vector<int> rows = rows_of(it, runs, n, &bad);
-    CHECK(!bad, "query tile %d", it.tile);
-    const int lo = it.tile * tg::kQTile, hi = std::min(n, lo + tg::kQTile);
-    std::vector<int> want;
-    for (int j = 0; j < n; ++j) {
-      bool any = false;
-      for (int i = lo; i < hi; ++i) any = any || sees(i, j);
-      if (any) want.push_back(j);
+  CHECK(a.m_runs % 2 == 0, "alignment");
+  for (int side = 0; side < 2; ++side) {
+    const tg::AttnLists& l = side ? a.k : a.q;
+    CHECK(l.n_tiles == (n + 127) / 128 && !l.cuts.empty(), "tiles");
+    for (size_t ci = 0; ci < l.cuts.size(); ++ci) {
+      const tg::AttnCut& c = l.cuts[ci];
+      CHECK(ci == 0 || c.most < l.cuts[ci - 1].most, "cuts get finer");
+      CHECK(c.m_items % 8 == 0 && c.m_parts % 4 == 0, "alignment");
+      CHECK(c.m_items + 8 * size_t(c.n_items) <= a.mirror.size() && c.m_parts + 4 * size_t(l.n_tiles) <= a.mirror.size(),
+            "size");
+      const AttnItem* items = reinterpret_cast<const AttnItem*>(a.mirror.data() + c.m_items);
+      const AttnParts* parts = reinterpret_cast<const AttnParts*>(a.mirror.data() + c.m_parts);
+      std::vector<std::vector<std::pair<int, int>>> cover(l.n_tiles);
+      std::vector<int> part_tile(c.n_items, -1);
+      int64_t total = 0;
+      int longest = 0;
+      for (int t = 0; t < c.n_items; ++t) {
+        const AttnItem& it = items[t];
+        CHECK(it.tile >= 0 && it.tile < l.n_tiles && it.n_runs > 0, "tile %d", it.tile);
+        CHECK(it.part >= 0 && it.part < c.n_items && part_tile[it.part] < 0, "part %d", it.part);
+        CHECK(it.v0 >= 0 && it.v0 < it.v1 && it.v1 <= it.n_total, "tile %d", it.tile);
+        CHECK(t == 0 || it.v1 - it.v0 <= items[t - 1].v1 - items[t - 1].v0, "longest first");
+        CHECK(it.v0 % 64 == 0 && (it.v1 % 64 == 0 || it.v1 == it.n_total) && it.v1 - it.v0 <= c.most, "part of %d",
+              it.tile);
+        longest = std::max(longest, it.v1 - it.v0);
+        total += it.v1 - it.v0;
+        cover[it.tile].push_back({it.v0, it.v1});
+        part_tile[it.part] = it.tile;
+        if (ci > 0 && it.v0 > 0) continue;  // the list itself has been looked at
+        int bad = 0;
+        std::vector<int> rows = rows_of(it, runs, n, &bad);
+        CHECK(!bad, "runs of tile %d", it.tile);
+        const int lo = it.tile * 128, hi = std::min(n, lo + 128);
+        const auto pair = [&](int mine, int other) { return side ? sees(other, mine) : sees(mine, other); };
+        std::vector<int> want;
+        for (int j = 0; j < n; ++j) {
+          bool any = false;
+          for (int i = lo; i < hi; ++i) any = any || pair(i, j);
+          if (any) want.push_back(j);
+        }
+        for (int v = 0; v < it.n_full; ++v)
+          for (int i = lo; i < hi; ++i) CHECK(pair(i, rows[v]), "tile %d: %d and %d are not a pair", it.tile, i, rows[v]);
+        std::sort(rows.begin(), rows.end());
+        CHECK(rows == want, "list of tile %d", it.tile);
+      }
+      CHECK(total == l.total && longest == c.longest, "totals");
+      int next = 0, multi = 0, multi_parts = 0;
+      for (int t = 0; t < l.n_tiles; ++t) {
+        const AttnParts& x = parts[t];
+        auto& r = cover[x.tile];
+        CHECK(static_cast<int>(r.size()) == x.n_parts, "parts of %d", x.tile);
+        std::sort(r.begin(), r.end());
+        int at = 0;
+        for (const auto& y : r) {
+          CHECK(y.first == at, "part of %d", x.tile);
+          at = y.second;
+        }
+        for (int i = 0; i < x.n_parts; ++i) CHECK(part_tile[x.part0 + i] == x.tile, "part %d", x.part0 + i);
+        // Parts are numbered along the list: the order their results are added in.
+        for (int i = 0; i < c.n_items; ++i)
+          if (items[i].tile == x.tile) {
+            const int k = items[i].part - x.part0;
+            CHECK(k >= 0 && k < x.n_parts && r[k].first == items[i].v0, "order of parts");
+          }
+        CHECK(x.part0 == next, "numbers of parts");
+        next += x.n_parts;
+        if (x.n_parts > 1) {
+          CHECK(multi == t, "tiles with several parts come first");
+          ++multi;
+          multi_parts += x.n_parts;
+        }
+        r.clear();
+      }
+      CHECK(next == c.n_items && multi == c.n_multi && multi_parts == c.n_multi_parts, "part counts");
     }
-    for (int v = 0; v < it.n_full; ++v)
-      for (int i = lo; i < hi; ++i) CHECK(sees(i, rows[v]), "query tile %d: row %d does not see %d", it.tile, i, rows[v]);
-    std::sort(rows.begin(), rows.end());
-    CHECK(rows == want, "keys of query tile %d", it.tile);
+    for (const int heads : {1, 2, 16, 1000})
+      for (const int steps : {1, 3, 8}) {
+        int32_t split = -1;
+        const tg::AttnCut& c = tg::choose_cut(l, heads, steps, &split);
+        CHECK(split >= 1 && split <= steps, "split %d", split);
+        CHECK(&c >= l.cuts.data() && &c < l.cuts.data() + l.cuts.size(), "a cut of these lists");
+        tg::choose_cut(l, heads, steps, nullptr);
+      }
   }
-  std::vector<std::vector<std::pair<int, int>>> cover(a.n_ktiles);
-  std::vector<int> part_tile(a.n_kitems, -1);
-  for (int t = 0; t < a.n_kitems; ++t) {
-    const AttnItem& it = k[t];
-    CHECK(it.tile >= 0 && it.tile < a.n_ktiles, "key tile %d", it.tile);
-    cover[it.tile].push_back({it.v0, it.v1});
-    CHECK(it.part >= 0 && it.part < a.n_kitems && part_tile[it.part] < 0, "part %d", it.part);
-    part_tile[it.part] = it.tile;
-    int bad = 0;
-    std::vector<int> rows = rows_of(it, runs, n, &bad);
-    CHECK(!bad, "key tile %d", it.tile);
-    const int lo = it.tile * tg::kKTile, hi = std::min(n, lo + tg::kKTile);
-    std::vector<int> want;
-    for (int i = 0; i < n; ++i) {
-      bool any = false;
-      for (int j = lo; j < hi; ++j) any = any || sees(i, j);
-      if (any) want.push_back(i);
-    }
-    for (int v = 0; v < it.n_full; ++v)
-      for (int j = lo; j < hi; ++j) CHECK(sees(rows[v], j), "key tile %d: row %d does not see %d", it.tile, rows[v], j);
-    std::sort(rows.begin(), rows.end());
-    CHECK(rows == want, "rows of key tile %d", it.tile);
-    CHECK(it.v0 % 64 == 0 && (it.v1 % 64 == 0 || it.v1 == it.n_total) && it.v1 - it.v0 <= tg::kPart, "part of %d",
-          it.tile);
-  }
-  int total = 0, multi = 0, multi_parts = 0;
-  for (int t = 0; t < a.n_ktiles; ++t) {
-    const AttnParts& x = parts[t];
-    auto& c = cover[x.tile];
-    CHECK(static_cast<int>(c.size()) == x.n_parts, "parts of %d", x.tile);
-    std::sort(c.begin(), c.end());
-    int at = 0;
-    for (const auto& r : c) {
-      CHECK(r.first == at && r.second > at, "part of %d", x.tile);
-      at = r.second;
-    }
-    for (int i = 0; i < x.n_parts; ++i) CHECK(part_tile[x.part0 + i] == x.tile, "part %d", x.part0 + i);
-    CHECK(x.part0 == total, "order of parts");
-    total += x.n_parts;
-    if (x.n_parts > 1) {
-      CHECK(multi == t, "tiles with several parts come first");
-      ++multi;
-      multi_parts += x.n_parts;
-    }
-    c.clear();
-  }
-  CHECK(total == a.n_kitems && multi == a.n_multi && multi_parts == a.n_multi_parts, "part counts");
 }
 
 int main() {

@@ -40,7 +40,7 @@ def test_attention_refusals_need_no_device():
     a = plan_of().attention()
     lib = _lib.load()
     good = dict(q=P, k=P, v=P, o=P2, lse=None, st=None, n=230, hq=4, hkv=2, d=128, scale=0.1,
-                dtype=1, aplan=a.handle, dplan=P, bytes=BIG, stream=None)
+                dtype=1, aplan=a.handle, dplan=P, bytes=BIG, ws=None, ws_bytes=0, stream=None)
 
     def call(**kw):
         return lib.tree_attention(*{**good, **kw}.values())
@@ -91,18 +91,35 @@ def test_attention_backward_refusals_need_no_device():
     assert call(dq=P) == -1 and call(dk=P2) == -1 and call(dv=P3) == -1
 
 
-def test_attention_workspace_counts_split_work():
-    """One part per key tile and heads enough: only delta; few tiles: partial
-    sums for every head of the group; more than 2048 rows below a key tile:
-    partial sums for its parts."""
+def test_attention_workspace_counts_cut_lists():
+    """Lists are cut, and need a workspace, only where whole ones would leave
+    the device idle: a long chain with few heads, one list much longer than the
+    rest; not a short chain, nor many equal ones."""
     lib = _lib.load()
+    fwd, bwd = lib.tree_attention_workspace_bytes, lib.tree_attention_backward_workspace_bytes
+    part = (128 * 130 * 4, 128 * 64 * 4, 2 * 128 * 64 * 4)  # o with maxima and sums; dq; dk and dv, of 64-wide heads
+
+    def delta(n, h):
+        return (2 * n * h * 4 + 255) // 256 * 256
+
+    assert fwd(None, 4, 64) == 0 and bwd(None, 4, 1, 64) == 0
     many = plan_of([-1] * 600, [128] * 600).attention()
-    assert lib.tree_attention_backward_workspace_bytes(many.handle, 2, 1, 64) == 2 * 600 * 128 * 2 * 4
-    few = plan_of([-1], [128]).attention()
-    assert lib.tree_attention_backward_workspace_bytes(few.handle, 4, 1, 64) == 2 * 128 * 4 * 4 + 4 * 2 * 128 * 64 * 4
-    part = plan_of([-1] + [-1] * 600, [4096] + [128] * 600).attention()  # tiles 0..15 have two parts
-    delta = 2 * (4096 + 600 * 128) * 4
-    assert lib.tree_attention_backward_workspace_bytes(part.handle, 1, 1, 64) == delta + 32 * 2 * 128 * 64 * 4
+    assert fwd(many.handle, 2, 64) == 0 and bwd(many.handle, 2, 1, 64) == delta(600 * 128, 2)
+    short = plan_of([-1], [512]).attention()
+    assert fwd(short.handle, 4, 64) == 0 and bwd(short.handle, 1, 1, 64) == delta(512, 1)
+    one = plan_of([-1], [2048]).attention()  # 256 positions a part: 2 of the 16 lists are not cut
+    f = fwd(one.handle, 1, 64)
+    assert f > 0 and f % (128 * 66 * 4) == 0
+    assert f // (128 * 66 * 4) == sum(-(-128 * i // 256) for i in range(3, 17))
+    b = bwd(one.handle, 8, 1, 64) - delta(2048, 8)
+    assert b > 0 and b % part[1] == 0
+    rc = lib.tree_attention(P, P, P, P2, None, None, 2048, 1, 1, 64, 0.1, 1, one.handle, P, BIG, P, f - 1, None)
+    assert rc == -5
+    rc = lib.tree_attention(P, P, P, P2, None, None, 2048, 1, 1, 64, 0.1, 1, one.handle, P, BIG, None, BIG, None)
+    assert rc == -5
+    rc = lib.tree_attention(P, P, P, P2, None, None, 2048, 1, 1, 64, 0.1, 1, one.handle, P, BIG,
+                            ctypes.c_void_p(0x1008), BIG, None)
+    assert rc == -1 and b"workspace" in lib.tree_last_error()
 
 
 def test_logprobs_refusals_need_no_device():

@@ -119,13 +119,33 @@ def test_attention_deep_trie_of_short_segments():
     run_case(parents, lens, 2, 1, 128, torch.bfloat16)
 
 
-def test_attention_many_rows_below_a_key_tile():
-    """More rows below the first tiles than one part holds (2048), and the
-    query heads of a group spread over work-groups."""
-    parents, lens = [-1] + [0] * 5, [70, 900, 1000, 700, 33, 1]
-    say(f"attention parts N={sum(lens)}")
+@pytest.mark.parametrize("case", ["fan", "chain", "mixed"])
+def test_attention_lists_cut_into_parts(case):
+    """Lists long enough to be spread over work-groups, forward and backward,
+    and the query heads of a group spread too; parts some rows see nothing of."""
+    parents, lens = {"fan": ([-1] + [0] * 5, [70, 900, 1000, 700, 33, 1]), "chain": ([-1], [2100]),
+                     "mixed": ([-1, 0, -1, 2, 2, -1], [1300, 77, 50, 400, 30, 9])}[case]
+    say(f"attention parts {case} N={sum(lens)}")
+    plan = ptp.tree_plan(parents, lens, 4)
+    assert _lib.load().tree_attention_workspace_bytes(plan.attention().handle, 1, 32) > 0
     run_case(parents, lens, 4, 1, 64, torch.bfloat16)
     run_case(parents, lens, 1, 1, 32, torch.float32)
+    run_case(parents, lens, 2, 2, 128, torch.bfloat16)
+
+
+def test_attention_nan_in_a_part():
+    """A NaN score makes its row NaN in whichever part of the list it is, and
+    no other row."""
+    n = 2100
+    q, k, v, do = tensors(n, 1, 1, 64, torch.bfloat16)
+    plan = ptp.tree_plan([-1], [n], 4)
+    o, lse = ptp.tree_attention(q, k, v, plan, return_lse=True)
+    for at in (0, 300, 2099):
+        k2 = k.clone()
+        k2[at] = float("nan")
+        o2, lse2 = ptp.tree_attention(q, k2, v, plan, return_lse=True)
+        assert torch.isnan(o2[at:]).all() and torch.isnan(lse2[at:]).all()
+        assert torch.equal(o2[:at], o[:at]) and torch.equal(lse2[:at], lse[:at])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -331,5 +351,6 @@ def test_attention_refusals():
     big = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
     for buf in (big, stale):
         rc = lib.tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None, None, 32, 4, 2,
-                                64, 0.125, 1, a.handle, buf.data_ptr(), max(buf.numel(), a.device_bytes()), None)
+                                64, 0.125, 1, a.handle, buf.data_ptr(), max(buf.numel(), a.device_bytes()), None, 0,
+                                None)
         assert rc == -1 and b"not an upload" in lib.tree_last_error()
