@@ -482,7 +482,7 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
  * work-groups (few tiles and heads, or very different path lengths); 0
  * otherwise and for a NULL or bad argument.
  */
-size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d);
+size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d, int32_t dtype);
 
 /*
  * tree_attention -- softmax attention in which token i sees exactly the tokens
@@ -526,7 +526,7 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
  * results of parts of a tile's work.  0 for a NULL or unsupported argument.
  */
 size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
-                                               int32_t d);
+                                               int32_t d, int32_t dtype);
 
 /*
  * tree_attention_backward -- gradients of tree_attention, the probabilities

@@ -80,10 +80,10 @@ SIGNATURES = {
     "tree_attention_plan_free": (None, [_P]),
     "tree_attention_plan_device_bytes": (_SZ, [_P]),
     "tree_attention_plan_upload": (ctypes.c_int, [_P, _P, _SZ, _P]),
-    "tree_attention_workspace_bytes": (_SZ, [_P, _I32, _I32]),
+    "tree_attention_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
     "tree_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P, _P, _SZ, _P, _SZ,
                                       _P]),
-    "tree_attention_backward_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32]),
+    "tree_attention_backward_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32, _I32]),
     "tree_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _F,
                                                _I32, _P, _P, _SZ, _P, _SZ, _P]),
     "tree_logprobs_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
@@ -618,7 +618,8 @@ def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, retur
         _need_shape(lse, "lse", (n, h_q))
     lib = load()
     aplan = plan.attention()
-    workspace, ws_bytes = _workspace(workspace, int(lib.tree_attention_workspace_bytes(aplan.handle, h_q, d)), dev)
+    need = int(lib.tree_attention_workspace_bytes(aplan.handle, h_q, d, _dtype_code(q)))
+    workspace, ws_bytes = _workspace(workspace, need, dev)
     dplan = aplan.on_device(dev)
     stream = torch.cuda.current_stream(dev).cuda_stream
     p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
@@ -650,7 +651,7 @@ def tree_attention_backward(q, k, v, o, lse, do, plan: TreePlan, scale: Optional
     dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
     lib = load()
     aplan = plan.attention()
-    need = int(lib.tree_attention_backward_workspace_bytes(aplan.handle, h_q, k.shape[1], d))
+    need = int(lib.tree_attention_backward_workspace_bytes(aplan.handle, h_q, k.shape[1], d, _dtype_code(q)))
     workspace, ws_bytes = _workspace(workspace, need, dev)
     dplan = aplan.on_device(dev)
     stream = torch.cuda.current_stream(dev).cuda_stream

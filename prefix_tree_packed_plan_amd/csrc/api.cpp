@@ -136,9 +136,14 @@ struct Work {
   const tg::AttnCut* cut;
   int32_t split, n_join, n_parts;
 };
-Work attention_work(const tg::AttnLists& l, int32_t heads, int32_t steps) {
+Work attention_work(const tg::AttnLists& l, int32_t heads, int32_t steps, int32_t d, int32_t dtype) {
   Work w{};
-  w.cut = &tg::choose_cut(l, heads, steps, steps > 1 ? &w.split : nullptr);
+  // Starting and joining a part costs about 4 tiles of bf16, and the join
+  // launch 2; fp32 products take 16 times as long (192 tokens in fp32, cut into
+  // parts of 64 or not: forward of one head of 32 22.4 / 16.8 us, backward of
+  // two heads of 64 34 / 56 us).
+  const bool f32 = dtype == TREE_DTYPE_F32;
+  w.cut = &tg::choose_cut(l, heads, steps, f32 ? 64 : 256, f32 ? 8192 / d : 128, steps > 1 ? &w.split : nullptr);
   if (w.split < 1) w.split = 1;
   w.n_join = w.split > 1 ? l.n_tiles : w.cut->n_multi;
   w.n_parts = w.split > 1 ? w.cut->n_items : w.cut->n_multi_parts;
@@ -821,9 +826,9 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
   return TREE_OK;
 }
 
-size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d) {
-  if (!aplan || h_q <= 0 || d <= 0) return 0;
-  const Work w = attention_work(aplan->p.q, h_q, 1);
+size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d, int32_t dtype) {
+  if (!aplan || h_q <= 0 || d <= 0 || !dtype_ok(dtype)) return 0;
+  const Work w = attention_work(aplan->p.q, h_q, 1, d, dtype);
   return static_cast<size_t>(w.n_parts) * h_q * tg::attention_part_floats(d) * sizeof(float);
 }
 
@@ -842,7 +847,7 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
   if (const int rc = make_heads(v, st_of(2), h_kv, d, dtype, "v", fn, &a.v)) return rc;
   if (const int rc = check_aligned(o, "o", fn)) return rc;
   if (o == q || o == k || o == v) return fail(TREE_ERR_INVALID_ARG, "%s: o must not alias q, k or v", fn);
-  const size_t need = tree_attention_workspace_bytes(aplan, h_q, d);
+  const size_t need = tree_attention_workspace_bytes(aplan, h_q, d, dtype);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, need);
   if (need > 0)
@@ -855,7 +860,7 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
   a.tok_d = base + p.m_d;
   a.tok_e = base + p.m_e;
   a.runs = reinterpret_cast<const tg::AttnRun*>(base + p.m_runs);
-  set_work(attention_work(p.q, h_q, 1), base, &a);
+  set_work(attention_work(p.q, h_q, 1, d, dtype), base, &a);
   a.n_tok = p.n_tokens;
   a.h_q = h_q;
   a.h_kv = h_kv;
@@ -866,10 +871,10 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
 }
 
 size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
-                                               int32_t d) {
-  if (!aplan || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0) return 0;
+                                               int32_t d, int32_t dtype) {
+  if (!aplan || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0 || !dtype_ok(dtype)) return 0;
   const tg::AttnPlan& p = aplan->p;
-  const Work wq = attention_work(p.q, h_q, 1), wk = attention_work(p.k, h_kv, h_q / h_kv);
+  const Work wq = attention_work(p.q, h_q, 1, d, dtype), wk = attention_work(p.k, h_kv, h_q / h_kv, d, dtype);
   const size_t dq = static_cast<size_t>(wq.n_parts) * h_q * tg::attention_dq_part_floats(d);
   const size_t dkv = static_cast<size_t>(wk.n_parts) * wk.split * h_kv * tg::attention_dkv_part_floats(d);
   return attention_delta_bytes(p, h_q) + std::max(dq, dkv) * sizeof(float);
@@ -901,7 +906,7 @@ int tree_attention_backward(const void* q, const void* k, const void* v, const v
     for (const void* y : ins)
       if (x == y) return fail(TREE_ERR_INVALID_ARG, "%s: gradients must not alias the inputs", fn);
   if (dq == dk || dq == dv || dk == dv) return fail(TREE_ERR_INVALID_ARG, "%s: gradients must not alias", fn);
-  const size_t need = tree_attention_backward_workspace_bytes(aplan, h_q, h_kv, d);
+  const size_t need = tree_attention_backward_workspace_bytes(aplan, h_q, h_kv, d, dtype);
   if (!ws || ws_bytes < need)
     return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, need);
   if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;
@@ -921,10 +926,10 @@ int tree_attention_backward(const void* q, const void* k, const void* v, const v
   a.h_kv = h_kv;
   a.scale = scale;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  set_work(attention_work(p.q, h_q, 1), base, &a);
+  set_work(attention_work(p.q, h_q, 1, d, dtype), base, &a);
   hipError_t e = tg::launch_attention_dq(a, d, dtype, st);  // also delta
   if (e == hipSuccess) {
-    set_work(attention_work(p.k, h_kv, h_q / h_kv), base, &a);
+    set_work(attention_work(p.k, h_kv, h_q / h_kv, d, dtype), base, &a);
     e = tg::launch_attention_dkv(a, d, dtype, st);  // its parts take dq's place in the workspace
   }
   if (e != hipSuccess) return hip_fail("tree_attention_backward: launch", e);

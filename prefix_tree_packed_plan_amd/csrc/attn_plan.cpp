@@ -86,7 +86,7 @@ AttnLists cut_all(const std::vector<AttnItem>& lists, std::vector<int32_t>* mirr
     return at;
   };
   static_assert(sizeof(AttnItem) == 32 && sizeof(AttnRun) == 8 && sizeof(AttnParts) == 16, "device layout");
-  for (int64_t most = int64_t(1) << 31; most >= 256; most = most > 8192 ? 8192 : most / 2) {
+  for (int64_t most = int64_t(1) << 31; most >= 64; most = most > 8192 ? 8192 : most / 2) {
     const bool whole = most > 8192;
     if (!whole && longest <= most) continue;  // the whole lists again
     if (!whole && l.total / most + l.n_tiles > AttnPlan::kMaxParts) break;
@@ -100,18 +100,23 @@ AttnLists cut_all(const std::vector<AttnItem>& lists, std::vector<int32_t>* mirr
 
 }  // namespace
 
-const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t* split) {
+const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t least, int32_t worth,
+                          int32_t* split) {
   if (split) *split = 1;
   const AttnCut& whole = l.cuts.front();
   const int64_t room = l.total * heads * steps;  // of kSlots slots
-  const auto fits = [&](int64_t len) { return 4 * len * kSlots <= 3 * room; };
-  for (const AttnCut& c : l.cuts) {
-    if (!fits(int64_t(c.longest) * steps) && &c != &l.cuts.back()) continue;
+  const auto fits = [&](int64_t len, bool uncut) { return 4 * len * kSlots <= (uncut ? 4 : 3) * room; };
+  for (size_t i = 0; i < l.cuts.size(); ++i) {
+    const AttnCut& c = l.cuts[i];
+    const bool last = i + 1 == l.cuts.size() || l.cuts[i + 1].most < least;
+    const int64_t items = int64_t(c.n_items) * heads;
+    const bool enough = items >= kSlots && c.most <= 4 * least;
+    if (!fits(int64_t(c.longest) * steps, i == 0) && !enough && !last) continue;
     int32_t s = 1;
     if (split)
-      while (s < steps && !fits(int64_t(c.longest) * ((steps + s - 1) / s))) ++s;
+      while (s < steps && items * s < kSlots && !fits(int64_t(c.longest) * ((steps + s - 1) / s), false)) ++s;
     const int64_t saved = int64_t(whole.longest) * steps - int64_t(c.longest) * ((steps + s - 1) / s);
-    if (saved < kWorth) return whole;
+    if (saved < worth) return whole;
     if (split) *split = s;
     return c;
   }

@@ -18,7 +18,7 @@
 //
 // A list may be cut into parts, worked on by different work-groups, whose
 // results are added in the order of the parts.  The tables hold every list
-// whole and cut into parts of at most 8192, 4096, .. 256 positions; a call
+// whole and cut into parts of at most 8192, 4096, .. 64 positions; a call
 // takes the coarsest cut that balances its work-groups (choose_cut).
 #pragma once
 
@@ -84,13 +84,19 @@ struct AttnPlan {
 
 // The cut for `heads` work items per part, each `steps` times as long as the
 // part, on a device that runs kSlots work-groups at a time: the coarsest whose
-// longest item is at most 3/4 of what a slot gets on average, else the finest
-// -- and whole lists where cutting would shorten the longest item by less than
-// kWorth positions, about what the joining costs.  *split (1..steps, may be
-// null) spreads the steps of the finest cut over further work-groups.
+// longest item is at most 3/4 of what a slot gets on average (whole lists: at
+// most all of it, as the shorter ones fill the gaps), or that has
+// kSlots items of at most 4 `least` positions, or that the next one would cut
+// below `least` (whose work is about what a part costs in starting and
+// joining); whole lists where that would shorten the longest item by less than
+// `worth` positions, what the join launch costs.  *split
+// (1..steps, may be null) spreads the steps over further work-groups.
+// Measured (bf16, 8/2 heads of 128, least = 256 / 128 / 64): forward on a chain
+// of 1024 tokens 21.8 / 24.2 / 36.0 us, backward on 600 tokens of 8/1 heads
+// 47.5 / 42.4 / 44.0 us; fp32 (600 tokens, 8/2 heads of 64) 85 / 57 / 46 us.
 constexpr int32_t kSlots = 512;
-constexpr int32_t kWorth = 768;
-const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t* split);
+const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t least, int32_t worth,
+                          int32_t* split);
 
 // Returns 0 or a negative TREE_ERR_* code; on failure *err holds a message.
 int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err);

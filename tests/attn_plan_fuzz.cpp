@@ -144,10 +144,13 @@ static void check(const std::vector<int32_t>& parents, const std::vector<int32_t
     for (const int heads : {1, 2, 16, 1000})
       for (const int steps : {1, 3, 8}) {
         int32_t split = -1;
-        const tg::AttnCut& c = tg::choose_cut(l, heads, steps, &split);
-        CHECK(split >= 1 && split <= steps, "split %d", split);
-        CHECK(&c >= l.cuts.data() && &c < l.cuts.data() + l.cuts.size(), "a cut of these lists");
-        tg::choose_cut(l, heads, steps, nullptr);
+        for (const int least : {64, 256}) {
+          const tg::AttnCut& c = tg::choose_cut(l, heads, steps, least, least / 2, &split);
+          CHECK(split >= 1 && split <= steps, "split %d", split);
+          CHECK(&c >= l.cuts.data() && &c < l.cuts.data() + l.cuts.size(), "a cut of these lists");
+          CHECK(&c == l.cuts.data() || c.most >= least, "too fine a cut");
+          tg::choose_cut(l, heads, steps, least, least / 2, nullptr);
+        }
       }
   }
 }

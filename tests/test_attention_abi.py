@@ -68,10 +68,10 @@ def test_attention_refusals_need_no_device():
 def test_attention_backward_refusals_need_no_device():
     a = plan_of().attention()
     lib = _lib.load()
-    need = lib.tree_attention_backward_workspace_bytes(a.handle, 4, 2, 128)
+    need = lib.tree_attention_backward_workspace_bytes(a.handle, 4, 2, 128, 1)
     assert need >= 230 * 4 * 4
-    assert lib.tree_attention_backward_workspace_bytes(None, 4, 2, 128) == 0
-    assert lib.tree_attention_backward_workspace_bytes(a.handle, 3, 2, 128) == 0
+    assert lib.tree_attention_backward_workspace_bytes(None, 4, 2, 128, 1) == 0
+    assert lib.tree_attention_backward_workspace_bytes(a.handle, 3, 2, 128, 1) == 0
     good = dict(q=P, k=P, v=P, o=P, lse=P, do=P, dq=P2, dk=P3, dv=P4, st=None, n=230, hq=4, hkv=2, d=128, scale=0.1, dtype=1, aplan=a.handle, dplan=P, bytes=BIG, ws=P, ws_bytes=need,
                 stream=None)
 
@@ -102,17 +102,18 @@ def test_attention_workspace_counts_cut_lists():
     def delta(n, h):
         return (2 * n * h * 4 + 255) // 256 * 256
 
-    assert fwd(None, 4, 64) == 0 and bwd(None, 4, 1, 64) == 0
+    assert fwd(None, 4, 64, 1) == 0 and bwd(None, 4, 1, 64, 1) == 0
     many = plan_of([-1] * 600, [128] * 600).attention()
-    assert fwd(many.handle, 2, 64) == 0 and bwd(many.handle, 2, 1, 64) == delta(600 * 128, 2)
-    short = plan_of([-1], [512]).attention()
-    assert fwd(short.handle, 4, 64) == 0 and bwd(short.handle, 1, 1, 64) == delta(512, 1)
+    assert fwd(many.handle, 2, 64, 1) == 0 and bwd(many.handle, 2, 1, 64, 1) == delta(600 * 128, 2)
+    short = plan_of([-1], [300]).attention()
+    assert fwd(short.handle, 4, 64, 1) == 0 and bwd(short.handle, 1, 1, 64, 1) == delta(300, 1)
     one = plan_of([-1], [2048]).attention()  # 256 positions a part: 2 of the 16 lists are not cut
-    f = fwd(one.handle, 1, 64)
+    f = fwd(one.handle, 1, 64, 1)
     assert f > 0 and f % (128 * 66 * 4) == 0
     assert f // (128 * 66 * 4) == sum(-(-128 * i // 256) for i in range(3, 17))
-    b = bwd(one.handle, 8, 1, 64) - delta(2048, 8)
+    b = bwd(one.handle, 8, 1, 64, 1) - delta(2048, 8)
     assert b > 0 and b % part[1] == 0
+    assert fwd(one.handle, 1, 64, 0) > f and fwd(one.handle, 1, 64, 2) == 0  # fp32: finer parts
     rc = lib.tree_attention(P, P, P, P2, None, None, 2048, 1, 1, 64, 0.1, 1, one.handle, P, BIG, P, f - 1, None)
     assert rc == -5
     rc = lib.tree_attention(P, P, P, P2, None, None, 2048, 1, 1, 64, 0.1, 1, one.handle, P, BIG, None, BIG, None)

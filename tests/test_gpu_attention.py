@@ -127,7 +127,7 @@ def test_attention_lists_cut_into_parts(case):
                      "mixed": ([-1, 0, -1, 2, 2, -1], [1300, 77, 50, 400, 30, 9])}[case]
     say(f"attention parts {case} N={sum(lens)}")
     plan = ptp.tree_plan(parents, lens, 4)
-    assert _lib.load().tree_attention_workspace_bytes(plan.attention().handle, 1, 32) > 0
+    assert _lib.load().tree_attention_workspace_bytes(plan.attention().handle, 1, 32, 0) > 0
     run_case(parents, lens, 4, 1, 64, torch.bfloat16)
     run_case(parents, lens, 1, 1, 32, torch.float32)
     run_case(parents, lens, 2, 2, 128, torch.bfloat16)
