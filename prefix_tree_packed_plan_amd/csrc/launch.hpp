@@ -282,7 +282,7 @@ struct LogprobArgs {
 };
 
 constexpr int kMaxTopK = 64;          // one list entry per lane
-constexpr int kMaxSlice = 1 << 17;    // columns a work-group takes at most
+constexpr int kMaxSlice = 1 << 13;    // columns a work-group of the backward takes at most
 
 hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_logprobs_backward(const LogprobArgs& a, int dtype, hipStream_t stream);

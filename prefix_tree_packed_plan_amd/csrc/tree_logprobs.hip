@@ -9,10 +9,12 @@
 // every child ("Tree Training" section 3.1 Eq. 6: each token's value is the
 // one of its own root-to-leaf path), whose gradients add up in that row.
 //
-// Both kernels read the logits once.  The forward keeps, per lane, a reference
-// value m (raised only when a value passes it by a factor 2^10, so nearly
-// never) and s = sum exp2(c (x - m)), t = sum exp2(c (x - m)) (x - m) with c =
-// log2(e) / T; then H = log s - t / (T s).
+// Both kernels read the logits once.  The forward works in powers of 2: with c
+// = log2(e) / T and a whole number M per lane (raised only when a value passes
+// 2^(M + 10), so nearly never), y = c x - M in one rounding, s = sum exp2(y)
+// and t = sum exp2(y) y; then lse = (M + log2 s) / log2(e), logp = (c x - M -
+// log2 s) / log2(e), H = (log2 s - t / s) / log2(e).  M being whole, changing it
+// is exact, and c's own rounding cancels in logp and H.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -124,6 +126,19 @@ __device__ __forceinline__ int token(const LogprobArgs& a, int t) {
 }
 
 // ---- the largest values of a row ------------------------------------------------
+// The k-th largest of the wave's 64 values (a bitonic sort).
+__device__ __forceinline__ float kth_largest(float x, int k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 64; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o; o /= 2) {
+      const float y = __shfl_xor(x, o, 64);
+      const bool down = (lane & size) == 0;  // this run is sorted downwards
+      x = ((lane & o) == 0) == down ? fmaxf(x, y) : fminf(x, y);
+    }
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), k - 1));
+}
+
 // A wave's list, best first: lane j < k holds entry j.  Ties go to the lowest
 // index.  (tv, ti) is the last entry, which a new one has to beat.
 struct TopList {
@@ -131,102 +146,148 @@ struct TopList {
   int id = kNoId, ti = kNoId, k;
   __device__ __forceinline__ explicit TopList(int k_) : k(k_) {}
   static __device__ __forceinline__ bool better(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
-  // One candidate per lane (index kNoId: none).
-  __device__ __forceinline__ void offer(float x, int i, int lane) {
-    uint64_t m = __ballot(better(x, i, tv, ti));
+  // One candidate per lane (index kNoId: none), if it is at least `floor`.
+  __device__ __forceinline__ void offer(float x, int i, int lane, float floor = kNegInf) {
+    uint64_t m = __ballot(x >= floor && better(x, i, tv, ti));
     while (m) {
       const int src = __builtin_ctzll(m);
       const float nx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), src));
       const int ni = __builtin_amdgcn_readlane(i, src);
       const int pos = __popcll(__ballot(lane < k && better(v, id, nx, ni)));
-      const float up = __shfl_up(v, 1, 64);
-      const int upi = __shfl_up(id, 1, 64);
-      if (lane > pos) {
-        v = up;
-        id = upi;
-      }
-      if (lane == pos) {
-        v = nx;
-        id = ni;
-      }
+      // The entries from pos on move up by one lane.
+      const float up = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x138, 0xf, 0xf, false));
+      const int upi = __builtin_amdgcn_update_dpp(0, id, 0x138, 0xf, 0xf, false);
+      v = lane > pos ? up : lane == pos ? nx : v;
+      id = lane > pos ? upi : lane == pos ? ni : id;
       tv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), k - 1));
       ti = __builtin_amdgcn_readlane(id, k - 1);
       m &= m - 1;
       m &= __ballot(better(x, i, tv, ti));
     }
   }
+  // What a value has to reach to be worth offering, given each lane's largest
+  // of those at hand: while the list is not full, the k-th largest of these
+  // (at least k values reach it), which spares most of the first insertions.
+  __device__ __forceinline__ float floor_of(float big, int lane) const {
+    return ti == kNoId ? kth_largest(big, k, lane) : tv;
+  }
 };
 
 // ---- forward --------------------------------------------------------------------
 struct Sums {
-  float m, s, t;  // reference value, sum of e = exp2(c (x - m)), sum of e (x - m)
+  float m, s, t;  // M (-inf: nothing yet), sum of e = exp2(y), sum of e y
+  float top;      // the largest value
 };
-// The sums of both, over the larger reference.
-__device__ __forceinline__ Sums join(const Sums a, const Sums b, float c) {
+// The sums of both, over the larger M.
+__device__ __forceinline__ Sums join(const Sums a, const Sums b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == kNegInf) return Sums{m, a.s + b.s, a.t + b.t};
-  Sums r{m, 0.f, 0.f};
+  const float top = fmaxf(a.top, b.top);
+  if (m == kNegInf) return Sums{m, a.s + b.s, a.t + b.t, top};
+  Sums r{m, 0.f, 0.f, top};
   // A factor of 0 (that side is empty, or far below) drops t, whose shift may
   // overflow; a NaN stays in s.
   const float da = a.m - m, db = b.m - m;
-  const float fa = ex2(da * c), fb = ex2(db * c);
+  const float fa = ex2(da), fb = ex2(db);
   r.s = a.s * fa + b.s * fb;
   r.t = (fa == 0.f ? 0.f : fmaf(da, a.s, a.t) * fa) + (fb == 0.f ? 0.f : fmaf(db, b.s, b.t) * fb);
   return r;
 }
 
+// The M for values up to x: c x rounded to a whole number, finite for every
+// finite x.
+__device__ __forceinline__ float whole(float x, float c) {
+  return x == kNegInf ? kNegInf : rintf(fminf(fmaxf(x * c, -3e38f), 3.4e38f));
+}
 template <typename T>
 struct Scan {
   static constexpr int N = Vec<T>::N;
-  float c, slack;  // slack: how far a value may pass m (10 / c)
-  float m = kNegInf, mr = 0.f, s = 0.f, t = 0.f;
-  __device__ __forceinline__ explicit Scan(float c_) : c(c_), slack(10.f / c_) {}
+  float c;
+  float limit = kNegInf;  // a value above this raises M
+  float m = kNegInf, mr = 0.f, s = 0.f, t = 0.f, top = kNegInf;
+  __device__ __forceinline__ explicit Scan(float c_) : c(c_) {}
   // n values (the others -inf).
   template <int n>
   __device__ __forceinline__ float add(const float* x) {
-    float top = x[0];
+    float big = x[0];
 #pragma unroll
-    for (int j = 1; j < n; ++j) top = fmaxf(top, x[j]);
-    if (__any(top > m + slack)) {
-      const float mn = fmaxf(m, top);
-      const float d = m == kNegInf ? 0.f : m - mn, f = ex2(d * c);
+    for (int j = 1; j < n; ++j) big = fmaxf(big, x[j]);
+    top = fmaxf(top, big);
+    if (__any(big > limit)) {
+      const float mn = fmaxf(m, whole(big, c));
+      const float d = m == kNegInf ? 0.f : m - mn, f = ex2(d);
       t = f == 0.f ? 0.f : fmaf(d, s, t) * f;
       s *= f;
       m = mn;
       mr = m == kNegInf ? 0.f : m;
+      limit = m == kNegInf ? kNegInf : (m + 10.f) / c;
     }
 #pragma unroll
     for (int j = 0; j < n; ++j) {
-      const float y = x[j] - mr, e = ex2(y * c);
+      const float y = fmaf(x[j], c, -mr), e = ex2(y);
       s += e;
       t = fmaf(e, fmaxf(y, -3.4e38f), t);  // e = 0 where y = -inf
     }
-    return top;
+    return big;
   }
 };
 
-// Everything a row's sums decide, by the threads tid, tid + nt, ...
+// Log probabilities of one row, from its sums.
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs& a, int lr, const Sums z, const Behind& b, int tid, int nt) {
-  const T* x = static_cast<const T*>(a.logits) + int64_t(lr) * a.ld;
-  const bool empty = z.m == kNegInf && z.s == 0.f;  // every logit is -inf
-  const float ls = __log2f(z.s) * kLn2;             // log s
+struct Row {
+  const T* x;
+  float c, m, ls;     // ls: log2 of the sum of exponentials
+  float entropy, lse;
+  bool empty;         // every logit is -inf
+  bool flat;          // c x overflows for the largest x already (a row of the type's lowest value)
+  float top;
+  // By a whole wave.
+  __device__ __forceinline__ Row(const LogprobArgs& a, int lr, const Sums z, int lane)
+      : x(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld), c(a.inv_t * kLog2e), m(z.m), top(z.top) {
+    empty = z.s == 0.f && top == kNegInf;
+    flat = z.s == 0.f && !empty;
+    ls = __log2f(z.s);
+    lse = (m + ls) * kLn2;
+    entropy = (ls - z.t / z.s) * kLn2;
+    if (flat) {  // only the values equal to the largest count
+      int n = 0;
+      for (int i = lane; i < a.vocab; i += 64) n += Vec<T>::one(x + i) == top;
+#pragma unroll
+      for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
+      ls = __log2f(float(n));
+      lse = fmaf(top, a.inv_t, ls * kLn2);
+      entropy = ls * kLn2;
+    }
+    if (empty) {
+      lse = kNegInf;
+      entropy = 0.f;
+    }
+  }
+  __device__ __forceinline__ float logp(float v) const {
+    if (empty || flat) return empty || v != top ? kNegInf : -ls * kLn2;
+    return (fmaf(v, c, -m) - ls) * kLn2;
+  }
+};
+
+// Everything a row's sums decide but the list, by the threads tid, tid + nt, ...
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, int lr, const Row<T>& row, const Behind& b, int tid,
+                                           int nt) {
   if (tid == 0) {
-    a.lse[lr] = empty ? kNegInf : z.m * a.inv_t + ls;
-    a.entropy[lr] = empty ? 0.f : ls - a.inv_t * (z.t / z.s);
+    a.lse[lr] = row.lse;
+    a.entropy[lr] = row.entropy;
     if (b.root_start) a.logp[a.first_row + lr] = 0.f;
   }
   for (int j = tid; j < b.n; j += nt) {
     const int t = b.at(j), id = token(a, t);
-    a.logp[t] = id < 0 ? 0.f : empty ? kNegInf : (Vec<T>::one(x + id) - z.m) * a.inv_t - ls;
+    a.logp[t] = id < 0 ? 0.f : row.logp(Vec<T>::one(row.x + id));
   }
 }
-__device__ __forceinline__ void put_top(const LogprobArgs& a, int lr, const Sums z, const TopList& l, int lane) {
+template <typename T>
+__device__ __forceinline__ void put_top(const LogprobArgs& a, int lr, const Row<T>& row, const TopList& l, int lane) {
   if (lane >= a.top_k) return;
-  const bool empty = z.m == kNegInf && z.s == 0.f;
   const int64_t o = int64_t(lr) * a.top_k + lane;
   a.top_id[o] = l.id == kNoId ? -1 : l.id;
-  a.top_logp[o] = empty ? kNegInf : (l.v - z.m) * a.inv_t - __log2f(z.s) * kLn2;
+  a.top_logp[o] = row.logp(l.v);
 }
 __device__ __forceinline__ float* part_lists(const LogprobArgs& a) {
   return a.part + int64_t(a.n_rows) * a.split * 4;
@@ -238,6 +299,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   __shared__ Sums sums[kThreads / 64];
   __shared__ float tv[TOP ? kThreads : 1];
   __shared__ int ti[TOP ? kThreads : 1];
+  __shared__ float last[kThreads / 64];  // each wave's last entry
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = blockIdx.x / a.split, part = blockIdx.x % a.split;
@@ -246,15 +308,26 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   Scan<T> sc(a.inv_t * kLog2e);
   TopList top(a.top_k);
 
+  // A value below another wave's last entry is not among the row's top_k
+  // either.  The waves read these whenever they come by: that decides how many
+  // values are offered in vain, not which stay.
+  volatile float* const lasts = last;
+  float others = kNegInf;
+  if constexpr (TOP) {
+    if (tid < kThreads / 64) last[tid] = kNegInf;
+    __syncthreads();
+  }
   const auto* pv = reinterpret_cast<const u32x4*>(sl.p + sl.head);
-  auto one = [&](const u32x4 w, int v) {
-    float x[N];
-    Vec<T>::unpack(w, x);
+  // A piece of N columns from col on (kNoId: none, all -inf).
+  auto one = [&](const float* x, int col) {
     const float big = sc.template add<N>(x);
     if constexpr (TOP) {
-      if (__any(big >= top.tv)) {
+      if (__any(big >= fmaxf(top.tv, others))) {
+        const float floor = fmaxf(top.floor_of(col == kNoId ? kNegInf : big, lane), others);
 #pragma unroll
-        for (int j = 0; j < N; ++j) top.offer(x[j], c0 + sl.head + v * N + j, lane);
+        for (int j = 0; j < N; ++j)
+          if (__any(x[j] >= floor)) top.offer(x[j], col == kNoId ? kNoId : col + j, lane, floor);
+        if (lane == 0) lasts[wave] = top.tv;
       }
     }
   };
@@ -263,8 +336,13 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     u32x4 w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+    if constexpr (TOP) others = fmaxf(fmaxf(lasts[0], lasts[1]), fmaxf(lasts[2], lasts[3]));
 #pragma unroll
-    for (int u = 0; u < U; ++u) one(w[u], v + u * kThreads);
+    for (int u = 0; u < U; ++u) {
+      float x[N];
+      Vec<T>::unpack(w[u], x);
+      one(x, c0 + sl.head + (v + u * kThreads) * N);
+    }
   }
   // The last pieces, and the columns outside of them; lanes without one add
   // -inf, which changes nothing.
@@ -274,13 +352,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
 #pragma unroll
     for (int j = 0; j < N; ++j) x[j] = kNegInf;
     if (v < sl.vecs) Vec<T>::unpack(__builtin_nontemporal_load(pv + v), x);
-    const float big = sc.template add<N>(x);
-    if constexpr (TOP) {
-      if (__any(big >= top.tv)) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) top.offer(x[j], v < sl.vecs ? c0 + sl.head + v * N + j : kNoId, lane);
-      }
-    }
+    one(x, v < sl.vecs ? c0 + sl.head + v * N : kNoId);
   }
   if (wave == 0) {
     const int i = lane;
@@ -290,12 +362,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     if constexpr (TOP) top.offer(x, has ? c0 + sl.end_col(i) : kNoId, lane);
   }
 
-  Sums z{sc.m, sc.s, sc.t};
+  Sums z{sc.m, sc.s, sc.t, sc.top};
 #pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const Sums y{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)};
-    z = join(z, y, sc.c);
-  }
+  for (int o = 32; o; o >>= 1)
+    z = join(z, Sums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64), __shfl_xor(z.top, o, 64)});
   if (lane == 0) sums[wave] = z;
   if constexpr (TOP) {
     tv[tid] = top.v;
@@ -304,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   __syncthreads();
   z = sums[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) z = join(z, sums[w], sc.c);
+  for (int w = 1; w < kThreads / 64; ++w) z = join(z, sums[w]);
   if constexpr (TOP) {
     if (wave == 0) {
 #pragma unroll
@@ -316,10 +386,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   }
   if (a.split == 1) {
     const Behind b(a, a.first_row + lr, lane);
-    finish_row<T>(a, lr, z, b, tid, kThreads);
-    if (TOP && wave == 0) put_top(a, lr, z, top, lane);
+    const Row<T> row(a, lr, z, lane);
+    finish_row<T>(a, lr, row, b, tid, kThreads);
+    if (TOP && wave == 0) put_top<T>(a, lr, row, top, lane);
   } else {
-    if (tid == 0) *reinterpret_cast<float4*>(a.part + int64_t(blockIdx.x) * 4) = make_float4(z.m, z.s, z.t, 0.f);
+    if (tid == 0) *reinterpret_cast<float4*>(a.part + int64_t(blockIdx.x) * 4) = make_float4(z.m, z.s, z.t, z.top);
     if (TOP && wave == 0 && lane < a.top_k)
       *reinterpret_cast<float2*>(part_lists(a) + (int64_t(blockIdx.x) * a.top_k + lane) * 2) =
           make_float2(top.v, __int_as_float(top.id));
@@ -330,28 +401,26 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
 template <typename T, bool TOP>
 __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
   const int lane = threadIdx.x, lr = blockIdx.x;
-  const float c = a.inv_t * kLog2e;
-  const Behind b(a, a.first_row + lr, lane);
-  Sums z{kNegInf, 0.f, 0.f};
+  Sums z{kNegInf, 0.f, 0.f, kNegInf};
   for (int i = lane; i < a.split; i += 64) {
     const float4 y = *reinterpret_cast<const float4*>(a.part + (int64_t(lr) * a.split + i) * 4);
-    z = join(z, Sums{y.x, y.y, y.z}, c);
+    z = join(z, Sums{y.x, y.y, y.z, y.w});
   }
+  const Behind b(a, a.first_row + lr, lane);
 #pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const Sums y{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)};
-    z = join(z, y, c);
-  }
-  finish_row<T>(a, lr, z, b, lane, 64);
+  for (int o = 32; o; o >>= 1)
+    z = join(z, Sums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64), __shfl_xor(z.top, o, 64)});
+  const Row<T> row(a, lr, z, lane);
+  finish_row<T>(a, lr, row, b, lane, 64);
   if constexpr (TOP) {
     TopList top(a.top_k);
     const float2* l = reinterpret_cast<const float2*>(part_lists(a)) + int64_t(lr) * a.split * a.top_k;
     const int n = a.split * a.top_k;
     for (int i = lane; i < n + lane; i += 64) {
       const float2 y = i < n ? l[i] : make_float2(kNegInf, __int_as_float(kNoId));
-      top.offer(y.x, __float_as_int(y.y), lane);
+      top.offer(y.x, __float_as_int(y.y), lane, top.floor_of(y.x, lane));
     }
-    put_top(a, lr, z, top, lane);
+    put_top<T>(a, lr, row, top, lane);
   }
 }
 
@@ -371,6 +440,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
   const int c0 = part * a.slice;
   const Slice<T> sl(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld + c0, min(a.slice, a.vocab - c0));
   T* out = static_cast<T*>(a.dlogits) + int64_t(lr) * a.ldd + c0;
+  // The first pieces are on their way while the tokens behind the row are
+  // looked up.
+  const auto* pv = reinterpret_cast<const u32x4*>(sl.p + sl.head);
+  const int rounds = sl.vecs / (U * kThreads);
+  u32x4 w[U] = {};
+  if (rounds > 0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + tid + u * kThreads);
+  }
   const Behind b(a, a.first_row + lr, lane);
   for (int i = tid; i < (sl.vecs + 31) / 32; i += kThreads) flag[i] = 0;
   __syncthreads();
@@ -416,7 +494,6 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
     }
     return s * a.inv_t;
   };
-  const auto* pv = reinterpret_cast<const u32x4*>(sl.p + sl.head);
   const bool aligned = (reinterpret_cast<uintptr_t>(out + sl.head) & 15) == 0;
   auto one = [&](const u32x4 w, int v) {
     float x[N];
@@ -436,10 +513,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
     }
   };
   int v = tid;
-  for (int i = 0; i < sl.vecs / (U * kThreads); ++i, v += U * kThreads) {
-    u32x4 w[U];
+  for (int i = 0; i < rounds; ++i, v += U * kThreads) {
+    if (i > 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+      for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) one(w[u], v + u * kThreads);
   }
