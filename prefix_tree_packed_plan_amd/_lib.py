@@ -566,6 +566,13 @@ def tree_ssd_scan(x, dt, A, B, C, plan: TreePlan, D=None, return_states: bool = 
     return y
 
 
+def _stream(dev):
+    """The current HIP stream of a device tensor's device (without making the
+    torch.cuda.Stream object, which takes longer than a small kernel's launch)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _need_heads(t, name, dtype=None, device=None):
     """A [N, H, d] device tensor whose heads' d elements are contiguous; returns
     the elements between token rows and between heads."""
@@ -587,9 +594,10 @@ def _need_heads(t, name, dtype=None, device=None):
 
 
 def _attention_shapes(q, k, v, plan):
-    if k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    qs, ks = q.shape, k.shape
+    if ks != v.shape or qs[0] != ks[0] or qs[2] != ks[2]:
         raise ValueError("shapes must be q [N, H_q, d] and k, v [N, H_kv, d]")
-    if q.shape[0] != plan.n_tokens:
+    if qs[0] != plan.n_tokens:
         raise ValueError(f"q has {q.shape[0]} tokens, the plan {plan.n_tokens}")
 
 
@@ -608,20 +616,23 @@ def tree_attention(q, k, v, plan: TreePlan, scale: Optional[float] = None, retur
     st += _need_heads(k, "k", q.dtype, dev) + _need_heads(v, "v", q.dtype, dev)
     _attention_shapes(q, k, v, plan)
     n, h_q, d = q.shape
-    o = torch.empty((n, h_q, d), dtype=q.dtype, device=dev) if out is None else out
-    _need(o, "out", q.dtype, dev)
-    _need_shape(o, "out", (n, h_q, d))
-    if return_lse and lse is None:
-        lse = torch.empty((n, h_q), dtype=torch.float32, device=dev)
+    if out is None:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        o = out
+        _need(o, "out", q.dtype, dev)
+        _need_shape(o, "out", (n, h_q, d))
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
         _need_shape(lse, "lse", (n, h_q))
+    elif return_lse:
+        lse = torch.empty((n, h_q), dtype=torch.float32, device=dev)
     lib = load()
     aplan = plan.attention()
     need = int(lib.tree_attention_workspace_bytes(aplan.handle, h_q, d, _dtype_code(q)))
     workspace, ws_bytes = _workspace(workspace, need, dev)
     dplan = aplan.on_device(dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream(dev)
     p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
     _check(lib.tree_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), p(lse), (_I64 * 6)(*st), n, h_q,
                               k.shape[1], d, d ** -0.5 if scale is None else float(scale), _dtype_code(q),
@@ -646,15 +657,15 @@ def tree_attention_backward(q, k, v, o, lse, do, plan: TreePlan, scale: Optional
     _need_shape(do, "do", (n, h_q, d))
     _need(lse, "lse", torch.float32, dev)
     _need_shape(lse, "lse", (n, h_q))
-    dq = torch.empty((n, h_q, d), dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+    dv = torch.empty_like(v, memory_format=torch.contiguous_format)
     lib = load()
     aplan = plan.attention()
     need = int(lib.tree_attention_backward_workspace_bytes(aplan.handle, h_q, k.shape[1], d, _dtype_code(q)))
     workspace, ws_bytes = _workspace(workspace, need, dev)
     dplan = aplan.on_device(dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream(dev)
     _check(lib.tree_attention_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                        do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), (_I64 * 10)(*st), n, h_q, k.shape[1], d, d ** -0.5 if scale is None else float(scale),
                                        _dtype_code(q), aplan.handle, dplan.data_ptr(), dplan.numel(),
@@ -710,16 +721,17 @@ def tree_logprobs(logits, tokens, plan: TreePlan, temperature: float = 1.0, top_
     if logp is None:
         whole = rows == plan.n_tokens
         logp = (torch.empty if whole else torch.zeros)((plan.n_tokens,), dtype=f32, device=dev)
-    _need(logp, "logp", f32, dev)
-    _need_shape(logp, "logp", (plan.n_tokens,))
+    else:
+        _need(logp, "logp", f32, dev)
+        _need_shape(logp, "logp", (plan.n_tokens,))
     entropy = torch.empty(rows, dtype=f32, device=dev)
-    lse = torch.empty(rows, dtype=f32, device=dev)
+    lse = torch.empty_like(entropy)
     top_logp = torch.empty((rows, top_k), dtype=f32, device=dev) if top_k > 0 else None
     top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
     lib = load()
     workspace, ws_bytes = _workspace(workspace, int(lib.tree_logprobs_workspace_bytes(rows, vocab, top_k)), dev)
     dplan = plan.on_device(dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream(dev)
     p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
     _check(lib.tree_logprobs(logits.data_ptr(), tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                              p(top_logp), p(top_ids), ld, plan.n_tokens, int(first_row), rows, vocab, token_bytes,
@@ -748,13 +760,13 @@ def tree_logprobs_backward(logits, tokens, lse, entropy, dlogp, plan: TreePlan, 
         _need(entropy, "entropy", f32, dev)
         _need_shape(entropy, "entropy", (rows,))
     if out is None:
-        out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     elif out is not logits:
         _need(out, "out", logits.dtype, dev)
         _need_shape(out, "out", (rows, vocab))
     ldd = ld if out is logits else vocab
     dplan = plan.on_device(dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream(dev)
     p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
     _check(load().tree_logprobs_backward(logits.data_ptr(), tokens.data_ptr(), lse.data_ptr(),
                                          p(entropy) if dentropy is not None else None, dlogp.data_ptr(), p(dentropy),

@@ -75,7 +75,7 @@ struct AttnPlan {
   // Entries a trie may need at most: the run lists of all tiles together.
   static constexpr int64_t kMaxRuns = int64_t(1) << 26;
   // A cut of more parts is not made (the coarser ones have parts enough).
-  static constexpr int64_t kMaxParts = 1 << 16;
+  static constexpr int64_t kMaxParts = 1 << 12;
 
   std::vector<int32_t> mirror;  // device copy
   size_t m_d = 0, m_e = 0, m_runs = 0;
