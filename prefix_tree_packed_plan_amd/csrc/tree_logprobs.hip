@@ -52,6 +52,7 @@ struct Vec<uint16_t> {
   static __device__ __forceinline__ u32x4 pack(const float* x) {
     return u32x4{pk2(x[0], x[1]), pk2(x[2], x[3]), pk2(x[4], x[5]), pk2(x[6], x[7])};
   }
+  static __device__ __forceinline__ u32x4 none() { return u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
   static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
   static __device__ __forceinline__ void put(uint16_t* p, float x) { *p = static_cast<uint16_t>(pk2(x, x)); }
 };
@@ -65,6 +66,7 @@ struct Vec<float> {
   static __device__ __forceinline__ u32x4 pack(const float* x) {
     return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
   }
+  static __device__ __forceinline__ u32x4 none() { return u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}; }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
   static __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 };
@@ -124,6 +126,21 @@ __device__ __forceinline__ int token(const LogprobArgs& a, int t) {
   const int32_t x = static_cast<const int32_t*>(a.tokens)[t];
   return x >= 0 && x < a.vocab ? x : -1;
 }
+
+// Thread j's token behind the row, if there is one, and its logit: half a dozen
+// dependent loads.
+template <typename T>
+struct Ahead {
+  int t = -1, id = -1;
+  float x = 0.f;
+  __device__ __forceinline__ Ahead(const LogprobArgs& a, int lr, const Behind& b, int j) {
+    if (j < b.n) {
+      t = b.at(j);
+      id = token(a, t);
+      if (id >= 0) x = Vec<T>::one(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld + id);
+    }
+  }
+};
 
 // ---- the largest values of a row ------------------------------------------------
 // The k-th largest of the wave's 64 values (a bitonic sort).
@@ -270,16 +287,17 @@ struct Row {
 
 // Everything a row's sums decide but the list, by the threads tid, tid + nt, ...
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs& a, int lr, const Row<T>& row, const Behind& b, int tid,
-                                           int nt) {
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, int lr, const Row<T>& row, const Behind& b,
+                                           const Ahead<T>& first, int tid, int nt) {
   if (tid == 0) {
     a.lse[lr] = row.lse;
     a.entropy[lr] = row.entropy;
     if (b.root_start) a.logp[a.first_row + lr] = 0.f;
   }
-  for (int j = tid; j < b.n; j += nt) {
-    const int t = b.at(j), id = token(a, t);
-    a.logp[t] = id < 0 ? 0.f : row.logp(Vec<T>::one(row.x + id));
+  if (first.t >= 0) a.logp[first.t] = first.id < 0 ? 0.f : row.logp(first.x);
+  for (int j = tid + nt; j < b.n; j += nt) {
+    const Ahead<T> next(a, lr, b, j);
+    a.logp[next.t] = next.id < 0 ? 0.f : row.logp(next.x);
   }
 }
 template <typename T>
@@ -293,7 +311,7 @@ __device__ __forceinline__ float* part_lists(const LogprobArgs& a) {
   return a.part + int64_t(a.n_rows) * a.split * 4;
 }
 
-template <typename T, bool TOP>
+template <typename T, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   constexpr int N = Vec<T>::N, U = 4;
   __shared__ Sums sums[kThreads / 64];
@@ -344,15 +362,23 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
       one(x, c0 + sl.head + (v + u * kThreads) * N);
     }
   }
-  // The last pieces, and the columns outside of them; lanes without one add
-  // -inf, which changes nothing.
+  // The last pieces, loaded together, and the columns outside of them; lanes
+  // without one add -inf, which changes nothing.
   const int turns = (sl.vecs - (v - tid) + kThreads - 1) / kThreads;
-  for (int i = 0; i < turns; ++i, v += kThreads) {
-    float x[N];
+  {
+    u32x4 w[U];
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = kNegInf;
-    if (v < sl.vecs) Vec<T>::unpack(__builtin_nontemporal_load(pv + v), x);
-    one(x, v < sl.vecs ? c0 + sl.head + v * N : kNoId);
+    for (int u = 0; u < U; ++u) {
+      w[u] = Vec<T>::none();
+      if (v + u * kThreads < sl.vecs) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u >= turns) break;
+      float x[N];
+      Vec<T>::unpack(w[u], x);
+      one(x, v + u * kThreads < sl.vecs ? c0 + sl.head + (v + u * kThreads) * N : kNoId);
+    }
   }
   if (wave == 0) {
     const int i = lane;
@@ -384,10 +410,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
       }
     }
   }
-  if (a.split == 1) {
+  if (!SPLIT) {
     const Behind b(a, a.first_row + lr, lane);
+    const Ahead<T> first(a, lr, b, tid);
     const Row<T> row(a, lr, z, lane);
-    finish_row<T>(a, lr, row, b, tid, kThreads);
+    finish_row<T>(a, lr, row, b, first, tid, kThreads);
     if (TOP && wave == 0) put_top<T>(a, lr, row, top, lane);
   } else {
     if (tid == 0) *reinterpret_cast<float4*>(a.part + int64_t(blockIdx.x) * 4) = make_float4(z.m, z.s, z.t, z.top);
@@ -401,17 +428,18 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
 template <typename T, bool TOP>
 __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
   const int lane = threadIdx.x, lr = blockIdx.x;
+  const Behind b(a, a.first_row + lr, lane);
+  const Ahead<T> first(a, lr, b, lane);
   Sums z{kNegInf, 0.f, 0.f, kNegInf};
   for (int i = lane; i < a.split; i += 64) {
     const float4 y = *reinterpret_cast<const float4*>(a.part + (int64_t(lr) * a.split + i) * 4);
     z = join(z, Sums{y.x, y.y, y.z, y.w});
   }
-  const Behind b(a, a.first_row + lr, lane);
 #pragma unroll
   for (int o = 32; o; o >>= 1)
     z = join(z, Sums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64), __shfl_xor(z.top, o, 64)});
   const Row<T> row(a, lr, z, lane);
-  finish_row<T>(a, lr, row, b, lane, 64);
+  finish_row<T>(a, lr, row, b, first, lane, 64);
   if constexpr (TOP) {
     TopList top(a.top_k);
     const float2* l = reinterpret_cast<const float2*>(part_lists(a)) + int64_t(lr) * a.split * a.top_k;
@@ -521,7 +549,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
 #pragma unroll
     for (int u = 0; u < U; ++u) one(w[u], v + u * kThreads);
   }
-  for (; v < sl.vecs; v += kThreads) one(__builtin_nontemporal_load(pv + v), v);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (v + u * kThreads < sl.vecs) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (v + u * kThreads < sl.vecs) one(w[u], v + u * kThreads);
   if (tid < sl.ends()) {
     const int col = sl.end_col(tid);
     const float x = Vec<T>::one(sl.p + col);
@@ -533,14 +566,13 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
 
 hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream) {
   const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
-  const bool top = a.top_k > 0;
-  if (dtype == TREE_DTYPE_BF16) {
-    if (top) logprobs_kernel<uint16_t, true><<<grid, block, 0, stream>>>(a);
-    else logprobs_kernel<uint16_t, false><<<grid, block, 0, stream>>>(a);
-  } else {
-    if (top) logprobs_kernel<float, true><<<grid, block, 0, stream>>>(a);
-    else logprobs_kernel<float, false><<<grid, block, 0, stream>>>(a);
-  }
+  const bool top = a.top_k > 0, split = a.split > 1;
+  const auto kernel = dtype == TREE_DTYPE_BF16
+                          ? (top ? (split ? logprobs_kernel<uint16_t, true, true> : logprobs_kernel<uint16_t, true, false>)
+                                 : (split ? logprobs_kernel<uint16_t, false, true> : logprobs_kernel<uint16_t, false, false>))
+                          : (top ? (split ? logprobs_kernel<float, true, true> : logprobs_kernel<float, true, false>)
+                                 : (split ? logprobs_kernel<float, false, true> : logprobs_kernel<float, false, false>));
+  kernel<<<grid, block, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split == 1) return e;
   const dim3 rows(a.n_rows);
