@@ -310,6 +310,55 @@ def test_attention_tokens_equal_their_own_path():
         assert np.all(np.abs(np64(alone) - np64(o[rows])) <= bound)
 
 
+def test_attention_rl_batch_beyond_32_bit_offsets():
+    """The RL batch trie (428,843 tokens), q, k, v cut from one 5.3 GB
+    projection: the last completion's outputs and gradients against the oracle
+    on its path alone (a leaf's dk, dv come from its own rows only); every value
+    finite."""
+    from workloads import make_trie
+    parents, lens, _ = make_trie(5)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    n, hq, hkv, d = int(off[-1]), 32, 8, 128
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    qkv = torch.empty((n, hq + 2 * hkv, d), dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    do = torch.empty((n, hq, d), dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    assert qkv.numel() * 2 > 1 << 32
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    say(f"attention rl_batch N={n}")
+    plan = ptp.tree_plan(parents, lens, 4)
+    o, lse = ptp.tree_attention(q, k, v, plan, return_lse=True)
+    torch.cuda.synchronize()
+    say("  forward done")
+    dq, dk, dv = ptp.tree_attention_backward(q, k, v, o, lse, do, plan)
+    torch.cuda.synchronize()
+    for t in (o, lse, dq, dk, dv):
+        assert torch.isfinite(t).all()
+    leaf = len(lens) - 1
+    path, s = [], leaf
+    while s >= 0:
+        path.insert(0, s)
+        s = int(parents[s])
+    rows = torch.cat([torch.arange(int(off[s]), int(off[s + 1]), device=DEV) for s in path])
+    m = int(lens[leaf])
+    for hk in (0, 7):
+        h = slice(4 * hk, 4 * hk + 2)  # two query heads of the group: dq, o; dk, dv need all four
+        ref = tree_attention_reference([-1], [len(rows)], np64(q[rows, h]), np64(k[rows, hk:hk + 1]),
+                                       np64(v[rows, hk:hk + 1]), d ** -0.5, do=np64(do[rows, h]))
+        for name, t in (("o", o), ("lse", lse), ("dq", dq)):
+            check(name, t[rows[-m:], h], tuple(x[-m:] for x in ref[name]))
+    own = rows[-m:]
+    grads = [np.zeros((m, d)) for _ in range(4)]
+    for h in range(28, 32):
+        ref = tree_attention_reference([-1], [len(rows)], np64(q[rows, h:h + 1]), np64(k[rows, 7:8]),
+                                       np64(v[rows, 7:8]), d ** -0.5, do=np64(do[rows, h:h + 1]))
+        for i, name in enumerate(("dk", "dv")):
+            grads[i] += ref[name][0][-m:, 0]
+            grads[2 + i] += ref[name][1][-m:, 0]
+    check("dk", dk[own, 7], (grads[0], grads[2]))
+    check("dv", dv[own, 7], (grads[1], grads[3]))
+
+
 def test_attention_refusals():
     """Misuse raises on the host; nothing is launched."""
     parents, lens = [-1, 0], [20, 12]

@@ -247,6 +247,32 @@ def test_logprobs_in_a_graph():
         assert all(torch.equal(p, q) for p, q in zip(r, gr)) and torch.equal(d, gd)
 
 
+def test_logprobs_beyond_32_bit_offsets():
+    """36,000 rows of 131,072 columns (9.4 GB): the last rows against the oracle,
+    the gradient written over the logits."""
+    n, vocab, last = 36_000, 131_072, 6
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(4)
+    x = torch.empty((n, vocab), dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    tok = torch.randint(0, vocab, (n,), generator=gen, device=DEV)
+    dlogp = torch.randn(n, generator=gen, device=DEV)
+    dent = torch.randn(n, generator=gen, device=DEV) * 0.1
+    plan = ptp.tree_plan([-1, 0], [n - last, last], 4)
+    say("logprobs 36000 x 131072")
+    r = ptp.tree_logprobs(x, tok, plan, top_k=3)
+    tail = np64(x[-last:])
+    d = ptp.tree_logprobs_backward(x, tok, r.lse, r.entropy, dlogp, plan, dentropy=dent, out=x)
+    torch.cuda.synchronize()
+    ref = tree_logprobs_reference([-1], [last], tail, tok[-last:].cpu().numpy(), 1.0, 3)
+    check("logp", r.logp[-last + 1:], ref["logp"][0][1:], ref["logp"][1][1:])
+    check("entropy", r.entropy[-last:], *ref["entropy"])
+    assert np.array_equal(r.top_ids[-last:].cpu().numpy(), ref["top_ids"][0])
+    want, bound = tree_logprobs_backward_reference([-1], [last], tail, tok[-last:].cpu().numpy(), np64(dlogp[-last:]),
+                                                   np64(dent[-last:]), 1.0, U[torch.bfloat16])
+    check("dlogits", d[-last:], want, bound)
+    assert torch.isfinite(r.logp).all() and d is x
+
+
 def test_logprobs_refusals():
     x, tok, dlogp, dent = inputs(22, 100, torch.bfloat16)
     plan = ptp.tree_plan(*TRIE, 4)
