@@ -486,6 +486,23 @@ __device__ __forceinline__ void store_row(T* p, const f32x16* acc, float f, int 
   }
 }
 
+// ---- work-groups to XCDs ---------------------------------------------------------
+// Consecutive work-groups go to the 8 XCDs in turn, each with an L2 of its own.
+// The query heads of one key/value head and tile, which read the same keys and
+// values, are therefore 8 apart.
+constexpr int kXcds = 8;
+__device__ __forceinline__ bool work_of(const AttnArgs& a, int block, int* item, int* h, int* hk) {
+  const int group = a.h_q / a.h_kv, slot = block / kXcds;
+  const int u = slot / group * kXcds + block % kXcds;  // tile part and key/value head
+  *item = u / a.h_kv;
+  *hk = u % a.h_kv;
+  *h = *hk * group + slot % group;
+  return *item < a.n_items;
+}
+inline dim3 work_grid(const AttnArgs& a) {
+  return dim3((a.n_items * a.h_kv + kXcds - 1) / kXcds * kXcds * (a.h_q / a.h_kv));
+}
+
 // ---- parts of a list --------------------------------------------------------------
 // What a work-group leaves of its part (floats): the forward's unnormalised
 // output rows, then every row's maximum and sum; rows of dq; rows of dk, then
@@ -539,8 +556,9 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
   __shared__ FwdSmem<T, D> sm;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.x % a.h_q, hk = h / (a.h_q / a.h_kv);
-  const AttnItem it = a.items[blockIdx.x / a.h_q];
+  int item, h, hk;
+  if (!work_of(a, blockIdx.x, &item, &h, &hk)) return;
+  const AttnItem it = a.items[item];
   const int64_t row = int64_t(it.tile) * kQTile + 32 * wave + (lane & 31);
   const bool on = row < a.n_tok;
   const int64_t r = on ? row : a.n_tok - 1;
@@ -713,8 +731,9 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
   __shared__ FwdSmem<T, D> sm;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.x % a.h_q, hk = h / (a.h_q / a.h_kv);
-  const AttnItem it = a.items[blockIdx.x / a.h_q];
+  int item, h, hk;
+  if (!work_of(a, blockIdx.x, &item, &h, &hk)) return;
+  const AttnItem it = a.items[item];
   const int64_t row = int64_t(it.tile) * kQTile + 32 * wave + (lane & 31);
   const bool on = row < a.n_tok;
   const int64_t r = on ? row : a.n_tok - 1;
@@ -1074,7 +1093,7 @@ hipError_t launch_attention(const AttnArgs& a, int d, int dtype, hipStream_t str
   return dispatch(d, dtype, [&](auto t, auto dd) {
     using T = decltype(t);
     constexpr int D = decltype(dd)::value;
-    attn_fwd_kernel<T, D><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
+    attn_fwd_kernel<T, D><<<work_grid(a), 256, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.n_join > 0) {
       attn_fwd_join_kernel<T, D><<<dim3(a.n_join, a.h_q, kQTile / kJoinRows), kJoinRows * D / 4, 0, stream>>>(a);
@@ -1088,7 +1107,7 @@ hipError_t launch_attention_dq(const AttnArgs& a, int d, int dtype, hipStream_t 
   return dispatch(d, dtype, [&](auto t, auto dd) {
     using T = decltype(t);
     constexpr int D = decltype(dd)::value;
-    attn_dq_kernel<T, D><<<dim3(a.n_items * a.h_q), 256, 0, stream>>>(a);
+    attn_dq_kernel<T, D><<<work_grid(a), 256, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.n_join > 0) {
       attn_grad_join_kernel<T, D, true>
