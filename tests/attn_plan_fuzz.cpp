@@ -87,7 +87,13 @@ static void check(const std::vector<int32_t>& parents, const std::vector<int32_t
         CHECK(it.tile >= 0 && it.tile < l.n_tiles && it.n_runs > 0, "tile %d", it.tile);
         CHECK(it.part >= 0 && it.part < c.n_items && part_tile[it.part] < 0, "part %d", it.part);
         CHECK(it.v0 >= 0 && it.v0 < it.v1 && it.v1 <= it.n_total, "tile %d", it.tile);
-        CHECK(t == 0 || it.v1 - it.v0 <= items[t - 1].v1 - items[t - 1].v0, "longest first");
+        const auto rank = [&](const AttnItem& x) {  // whole length, or its power of 2 where there are many
+          int len = x.v1 - x.v0, r = 0;
+          if (c.n_items <= 1024) return len;
+          while (len >>= 1) ++r;
+          return r;
+        };
+        CHECK(t == 0 || rank(it) <= rank(items[t - 1]), "longest first");
         CHECK(it.v0 % 64 == 0 && (it.v1 % 64 == 0 || it.v1 == it.n_total) && it.v1 - it.v0 <= c.most, "part of %d",
               it.tile);
         longest = std::max(longest, it.v1 - it.v0);
