@@ -494,7 +494,8 @@ size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_
  *
  * j over that path.  Query head h uses key/value head h / (h_q / h_kv).
  * A token that is not on the path has no influence, whatever it holds
- * (infinities and NaN included).
+ * (infinities and NaN included).  A visible value of v that is not finite
+ * reaches an output through probabilities that do not underflow.
  *
  * q      device, [n_tokens, h_q, d], dtype                (read)
  * k, v   device, [n_tokens, h_kv, d], dtype               (read)
@@ -504,7 +505,7 @@ size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_
  *        k and v, >= 0 (a head's d elements are contiguous; slices of one
  *        projection's output and head-major tensors need no copy), or NULL:
  *        all contiguous.  Pointers, rows and heads start on 16 bytes.
- * scale  > 0 and finite (1 / sqrt(d) as a rule).
+ * scale  in 1e-30 .. 1e30 (1 / sqrt(d) as a rule).
  * dtype  TREE_DTYPE_BF16 (bf16 MFMA; scores, maxima, sums and the output's
  *        accumulation in fp32, probabilities rounded to bf16 for their
  *        product with v) or TREE_DTYPE_F32 (fp32 MFMA throughout).
@@ -545,7 +546,9 @@ size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* apla
  * strides    host, [5][2], of q, k, v, o and dout, or NULL, as above
  * ws         device workspace, ws_bytes >= tree_attention_backward_workspace_bytes.
  * Everything else as for tree_attention; ds and p are rounded to bf16 for
- * their products under TREE_DTYPE_BF16.
+ * their products under TREE_DTYPE_BF16.  A token whose q, dout or o is not
+ * finite may make dk and dv of the tokens it sees NaN throughout, one whose k
+ * is not finite dq of those that see it; no others.
  * Errors: as tree_attention.
  */
 int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -586,11 +589,14 @@ size_t tree_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_
  * top_logp, top_id  device, [n_rows, top_k] fp32 and int32 (NULL if top_k =
  *          0): the top_k most likely tokens, best first, the lowest index
  *          first among equal logits                      (written)
- * temperature  > 0 and finite.   0 <= top_k <= min(vocab, TREE_MAX_TOP_K).
+ * temperature  in 1e-30 .. 1e30.   0 <= top_k <= min(vocab, TREE_MAX_TOP_K).
  * A row of nothing but -inf has lse -inf, entropy 0 and log probabilities
  * -inf.  A NaN or +inf makes its row's sums NaN; a NaN logit is never among
  * the top_k (missing entries have id -1).
  * Arithmetic in fp32, relative to a reference value near the row's maximum.
+ * Values so low that x / (temperature ln 2) overflows (masks of the type's
+ * lowest value) count as -inf, unless the row has no larger one: then its
+ * largest values share the probability.
  * dplan, dplan_bytes  device copy of `plan`, as for tree_conv.
  * Errors: INVALID_ARG, SIZE, WORKSPACE, HIP.
  */

@@ -89,7 +89,11 @@ int check_dplan(const tree_attention_plan_t* aplan, const void* dplan, size_t dp
               fn, dplan);
 }
 
-bool positive(float x) { return std::isfinite(x) && x > 0.f; }
+// A factor whose products with log2(e) and with fp32 values of ordinary size
+// neither overflow nor vanish.
+bool ordinary(float x) { return x >= 1e-30f && x <= 1e30f; }
+// Work-groups of 256 a launch may have (its work items are counted in 32 bits).
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 64;
 
 // Sizes, head layout and scale of an attention call.
 int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale,
@@ -103,9 +107,9 @@ int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_
     return fail(TREE_ERR_UNSUPPORTED, "%s: h_q %d is not a multiple of h_kv %d", fn, h_q, h_kv);
   if (!tg::attention_supported(d, dtype))
     return fail(TREE_ERR_UNSUPPORTED, "%s: d=%d dtype=%d not compiled in", fn, d, dtype);
-  if (!positive(scale)) return fail(TREE_ERR_INVALID_ARG, "%s: scale must be > 0 and finite", fn);
+  if (!ordinary(scale)) return fail(TREE_ERR_INVALID_ARG, "%s: scale must be in 1e-30..1e30", fn);
   // Grids: parts x heads; and heads along the join launches' second axis.
-  if (h_q > 65535 || (static_cast<int64_t>(p.q.n_tiles) + tg::AttnPlan::kMaxParts) * h_q >= (int64_t(1) << 31))
+  if (h_q > 65535 || (static_cast<int64_t>(p.q.n_tiles) + tg::AttnPlan::kMaxParts) * h_q > kMaxGroups)
     return fail(TREE_ERR_UNSUPPORTED, "%s: too many heads (%d) for %d tiles", fn, h_q, p.q.n_tiles);
   return TREE_OK;
 }
@@ -200,9 +204,7 @@ int check_logprobs(const tg::Plan& p, int64_t ld, int64_t n_tokens, int32_t firs
     return fail(TREE_ERR_INVALID_ARG, "%s: rows %lld elements apart hold %d", fn, static_cast<long long>(ld), vocab);
   if (token_bytes != 4 && token_bytes != 8)
     return fail(TREE_ERR_INVALID_ARG, "%s: token_bytes must be 4 or 8 (got %d)", fn, token_bytes);
-  if (!positive(temperature)) return fail(TREE_ERR_INVALID_ARG, "%s: temperature must be > 0 and finite", fn);
-  if (!positive(1.f / temperature))
-    return fail(TREE_ERR_INVALID_ARG, "%s: 1 / temperature must be > 0 and finite", fn);
+  if (!ordinary(temperature)) return fail(TREE_ERR_INVALID_ARG, "%s: temperature must be in 1e-30..1e30", fn);
   if (!dtype_ok(dtype)) return fail(TREE_ERR_INVALID_ARG, "%s: bad dtype %d", fn, dtype);
   return TREE_OK;
 }
@@ -1018,8 +1020,6 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
   if (const int rc = check_dplan(plan, dplan, dplan_bytes, fn)) return rc;
   const int32_t* base = static_cast<const int32_t*>(dplan);
   const Spread s = logprob_backward_spread(n_rows, vocab, dtype);
-  if (static_cast<int64_t>(n_rows) * s.split >= (int64_t(1) << 31))
-    return fail(TREE_ERR_INVALID_ARG, "%s: %d rows of %d columns are too many for one call", fn, n_rows, vocab);
   tg::LogprobArgs a{};
   a.logits = logits;
   a.ld = ld;

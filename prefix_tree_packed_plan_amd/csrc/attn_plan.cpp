@@ -115,8 +115,8 @@ const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int3
                           int32_t* split) {
   if (split) *split = 1;
   const AttnCut& whole = l.cuts.front();
-  const int64_t room = l.total * heads * steps;  // of kSlots slots
-  const auto fits = [&](int64_t len, bool uncut) { return 4 * len * kSlots <= (uncut ? 4 : 3) * room; };
+  const double room = double(l.total) * heads * steps / kSlots;  // of a slot
+  const auto fits = [&](int64_t len, bool uncut) { return double(len) <= (uncut ? 1.0 : 0.75) * room; };
   for (size_t i = 0; i < l.cuts.size(); ++i) {
     const AttnCut& c = l.cuts[i];
     const bool last = i + 1 == l.cuts.size() || l.cuts[i + 1].most < least;

@@ -564,33 +564,63 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
 
 }  // namespace
 
-hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
-  const bool top = a.top_k > 0, split = a.split > 1;
-  const auto kernel = dtype == TREE_DTYPE_BF16
-                          ? (top ? (split ? logprobs_kernel<uint16_t, true, true> : logprobs_kernel<uint16_t, true, false>)
-                                 : (split ? logprobs_kernel<uint16_t, false, true> : logprobs_kernel<uint16_t, false, false>))
-                          : (top ? (split ? logprobs_kernel<float, true, true> : logprobs_kernel<float, true, false>)
-                                 : (split ? logprobs_kernel<float, false, true> : logprobs_kernel<float, false, false>));
-  kernel<<<grid, block, 0, stream>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.split == 1) return e;
-  const dim3 rows(a.n_rows);
-  if (dtype == TREE_DTYPE_BF16) {
-    if (top) logprobs_join_kernel<uint16_t, true><<<rows, 64, 0, stream>>>(a);
-    else logprobs_join_kernel<uint16_t, false><<<rows, 64, 0, stream>>>(a);
-  } else {
-    if (top) logprobs_join_kernel<float, true><<<rows, 64, 0, stream>>>(a);
-    else logprobs_join_kernel<float, false><<<rows, 64, 0, stream>>>(a);
+namespace {
+
+// Calls f on as many rows at a time as one launch may have work-groups (its
+// work items are counted in 32 bits).
+template <typename F>
+hipError_t by_rows(const LogprobArgs& a, int dtype, F f) {
+  const int64_t size = dtype == TREE_DTYPE_BF16 ? 2 : 4, most = ((int64_t(1) << 24) - 64) / a.split;
+  for (int64_t r = 0; r < a.n_rows; r += most) {
+    LogprobArgs b = a;
+    const int64_t n = a.n_rows - r < most ? a.n_rows - r : most;
+    b.n_rows = static_cast<int32_t>(n);
+    b.first_row = static_cast<int32_t>(a.first_row + r);
+    b.logits = static_cast<const char*>(a.logits) + r * a.ld * size;
+    b.entropy = a.entropy ? a.entropy + r : nullptr;
+    b.lse = a.lse ? a.lse + r : nullptr;
+    b.top_logp = a.top_logp ? a.top_logp + r * a.top_k : nullptr;
+    b.top_id = a.top_id ? a.top_id + r * a.top_k : nullptr;
+    b.dentropy = a.dentropy ? a.dentropy + r : nullptr;
+    b.lse_in = a.lse_in ? a.lse_in + r : nullptr;
+    b.entropy_in = a.entropy_in ? a.entropy_in + r : nullptr;
+    b.dlogits = a.dlogits ? static_cast<char*>(a.dlogits) + r * a.ldd * size : nullptr;
+    const hipError_t e = f(b);
+    if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
-hipError_t launch_logprobs_backward(const LogprobArgs& a, int dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
-  if (dtype == TREE_DTYPE_BF16) logprobs_backward_kernel<uint16_t><<<grid, block, 0, stream>>>(a);
-  else logprobs_backward_kernel<float><<<grid, block, 0, stream>>>(a);
-  return hipGetLastError();
+}  // namespace
+
+hipError_t launch_logprobs(const LogprobArgs& args, int dtype, hipStream_t stream) {
+  return by_rows(args, dtype, [&](const LogprobArgs& a) {
+    const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
+    const bool top = a.top_k > 0, split = a.split > 1;
+    const auto kernel =
+        dtype == TREE_DTYPE_BF16
+            ? (top ? (split ? logprobs_kernel<uint16_t, true, true> : logprobs_kernel<uint16_t, true, false>)
+                   : (split ? logprobs_kernel<uint16_t, false, true> : logprobs_kernel<uint16_t, false, false>))
+            : (top ? (split ? logprobs_kernel<float, true, true> : logprobs_kernel<float, true, false>)
+                   : (split ? logprobs_kernel<float, false, true> : logprobs_kernel<float, false, false>));
+    kernel<<<grid, block, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !split) return e;
+    const auto join = dtype == TREE_DTYPE_BF16
+                          ? (top ? logprobs_join_kernel<uint16_t, true> : logprobs_join_kernel<uint16_t, false>)
+                          : (top ? logprobs_join_kernel<float, true> : logprobs_join_kernel<float, false>);
+    join<<<dim3(a.n_rows), 64, 0, stream>>>(a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_logprobs_backward(const LogprobArgs& args, int dtype, hipStream_t stream) {
+  return by_rows(args, dtype, [&](const LogprobArgs& a) {
+    const dim3 grid(static_cast<uint32_t>(a.n_rows) * a.split), block(kThreads);
+    if (dtype == TREE_DTYPE_BF16) logprobs_backward_kernel<uint16_t><<<grid, block, 0, stream>>>(a);
+    else logprobs_backward_kernel<float><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace tg

@@ -52,7 +52,7 @@ def test_attention_refusals_need_no_device():
     assert call(n=229) == -3
     assert call(hq=0) == -1 and call(hkv=0) == -1 and call(d=0) == -1 and call(dtype=2) == -1
     assert call(hq=3) == -4 and call(d=48) == -4 and call(d=256) == -4
-    for scale in (0.0, -0.1, NAN, INF):
+    for scale in (0.0, -0.1, NAN, INF, 1e-31, 1e31):
         assert call(scale=scale) == -1
     ok = [512, 128, 256, 128, 256, 128]
     assert call(st=strides(ok)) == -1 and b"not an upload" in lib.tree_last_error()
@@ -141,7 +141,7 @@ def test_logprobs_refusals_need_no_device():
     assert call(n=229) == -3
     assert call(first=-1) == -1 and call(first=1) == -1 and call(rows=0) == -1 and call(rows=231) == -1
     assert call(vocab=0) == -1 and call(ld=4999) == -1 and call(tb=2) == -1 and call(dtype=7) == -1
-    for t in (0.0, -1.0, NAN, INF):
+    for t in (0.0, -1.0, NAN, INF, 1e-31, 1e31):
         assert call(temp=t) == -1
     assert call(k=-1) == -1 and call(k=65) == -1 and call(vocab=4, ld=4, k=5) == -1
     assert call(ws=None) == -5 and call(ws_bytes=need - 1) == -5 and call(bytes=8) == -5

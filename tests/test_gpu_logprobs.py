@@ -273,6 +273,32 @@ def test_logprobs_beyond_32_bit_offsets():
     assert torch.isfinite(r.logp).all() and d is x
 
 
+def test_logprobs_more_rows_than_one_launch_takes():
+    """17 million rows of 4 columns, forward and backward, against torch in
+    fp64 on the same device."""
+    n, vocab = 17_000_000, 4
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    x = torch.empty((n, vocab), device=DEV).normal_(generator=gen)
+    tok = torch.randint(0, vocab, (n,), generator=gen, device=DEV, dtype=torch.int32)
+    g = torch.empty(n, device=DEV).normal_(generator=gen)
+    plan = ptp.tree_plan([-1], [n], 4)
+    say("logprobs 17000000 x 4")
+    r = ptp.tree_logprobs(x, tok, plan, top_k=1)
+    d = ptp.tree_logprobs_backward(x, tok, r.lse, None, g, plan)
+    torch.cuda.synchronize()
+    ls = x.double().log_softmax(-1)
+    bound = 200 * 2.0 ** -24  # a few roundings of values below 12
+    want = torch.cat([ls.new_zeros(1), ls[:-1].gather(1, tok[1:, None].long())[:, 0]])
+    assert (r.logp - want).abs().max() <= bound
+    assert (r.entropy + (ls.exp() * ls).sum(-1)).abs().max() <= bound
+    assert torch.equal(r.top_ids[:, 0].long(), x.argmax(-1))
+    gd = torch.cat([g[1:].double(), g.new_zeros(1).double()])[:, None]
+    one = torch.zeros_like(ls)
+    one[:-1].scatter_(1, tok[1:, None].long(), 1.0)
+    assert ((d - gd * (one - ls.exp())).abs() <= bound * (1 + gd.abs())).all()
+
+
 def test_logprobs_refusals():
     x, tok, dlogp, dent = inputs(22, 100, torch.bfloat16)
     plan = ptp.tree_plan(*TRIE, 4)
