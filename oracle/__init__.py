@@ -22,6 +22,11 @@ root-to-leaf path produces.  So the oracle simply runs each path on its own:
 * ssd.py   -- token-by-token Mamba2 (SSD) recurrence over every path, the
               forked state of the tree Mamba2 forward.
 
+* attention.py -- softmax attention of every segment over its own path's keys,
+              its gradients, and bounds on the error of given roundings.
+* logprobs.py -- log probabilities under the row in front of each token on
+              its path, entropies, largest entries, the logits' gradient.
+
 Arithmetic is fp64 by default.  Parity status of every function is pinned by
 tests (see tests/test_oracle_*.py); nothing here is "parity unpinned".
 """

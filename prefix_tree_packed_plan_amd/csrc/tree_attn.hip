@@ -104,7 +104,7 @@ struct Cfg {
 };
 
 // Fragment s of 32 accumulator rows as the B operand of the next product
-// (bf16: rounded to nearest even, at most 2^-9 of the value).
+// (bf16: rounded to nearest even, at most 2^-8 of the value).
 template <typename T>
 __device__ __forceinline__ uint4 frag(const f32x16& p, int s);
 template <>
@@ -549,7 +549,17 @@ __device__ __forceinline__ void span(int dq, int& lo, int& hi) {
   hi = __builtin_amdgcn_readfirstlane(hi);
 }
 
-// One work-group of four waves: kQTile rows of one query head, 32 a wave.
+// One work-group of four waves: kQTile rows of one query head, 32 a wave; two
+// work-groups a CU (96 registers of queries and sums at d = 128, 65 KB of LDS).
+// What bounds it is issue: 64 keys are 32 MFMA (1024 cycles of a SIMD) and
+// about 200 vector instructions, 32 of them exponentials, of which the SIMD's
+// other wave covers a part; both units are busy 45% of the time, LDS reads
+// have no conflicts, and the keys come out of L2.  More rows a wave would halve
+// the LDS reads, which are not the bound, and need twice the registers; blocks
+// of 32 keys, one's exponentials between the other's products, cost 3%.
+// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 554 us (970 TFLOP/s; a large
+// matrix product reaches 1359 there); 10240 tokens of 16 responses, 16/4 heads,
+// 229 us; d = 64, 13941 tokens, 12/4 heads: 59 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -690,7 +700,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
 }
 
 // The output of a query tile from its parts, in their order: 16 rows a
-// work-group.
+// work-group, bound by memory (the parts are written and read once, in fp32).
 template <typename T, int D>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attn_fwd_join_kernel(AttnArgs a) {
   const int h = blockIdx.y, key = kJoinRows * blockIdx.z + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
@@ -724,7 +734,11 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attn_fwd_join_kernel(AttnAr
 
 // ---- gradient of q -----------------------------------------------------------------
 // Same tiles as the forward; also leaves -delta and -lse / scale, which the
-// other gradients' sums start from.
+// other gradients' sums start from.  Three products and one exponential a pair:
+// the matrix units are busy 56% of the time (chain of 16383 tokens, 8/2 heads of
+// 128: 755 us).  S and dP are computed here and again for dk and dv, seven
+// products in all: a single pass of five would add to dq from every key tile,
+// by atomics in an order that changes, or keep a part per tile.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -882,7 +896,13 @@ struct BwdSmem {
 
 // One work-group of four waves: kKTile keys of one key/value head, 32 a wave,
 // over this item's part of the rows that see them and every split-th query
-// head of the group.
+// head of the group.  K and V of a wave's keys and both sums stay in registers
+// (192 of 256 at d = 128); rows of q and dO pass through LDS, each read twice:
+// by rows for S and dP, transposed for dv and dk.  What bounds it are those reads
+// between the products, two or three in flight being all that the registers
+// leave: matrix units 49% busy, chain of 16383 tokens, 8/2 heads of 128: 1084 us.
+// 64 keys a wave at one wave a SIMD spilled (7.6 ms); an order left to the
+// compiler took 1849 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -1037,7 +1057,8 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
 }
 
 // A tile's gradients (dq, or dk and dv) from its parts, in their order: 16 rows
-// a work-group.
+// a work-group, bound by memory (25 us on a chain of 16383 tokens, 8/2 heads of
+// 128).
 template <typename T, int D, bool DQ>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attn_grad_join_kernel(AttnArgs a) {
   const int heads = DQ ? a.h_q : a.h_kv, h = blockIdx.y;

@@ -311,6 +311,13 @@ __device__ __forceinline__ float* part_lists(const LogprobArgs& a) {
   return a.part + int64_t(a.n_rows) * a.split * 4;
 }
 
+// One work-group a row, or a slice of one (SPLIT: `split` slices a row, where
+// rows alone do not fill the card), U 16-byte non-temporal loads in flight a
+// thread.  8192 x 131072 bf16: 324 us, 6.6 TB/s of reads, with the vector units
+// 82% busy (about 8 instructions an element): memory and issue are near their
+// ends together, which is why the sums take y from one fma and no maximum is
+// exchanged between lanes.  With 5 alternatives the insertions are what is left:
+// 4283 x 50001 bf16, 98 us against 73 without.
 template <typename T, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   constexpr int N = Vec<T>::N, U = 4;
@@ -455,6 +462,11 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
 // ---- backward ---------------------------------------------------------------------
 constexpr int kListed = 512;  // tokens behind a row that are kept in LDS
 
+// One slice of a row a work-group, read and written once: 8192 x 131072 bf16 in
+// 701 us, 1685 x 50001 fp32 in 117 us (6.1 and 5.7 TB/s).  Slices of 16 KB, so
+// that work-groups that run together stream through neighbouring memory: whole
+// rows took 819 us, 64 KB 778, 32 KB 744.  The pieces that hold a token behind
+// the row are marked in a bitmap, so that the others cost nothing for it.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a) {
   constexpr int N = Vec<T>::N, U = 4;
