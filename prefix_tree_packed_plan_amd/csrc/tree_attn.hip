@@ -373,16 +373,27 @@ __device__ __forceinline__ void dma16(const void* src, char* lds) {
                : "s"(lds_at(lds)), "v"(src)
                : "memory");
 }
-// From src + off, src the same for all lanes.
-__device__ __forceinline__ void dma16(const char* src, int off, char* lds) {
-  const uint64_t p = reinterpret_cast<uint64_t>(src);
-  const uint64_t u = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p)))) |
-                     uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p >> 32)))) << 32;
+// From src + off, src the same for all lanes; lds as an LDS address.
+__device__ __forceinline__ void dma16(uint64_t src, int off, uint32_t lds) {
   int m0;
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
                : "=&s"(m0)
-               : "s"(lds_at(lds)), "v"(off), "s"(u)
+               : "s"(lds), "v"(off), "s"(src)
                : "memory");
+}
+// The same of four sources, to LDS 4096 bytes apart.
+__device__ __forceinline__ void dma16x4(uint64_t s0, uint64_t s1, uint64_t s2, uint64_t s3, int off, uint32_t lds) {
+  int m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+      "s_add_u32 m0, m0, 0x1000\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %4\n\t"
+      "s_add_u32 m0, m0, 0x1000\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %5\n\t"
+      "s_add_u32 m0, m0, 0x1000\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %6\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(lds), "v"(off), "s"(s0), "s"(s1), "s"(s2), "s"(s3)
+      : "memory", "scc");
 }
 __device__ __forceinline__ void dma4(const void* src, char* lds) {
   int m0;
@@ -399,6 +410,29 @@ __device__ __forceinline__ void wait_dma() {
   asm volatile("" ::: "memory");
 }
 
+// The kRows rows from `first` on (lda bytes apart, lda < 2^24) into LDS tile ta,
+// this wave's groups of them: one base for all lanes, a group apart.  Every
+// instruction in front of a tile's products counts: with an address of their
+// own for each load, they took a tenth of the forward.
+template <typename T, int D>
+__device__ __forceinline__ void stage_run(int64_t first, const char* a, int64_t lda, char* ta, int wave, int lane) {
+  using C = Cfg<T, D>;
+  constexpr int PER = 1024 / C::RB;  // rows of a group
+  const uint32_t ld = uint32_t(lda), lds = lds_at(ta + 1024 * wave);
+  const uint64_t src = reinterpret_cast<uint64_t>(a) + uint64_t(uint32_t(first) + uint32_t(wave * PER)) * ld;
+  const uint64_t step = uint64_t(4 * PER) * ld;
+  const int r = wave * PER + lane / C::NC;
+  const auto off = [&](int i) {
+    return (lane / C::NC) * int(ld) + 16 * ((lane % C::NC) ^ swz<C::RB>(4 * PER % 16 ? r + 4 * PER * i : r));
+  };
+  if constexpr (C::NI == 4) {
+    dma16x4(src, src + step, src + 2 * step, src + 3 * step, off(0), lds);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) dma16(src + i * step, off(i), lds + 4096 * i);
+  }
+}
+
 // The 64 rows at virtual position v0 of two tensors (a head's first row at a,
 // b; bytes lda, ldb between rows) into LDS tiles ta, tb, by 4 waves (wave w:
 // every fourth group of 1024 bytes).  Rows of one run need no address
@@ -406,18 +440,13 @@ __device__ __forceinline__ void wait_dma() {
 // row of the tile (lane l: row l), used otherwise.
 template <typename T, int D>
 __device__ __forceinline__ void stage(const Cursor& cs, int v0, int row, const char* a, int64_t lda, char* ta,
-                                      const char* b, int64_t ldb, char* tb, int wave) {
+                                      const char* b, int64_t ldb, char* tb, int wave, int lane) {
   using C = Cfg<T, D>;
   constexpr int PER = 1024 / C::RB;  // rows of a group
-  const int lane = lane_id();
-  if (cs.whole(v0) && lda < (1 << 24) && ldb < (1 << 24)) {
+  if (cs.whole(v0) && uint64_t(lda) < (1 << 24) && uint64_t(ldb) < (1 << 24)) {
     const int64_t first = cs.row0 + (v0 - cs.virt);
-#pragma unroll
-    for (int i = 0; i < C::NI; ++i) {
-      const int g = 4 * i + wave, c = 16 * ((lane % C::NC) ^ swz<C::RB>(g * PER + lane / C::NC));
-      dma16(a + (first + g * PER) * lda, (lane / C::NC) * int(lda) + c, ta + 1024 * g);
-      dma16(b + (first + g * PER) * ldb, (lane / C::NC) * int(ldb) + c, tb + 1024 * g);
-    }
+    stage_run<T, D>(first, a, lda, ta, wave, lane);
+    stage_run<T, D>(first, b, ldb, tb, wave, lane);
   } else {
 #pragma unroll 1
     for (int i = 0; i < C::NI; ++i) {
@@ -580,7 +609,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     cs.seek(v0);
     const bool part = v0 + kRows > it.n_full;
     const int row = part || !cs.whole(v0) ? cs.row(v0, lane) : 0;
-    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave);
+    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
     if (part && wave < 2) {
       const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
@@ -621,12 +650,8 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     f32x16 p[2];
     if (!skip) {
       matrix_first(true);
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        p[kb] = zero16();
-#pragma unroll
-        for (int ks = 0; ks < C::NK; ++ks) p[kb] = mm<T>(rd.rows(kt, kb, ks), q[ks], p[kb]);
-      }
+      pipe<2 * C::NK, 3>([&](int i) { return rd.rows(kt, i & 1, i >> 1); },
+                       [&](int i, const uint4 x) { p[i & 1] = mm<T>(x, q[i >> 1], i < 2 ? zero16() : p[i & 1]); });
       matrix_first(false);
       if (masked) {
 #pragma unroll
@@ -759,7 +784,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
     cs.seek(v0);
     const bool part = v0 + kRows > it.n_full;
     const int row = part || !cs.whole(v0) ? cs.row(v0, lane) : 0;
-    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave);
+    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane_id());
     if (part && wave < 2) {
       const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
@@ -919,7 +944,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
     cs.seek(v0);
     const int lane = lane_id();
     const int row = cs.row(v0, lane);
-    stage<T, D>(cs, v0, row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave);
+    stage<T, D>(cs, v0, row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave, lane_id());
     const int64_t x = int64_t(row) * a.h_q + h;
     if (wave == 0) dma4(a.delta + int64_t(a.n_tok) * a.h_q + x, reinterpret_cast<char*>(sm.lse[buf]));
     else if (wave == 1) dma4(a.delta + x, reinterpret_cast<char*>(sm.delta[buf]));
