@@ -290,8 +290,9 @@ __device__ __forceinline__ void contract(f32x16 (&acc)[D / 32], const f32x16& w,
 }
 
 // use(i, load(i)) for i < N with the next F loads in flight, in exactly this
-// order: left to itself the compiler takes either one operand at a time
-// or more than the registers hold.
+// order: left to itself the compiler takes either one operand at a time (of the
+// forward's scores; three: chain of 16383 tokens 554 -> 535 us) or more than the
+// registers hold.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 template <int N, int F, typename Load, typename Use>
 __device__ __forceinline__ void pipe(Load load, Use use) {
@@ -412,8 +413,9 @@ __device__ __forceinline__ void wait_dma() {
 
 // The kRows rows from `first` on (lda bytes apart, lda < 2^24) into LDS tile ta,
 // this wave's groups of them: one base for all lanes, a group apart.  Every
-// instruction in front of a tile's products counts: with an address of their
-// own for each load, they took a tenth of the forward.
+// instruction in front of a tile's products counts: with each load's address
+// made by itself, the forward took 535 us instead of 519 (chain of 16383 tokens,
+// 8/2 heads of 128), and 217 instead of 201 (10240 tokens, 16/4 heads).
 template <typename T, int D>
 __device__ __forceinline__ void stage_run(int64_t first, const char* a, int64_t lda, char* ta, int wave, int lane) {
   using C = Cfg<T, D>;
@@ -467,7 +469,7 @@ __device__ __forceinline__ float half_swap(float x) {
 
 // A wave in its matrix products goes before one in its exponentials: the two
 // waves of a SIMD then take turns, and the matrix unit waits less (chain of
-// 16383 tokens, 8 heads of 128: 609 -> 567 us).
+// 16383 tokens, 8/2 heads of 128: 566 -> 536 us).
 __device__ __forceinline__ void matrix_first(bool on) {
   if (on) __builtin_amdgcn_s_setprio(1);
   else __builtin_amdgcn_s_setprio(0);
@@ -581,14 +583,17 @@ __device__ __forceinline__ void span(int dq, int& lo, int& hi) {
 // One work-group of four waves: kQTile rows of one query head, 32 a wave; two
 // work-groups a CU (96 registers of queries and sums at d = 128, 65 KB of LDS).
 // What bounds it is issue: 64 keys are 32 MFMA (1024 cycles of a SIMD) and
-// about 200 vector instructions, 32 of them exponentials, of which the SIMD's
-// other wave covers a part; both units are busy 45% of the time, LDS reads
-// have no conflicts, and the keys come out of L2.  More rows a wave would halve
-// the LDS reads, which are not the bound, and need twice the registers; blocks
-// of 32 keys, one's exponentials between the other's products, cost 3%.
-// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 554 us (970 TFLOP/s; a large
-// matrix product reaches 1359 there); 10240 tokens of 16 responses, 16/4 heads,
-// 229 us; d = 64, 13941 tokens, 12/4 heads: 59 us.
+// about 150 vector instructions, 32 of them exponentials (600 and more), of
+// which the SIMD's other wave covers a part: matrix units are busy 50%, vector
+// units 43% of the time; LDS reads have no conflicts and the keys come out of
+// L2.  Tried: the exponentials of a tile between the products of the next one's
+// scores, instruction by instruction, takes 15% longer (every wave then waits
+// in turn for each operand, product and exponential); so do blocks of 32 keys
+// (3%); the first values read before the exponentials, 1%.  More rows a wave
+// would halve the LDS reads and need twice the registers.
+// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 533 us (1030 TFLOP/s; a large
+// matrix product reaches 1371 there); 10240 tokens of 16 responses, 16/4 heads,
+// 206 us; d = 64, 13941 tokens, 12/4 heads: 58 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -760,8 +765,8 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attn_fwd_join_kernel(AttnAr
 // ---- gradient of q -----------------------------------------------------------------
 // Same tiles as the forward; also leaves -delta and -lse / scale, which the
 // other gradients' sums start from.  Three products and one exponential a pair:
-// the matrix units are busy 56% of the time (chain of 16383 tokens, 8/2 heads of
-// 128: 755 us).  S and dP are computed here and again for dk and dv, seven
+// the matrix units are busy 59% of the time (chain of 16383 tokens, 8/2 heads of
+// 128: 735 us).  S and dP are computed here and again for dk and dv, seven
 // products in all: a single pass of five would add to dq from every key tile,
 // by atomics in an order that changes, or keep a part per tile.
 template <typename T, int D>
@@ -925,7 +930,7 @@ struct BwdSmem {
 // (192 of 256 at d = 128); rows of q and dO pass through LDS, each read twice:
 // by rows for S and dP, transposed for dv and dk.  What bounds it are those reads
 // between the products, two or three in flight being all that the registers
-// leave: matrix units 49% busy, chain of 16383 tokens, 8/2 heads of 128: 1084 us.
+// leave: matrix units 55% busy, chain of 16383 tokens, 8/2 heads of 128: 1010 us.
 // 64 keys a wave at one wave a SIMD spilled (7.6 ms); an order left to the
 // compiler took 1849 us.
 template <typename T, int D>
