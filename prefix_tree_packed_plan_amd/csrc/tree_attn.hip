@@ -584,16 +584,17 @@ __device__ __forceinline__ void span(int dq, int& lo, int& hi) {
 // work-groups a CU (96 registers of queries and sums at d = 128, 65 KB of LDS).
 // What bounds it is issue: 64 keys are 32 MFMA (1024 cycles of a SIMD) and
 // about 150 vector instructions, 32 of them exponentials (600 and more), of
-// which the SIMD's other wave covers a part: matrix units are busy 50%, vector
-// units 43% of the time; LDS reads have no conflicts and the keys come out of
-// L2.  Tried: the exponentials of a tile between the products of the next one's
+// which the SIMD's other wave covers a part: matrix units are busy 56%, vector
+// units 47% of the time, at 1.8 GHz, the clock that the load leaves (20% fewer
+// cycles in the last steps took 7% less time); LDS reads have no conflicts and
+// the keys come out of L2.  Tried: the exponentials of a tile between the products of the next one's
 // scores, instruction by instruction, takes 15% longer (every wave then waits
 // in turn for each operand, product and exponential); so do blocks of 32 keys
 // (3%); the first values read before the exponentials, 1%.  More rows a wave
 // would halve the LDS reads and need twice the registers.
-// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 533 us (1030 TFLOP/s; a large
-// matrix product reaches 1371 there); 10240 tokens of 16 responses, 16/4 heads,
-// 206 us; d = 64, 13941 tokens, 12/4 heads: 58 us.
+// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 517 us (1063 TFLOP/s; a large
+// matrix product reaches 1336 there); 10240 tokens of 16 responses, 16/4 heads,
+// 207 us; d = 64, 13941 tokens, 12/4 heads: 56 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -777,7 +778,7 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attn_fwd_join_kernel(AttnAr
 // ---- gradient of q -----------------------------------------------------------------
 // Same tiles as the forward; also leaves -delta and -lse / scale, which the
 // other gradients' sums start from.  Three products and one exponential a pair:
-// the matrix units are busy 59% of the time (chain of 16383 tokens, 8/2 heads of
+// the matrix units are busy 60% of the time (chain of 16383 tokens, 8/2 heads of
 // 128: 735 us).  S and dP are computed here and again for dk and dv, seven
 // products in all: a single pass of five would add to dq from every key tile,
 // by atomics in an order that changes, or keep a part per tile.
