@@ -593,10 +593,10 @@ size_t tree_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t top_
  * A row of nothing but -inf has lse -inf, entropy 0 and log probabilities
  * -inf.  A NaN or +inf makes its row's sums NaN; a NaN logit is never among
  * the top_k (missing entries have id -1).
- * Arithmetic in fp32, relative to a reference value near the row's maximum.
- * Values so low that x / (temperature ln 2) overflows (masks of the type's
- * lowest value) count as -inf, unless the row has no larger one: then its
- * largest values share the probability.
+ * Arithmetic in fp32, relative to a value near the row's maximum (the maximum
+ * itself where |x| / (temperature ln 2) of it is above 2^22: such a row is read
+ * twice), so that masked values of any size, -1e9 or the type's lowest, take
+ * nothing from the others.  lse is held at the largest fp32 value.
  * dplan, dplan_bytes  device copy of `plan`, as for tree_conv.
  * Errors: INVALID_ARG, SIZE, WORKSPACE, HIP.
  */

@@ -14,7 +14,10 @@
 // 2^(M + 10), so nearly never), y = c x - M in one rounding, s = sum exp2(y)
 // and t = sum exp2(y) y; then lse = (M + log2 s) / log2(e), logp = (c x - M -
 // log2 s) / log2(e), H = (log2 s - t / s) / log2(e).  M being whole, changing it
-// is exact, and c's own rounding cancels in logp and H.
+// is exact, and c's own rounding cancels in logp and H.  M stays within +-2^22,
+// where c x rounded to fp32 still tells whole numbers apart: masked values far
+// below add 0.  A row whose largest c x lies outside (nothing but masked values,
+// or values of millions) is read a second time, relative to its largest x.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -34,6 +37,7 @@ using chunk::pk2;
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kFltMax = 3.40282347e38f;
 constexpr int kNoId = 0x7FFFFFFF;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -190,6 +194,12 @@ struct TopList {
   }
 };
 
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
 // ---- forward --------------------------------------------------------------------
 struct Sums {
   float m, s, t;  // M (-inf: nothing yet), sum of e = exp2(y), sum of e y
@@ -210,10 +220,28 @@ __device__ __forceinline__ Sums join(const Sums a, const Sums b) {
   return r;
 }
 
-// The M for values up to x: c x rounded to a whole number, finite for every
-// finite x.
+// The M for values up to x: c x rounded to a whole number, within +-kMostM.
+// Past 2^23 or so a rounded c x is off by more than exp2 allows.
+constexpr float kMostM = 4194304.f;
 __device__ __forceinline__ float whole(float x, float c) {
-  return x == kNegInf ? kNegInf : rintf(fminf(fmaxf(x * c, -3e38f), 3.4e38f));
+  return x == kNegInf ? kNegInf : rintf(fminf(fmaxf(x * c, -kMostM), kMostM));
+}
+// Whether a row's sums by M are none, because its largest value is outside
+// what M covers (+inf too: its row becomes NaN).
+__device__ __forceinline__ bool far(float top, float c) { return top != kNegInf && fabsf(top * c) > kMostM; }
+
+// The sums of such a row, y = c (x - top): this thread's share, columns tid,
+// tid + nt, ..
+template <typename T>
+__device__ __forceinline__ Sums far_sums(const T* x, int n, float top, float c, int tid, int nt) {
+  Sums z{0.f, 0.f, 0.f, top};
+#pragma unroll 4
+  for (int i = tid; i < n; i += nt) {
+    const float y = (Vec<T>::one(x + i) - top) * c, e = ex2(y);
+    z.s += e;
+    z.t = fmaf(e, fmaxf(y, -3.4e38f), z.t);  // e = 0 where y = -inf
+  }
+  return z;
 }
 template <typename T>
 struct Scan {
@@ -248,40 +276,31 @@ struct Scan {
   }
 };
 
-// Log probabilities of one row, from its sums.
+// Log probabilities of one row, from its sums (far_sums where `away`).
 template <typename T>
 struct Row {
-  const T* x;
-  float c, m, ls;     // ls: log2 of the sum of exponentials
+  float c, m, top, ls;  // ls: log2 of the sum of exponentials
   float entropy, lse;
-  bool empty;         // every logit is -inf
-  bool flat;          // c x overflows for the largest x already (a row of the type's lowest value)
-  float top;
-  // By a whole wave.
-  __device__ __forceinline__ Row(const LogprobArgs& a, int lr, const Sums z, int lane)
-      : x(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld), c(a.inv_t * kLog2e), m(z.m), top(z.top) {
+  bool empty;           // every logit is -inf
+  bool away;
+  __device__ __forceinline__ Row(const LogprobArgs& a, const Sums z, bool away_)
+      : c(a.inv_t * kLog2e), m(z.m), top(z.top), away(away_) {
     empty = z.s == 0.f && top == kNegInf;
-    flat = z.s == 0.f && !empty;
     ls = __log2f(z.s);
     lse = (m + ls) * kLn2;
-    entropy = (ls - z.t / z.s) * kLn2;
-    if (flat) {  // only the values equal to the largest count
-      int n = 0;
-      for (int i = lane; i < a.vocab; i += 64) n += Vec<T>::one(x + i) == top;
-#pragma unroll
-      for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
-      ls = __log2f(float(n));
+    if (away) {  // held at the type's largest value; a NaN stays one
       lse = fmaf(top, a.inv_t, ls * kLn2);
-      entropy = ls * kLn2;
+      lse = lse < -kFltMax ? -kFltMax : lse > kFltMax ? kFltMax : lse;
     }
+    entropy = (ls - z.t / z.s) * kLn2;
     if (empty) {
       lse = kNegInf;
       entropy = 0.f;
     }
   }
   __device__ __forceinline__ float logp(float v) const {
-    if (empty || flat) return empty || v != top ? kNegInf : -ls * kLn2;
-    return (fmaf(v, c, -m) - ls) * kLn2;
+    if (empty) return kNegInf;
+    return ((away ? (v - top) * c : fmaf(v, c, -m)) - ls) * kLn2;
   }
 };
 
@@ -420,7 +439,22 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   if (!SPLIT) {
     const Behind b(a, a.first_row + lr, lane);
     const Ahead<T> first(a, lr, b, tid);
-    const Row<T> row(a, lr, z, lane);
+    const bool away = far(z.top, sc.c);
+    if (away) {  // uniform over the work-group
+      z = far_sums<T>(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld, a.vocab, z.top, sc.c, tid, kThreads);
+      z.s = wave_sum(z.s);
+      z.t = wave_sum(z.t);
+      __syncthreads();  // sums has been read
+      if (lane == 0) sums[wave] = z;
+      __syncthreads();
+      z = sums[0];
+#pragma unroll
+      for (int w = 1; w < kThreads / 64; ++w) {
+        z.s += sums[w].s;
+        z.t += sums[w].t;
+      }
+    }
+    const Row<T> row(a, z, away);
     finish_row<T>(a, lr, row, b, first, tid, kThreads);
     if (TOP && wave == 0) put_top<T>(a, lr, row, top, lane);
   } else {
@@ -445,7 +479,14 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
 #pragma unroll
   for (int o = 32; o; o >>= 1)
     z = join(z, Sums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64), __shfl_xor(z.top, o, 64)});
-  const Row<T> row(a, lr, z, lane);
+  const float c = a.inv_t * kLog2e;
+  const bool away = far(z.top, c);
+  if (away) {
+    z = far_sums<T>(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld, a.vocab, z.top, c, lane, 64);
+    z.s = wave_sum(z.s);
+    z.t = wave_sum(z.t);
+  }
+  const Row<T> row(a, z, away);
   finish_row<T>(a, lr, row, b, first, lane, 64);
   if constexpr (TOP) {
     TopList top(a.top_k);
@@ -505,8 +546,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
     const int at = id - c0 - sl.head;
     if (id >= 0 && at >= 0 && at < sl.vecs * N) atomicOr(&flag[at / N >> 5], 1u << (at / N & 31));
   }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) g += __shfl_xor(g, o, 64);
+  g = wave_sum(g);
   if (lane == 0) wsum[wave] = g;
   __syncthreads();
   g = 0.f;
