@@ -411,7 +411,13 @@ __device__ __forceinline__ void wait_dma() {
   asm volatile("" ::: "memory");
 }
 
-// The kRows rows from `first` on (lda bytes apart, lda < 2^24) into LDS tile ta,
+// Whether rows so many bytes apart can be staged from one address (stage_run: a
+// lane's offset from it is below 16 of them, and a product in 32 bits).
+__device__ __forceinline__ bool one_base(int64_t lda, int64_t ldb) {
+  return uint64_t(lda) < (1 << 24) && uint64_t(ldb) < (1 << 24);
+}
+
+// The kRows rows from `first` on (lda bytes apart, one_base) into LDS tile ta,
 // this wave's groups of them: one base for all lanes, a group apart.  Every
 // instruction in front of a tile's products counts: with each load's address
 // made by itself, the forward took 535 us instead of 519 (chain of 16383 tokens,
@@ -437,15 +443,15 @@ __device__ __forceinline__ void stage_run(int64_t first, const char* a, int64_t 
 
 // The 64 rows at virtual position v0 of two tensors (a head's first row at a,
 // b; bytes lda, ldb between rows) into LDS tiles ta, tb, by 4 waves (wave w:
-// every fourth group of 1024 bytes).  Rows of one run need no address
-// arithmetic in the vector unit: all lanes share a base.  `row` is this lane's
-// row of the tile (lane l: row l), used otherwise.
+// every fourth group of 1024 bytes).  Where `run` (kRows rows of one run, and
+// one_base) no address arithmetic in the vector unit is needed: all lanes share
+// a base.  `row` is this lane's row of the tile (lane l: row l), used otherwise.
 template <typename T, int D>
-__device__ __forceinline__ void stage(const Cursor& cs, int v0, int row, const char* a, int64_t lda, char* ta,
-                                      const char* b, int64_t ldb, char* tb, int wave, int lane) {
+__device__ __forceinline__ void stage(bool run, const Cursor& cs, int v0, int row, const char* a, int64_t lda,
+                                      char* ta, const char* b, int64_t ldb, char* tb, int wave, int lane) {
   using C = Cfg<T, D>;
   constexpr int PER = 1024 / C::RB;  // rows of a group
-  if (cs.whole(v0) && uint64_t(lda) < (1 << 24) && uint64_t(ldb) < (1 << 24)) {
+  if (run) {
     const int64_t first = cs.row0 + (v0 - cs.virt);
     stage_run<T, D>(first, a, lda, ta, wave, lane);
     stage_run<T, D>(first, b, ldb, tb, wave, lane);
@@ -610,12 +616,13 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
   const char* kp = a.k.at(0, hk);
   const char* vp = a.v.at(0, hk);
 
+  const bool fast = one_base(a.k.row, a.v.row);
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int buf) {
     cs.seek(v0);
-    const bool part = v0 + kRows > it.n_full;
-    const int row = part || !cs.whole(v0) ? cs.row(v0, lane) : 0;
-    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
+    const bool part = v0 + kRows > it.n_full, run = fast && cs.whole(v0);
+    const int row = part || !run ? cs.row(v0, lane) : 0;
+    stage<T, D>(run, cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane);
     if (part && wave < 2) {
       const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
@@ -623,12 +630,6 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     }
   };
   fetch(it.v0, 0);
-  // Where the next tile is seen whole (so this one is, too) and goes on in the
-  // same run, it is staged behind this one's scores, whose products then start
-  // at once (chain of 16383 tokens, 8/2 heads of 128: 532 -> 504 us).  Any tile
-  // behind the scores: chain 513, but tiles with masked pairs then wait for their
-  // keys (220 short segments, 12/4 heads of 64: 56 -> 67 us).
-  const bool fast = uint64_t(a.k.row) < (1 << 24) && uint64_t(a.v.row) < (1 << 24);
 
   uint4 q[C::NK];
   load_frags<T, D>(q, a.q.at(r, h), half);
@@ -649,6 +650,11 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
     constexpr int buf = decltype(buffer)::value;
     wait_dma();
     __syncthreads();
+    // Where the next tile is seen whole (so this one is, too) and goes on in the
+    // same run, it is staged behind this one's scores, whose products then start
+    // at once (chain of 16383 tokens, 8/2 heads of 128: 532 -> 504 us).  Any tile
+    // behind the scores: chain 513, but tiles with masked pairs then wait for their
+    // keys (220 short segments, 12/4 heads of 64: 56 -> 67 us).
     const bool late = fast && v0 + 2 * kRows <= min(min(it.n_full, it.v1), cs.next);
     if (!late && v0 + kRows < it.v1) fetch(v0 + kRows, buf ^ 1);
     const char* kt = sm.k[buf];
@@ -797,12 +803,13 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dq_ker
   const char* kp = a.k.at(0, hk);
   const char* vp = a.v.at(0, hk);
 
+  const bool fast = one_base(a.k.row, a.v.row);
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int buf) {
     cs.seek(v0);
-    const bool part = v0 + kRows > it.n_full;
-    const int row = part || !cs.whole(v0) ? cs.row(v0, lane) : 0;
-    stage<T, D>(cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane_id());
+    const bool part = v0 + kRows > it.n_full, run = fast && cs.whole(v0);
+    const int row = part || !run ? cs.row(v0, lane) : 0;
+    stage<T, D>(run, cs, v0, row, kp, a.k.row, sm.k[buf], vp, a.v.row, sm.v[buf], wave, lane_id());
     if (part && wave < 2) {
       const int x = v0 + lane < cs.end ? row : a.n_tok;
       if (wave == 0) dma4(a.tok_d + x, reinterpret_cast<char*>(sm.d[buf]));
@@ -957,12 +964,14 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_dkv_ke
   const int group = a.h_q / a.h_kv;
   const int64_t r = min(int64_t(it.tile) * kKTile + 32 * wave + (lane & 31), int64_t(a.n_tok) - 1);
 
+  const bool fast = one_base(a.q.row, a.dout.row);
   Cursor cs(a.runs, it);
   auto fetch = [&](int v0, int h, int buf) {
     cs.seek(v0);
     const int lane = lane_id();
     const int row = cs.row(v0, lane);
-    stage<T, D>(cs, v0, row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row, sm.g[buf], wave, lane_id());
+    stage<T, D>(fast && cs.whole(v0), cs, v0, row, a.q.at(0, h), a.q.row, sm.q[buf], a.dout.at(0, h), a.dout.row,
+                sm.g[buf], wave, lane_id());
     const int64_t x = int64_t(row) * a.h_q + h;
     if (wave == 0) dma4(a.delta + int64_t(a.n_tok) * a.h_q + x, reinterpret_cast<char*>(sm.lse[buf]));
     else if (wave == 1) dma4(a.delta + x, reinterpret_cast<char*>(sm.delta[buf]));
