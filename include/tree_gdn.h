@@ -621,7 +621,9 @@ int tree_logprobs(const void* logits, const void* tokens, float* logp, float* en
  * dlogits    device, [n_rows, vocab], dtype, ldd elements between rows; may be
  *            `logits` itself (with ldd = ld)             (written)
  * A row of nothing but -inf gets a zero gradient.  p is recomputed from the
- * fp32 lse, to a relative error of about 2^-24 (|lse| + |log p|).
+ * fp32 lse, to a relative error of about 2^-24 (|lse| + |log p|); where |lse| is
+ * 2^14 or more (rows of nothing but large masked values among them) the row is
+ * read three times, and p taken relative to its largest logit.
  * Errors: INVALID_ARG, SIZE, WORKSPACE, HIP.
  */
 int tree_logprobs_backward(const void* logits, const void* tokens, const float* lse, const float* entropy,

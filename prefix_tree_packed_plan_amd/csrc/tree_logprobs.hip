@@ -508,6 +508,15 @@ constexpr int kListed = 512;  // tokens behind a row that are kept in LDS
 // that work-groups that run together stream through neighbouring memory: whole
 // rows took 819 us, 64 KB 778, 32 KB 744.  The pieces that hold a token behind
 // the row are marked in a bitmap, so that the others cost nothing for it.
+//
+// p = exp(x / T - lse) is off by 2^-24 |lse|, half a unit of lse.  From kFarLse on
+// (a row of nothing but masked values, logits of tens of thousands) one of the
+// row's work-groups therefore takes all of it, reading it once for its largest
+// value and once for its sum relative to that; the others leave, so that the
+// gradient may still be written over the logits.  Which one changes with the
+// row, or one XCD had them all (8192 x 131072 bf16, all rows such: 2.1 ms against
+// 9.7).
+constexpr float kFarLse = 16384.f;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a) {
   constexpr int N = Vec<T>::N, U = 4;
@@ -533,6 +542,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
   const Behind b(a, a.first_row + lr, lane);
   for (int i = tid; i < (sl.vecs + 31) / 32; i += kThreads) flag[i] = 0;
   __syncthreads();
+  const auto mark = [&](const Slice<T>& sl, int c0, int id) {
+    const int at = id - c0 - sl.head;
+    if (id >= 0 && at >= 0 && at < sl.vecs * N) atomicOr(&flag[at / N >> 5], 1u << (at / N & 31));
+  };
   // The gradients behind the row: their sum, and which pieces they touch.
   float g = 0.f;
   for (int j = tid; j < b.n; j += kThreads) {
@@ -543,8 +556,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
       ids[j] = id;
       gs[j] = gj;
     }
-    const int at = id - c0 - sl.head;
-    if (id >= 0 && at >= 0 && at < sl.vecs * N) atomicOr(&flag[at / N >> 5], 1u << (at / N & 31));
+    mark(sl, c0, id);
   }
   g = wave_sum(g);
   if (lane == 0) wsum[wave] = g;
@@ -556,11 +568,6 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
   const float lse = a.lse_in[lr], dh = a.dentropy ? a.dentropy[lr] : 0.f;
   const bool empty = lse == kNegInf;
   const float ca = empty ? 0.f : -(g + dh * (a.dentropy ? a.entropy_in[lr] : 0.f)) * a.inv_t, cb = empty ? 0.f : -dh * a.inv_t;
-  // The gradient of a value whose token is not behind the row.
-  auto grad = [&](float x) {
-    const float lp = fmaf(x, a.inv_t, -lse);
-    return ex2(lp * kLog2e) * fmaf(cb, fmaxf(lp, -1e4f), ca);  // exp is 0 below -104
-  };
   // What the tokens behind the row that equal `id` add, in their order.
   auto direct = [&](int id) {
     float s = 0.f;
@@ -574,43 +581,98 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
     }
     return s * a.inv_t;
   };
-  const bool aligned = (reinterpret_cast<uintptr_t>(out + sl.head) & 15) == 0;
-  auto one = [&](const u32x4 w, int v) {
-    float x[N];
-    Vec<T>::unpack(w, x);
+  // The 16-byte pieces of a slice (the first ones are in w if `loaded`).
+  auto pieces = [&](const Slice<T>& sl, bool loaded, auto use) {
+    const auto* pv = reinterpret_cast<const u32x4*>(sl.p + sl.head);
+    const int rounds = sl.vecs / (U * kThreads);
+    int v = tid;
+    for (int i = 0; i < rounds; ++i, v += U * kThreads) {
+      if (i > 0 || !loaded) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = empty ? 0.f : grad(x[j]);
-    if ((flag[v >> 5] >> (v & 31)) & 1 && !empty) {
+        for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+      }
 #pragma unroll
-      for (int j = 0; j < N; ++j) x[j] += direct(c0 + sl.head + v * N + j);
+      for (int u = 0; u < U; ++u) use(w[u], v + u * kThreads);
     }
-    T* o = out + sl.head + v * N;
-    if (aligned) {
-      __builtin_nontemporal_store(Vec<T>::pack(x), reinterpret_cast<u32x4*>(o));
-    } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) Vec<T>::put(o + j, x[j]);
+    for (int u = 0; u < U; ++u)
+      if (v + u * kThreads < sl.vecs) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v + u * kThreads < sl.vecs) use(w[u], v + u * kThreads);
+  };
+  // The gradients of a slice from column c0 on, to `out`.
+  auto stream = [&](const Slice<T>& sl, T* out, int c0, bool loaded, auto grad) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(out + sl.head) & 15) == 0;
+    pieces(sl, loaded, [&](const u32x4 w, int v) {
+      float x[N];
+      Vec<T>::unpack(w, x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = empty ? 0.f : grad(x[j]);
+      if ((flag[v >> 5] >> (v & 31)) & 1 && !empty) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] += direct(c0 + sl.head + v * N + j);
+      }
+      T* o = out + sl.head + v * N;
+      if (aligned) {
+        __builtin_nontemporal_store(Vec<T>::pack(x), reinterpret_cast<u32x4*>(o));
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) Vec<T>::put(o + j, x[j]);
+      }
+    });
+    if (tid < sl.ends()) {
+      const int col = sl.end_col(tid);
+      const float x = Vec<T>::one(sl.p + col);
+      Vec<T>::put(out + col, empty ? 0.f : grad(x) + direct(c0 + col));
     }
   };
-  int v = tid;
-  for (int i = 0; i < rounds; ++i, v += U * kThreads) {
-    if (i > 0) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) one(w[u], v + u * kThreads);
+
+  if (fabsf(lse) < kFarLse || empty || lse != lse) {
+    // The gradient of a value whose token is not behind the row.
+    stream(sl, out, c0, rounds > 0, [&](float x) {
+      const float lp = fmaf(x, a.inv_t, -lse);
+      return ex2(lp * kLog2e) * fmaf(cb, fmaxf(lp, -1e4f), ca);  // exp is 0 below -104
+    });
+    return;
   }
+  if (part != lr % a.split) return;  // uniform, as the branch above
+  const Slice<T> all(static_cast<const T*>(a.logits) + int64_t(lr) * a.ld, a.vocab);
+  const float c = a.inv_t * kLog2e;
+  auto each = [&](auto use) {
+    pieces(all, false, [&](const u32x4 w, int) {
+      float x[N];
+      Vec<T>::unpack(w, x);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (v + u * kThreads < sl.vecs) w[u] = __builtin_nontemporal_load(pv + v + u * kThreads);
+      for (int j = 0; j < N; ++j) use(x[j]);
+    });
+    if (tid < all.ends()) use(Vec<T>::one(all.p + all.end_col(tid)));
+  };
+  float top = kNegInf, s = 0.f;
+  each([&](float x) { top = fmaxf(top, x); });
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (v + u * kThreads < sl.vecs) one(w[u], v + u * kThreads);
-  if (tid < sl.ends()) {
-    const int col = sl.end_col(tid);
-    const float x = Vec<T>::one(sl.p + col);
-    Vec<T>::put(out + col, empty ? 0.f : grad(x) + direct(c0 + col));
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  __syncthreads();  // wsum has been read
+  if (lane == 0) wsum[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(wsum[0], wsum[1]), fmaxf(wsum[2], wsum[3]));
+  each([&](float x) { s += ex2((x - top) * c); });
+  s = wave_sum(s);
+  __syncthreads();
+  if (lane == 0) wsum[wave] = s;
+  __syncthreads();
+  const float ls = __log2f(wsum[0] + wsum[1] + wsum[2] + wsum[3]);
+  for (int q0 = 0; q0 < a.vocab; q0 += kMaxSlice) {
+    const Slice<T> cur(all.p + q0, min(kMaxSlice, a.vocab - q0));
+    __syncthreads();  // flag has been read
+    for (int i = tid; i < (cur.vecs + 31) / 32; i += kThreads) flag[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < b.n; j += kThreads) mark(cur, q0, j < kListed ? ids[j] : token(a, b.at(j)));
+    __syncthreads();
+    stream(cur, static_cast<T*>(a.dlogits) + int64_t(lr) * a.ldd + q0, q0, false, [&](float x) {
+      const float y = (x - top) * c - ls;
+      return ex2(y) * fmaf(cb, fmaxf(y * kLn2, -1e4f), ca);
+    });
   }
 }
 
