@@ -147,7 +147,8 @@ struct Ahead {
 };
 
 // ---- the largest values of a row ------------------------------------------------
-// The k-th largest of the wave's 64 values (a bitonic sort).
+// The k-th largest of the wave's 64 values, none of them NaN (a bitonic sort, in
+// which fmaxf and fminf would replace a NaN by a second copy of its partner).
 __device__ __forceinline__ float kth_largest(float x, int k, int lane) {
 #pragma unroll
   for (int size = 2; size <= 64; size *= 2)
@@ -188,9 +189,10 @@ struct TopList {
   }
   // What a value has to reach to be worth offering, given each lane's largest
   // of those at hand: while the list is not full, the k-th largest of these
-  // (at least k values reach it), which spares most of the first insertions.
+  // (at least k values reach it), which spares most of the first insertions.  A
+  // lane with nothing but NaN has none.
   __device__ __forceinline__ float floor_of(float big, int lane) const {
-    return ti == kNoId ? kth_largest(big, k, lane) : tv;
+    return ti == kNoId ? kth_largest(big == big ? big : kNegInf, k, lane) : tv;
   }
 };
 
