@@ -95,6 +95,10 @@ bool ordinary(float x) { return x >= 1e-30f && x <= 1e30f; }
 // Work-groups of 256 a launch may have (its work items are counted in 32 bits).
 constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 64;
 
+// Grids: parts x heads; and heads along the join launches' second axis.
+bool heads_fit(const tg::AttnPlan& p, int32_t h_q) {
+  return h_q <= 65535 && (static_cast<int64_t>(p.q.n_tiles) + tg::AttnPlan::kMaxParts) * h_q <= kMaxGroups;
+}
 // Sizes, head layout and scale of an attention call.
 int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_t h_kv, int32_t d, float scale,
                     int32_t dtype, const char* fn) {
@@ -108,8 +112,7 @@ int check_attention(const tg::AttnPlan& p, int64_t n_tokens, int32_t h_q, int32_
   if (!tg::attention_supported(d, dtype))
     return fail(TREE_ERR_UNSUPPORTED, "%s: d=%d dtype=%d not compiled in", fn, d, dtype);
   if (!ordinary(scale)) return fail(TREE_ERR_INVALID_ARG, "%s: scale must be in 1e-30..1e30", fn);
-  // Grids: parts x heads; and heads along the join launches' second axis.
-  if (h_q > 65535 || (static_cast<int64_t>(p.q.n_tiles) + tg::AttnPlan::kMaxParts) * h_q > kMaxGroups)
+  if (!heads_fit(p, h_q))
     return fail(TREE_ERR_UNSUPPORTED, "%s: too many heads (%d) for %d tiles", fn, h_q, p.q.n_tiles);
   return TREE_OK;
 }
@@ -838,7 +841,7 @@ int tree_attention_plan_upload(const tree_attention_plan_t* aplan, void* dplan, 
 }
 
 size_t tree_attention_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t d, int32_t dtype) {
-  if (!aplan || h_q <= 0 || d <= 0 || !dtype_ok(dtype)) return 0;
+  if (!aplan || h_q <= 0 || !tg::attention_supported(d, dtype) || !heads_fit(aplan->p, h_q)) return 0;
   const Work w = attention_work(aplan->p.q, h_q, 1, d, dtype);
   return static_cast<size_t>(w.n_parts) * h_q * tg::attention_part_floats(d) * sizeof(float);
 }
@@ -883,8 +886,9 @@ int tree_attention(const void* q, const void* k, const void* v, void* o, float* 
 
 size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* aplan, int32_t h_q, int32_t h_kv,
                                                int32_t d, int32_t dtype) {
-  if (!aplan || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0 || !dtype_ok(dtype)) return 0;
+  if (!aplan || h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0 || !tg::attention_supported(d, dtype)) return 0;
   const tg::AttnPlan& p = aplan->p;
+  if (!heads_fit(p, h_q)) return 0;
   const Work wq = attention_work(p.q, h_q, 1, d, dtype), wk = attention_work(p.k, h_kv, h_q / h_kv, d, dtype);
   const size_t dq = static_cast<size_t>(wq.n_parts) * h_q * tg::attention_dq_part_floats(d);
   const size_t dkv = static_cast<size_t>(wk.n_parts) * wk.split * h_kv * tg::attention_dkv_part_floats(d);
