@@ -455,10 +455,13 @@ int tree_ssd_scan(const void* x, const float* dt, const float* A, const void* B,
  * tokens see, those all of them see first; for every 128 keys, the runs of
  * rows that see them; both whole and cut into parts, for calls with few tiles
  * or lists of very different lengths; and every token's place in a depth-first
- * walk with the end of its segment's subtree, which decide single pairs.  Any numbering with parents before children is accepted.  The
- * tables are copies: the plan may be freed before them.
+ * walk with the end of its segment's subtree, which decide single pairs.  Any
+ * numbering with parents before children is accepted.  The tables are copies:
+ * the plan may be freed before them.
  * Errors: INVALID_ARG (also: out of host memory), UNSUPPORTED (a trie whose
- * run lists exceed 2^26 entries: very deep and branched all along).
+ * run lists exceed 2^26 entries, very deep and branched all along, or take more
+ * than 2^31 steps over segments: for every 128 rows the segments below them,
+ * unless segments are numbered depth first; the message says which).
  */
 typedef struct tree_attention_plan tree_attention_plan_t; /* opaque, host memory, immutable once built */
 int tree_attention_plan(const tree_plan_t* plan, tree_attention_plan_t** out);

@@ -145,7 +145,7 @@ const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int3
   return whole;
 }
 
-int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
+int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err, int64_t max_runs, int64_t max_steps) {
   const int32_t n_seg = p.n_seg;
   const int32_t n = static_cast<int32_t>(p.n_tokens);
   AttnPlan a;
@@ -190,9 +190,17 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
 
   std::vector<AttnRun> runs;
   std::vector<AttnItem> qlists, klists;
+  int64_t steps = 0;
   const auto too_large = [&] {
-    *err = "tree_attention_plan: the tiles' run lists exceed 2^26 entries";
-    return TREE_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(runs.size()) > max_runs)
+      *err = "tree_attention_plan: the tiles' run lists exceed " + std::to_string(max_runs) + " entries";
+    else if (steps > max_steps)
+      *err = "tree_attention_plan: the tiles' lists take more than " + std::to_string(max_steps) +
+             " steps over their segments (" + (dfs ? "a very deep and branched trie" : "a depth-first numbering takes fewer") +
+             ")";
+    else
+      return false;
+    return true;
   };
 
   // Query tiles: walk up from every segment of the tile, stopping where an
@@ -200,7 +208,6 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
   std::vector<int32_t> stamp(n_seg, -1), reach(n_seg, 0), touched;
   std::vector<Range> full, part;
   const int32_t n_qt = (n + kQTile - 1) / kQTile;
-  int64_t steps = 0;
   for (int32_t t = 0, s1 = 0; t < n_qt; ++t) {
     const int32_t lo = t * kQTile, hi = std::min<int64_t>(n, int64_t(lo) + kQTile);
     while (p.seg_off[s1 + 1] <= lo) ++s1;
@@ -242,7 +249,7 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
     it.n_total = emit(&part, it.n_full, &runs);
     it.n_runs = static_cast<int32_t>(runs.size()) - it.run_off;
     qlists.push_back(it);
-    if (static_cast<int64_t>(runs.size()) > AttnPlan::kMaxRuns || steps > (int64_t(1) << 31)) return too_large();
+    if (too_large()) return TREE_ERR_UNSUPPORTED;
   }
 
   // Key tiles: the subtrees of the tile's segments.
@@ -293,7 +300,7 @@ int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err) {
     it.n_total = emit(&part, it.n_full, &runs);
     it.n_runs = static_cast<int32_t>(runs.size()) - it.run_off;
     klists.push_back(it);
-    if (static_cast<int64_t>(runs.size()) > AttnPlan::kMaxRuns || steps > (int64_t(1) << 31)) return too_large();
+    if (too_large()) return TREE_ERR_UNSUPPORTED;
   }
   const auto up = [](size_t x) { return (x + 7) / 8 * 8; };
   a.m_d = 0;

@@ -74,6 +74,9 @@ struct AttnPlan {
   AttnLists q, k;
   // Entries a trie may need at most: the run lists of all tiles together.
   static constexpr int64_t kMaxRuns = int64_t(1) << 26;
+  // Segments looked at for all lists (a few seconds).  A key tile's list costs
+  // its stretches in depth-first numbering, every segment below it in others.
+  static constexpr int64_t kMaxSteps = int64_t(1) << 31;
   // A cut of more parts is not made (the coarser ones have parts enough).
   static constexpr int64_t kMaxParts = 1 << 12;
 
@@ -98,7 +101,9 @@ constexpr int32_t kSlots = 512;
 const AttnCut& choose_cut(const AttnLists& l, int32_t heads, int32_t steps, int32_t least, int32_t worth,
                           int32_t* split);
 
-// Returns 0 or a negative TREE_ERR_* code; on failure *err holds a message.
-int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err);
+// Returns 0 or a negative TREE_ERR_* code; on failure *err holds a message and
+// *out is as it was.
+int build_attn_plan(const Plan& p, AttnPlan* out, std::string* err, int64_t max_runs = AttnPlan::kMaxRuns,
+                    int64_t max_steps = AttnPlan::kMaxSteps);
 
 }  // namespace tg
