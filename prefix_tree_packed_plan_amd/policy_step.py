@@ -13,6 +13,7 @@ program prints the loss of each step.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 import prefix_tree_packed_plan_amd as ptp
 
@@ -25,6 +26,7 @@ class Conv(torch.autograd.Function):
         return ptp.tree_conv(x, w, plan, act="silu")
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
         dx, dw, _, _ = ptp.tree_conv_backward(x, w, dy.contiguous(), ctx.plan, act="silu")
@@ -40,6 +42,7 @@ class Scan(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, g, beta, states = ctx.saved_tensors
         dq, dk, dv, dg, db, _ = ptp.tree_gdn_scan_backward(q, k, v, g, beta, do.contiguous(), ctx.plan, states)
@@ -55,6 +58,7 @@ class Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         return (*ptp.tree_attention_backward(*ctx.saved_tensors, do, ctx.plan), None)
 
@@ -70,6 +74,7 @@ class Logprobs(torch.autograd.Function):
         return r.logp, r.entropy
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dlogp, dentropy):
         logits, tokens, lse, entropy = ctx.saved_tensors
         d = ptp.tree_logprobs_backward(logits, tokens, lse, entropy, dlogp.contiguous(), ctx.plan,
