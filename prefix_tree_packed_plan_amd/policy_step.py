@@ -60,7 +60,7 @@ class Attention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
-        return (*ptp.tree_attention_backward(*ctx.saved_tensors, do, ctx.plan), None)
+        return (*ptp.tree_attention_backward(*ctx.saved_tensors, do.contiguous(), ctx.plan), None)
 
 
 class Logprobs(torch.autograd.Function):

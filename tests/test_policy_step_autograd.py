@@ -1,5 +1,7 @@
 """The policy update's autograd functions: second derivatives are refused, not
-left out."""
+left out, and expanded gradients are taken."""
+import sys
+
 import pytest
 import torch
 
@@ -39,3 +41,28 @@ def test_second_derivatives_are_refused(name, monkeypatch):
     (g,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (g * g).sum().backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("part", ["sum", "row"])
+def test_attention_takes_expanded_gradients(part):
+    """The gradient of o.sum() is one number repeated, of a sum over heads a
+    row repeated."""
+    plan = ptp.tree_plan([-1, 0, 0], [40, 30, 20], 4)
+    gen = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn((90, h, 32), generator=gen).to("cuda:0") for h in (4, 2, 2))
+    w = torch.randn((90, 1, 32), generator=gen).to("cuda:0")
+
+    def grads(spread):
+        t = [x.clone().requires_grad_() for x in (q, k, v)]
+        o = ps.Attention.apply(*t, plan)
+        if spread:
+            loss = o.sum() if part == "sum" else (o.sum(1, keepdim=True) * w).sum()
+            loss.backward()
+        else:
+            o.backward((torch.ones_like(o) if part == "sum" else w.expand_as(o)).contiguous())
+        torch.cuda.synchronize()
+        return [x.grad for x in t]
+
+    print(f"expanded gradients, {part}", file=sys.stderr, flush=True)
+    assert all(torch.equal(a, b) for a, b in zip(grads(True), grads(False)))
