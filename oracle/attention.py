@@ -83,3 +83,56 @@ def tree_attention_reference(parents, lens, q, k, v, scale, do=None, u=2.0 ** -8
         if x in out:
             tol[x] += u * np.abs(out[x]) + 1e-30
     return {x: (out[x], tol[x]) for x in out}
+
+
+def tree_attention_rms(parents, lens, q, k, v, scale, do, u=2.0 ** -8):
+    """Returns {name: root mean square error} for o, dq, dk, dv, element by
+    element, of arithmetic whose roundings to u are independent of each other:
+    one of relative size u at most is u / sqrt(3) at most in the mean.  Far
+    tighter than the bounds above, which add every rounding at its worst, and
+    so what a lost part of a list or a wrong delta shows against (rms_ratio).
+
+    o: the probabilities as operands, and its own rounding.  delta takes o's
+    error, the same for all keys of a row.  dq, dk: delta, ds as operands, their
+    own rounding; dv: p as operands, and its own."""
+    q, k, v, do = (np.asarray(x, np.float64) for x in (q, k, v, do))
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    off, paths = _paths(parents, lens)
+    r2 = u * u / 3
+    var = {"o": np.zeros(q.shape), "dq": np.zeros(q.shape), "dk": np.zeros(k.shape), "dv": np.zeros(v.shape)}
+    sums = {"dk": np.zeros(k.shape), "dv": np.zeros(v.shape)}
+    for s in range(len(parents)):
+        rows, a, b = paths[s], int(off[s]), int(off[s + 1])
+        see = np.arange(len(rows))[None, :] <= len(rows) - (b - a) + np.arange(b - a)[:, None]
+        for h in range(hq):
+            g = h // (hq // hkv)
+            kk, vv, qq, dd = k[rows, g], v[rows, g], q[a:b, h], do[a:b, h]
+            w = np.where(see, qq @ kk.T * scale, -np.inf)
+            p = np.exp(w - w.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            o = p @ vv
+            vo = r2 * ((p * p) @ (vv * vv) + o * o)
+            vdelta = (dd * dd * vo).sum(1, keepdims=True)
+            ds = p * (dd @ vv.T - (dd * o).sum(1, keepdims=True))
+            dq = scale * ds @ kk
+            var["o"][a:b, h] = vo
+            var["dq"][a:b, h] = scale ** 2 * (r2 * (ds * ds) @ (kk * kk) + vdelta * (p @ kk) ** 2) + r2 * dq * dq
+            np.add.at(var["dk"], (rows, g), scale ** 2 * (r2 * ds * ds + vdelta * p * p).T @ (qq * qq))
+            np.add.at(var["dv"], (rows, g), r2 * (p * p).T @ (dd * dd))
+            np.add.at(sums["dk"], (rows, g), scale * ds.T @ qq)
+            np.add.at(sums["dv"], (rows, g), p.T @ dd)
+    for x in sums:
+        var[x] += r2 * sums[x] ** 2
+    return {x: np.sqrt(var[x]) + 1e-30 for x in var}
+
+
+def rms_ratio(err, rms, rows=64):
+    """The largest root mean square of err / rms over `rows` consecutive rows
+    (a rest of less than half as many belongs to the ones before) of one head."""
+    n, h, d = err.shape
+    z = ((err / rms) ** 2).mean(-1)
+    cuts = list(range(0, n, rows))
+    if len(cuts) > 1 and n - cuts[-1] < rows // 2:
+        cuts.pop()
+    return float(np.sqrt(max(z[a:b].mean(0).max() for a, b in zip(cuts, cuts[1:] + [n]))))
