@@ -550,6 +550,11 @@ __host__ __device__ constexpr int64_t dkv_part(int d) { return int64_t(kKTile) *
 constexpr int kJoinRows = 16;
 
 // ---- forward --------------------------------------------------------------------
+// The exponent c s - c m takes one fma with c m rounded, which is off by the same
+// for all of a row's keys and cancels, but may be more than exp2 holds where c m
+// is past 2^30.  From here on it is c (s - m).
+constexpr float kWide = 16777216.f;
+
 template <typename T, int D>
 struct FwdSmem {
   alignas(16) char k[2][Cfg<T, D>::TILE];
@@ -643,6 +648,7 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
 #pragma unroll
   for (int db = 0; db < C::NDB; ++db) acc[db] = zero16();
   float m = kNegInf, l = 0.f;  // running maximum of q.k (both halves of the wave agree), this lane's part of the sum
+  bool wide = false;           // a row of this wave has scores past kWide
 
   // The tile at v0 is in buffer `buf`, a constant: LDS addresses then are a
   // lane's offset plus an immediate.
@@ -699,13 +705,23 @@ __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_ke
         const float mn = grown ? mt : m;
         const float al = m == kNegInf ? 0.f : ex2((m - mn) * c);
         m = mn;
+        wide = __any(m != kNegInf && fabsf(m * c) > kWide);
         l *= al;
 #pragma unroll
         for (int db = 0; db < C::NDB; ++db)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[db][i] *= al;
       }
-      const float mc = m == kNegInf ? 0.f : m * c;  // -inf: this row has seen no key yet
+      const float m0 = m == kNegInf ? 0.f : m;  // -inf: this row has seen no key yet
+      float mc = m0 * c;
+      if (wide) {
+        const float by = fabsf(mc) > kWide ? m0 : 0.f;  // other rows keep their bits
+        mc = by != 0.f ? 0.f : mc;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[kb][i] -= by;
+      }
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
