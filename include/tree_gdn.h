@@ -552,6 +552,9 @@ size_t tree_attention_backward_workspace_bytes(const tree_attention_plan_t* apla
  * their products under TREE_DTYPE_BF16.  A token whose q, dout or o is not
  * finite may make dk and dv of the tokens it sees NaN throughout, one whose k
  * is not finite dq of those that see it; no others.
+ * lse being fp32, a probability is off by some 2^-22 |lse| of itself: scores
+ * (scale q . k) beyond 2^16 make gradients inexact by percents, and beyond 2^24
+ * they have no meaning and may not be finite, while o and lse stay right.
  * Errors: as tree_attention.
  */
 int tree_attention_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
