@@ -667,7 +667,8 @@ def tree_attention_backward(q, k, v, o, lse, do, plan: TreePlan, scale: Optional
     dplan = aplan.on_device(dev)
     stream = _stream(dev)
     _check(lib.tree_attention_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                       do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), (_I64 * 10)(*st), n, h_q, k.shape[1], d, d ** -0.5 if scale is None else float(scale),
+                                       do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), (_I64 * 10)(*st), n,
+                                       h_q, k.shape[1], d, d ** -0.5 if scale is None else float(scale),
                                        _dtype_code(q), aplan.handle, dplan.data_ptr(), dplan.numel(),
                                        workspace.data_ptr() if workspace is not None else None, ws_bytes, stream))
     return dq, dk, dv

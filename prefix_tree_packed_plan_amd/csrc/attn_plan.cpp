@@ -72,7 +72,7 @@ AttnCut cut_lists(const std::vector<AttnItem>& lists, int64_t most, bool from_en
   c.n_items = next;
   // Longest first; with items enough to fill the device many times, only by
   // powers of 2, in the order of the tiles within them: neighbours then read the
-  // same keys (RL-batch-shaped trie of 402 segments, 16/4 heads of 128: forward
+  // same keys (32 prompts of 8 completions, 282665 tokens, 16/4 heads of 128: forward
   // 7.09 -> 6.67 ms, backward 21.9 -> 20.8 ms; a trie of 80 tiles loses 3%).
   const bool many = items->size() > 1024;
   const auto rank = [&](const AttnItem& x) {

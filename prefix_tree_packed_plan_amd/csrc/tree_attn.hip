@@ -103,8 +103,11 @@ struct Cfg {
   static constexpr int NI = TILE / 1024 / 4;     // DMA instructions of each of 4 waves
 };
 
-// Fragment s of 32 accumulator rows as the B operand of the next product
-// (bf16: rounded to nearest even, at most 2^-8 of the value).
+// Fragment s of 32 accumulator rows as the B operand of the next product.  bf16
+// inputs: rounded to nearest even, by 2^-8 of the value at most, as the MFMA with
+// the other operand's bf16 takes it (fp32 operands would take 16 times as long);
+// sums stay in fp32.  Errors against 64 bits are 0.0021 (o) and 0.0024 (dq, dk,
+// dv) of the result's norm, 0.0015 and 0.0018 with fp32 operands.
 template <typename T>
 __device__ __forceinline__ uint4 frag(const f32x16& p, int s);
 template <>
@@ -595,17 +598,17 @@ __device__ __forceinline__ void span(int dq, int& lo, int& hi) {
 // work-groups a CU (96 registers of queries and sums at d = 128, 65 KB of LDS).
 // What bounds it is issue: 64 keys are 32 MFMA (1024 cycles of a SIMD) and
 // about 150 vector instructions, 32 of them exponentials (600 and more), of
-// which the SIMD's other wave covers a part: matrix units are busy 56%, vector
-// units 47% of the time, at 1.8 GHz, the clock that the load leaves (20% fewer
+// which the SIMD's other wave covers a part: matrix units are busy 58%, vector
+// units 48% of the time, at 1.8 GHz, the clock that the load leaves (20% fewer
 // cycles in the last steps took 7% less time); LDS reads have no conflicts and
 // the keys come out of L2.  Tried: the exponentials of a tile between the products of the next one's
 // scores, instruction by instruction, takes 15% longer (every wave then waits
 // in turn for each operand, product and exponential); so do blocks of 32 keys
 // (3%); the first values read before the exponentials, 1%.  More rows a wave
 // would halve the LDS reads and need twice the registers.
-// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 517 us (1063 TFLOP/s; a large
-// matrix product reaches 1336 there); 10240 tokens of 16 responses, 16/4 heads,
-// 207 us; d = 64, 13941 tokens, 12/4 heads: 56 us.
+// bf16, d = 128: chain of 16383 tokens, 8/2 heads, 499 us (1103 TFLOP/s; a large
+// matrix product reaches 1380 there); 10240 tokens of 8 responses, 16/4 heads,
+// 203 us; d = 64, 13941 tokens, 12/4 heads: 56 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256, D * sizeof(T) <= 256 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
   using C = Cfg<T, D>;
@@ -800,8 +803,8 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attn_fwd_join_kernel(AttnAr
 // ---- gradient of q -----------------------------------------------------------------
 // Same tiles as the forward; also leaves -delta and -lse / scale, which the
 // other gradients' sums start from.  Three products and one exponential a pair:
-// the matrix units are busy 60% of the time (chain of 16383 tokens, 8/2 heads of
-// 128: 735 us).  S and dP are computed here and again for dk and dv, seven
+// the matrix units are busy 58% of the time (chain of 16383 tokens, 8/2 heads of
+// 128: 740 us).  S and dP are computed here and again for dk and dv, seven
 // products in all: a single pass of five would add to dq from every key tile,
 // by atomics in an order that changes, or keep a part per tile.
 template <typename T, int D>
@@ -966,7 +969,7 @@ struct BwdSmem {
 // (192 of 256 at d = 128); rows of q and dO pass through LDS, each read twice:
 // by rows for S and dP, transposed for dv and dk.  What bounds it are those reads
 // between the products, two or three in flight being all that the registers
-// leave: matrix units 55% busy, chain of 16383 tokens, 8/2 heads of 128: 1010 us.
+// leave: matrix units 56% busy, chain of 16383 tokens, 8/2 heads of 128: 1005 us.
 // 64 keys a wave at one wave a SIMD spilled (7.6 ms); an order left to the
 // compiler took 1849 us.
 template <typename T, int D>

@@ -506,7 +506,7 @@ __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobArgs a) {
 constexpr int kListed = 512;  // tokens behind a row that are kept in LDS
 
 // One slice of a row a work-group, read and written once: 8192 x 131072 bf16 in
-// 701 us, 1685 x 50001 fp32 in 117 us (6.1 and 5.7 TB/s).  Slices of 16 KB, so
+// 704 us, 1685 x 50001 fp32 in 113 us (6.1 and 5.9 TB/s).  Slices of 16 KB, so
 // that work-groups that run together stream through neighbouring memory: whole
 // rows took 819 us, 64 KB 778, 32 KB 744.  The pieces that hold a token behind
 // the row are marked in a bitmap, so that the others cost nothing for it.
