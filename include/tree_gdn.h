@@ -638,6 +638,50 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
                            float temperature, int32_t dtype, const tree_plan_t* plan, const void* dplan,
                            size_t dplan_bytes, void* stream);
 
+/*
+ * tree_embedding -- the rows of a table that a model's tokens name, scaled:
+ *   out[n] = scale * table[tokens[n]],
+ * where a packed trie's model begins ("Tree Training" section 3.1 Eq. 8: every
+ * packed token once).  A token outside [0, vocab), such as padding, has no row:
+ * its output is zero.  Any tokens, in any order; no plan is needed.
+ *
+ * tokens  device, [n_tokens] int32 or int64 (token_bytes 4 or 8)  (read)
+ * table   device, [vocab, width], dtype                     (read)
+ * out     device, [n_tokens, width], dtype                  (written; no alias)
+ * Rows are contiguous, of any width, aligned to an element.
+ * scale   in 1e-30 .. 1e30; the product is rounded once, 1 copies the row.
+ * n_tokens in 0 .. 2^30, vocab in 1 .. 2^30, width in 1 .. 2^24.
+ * Errors: INVALID_ARG, HIP.
+ */
+int tree_embedding(const void* tokens, const void* table, void* out, int64_t n_tokens, int32_t vocab, int32_t width,
+                   int32_t token_bytes, float scale, int32_t dtype, void* stream);
+
+/*
+ * tree_embedding_backward_workspace_bytes -- device workspace of
+ * tree_embedding_backward: the tokens sorted by row, and sums of parts of
+ * long rows' lists.  0 for sizes out of range.
+ */
+size_t tree_embedding_backward_workspace_bytes(int64_t n_tokens, int32_t vocab, int32_t width);
+
+/*
+ * tree_embedding_backward -- the table's gradient for gradients dout of
+ * tree_embedding's out:
+ *   dtable[v] = scale * sum of dout[n] over all n with tokens[n] = v,
+ * in fp32 and in a fixed order (the result is deterministic), rounded once.
+ * All of dtable is written; rows without a token are zero.
+ *
+ * tokens  device, [n_tokens] int32 or int64                 (read)
+ * dout    device, [n_tokens, width], dtype                  (read)
+ * dtable  device, [vocab, width], dtype                     (written; no alias)
+ * ws      device workspace, ws_bytes >= tree_embedding_backward_workspace_bytes,
+ *         aligned to 16 bytes.
+ * Everything else as for tree_embedding.
+ * Errors: INVALID_ARG, WORKSPACE, HIP.
+ */
+int tree_embedding_backward(const void* tokens, const void* dout, void* dtable, int64_t n_tokens, int32_t vocab,
+                            int32_t width, int32_t token_bytes, float scale, int32_t dtype, void* ws, size_t ws_bytes,
+                            void* stream);
+
 /* Message for the last failed call on this thread ("" if none). */
 const char* tree_last_error(void);
 

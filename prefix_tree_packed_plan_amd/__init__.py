@@ -19,6 +19,8 @@ from ._lib import (  # noqa: F401
     tree_attention_backward,
     tree_conv,
     tree_conv_backward,
+    tree_embedding,
+    tree_embedding_backward,
     tree_gdn_scan,
     tree_gdn_scan_backward,
     tree_logprobs,

@@ -91,6 +91,9 @@ SIGNATURES = {
                                      _P, _P, _SZ, _P, _SZ, _P]),
     "tree_logprobs_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32,
                                               _F, _I32, _P, _P, _SZ, _P]),
+    "tree_embedding": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P]),
+    "tree_embedding_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "tree_embedding_backward": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P, _SZ, _P]),
     "tree_last_error": (ctypes.c_char_p, []),
 }
 
@@ -573,6 +576,25 @@ def _stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+class _on:
+    """Makes `dev` the current device while kernels are launched on it (nothing
+    to do, and nothing spent, where it is already)."""
+
+    def __init__(self, dev):
+        import torch
+        self._cuda, self._dev = torch._C, dev.index
+
+    def __enter__(self):
+        was = self._cuda._cuda_getDevice()
+        self._was = None if was == self._dev else was
+        if self._was is not None:
+            self._cuda._cuda_setDevice(self._dev)
+
+    def __exit__(self, *_):
+        if self._was is not None:
+            self._cuda._cuda_setDevice(self._was)
+
+
 def _need_heads(t, name, dtype=None, device=None):
     """A [N, H, d] device tensor whose heads' d elements are contiguous; returns
     the elements between token rows and between heads."""
@@ -774,4 +796,63 @@ def tree_logprobs_backward(logits, tokens, lse, entropy, dlogp, plan: TreePlan, 
                                          out.data_ptr(), ld, ldd, plan.n_tokens, int(first_row), rows, vocab,
                                          token_bytes, float(temperature), _dtype_code(logits), plan.handle,
                                          dplan.data_ptr(), dplan.numel(), stream))
+    return out
+
+
+def _need_tokens(tokens, device):
+    import torch
+    _need(tokens, "tokens", device=device)
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"tokens must be int32 or int64, got {tokens.dtype}")
+    if tokens.dim() != 1:
+        raise ValueError("tokens must be [N]")
+
+
+def tree_embedding(tokens, table, scale: float = 1.0, out=None):
+    """scale * table[tokens]: [N, C] of the table's dtype (bf16 or fp32).  tokens
+    [N] int32 or int64; one outside the table [V, C] gets a row of zeros."""
+    import torch
+    _need(table, "table")
+    dev = table.device
+    _need_tokens(tokens, dev)
+    if table.dim() != 2:
+        raise ValueError("table must be [V, C]")
+    n, (vocab, width) = tokens.shape[0], table.shape
+    dtype = _dtype_code(table)
+    if out is None:
+        out = torch.empty((n, width), dtype=table.dtype, device=dev)
+    else:
+        _need(out, "out", table.dtype, dev)
+        _need_shape(out, "out", (n, width))
+    with _on(dev):
+        _check(load().tree_embedding(tokens.data_ptr(), table.data_ptr(), out.data_ptr(), n, vocab, width,
+                                     tokens.element_size(), float(scale), dtype, _stream(dev)))
+    return out
+
+
+def tree_embedding_backward(tokens, dout, vocab: int, scale: float = 1.0, out=None, workspace=None):
+    """The table's gradient [vocab, C] (in dout's dtype) for gradients dout [N, C]
+    of tree_embedding's rows: equal tokens added up in fp32, in a fixed order.
+    Rows without a token are zero."""
+    import torch
+    _need(dout, "dout")
+    dev = dout.device
+    _need_tokens(tokens, dev)
+    if dout.dim() != 2 or dout.shape[0] != tokens.shape[0]:
+        raise ValueError("shapes must be tokens [N] and dout [N, C]")
+    (n, width), vocab = dout.shape, int(vocab)
+    dtype = _dtype_code(dout)
+    if out is None:
+        out = torch.empty((vocab, width), dtype=dout.dtype, device=dev)
+    else:
+        _need(out, "out", dout.dtype, dev)
+        _need_shape(out, "out", (vocab, width))
+    lib = load()
+    with _on(dev):
+        workspace, ws_bytes = _workspace(workspace, int(lib.tree_embedding_backward_workspace_bytes(n, vocab, width)),
+                                         dev)
+        _check(lib.tree_embedding_backward(tokens.data_ptr(), dout.data_ptr(), out.data_ptr(), n, vocab, width,
+                                           tokens.element_size(), float(scale), dtype,
+                                           workspace.data_ptr() if workspace is not None else None, ws_bytes,
+                                           _stream(dev)))
     return out

@@ -138,6 +138,12 @@ int check_aligned(const void* ptr, const char* name, const char* fn) {
   return TREE_OK;
 }
 
+int check_element_aligned(const void* ptr, int32_t dtype, const char* name, const char* fn) {
+  if (reinterpret_cast<uintptr_t>(ptr) % (dtype == TREE_DTYPE_F32 ? 4 : 2) != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", fn, name);
+  return TREE_OK;
+}
+
 // How a call's lists are cut, and the parts whose results go to the workspace.
 struct Work {
   const tg::AttnCut* cut;
@@ -210,6 +216,40 @@ int check_logprobs(const tg::Plan& p, int64_t ld, int64_t n_tokens, int32_t firs
   if (!ordinary(temperature)) return fail(TREE_ERR_INVALID_ARG, "%s: temperature must be in 1e-30..1e30", fn);
   if (!dtype_ok(dtype)) return fail(TREE_ERR_INVALID_ARG, "%s: bad dtype %d", fn, dtype);
   return TREE_OK;
+}
+
+// Sizes of an embedding call.  Up to 2^30 tokens and rows of the table: positions
+// and rows are counted in 32 bits, with room for what a wave reads past the end.
+bool embed_sizes_ok(int64_t n_tokens, int32_t vocab, int32_t width) {
+  return n_tokens >= 0 && n_tokens <= (int64_t(1) << 30) && vocab > 0 && vocab <= (1 << 30) && width > 0 &&
+         width <= (1 << 24);
+}
+int check_embed(int64_t n_tokens, int32_t vocab, int32_t width, int32_t token_bytes, float scale, int32_t dtype,
+                const char* fn) {
+  if (!embed_sizes_ok(n_tokens, vocab, width))
+    return fail(TREE_ERR_INVALID_ARG, "%s: n_tokens %lld must be in 0..2^30, vocab %d in 1..2^30, width %d in 1..2^24", fn,
+                static_cast<long long>(n_tokens), vocab, width);
+  if (token_bytes != 4 && token_bytes != 8)
+    return fail(TREE_ERR_INVALID_ARG, "%s: token_bytes must be 4 or 8 (got %d)", fn, token_bytes);
+  if (!dtype_ok(dtype)) return fail(TREE_ERR_INVALID_ARG, "%s: bad dtype %d", fn, dtype);
+  if (!ordinary(scale)) return fail(TREE_ERR_INVALID_ARG, "%s: scale must be in 1e-30..1e30", fn);
+  return TREE_OK;
+}
+// The workspace of the embedding's gradient.
+struct EmbedWork {
+  size_t order, part, bytes;  // offsets, and all of it
+  int32_t n_parts, span;
+};
+EmbedWork embed_work(int64_t n_tokens, int32_t vocab, int32_t width) {
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  EmbedWork w{};
+  w.n_parts = n_tokens > tg::kEmbedPart ? static_cast<int32_t>((n_tokens + tg::kEmbedPart - 1) / tg::kEmbedPart) : 0;
+  w.order = up((static_cast<size_t>(vocab) + 1) * sizeof(int32_t));
+  w.part = w.order + up(static_cast<size_t>(n_tokens) * sizeof(int32_t));
+  w.bytes = w.part + static_cast<size_t>(w.n_parts) * 2 * width * sizeof(float);
+  // 512 work-groups (two on each CU) share the table, as long as their rows fit.
+  w.span = std::min<int32_t>((vocab + 511) / 512, tg::kEmbedSpan);
+  return w;
 }
 
 // Blocks along the tokens of the conv backward (each walks every n-th tile).
@@ -1048,6 +1088,66 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
   a.n_seg = p.n_seg;
   const hipError_t e = tg::launch_logprobs_backward(a, dtype, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("tree_logprobs_backward: launch", e);
+  return TREE_OK;
+}
+
+int tree_embedding(const void* tokens, const void* table, void* out, int64_t n_tokens, int32_t vocab, int32_t width,
+                   int32_t token_bytes, float scale, int32_t dtype, void* stream) {
+  const char* fn = "tree_embedding";
+  if (const int rc = check_embed(n_tokens, vocab, width, token_bytes, scale, dtype, fn)) return rc;
+  if (!table || (n_tokens > 0 && (!tokens || !out))) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  if (out == table) return fail(TREE_ERR_INVALID_ARG, "%s: out must not alias the table", fn);
+  if (const int rc = check_element_aligned(table, dtype, "table", fn)) return rc;
+  if (const int rc = check_element_aligned(out, dtype, "out", fn)) return rc;
+  if (n_tokens == 0) return TREE_OK;
+  tg::EmbedArgs a{};
+  a.tokens = tokens;
+  a.table = table;
+  a.out = out;
+  a.n_tokens = n_tokens;
+  a.vocab = vocab;
+  a.width = width;
+  a.scale = scale;
+  a.lanes_log2 = tg::embed_lanes_log2(width, dtype);
+  const hipError_t e = tg::launch_embed(a, dtype, token_bytes == 8, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_embedding: launch", e);
+  return TREE_OK;
+}
+
+size_t tree_embedding_backward_workspace_bytes(int64_t n_tokens, int32_t vocab, int32_t width) {
+  return embed_sizes_ok(n_tokens, vocab, width) ? embed_work(n_tokens, vocab, width).bytes : 0;
+}
+
+int tree_embedding_backward(const void* tokens, const void* dout, void* dtable, int64_t n_tokens, int32_t vocab,
+                            int32_t width, int32_t token_bytes, float scale, int32_t dtype, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const char* fn = "tree_embedding_backward";
+  if (const int rc = check_embed(n_tokens, vocab, width, token_bytes, scale, dtype, fn)) return rc;
+  if (!dtable || (n_tokens > 0 && (!tokens || !dout))) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  if (dtable == dout) return fail(TREE_ERR_INVALID_ARG, "%s: dtable must not alias dout", fn);
+  if (const int rc = check_element_aligned(dout, dtype, "dout", fn)) return rc;
+  if (const int rc = check_element_aligned(dtable, dtype, "dtable", fn)) return rc;
+  const EmbedWork w = embed_work(n_tokens, vocab, width);
+  if (!ws || ws_bytes < w.bytes)
+    return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, w.bytes);
+  if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;
+  char* base = static_cast<char*>(ws);
+  tg::EmbedArgs a{};
+  a.tokens = tokens;
+  a.dout = dout;
+  a.out = dtable;
+  a.n_tokens = n_tokens;
+  a.vocab = vocab;
+  a.width = width;
+  a.scale = scale;
+  a.lanes_log2 = tg::embed_lanes_log2(width, dtype);
+  a.span = w.span;
+  a.n_parts = w.n_parts;
+  a.start = reinterpret_cast<int32_t*>(base);
+  a.order = reinterpret_cast<int32_t*>(base + w.order);
+  a.part = reinterpret_cast<float*>(base + w.part);
+  const hipError_t e = tg::launch_embed_backward(a, dtype, token_bytes == 8, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_embedding_backward: launch", e);
   return TREE_OK;
 }
 

@@ -287,4 +287,30 @@ constexpr int kMaxSlice = 1 << 13;    // columns a work-group of the backward ta
 hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_logprobs_backward(const LogprobArgs& a, int dtype, hipStream_t stream);
 
+// Token embedding and its gradient (tree_embed.hip).
+struct EmbedArgs {
+  const void* tokens;   // [n_tokens], int32 or int64
+  const void* table;    // [vocab, width] (forward)
+  const void* dout;     // [n_tokens, width] (backward)
+  void* out;            // [n_tokens, width], or the table's gradient [vocab, width]
+  int64_t n_tokens;
+  int32_t vocab, width;
+  float scale;
+  int32_t lanes_log2;   // embed_lanes_log2
+  // backward
+  int32_t span;         // rows of the table a work-group sorts the tokens of
+  int32_t n_parts;      // parts of kEmbedPart tokens, 0 if no row can have more
+  int32_t* start;       // workspace [vocab + 1]: where each row's tokens begin in `order`
+  int32_t* order;       // workspace [n_tokens]: the tokens by row, ascending
+  float* part;          // workspace [n_parts, 2, width]
+};
+
+constexpr int kEmbedSpanLog2 = 10;
+constexpr int kEmbedSpan = 1 << kEmbedSpanLog2;  // most rows of a sorting work-group
+constexpr int kEmbedPart = 64;
+
+int embed_lanes_log2(int32_t width, int dtype);
+hipError_t launch_embed(const EmbedArgs& a, int dtype, bool token64, hipStream_t stream);
+hipError_t launch_embed_backward(const EmbedArgs& a, int dtype, bool token64, hipStream_t stream);
+
 }  // namespace tg
