@@ -639,6 +639,90 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
                            size_t dplan_bytes, void* stream);
 
 /*
+ * tree_linear_logprobs_workspace_bytes -- device workspace of
+ * tree_linear_logprobs: for every row and 128 or 256 entries of the vocabulary
+ * 16 bytes, 1 GiB at most (more rows go one part after another).  0 for sizes
+ * that the call refuses.
+ */
+size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t width, int32_t dtype);
+
+/*
+ * tree_linear_logprobs -- tree_logprobs of logits = hidden weight^T, which are
+ * neither stored nor rounded: the matrix product, its softmax and the tokens'
+ * log probabilities, with z = hidden weight^T / temperature of a row:
+ *   lse = log sum_i exp(z_i),  entropy = -sum_i p_i log p_i, p_i = exp(z_i - lse),
+ *   logp[t] = z_{tokens[t]} - lse   for every token t behind the row,
+ * the next token of its segment or the first token of every child ("Tree
+ * Training" section 3.1 Eq. 6), 0 for a root's first token.
+ *
+ * hidden   device, [n_rows, width], dtype, ld elements between rows: those of
+ *          packed rows first_row .. first_row + n_rows - 1 (a part of the trie
+ *          at a time is fine)                             (read)
+ * weight   device, [vocab, width], dtype, contiguous      (read)
+ * tokens   device, [n_tokens] int32 or int64 (token_bytes 4 or 8); one outside
+ *          [0, vocab) is not asked for: its logp is 0     (read)
+ * logp     device, [n_tokens] fp32: the entries of tokens behind these rows
+ *                                                         (written)
+ * entropy, lse  device, [n_rows] fp32                     (written)
+ * temperature  in 1e-30 .. 1e30.
+ * width    a multiple of 8 (bf16) or 4 (fp32), at most 65536; vocab at most
+ *          2^22; ld at most 2^20.  hidden, its rows, weight and ws start on 16
+ *          bytes.
+ * dtype    TREE_DTYPE_BF16 (bf16 MFMA, sums and all that follows in fp32) or
+ *          TREE_DTYPE_F32 (each value as three bf16, the six largest partial
+ *          products: fp32 accuracy; values above 3.38e38 are taken as infinite).
+ * A row whose logits are all -inf has lse -inf, entropy 0 and log probabilities
+ * -inf; a logit of NaN or +inf (of hidden or weight not finite, or products too
+ * large) makes its row's results NaN.
+ * dplan, dplan_bytes  device copy of `plan`, as for tree_conv.
+ * ws       device workspace, ws_bytes >= tree_linear_logprobs_workspace_bytes.
+ * Errors: INVALID_ARG, SIZE, UNSUPPORTED (width, vocab), WORKSPACE, HIP.
+ */
+int tree_linear_logprobs(const void* hidden, const void* weight, const void* tokens, float* logp, float* entropy,
+                         float* lse, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab,
+                         int32_t width, int32_t token_bytes, float temperature, int32_t dtype, const tree_plan_t* plan,
+                         const void* dplan, size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * tree_linear_logprobs_backward_workspace_bytes -- device workspace of
+ * tree_linear_logprobs_backward: the logits' gradient of up to 16384 rows and a
+ * piece of the vocabulary (2^28 elements at most), and fp32 sums of gradients
+ * that several pieces or parts add to.  0 for sizes that the call refuses.
+ */
+size_t tree_linear_logprobs_backward_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t width, int32_t dtype);
+
+/*
+ * tree_linear_logprobs_backward -- the gradients of hidden and weight for
+ * gradients dlogp of the log probabilities and dentropy of the entropies, the
+ * logits computed again a piece of the vocabulary at a time.  With D the logits'
+ * gradient (tree_logprobs_backward's formula):
+ *   dhidden = D weight,   dweight = D^T hidden.
+ * Sums run in fp32 and a fixed order (the result is deterministic); D is rounded
+ * to dtype for its products, the gradients once at the end.
+ *
+ * hidden, weight, tokens, ld, first_row, n_rows ..  as for tree_linear_logprobs.
+ * lse, entropy  device, [n_rows] fp32: tree_linear_logprobs' results (read)
+ * dlogp      device, [n_tokens] fp32 (entries of tokens outside the vocabulary
+ *            are not read)                                (read)
+ * dentropy   device, [n_rows] fp32, or NULL (zeros; entropy may then be NULL)
+ * dhidden    device, [n_rows, width], dtype, contiguous   (written; no alias)
+ * dweight    device, [vocab, width], dtype, contiguous: of these rows alone
+ *                                                         (written; no alias)
+ * A row whose logits are all -inf adds nothing; one whose results are NaN makes
+ * all of dweight NaN.  p is recomputed from the fp32 lse, to a relative error of
+ * about 2^-24 (|lse| + |log p|): a percent where |lse| is 2^17.
+ * ws         device workspace, ws_bytes >=
+ *            tree_linear_logprobs_backward_workspace_bytes.
+ * Errors: as tree_linear_logprobs.
+ */
+int tree_linear_logprobs_backward(const void* hidden, const void* weight, const void* tokens, const float* lse,
+                                  const float* entropy, const float* dlogp, const float* dentropy, void* dhidden,
+                                  void* dweight, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows,
+                                  int32_t vocab, int32_t width, int32_t token_bytes, float temperature, int32_t dtype,
+                                  const tree_plan_t* plan, const void* dplan, size_t dplan_bytes, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/*
  * tree_embedding -- the rows of a table that a model's tokens name, scaled:
  *   out[n] = scale * table[tokens[n]],
  * where a packed trie's model begins ("Tree Training" section 3.1 Eq. 8: every

@@ -26,6 +26,8 @@ root-to-leaf path produces.  So the oracle simply runs each path on its own:
               its gradients, and bounds on the error of given roundings.
 * logprobs.py -- log probabilities under the row in front of each token on
               its path, entropies, largest entries, the logits' gradient.
+* linear.py -- the same from hidden states and an output weight, and the
+              gradients of both.
 
 Arithmetic is fp64 by default.  Parity status of every function is pinned by
 tests (see tests/test_oracle_*.py); nothing here is "parity unpinned".

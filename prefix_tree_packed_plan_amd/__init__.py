@@ -23,6 +23,8 @@ from ._lib import (  # noqa: F401
     tree_embedding_backward,
     tree_gdn_scan,
     tree_gdn_scan_backward,
+    tree_linear_logprobs,
+    tree_linear_logprobs_backward,
     tree_logprobs,
     tree_logprobs_backward,
     tree_plan,

@@ -91,6 +91,12 @@ SIGNATURES = {
                                      _P, _P, _SZ, _P, _SZ, _P]),
     "tree_logprobs_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32,
                                               _F, _I32, _P, _P, _SZ, _P]),
+    "tree_linear_logprobs_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "tree_linear_logprobs": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _F, _I32,
+                                            _P, _P, _SZ, _P, _SZ, _P]),
+    "tree_linear_logprobs_backward_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "tree_linear_logprobs_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32,
+                                                     _I32, _I32, _F, _I32, _P, _P, _SZ, _P, _SZ, _P]),
     "tree_embedding": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P]),
     "tree_embedding_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
     "tree_embedding_backward": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _F, _I32, _P, _SZ, _P]),
@@ -856,3 +862,99 @@ def tree_embedding_backward(tokens, dout, vocab: int, scale: float = 1.0, out=No
                                            workspace.data_ptr() if workspace is not None else None, ws_bytes,
                                            _stream(dev)))
     return out
+
+
+def _linear_args(hidden, weight, tokens, plan, first_row):
+    """Checks the hidden states of packed rows first_row .. and the weight; returns
+    the elements between rows of hidden."""
+    import torch
+    if not isinstance(hidden, torch.Tensor):
+        raise TypeError("hidden must be a torch.Tensor")
+    if not hidden.is_cuda:
+        raise ValueError("hidden must be a device tensor")
+    if hidden.dim() != 2 or (hidden.shape[1] > 1 and hidden.stride(1) != 1):
+        raise ValueError("hidden must be [n_rows, C] with contiguous rows")
+    _need(weight, "weight", hidden.dtype, hidden.device)
+    if weight.dim() != 2 or weight.shape[1] != hidden.shape[1]:
+        raise ValueError("weight must be [V, C]")
+    _need_tokens(tokens, hidden.device)
+    _need_shape(tokens, "tokens", (plan.n_tokens,))
+    if first_row < 0 or hidden.shape[0] < 1 or first_row + hidden.shape[0] > plan.n_tokens:
+        raise ValueError(f"rows {first_row} .. {first_row + hidden.shape[0]} are not rows of the plan's "
+                         f"{plan.n_tokens} tokens")
+    return hidden.stride(0) if hidden.shape[0] > 1 else hidden.shape[1]
+
+
+def tree_linear_logprobs(hidden, weight, tokens, plan: TreePlan, temperature: float = 1.0, first_row: int = 0,
+                         logp=None, workspace=None) -> TokenLogprobs:
+    """tree_logprobs of the logits hidden @ weight.T, without storing them: log
+    probabilities of the trie's tokens, each from the row in front of it on its
+    own path, and the entropy and log-sum-exp of every row.
+
+    hidden [n_rows, C] (bf16 or fp32; rows may be further apart than C) belongs to
+    packed rows first_row, first_row + 1, ...; weight [V, C] of the same type; C a
+    multiple of 8 (bf16) or 4 (fp32).  tokens [N] int32 or int64, one outside the
+    vocabulary gets 0.  logp as for tree_logprobs.  There are no top alternatives:
+    top_logp and top_ids are None."""
+    import torch
+    ld = _linear_args(hidden, weight, tokens, plan, first_row)
+    dev, f32 = hidden.device, torch.float32
+    (rows, width), vocab = hidden.shape, weight.shape[0]
+    dtype = _dtype_code(hidden)
+    if logp is None:
+        whole = rows == plan.n_tokens
+        logp = (torch.empty if whole else torch.zeros)((plan.n_tokens,), dtype=f32, device=dev)
+    else:
+        _need(logp, "logp", f32, dev)
+        _need_shape(logp, "logp", (plan.n_tokens,))
+    entropy = torch.empty(rows, dtype=f32, device=dev)
+    lse = torch.empty_like(entropy)
+    lib = load()
+    with _on(dev):
+        workspace, ws_bytes = _workspace(workspace, int(lib.tree_linear_logprobs_workspace_bytes(rows, vocab, width,
+                                                                                                dtype)), dev)
+        dplan = plan.on_device(dev)
+        _check(lib.tree_linear_logprobs(hidden.data_ptr(), weight.data_ptr(), tokens.data_ptr(), logp.data_ptr(),
+                                        entropy.data_ptr(), lse.data_ptr(), ld, plan.n_tokens, int(first_row), rows,
+                                        vocab, width, tokens.element_size(), float(temperature), dtype, plan.handle,
+                                        dplan.data_ptr(), dplan.numel(),
+                                        workspace.data_ptr() if workspace is not None else None, ws_bytes,
+                                        _stream(dev)))
+    return TokenLogprobs(logp, entropy, lse, None, None)
+
+
+def tree_linear_logprobs_backward(hidden, weight, tokens, lse, entropy, dlogp, plan: TreePlan, dentropy=None,
+                                  temperature: float = 1.0, first_row: int = 0, workspace=None):
+    """Gradients (dhidden [n_rows, C], dweight [V, C]) in the inputs' dtype, for
+    gradients dlogp [N] fp32 of tree_linear_logprobs' logp and dentropy [n_rows]
+    fp32 of its entropy (default zero; entropy may then be None).  lse and entropy
+    are that call's results; dweight is that of these rows alone.  Deterministic."""
+    import torch
+    ld = _linear_args(hidden, weight, tokens, plan, first_row)
+    dev, f32 = hidden.device, torch.float32
+    (rows, width), vocab = hidden.shape, weight.shape[0]
+    dtype = _dtype_code(hidden)
+    _need(lse, "lse", f32, dev)
+    _need_shape(lse, "lse", (rows,))
+    _need(dlogp, "dlogp", f32, dev)
+    _need_shape(dlogp, "dlogp", (plan.n_tokens,))
+    if dentropy is not None:
+        _need(dentropy, "dentropy", f32, dev)
+        _need_shape(dentropy, "dentropy", (rows,))
+        _need(entropy, "entropy", f32, dev)
+        _need_shape(entropy, "entropy", (rows,))
+    dhidden = torch.empty((rows, width), dtype=hidden.dtype, device=dev)
+    dweight = torch.empty((vocab, width), dtype=hidden.dtype, device=dev)
+    lib = load()
+    p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    with _on(dev):
+        workspace, ws_bytes = _workspace(
+            workspace, int(lib.tree_linear_logprobs_backward_workspace_bytes(rows, vocab, width, dtype)), dev)
+        dplan = plan.on_device(dev)
+        _check(lib.tree_linear_logprobs_backward(
+            hidden.data_ptr(), weight.data_ptr(), tokens.data_ptr(), lse.data_ptr(),
+            p(entropy) if dentropy is not None else None, dlogp.data_ptr(), p(dentropy), dhidden.data_ptr(),
+            dweight.data_ptr(), ld, plan.n_tokens, int(first_row), rows, vocab, width, tokens.element_size(),
+            float(temperature), dtype, plan.handle, dplan.data_ptr(), dplan.numel(), p(workspace), ws_bytes,
+            _stream(dev)))
+    return dhidden, dweight

@@ -25,7 +25,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 SOURCES = ["plan.cpp", "attn_plan.cpp", "api.cpp", "tree_conv.hip", "gdn_scan.hip", "gdn_scan_d128.hip",
            "gdn_backward.hip", "ssd_scan.hip", "tree_attn.hip", "tree_logprobs.hip",
-           "tree_embed.hip"]
+           "tree_embed.hip",
+           "tree_linear.hip"]
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -252,6 +252,103 @@ EmbedWork embed_work(int64_t n_tokens, int32_t vocab, int32_t width) {
   return w;
 }
 
+// ---- log probabilities from hidden states -----------------------------------------
+constexpr int32_t kLinearVocab = 1 << 22, kLinearWidth = 1 << 16;
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile sizes and splits of a sum product of m x n over k.  256 x 256 tiles, one
+// work-group a CU, reach the highest rate; smaller ones where those would leave CUs
+// idle.
+int32_t product_size(int64_t m, int64_t n, bool rows_only) {
+  if (!rows_only && n <= 64) return 0;
+  return ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 2 : 1;
+}
+void product_splits(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t size, int32_t* splits) {
+  const int64_t bm = size == 2 ? 256 : 128, bn = size == 2 ? 256 : size == 1 ? 128 : 64;
+  const int64_t tiles = ceil_div(m, bm) * ceil_div(n, bn), steps = ceil_div(k, dtype == TREE_DTYPE_F32 ? 32 : 64);
+  const int64_t want = size == 2 ? 256 : 512;
+  *splits = static_cast<int32_t>(std::max<int64_t>(1, std::min(want / tiles, steps / 8)));
+}
+bool linear_sizes_ok(int64_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
+  return n_rows > 0 && n_rows < (int64_t(1) << 31) && vocab > 0 && vocab <= kLinearVocab && width > 0 &&
+         width <= kLinearWidth && dtype_ok(dtype) && width % (dtype == TREE_DTYPE_F32 ? 4 : 8) == 0;
+}
+// The forward's: the tiles' sums of up to 32768 rows, 1 GiB of them at most.
+tg::LinearWork linear_work(int64_t n_rows, int32_t vocab) {
+  tg::LinearWork w{};
+  w.rows = std::min<int64_t>(n_rows, 32768);
+  w.size = product_size(vocab, w.rows, false);
+  const int64_t slots = ceil_div(vocab, w.size == 2 ? 256 : 128);
+  w.rows = std::min(w.rows, std::max<int64_t>(256, (int64_t(1) << 26) / slots / 256 * 256));
+  w.bytes = static_cast<size_t>(w.rows) * slots * 16;
+  return w;
+}
+// The backward's: D of up to 16384 rows and a piece of the vocabulary, 256 Mi elements
+// at most; dhidden and dweight in fp32 where they are added up over several.
+tg::LinearWork linear_backward_work(int64_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
+  tg::LinearWork w{};
+  const size_t es = dtype == TREE_DTYPE_F32 ? 4 : 2;
+  w.rows = std::min<int64_t>(n_rows, 16384);
+  const int64_t rows_up = ceil_div(w.rows, 256) * 256;
+  w.piece = std::min<int64_t>(vocab, (int64_t(1) << 28) / rows_up / 256 * 256);
+  w.ldd = ceil_div(w.piece, 256) * 256;
+  w.size = product_size(w.piece, w.rows, false);
+  w.size_h = product_size(width, w.rows, false);
+  product_splits(width, w.rows, w.piece, dtype, w.size_h, &w.splits_h);
+  w.size_w = product_size(width, w.piece, true);
+  product_splits(width, w.piece, w.rows, dtype, w.size_w, &w.splits_w);
+  const size_t fw = static_cast<size_t>(width) * sizeof(float);
+  w.ids = up256(w.rows * 16);
+  w.d = w.ids + up256(w.rows * 16);
+  w.dhidden = w.d + static_cast<size_t>(rows_up) * w.ldd * es;
+  w.dweight = w.dhidden + (w.piece < vocab ? up256(w.rows * fw) : 0);
+  w.parts = w.dweight + (w.rows < n_rows ? up256(vocab * fw) : 0);
+  const size_t ph = w.splits_h > 1 ? w.splits_h * w.rows * fw : 0, pw = w.splits_w > 1 ? w.splits_w * w.piece * fw : 0;
+  w.bytes = w.parts + std::max(ph, pw);
+  return w;
+}
+// What both directions check (the rows and tokens as check_logprobs does).
+int check_linear(const tg::Plan& p, const void* hidden, int64_t ld, const void* weight, int64_t n_tokens,
+                 int32_t first_row, int32_t n_rows, int32_t vocab, int32_t width, int32_t token_bytes,
+                 float temperature, int32_t dtype, const char* fn) {
+  if (const int rc = check_logprobs(p, vocab, n_tokens, first_row, n_rows, vocab, token_bytes, temperature, dtype, fn))
+    return rc;
+  if (width <= 0) return fail(TREE_ERR_INVALID_ARG, "%s: width must be > 0", fn);
+  const int64_t es = dtype == TREE_DTYPE_F32 ? 4 : 2;
+  if (!linear_sizes_ok(n_rows, vocab, width, dtype))
+    return fail(TREE_ERR_UNSUPPORTED, "%s: width %d must be a multiple of %lld up to %d, vocab %d at most %d", fn, width,
+                static_cast<long long>(16 / es), kLinearWidth, vocab, kLinearVocab);
+  if (ld < width || ld > (1 << 20))
+    return fail(TREE_ERR_INVALID_ARG, "%s: rows of hidden %lld elements apart must hold %d, at most 2^20", fn,
+                static_cast<long long>(ld), width);
+  if (ld * es % 16 != 0)
+    return fail(TREE_ERR_INVALID_ARG, "%s: rows of hidden are not aligned to 16 bytes", fn);
+  if (const int rc = check_aligned(hidden, "hidden", fn)) return rc;
+  return check_aligned(weight, "weight", fn);
+}
+void set_linear(const tg::Plan& p, const void* hidden, int64_t ld, const void* weight, const void* tokens,
+                int32_t first_row, int32_t n_rows, int32_t vocab, int32_t width, int32_t token_bytes,
+                float temperature, const void* dplan, void* ws, tg::LinearArgs* a) {
+  const int32_t* base = static_cast<const int32_t*>(dplan);
+  a->hidden = hidden;
+  a->ld = ld;
+  a->weight = weight;
+  a->tokens = tokens;
+  a->token64 = token_bytes == 8;
+  a->first_row = first_row;
+  a->n_rows = n_rows;
+  a->vocab = vocab;
+  a->width = width;
+  a->inv_t = 1.f / temperature;
+  a->ws = ws;
+  a->seg_off = base + p.m_seg_off;
+  a->parent = base + p.m_parent;
+  a->kid_off = base + p.m_kid_off;
+  a->kid = base + p.m_kid;
+  a->n_seg = p.n_seg;
+}
+
 // Blocks along the tokens of the conv backward (each walks every n-th tile).
 int32_t conv_bwd_parts(const tg::Plan& p) {
   const int64_t tiles = (p.n_tokens + 63) / 64;
@@ -1088,6 +1185,77 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
   a.n_seg = p.n_seg;
   const hipError_t e = tg::launch_logprobs_backward(a, dtype, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("tree_logprobs_backward: launch", e);
+  return TREE_OK;
+}
+
+size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
+  return linear_sizes_ok(n_rows, vocab, width, dtype) ? linear_work(n_rows, vocab).bytes : 0;
+}
+
+int tree_linear_logprobs(const void* hidden, const void* weight, const void* tokens, float* logp, float* entropy,
+                         float* lse, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows, int32_t vocab,
+                         int32_t width, int32_t token_bytes, float temperature, int32_t dtype, const tree_plan_t* plan,
+                         const void* dplan, size_t dplan_bytes, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "tree_linear_logprobs";
+  if (!plan || !hidden || !weight || !tokens || !logp || !entropy || !lse || !dplan)
+    return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  const tg::Plan& p = plan->p;
+  if (const int rc = check_linear(p, hidden, ld, weight, n_tokens, first_row, n_rows, vocab, width, token_bytes,
+                                  temperature, dtype, fn))
+    return rc;
+  const tg::LinearWork w = linear_work(n_rows, vocab);
+  if (!ws || ws_bytes < w.bytes)
+    return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, w.bytes);
+  if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;
+  if (const int rc = check_dplan(plan, dplan, dplan_bytes, fn)) return rc;
+  tg::LinearArgs a{};
+  set_linear(p, hidden, ld, weight, tokens, first_row, n_rows, vocab, width, token_bytes, temperature, dplan, ws, &a);
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  const hipError_t e = tg::launch_linear(a, w, dtype, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_linear_logprobs: launch", e);
+  return TREE_OK;
+}
+
+size_t tree_linear_logprobs_backward_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
+  return linear_sizes_ok(n_rows, vocab, width, dtype) ? linear_backward_work(n_rows, vocab, width, dtype).bytes : 0;
+}
+
+int tree_linear_logprobs_backward(const void* hidden, const void* weight, const void* tokens, const float* lse,
+                                  const float* entropy, const float* dlogp, const float* dentropy, void* dhidden,
+                                  void* dweight, int64_t ld, int64_t n_tokens, int32_t first_row, int32_t n_rows,
+                                  int32_t vocab, int32_t width, int32_t token_bytes, float temperature, int32_t dtype,
+                                  const tree_plan_t* plan, const void* dplan, size_t dplan_bytes, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  const char* fn = "tree_linear_logprobs_backward";
+  if (!plan || !hidden || !weight || !tokens || !lse || !dlogp || !dhidden || !dweight || !dplan ||
+      (dentropy && !entropy))
+    return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
+  const tg::Plan& p = plan->p;
+  if (const int rc = check_linear(p, hidden, ld, weight, n_tokens, first_row, n_rows, vocab, width, token_bytes,
+                                  temperature, dtype, fn))
+    return rc;
+  if (const int rc = check_aligned(dhidden, "dhidden", fn)) return rc;
+  if (const int rc = check_aligned(dweight, "dweight", fn)) return rc;
+  for (const void* x : {hidden, weight})
+    if (x == dhidden || x == dweight) return fail(TREE_ERR_INVALID_ARG, "%s: gradients must not alias the inputs", fn);
+  if (dhidden == dweight) return fail(TREE_ERR_INVALID_ARG, "%s: gradients must not alias", fn);
+  const tg::LinearWork w = linear_backward_work(n_rows, vocab, width, dtype);
+  if (!ws || ws_bytes < w.bytes)
+    return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, w.bytes);
+  if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;
+  if (const int rc = check_dplan(plan, dplan, dplan_bytes, fn)) return rc;
+  tg::LinearArgs a{};
+  set_linear(p, hidden, ld, weight, tokens, first_row, n_rows, vocab, width, token_bytes, temperature, dplan, ws, &a);
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  a.lse_in = lse;
+  a.entropy_in = entropy;
+  a.dhidden = dhidden;
+  a.dweight = dweight;
+  const hipError_t e = tg::launch_linear_backward(a, w, dtype, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("tree_linear_logprobs_backward: launch", e);
   return TREE_OK;
 }
 

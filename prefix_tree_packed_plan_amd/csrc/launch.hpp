@@ -287,6 +287,49 @@ constexpr int kMaxSlice = 1 << 13;    // columns a work-group of the backward ta
 hipError_t launch_logprobs(const LogprobArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_logprobs_backward(const LogprobArgs& a, int dtype, hipStream_t stream);
 
+// Log probabilities from hidden states and the output weight, and their
+// gradients (tree_linear.hip); rows as for LogprobArgs.
+struct LinearArgs {
+  const void* hidden;   // [n_rows, width], ld elements between rows
+  int64_t ld;
+  const void* weight;   // [vocab, width]
+  const void* tokens;   // [N], int32 or int64
+  int32_t token64;
+  int32_t first_row, n_rows, vocab, width;
+  float inv_t;          // 1 / temperature
+  float* logp;          // [N]
+  float* entropy;       // [n_rows]
+  float* lse;           // [n_rows]
+  void* ws;
+  // backward
+  const float* dlogp;       // [N]
+  const float* dentropy;    // [n_rows] or null
+  const float* lse_in;
+  const float* entropy_in;
+  void* dhidden;            // [n_rows, width]
+  void* dweight;            // [vocab, width]
+  const int32_t* seg_off;
+  const int32_t* parent;
+  const int32_t* kid_off;
+  const int32_t* kid;
+  int32_t n_seg;
+};
+
+// How a call is cut: `rows` rows at a time and, in the backward, `piece` entries of
+// the vocabulary; the tile sizes (0: 128 x 64, 1: 128 x 128, 2: 256 x 256) and splits
+// of the contraction of its products; and its workspace.
+struct LinearWork {
+  int64_t rows, piece;
+  int32_t size;                // logits
+  int32_t size_h, splits_h;    // dhidden
+  int32_t size_w, splits_w;    // dweight
+  int64_t ldd;                 // elements between rows of D
+  size_t ids, d, dhidden, dweight, parts, bytes;
+};
+
+hipError_t launch_linear(const LinearArgs& a, const LinearWork& w, int dtype, hipStream_t stream);
+hipError_t launch_linear_backward(const LinearArgs& a, const LinearWork& w, int dtype, hipStream_t stream);
+
 // Token embedding and its gradient (tree_embed.hip).
 struct EmbedArgs {
   const void* tokens;   // [n_tokens], int32 or int64

@@ -1,0 +1,498 @@
+// Log probabilities of a trie's tokens from hidden states and the output weight,
+// and the gradients of both (gfx950).  With z = hidden weight^T / T, of row r and
+// vocabulary entry v:
+//     lse_r = log sum_v exp(z_rv),  p_rv = exp(z_rv - lse_r),
+//     H_r = lse_r - sum_v p_rv z_rv,  logp_t = z_{r, tok t} - lse_r
+// for every token t behind row r, and, for gradients g_t and h_r,
+//     D_rv = (1 / T) (sum_t g_t [tok t = v] - G_r p_rv - h_r p_rv (log p_rv + H_r)),
+//     dhidden = D weight,  dweight = D^T hidden,   G_r = sum_t g_t.
+//
+// The logits are never stored.  The forward computes them a tile of vocabulary x
+// rows at a time (product_tile.hpp, vocabulary along m, so that a lane holds
+// values of one row) and keeps each tile's largest value, sum of exponentials and
+// sum of exponentials times exponent; a wave a row joins these and takes the dot
+// products of the tokens behind it.  The backward goes through the vocabulary in
+// pieces: a piece's D is computed from the same products, stored (rounded to the
+// inputs' type, as the operand of the two products that follow), and multiplied
+// into dhidden, in fp32 over the pieces, and the piece's dweight.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tree_gdn.h"
+#include "launch.hpp"
+#include "product_tile.hpp"
+#include "trie_rows.hpp"
+
+namespace tg {
+
+namespace {
+
+using chunk::ex2;
+using chunk::kLog2e;
+using product::f32x16;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Of some values z / T, in powers of 2: m (largest z log2(e) / T; -inf: nothing
+// yet), sum of e = exp2(y) with y = z log2(e) / T - m, sum of e y.
+struct LinearSums {
+  float m, s, t;
+};
+__device__ __forceinline__ LinearSums join(const LinearSums a, const LinearSums b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == kNegInf) return LinearSums{m, a.s + b.s, a.t + b.t};
+  LinearSums r;
+  r.m = m;
+  // A factor of 0 (that side is empty, or far below) drops t, whose shift may
+  // overflow; a NaN stays in s.
+  const float da = a.m - m, db = b.m - m;
+  const float fa = ex2(da), fb = ex2(db);
+  r.s = a.s * fa + b.s * fb;
+  r.t = (fa == 0.f ? 0.f : fmaf(da, a.s, a.t) * fa) + (fb == 0.f ? 0.f : fmaf(db, b.s, b.t) * fb);
+  return r;
+}
+
+// Four neighbouring values to a row of T.
+template <typename T>
+__device__ __forceinline__ void put4(void* p, int64_t i, float a, float b, float c, float d);
+template <>
+__device__ __forceinline__ void put4<uint16_t>(void* p, int64_t i, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(chunk::pk2(a, b), chunk::pk2(c, d));
+}
+template <>
+__device__ __forceinline__ void put4<float>(void* p, int64_t i, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
+}
+
+enum Use { kStats, kGrad, kSum };
+
+// A product's operands and where its tiles stand.
+struct Job {
+  const char *a, *b;
+  int64_t lda, ldb;         // bytes between stored rows
+  int32_t m, n, k;
+  int32_t m_tiles, n_tiles, band;  // tiles run through `band` n for each m
+  int32_t splits, k_split;  // k is cut into `splits` of k_split (a multiple of a step)
+  // kStats: z of entry m, row n, times c
+  float c;
+  float4* part;             // [n, m_tiles]: largest z c, sum, weighted sum
+  // kGrad: entry v0 + m
+  const float4* row;        // RowGrad of each row
+  const int4* ids;
+  float inv_t;
+  int32_t v0;
+  void* d;                  // [padded n, ldd]
+  int64_t ldd;
+  // kSum: out[n][m], or fp32 sums (of a split) in acc
+  void* out;
+  float* acc;
+  const float* add;         // or null: what `acc` or `out` starts from
+  int64_t acc_split;        // elements between splits' sums
+};
+
+// The gradient's coefficients of a row: D = exp(z - lse) (cb log p + ca), plus g /
+// T at the entries that stand behind it.
+//   row: (lse, ca, cb, g of the first token)
+//   ids: (the first token's entry or -1, tokens behind, first of them in kid or -1, 0)
+template <typename T, bool TA, bool TB, int BM, int BN, int WM, int WN, int S, Use USE, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, LinearArgs la) {
+  using C = product::Tile<T, TA, TB, BM, BN, WM, WN, S>;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int tiles = j.m_tiles * j.n_tiles;
+  const int id = product::of_xcd(blockIdx.x, gridDim.x);
+  const int split = id / tiles, tile = id % tiles;
+  // Bands of `band` n tiles; within one, all n of an m.
+  const int in_band = j.band * j.m_tiles, band = tile / in_band, at = tile % in_band;
+  const int width = min(j.band, j.n_tiles - band * j.band);
+  const int mt = at / width, nt = band * j.band + at % width;
+  const int m0 = mt * BM, n0 = nt * BN;
+  const int k0 = split * j.k_split, k = min(j.k - k0, j.k_split);
+
+  typename C::OpA A;
+  typename C::OpB B;
+  A.init(j.a, j.lda, m0, j.m - m0, k0, wave, lane);
+  B.init(j.b, j.ldb, n0, j.n - n0, k0, wave, lane);
+  const typename C::RdA ra(wm * C::MB, lane);
+  const typename C::RdB rb(wn * C::NB, lane);
+  f32x16 acc[C::MB][C::NB];
+  product::run<C>(acc, A, B, ra, rb, k, lds);
+
+  const int l32 = lane & 31, h = lane >> 5;
+  const int mw = m0 + wm * C::MB * 32 + 4 * h;  // this lane's first m
+  const int nw = n0 + wn * C::NB * 32 + l32;    // and n
+  if constexpr (USE == kStats) {
+    float* red = reinterpret_cast<float*>(lds);  // [3][WM][BN]
+    product::barrier();                          // the last step has been read
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+      float top = kNegInf;
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (mw + 32 * mb + 8 * (i >> 2) + (i & 3) >= j.m) acc[mb][nb][i] = kNegInf;
+          top = fmaxf(top, acc[mb][nb][i]);
+        }
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float m = top == kNegInf ? 0.f : top * j.c;
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float y = fmaf(acc[mb][nb][i], j.c, -m), e = ex2(y);
+          s += e;
+          t = fmaf(e, fmaxf(y, -3.4e38f), t);  // e = 0 where y = -inf
+        }
+      s += __shfl_xor(s, 32, 64);
+      t += __shfl_xor(t, 32, 64);
+      if (h == 0) {
+        const int o = wm * BN + (wn * C::NB + nb) * 32 + l32;
+        red[o] = top == kNegInf ? kNegInf : m;
+        red[o + WM * BN] = s;
+        red[o + 2 * WM * BN] = t;
+      }
+    }
+    __syncthreads();
+    for (int n = tid; n < BN && n0 + n < j.n; n += C::THREADS) {
+      LinearSums z{red[n], red[n + WM * BN], red[n + 2 * WM * BN]};
+#pragma unroll
+      for (int w = 1; w < WM; ++w)
+        z = join(z, LinearSums{red[n + w * BN], red[n + (WM + w) * BN], red[n + (2 * WM + w) * BN]});
+      j.part[int64_t(n0 + n) * j.m_tiles + mt] = make_float4(z.m, z.s, z.t, 0.f);
+    }
+  } else if constexpr (USE == kGrad) {
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+      const int n = nw + 32 * nb;
+      const bool valid = n < j.n;
+      const float4 rc = j.row[valid ? n : 0];
+      const int4 who = j.ids[valid ? n : 0];
+      const bool live = valid && rc.x != kNegInf;
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int m = mw + 32 * mb + 8 * (i >> 2) + (i & 3);
+          const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x);
+          const float d = ex2(lp * kLog2e) * fmaf(rc.z, fmaxf(lp, -1e4f), rc.y);  // exp is 0 below -104
+          acc[mb][nb][i] = live && m < j.m ? d : 0.f;
+        }
+      // The tokens behind the row: the first, and where there are more the others.
+      const int mine = live ? who.y : 0;
+      for (int t = 0; __any(t < mine); ++t) {
+        int v = -1;
+        float g = 0.f;
+        if (t < mine) {
+          if (t == 0) {
+            v = who.x;
+            g = rc.w;
+          } else {
+            const int at = la.seg_off[la.kid[who.z + t]];
+            v = token(la, at);
+            g = v >= 0 ? la.dlogp[at] * j.inv_t : 0.f;
+          }
+        }
+        const int o = v < 0 ? -1 : v - j.v0 - mw;  // from this lane's first m
+        if (!__any(v >= 0 && o >= 0 && o < 32 * C::MB)) continue;
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (v >= 0 && o == 32 * mb + 8 * (i >> 2) + (i & 3)) acc[mb][nb][i] += g;
+      }
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          put4<T>(j.d, int64_t(n) * j.ldd + mw + 32 * mb + 8 * i, acc[mb][nb][4 * i], acc[mb][nb][4 * i + 1],
+                  acc[mb][nb][4 * i + 2], acc[mb][nb][4 * i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+      const int n = nw + 32 * nb;
+      if (n >= j.n) continue;
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = mw + 32 * mb + 8 * i;
+          if (m >= j.m) continue;
+          const int64_t o = int64_t(n) * j.m + m;
+          float4 x = make_float4(acc[mb][nb][4 * i], acc[mb][nb][4 * i + 1], acc[mb][nb][4 * i + 2],
+                                 acc[mb][nb][4 * i + 3]);
+          if (j.add) {
+            const float4 y = *reinterpret_cast<const float4*>(j.add + o);
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+          }
+          if (j.out) put4<T>(j.out, o, x.x, x.y, x.z, x.w);
+          else *reinterpret_cast<float4*>(j.acc + split * j.acc_split + o) = x;
+        }
+    }
+  }
+}
+
+// The sums of splits (and of `add`), to fp32 or the gradient itself; quads of
+// elements, n of them.
+template <typename T>
+__global__ __launch_bounds__(256) void split_sum_kernel(const float* part, int64_t acc_split, int splits,
+                                                        const float* add, float* acc, void* out, int64_t quads) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < quads; i += int64_t(gridDim.x) * 256) {
+    float4 x = add ? reinterpret_cast<const float4*>(add)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 y = reinterpret_cast<const float4*>(part + s * acc_split)[i];
+      x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+    if (out) put4<T>(out, 4 * i, x.x, x.y, x.z, x.w);
+    else reinterpret_cast<float4*>(acc)[i] = x;
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+// A wave a row: joins the tiles' sums; log probabilities of the tokens behind it.
+template <typename T>
+__global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4* part, int slots) {
+  constexpr int N = 16 / sizeof(T);
+  const int lane = threadIdx.x & 63;
+  const int lr = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (lr >= a.n_rows) return;
+  const Behind b(a, a.first_row + lr, lane);
+  LinearSums z{kNegInf, 0.f, 0.f};
+  for (int i = lane; i < slots; i += 64) {
+    const float4 y = part[int64_t(lr) * slots + i];
+    z = join(z, LinearSums{y.x, y.y, y.z});
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1)
+    z = join(z, LinearSums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)});
+  const bool empty = z.m == kNegInf && z.s == 0.f;  // every logit is -inf
+  const float ls = __log2f(z.s);
+  if (lane == 0) {
+    a.lse[lr] = empty ? kNegInf : (z.m + ls) * kLn2;
+    a.entropy[lr] = empty ? 0.f : (ls - z.t / z.s) * kLn2;
+    if (b.root_start) a.logp[a.first_row + lr] = 0.f;
+  }
+  const float c = a.inv_t * kLog2e;
+  const char* hrow = static_cast<const char*>(a.hidden) + int64_t(lr) * a.ld * sizeof(T);
+  for (int j = 0; j < b.n; ++j) {
+    const int t = b.at(j), id = token(a, t);
+    float x = 0.f;
+    if (id >= 0) {
+      const char* wrow = static_cast<const char*>(a.weight) + int64_t(id) * a.width * sizeof(T);
+      for (int i = lane; i < a.width / N; i += 64) {
+        const uint4 u = reinterpret_cast<const uint4*>(hrow)[i], w = reinterpret_cast<const uint4*>(wrow)[i];
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (sizeof(T) == 4) {
+            x = fmaf(__uint_as_float(uu[q]), __uint_as_float(ww[q]), x);
+          } else {
+            x = fmaf(chunk::lo_f(uu[q]), chunk::lo_f(ww[q]), x);
+            x = fmaf(chunk::hi_f(uu[q]), chunk::hi_f(ww[q]), x);
+          }
+        }
+      }
+      x = wave_sum(x);
+    }
+    if (lane == 0) a.logp[t] = id < 0 ? 0.f : empty ? kNegInf : (fmaf(x, c, -z.m) - ls) * kLn2;
+  }
+}
+
+// A wave a row: the coefficients of its gradient.
+__global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int4* ids) {
+  const int lane = threadIdx.x & 63;
+  const int lr = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (lr >= a.n_rows) return;
+  const Behind b(a, a.first_row + lr, lane);
+  float g = 0.f, g0 = 0.f;
+  int id0 = -1;
+  for (int j = lane; j < b.n; j += 64) {
+    const int t = b.at(j), id = token(a, t);
+    const float gj = id < 0 ? 0.f : a.dlogp[t];
+    g += gj;
+    if (j == 0) {
+      g0 = gj;
+      id0 = id;
+    }
+  }
+  g = wave_sum(g);
+  if (lane != 0) return;
+  const float dh = a.dentropy ? a.dentropy[lr] : 0.f;
+  row[lr] = make_float4(a.lse_in[lr], -(g + (a.dentropy ? dh * a.entropy_in[lr] : 0.f)) * a.inv_t, -dh * a.inv_t,
+                        g0 * a.inv_t);
+  ids[lr] = make_int4(id0, b.n, b.kid ? static_cast<int>(b.kid - a.kid) : -1, 0);
+}
+
+// ---- launches -----------------------------------------------------------------------
+int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
+
+template <typename T, bool TA, bool TB, int BM, int BN, int WM, int WN, int S, Use USE, int OCC>
+hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
+  constexpr int BK = product::kStep / int(sizeof(T));
+  j.m_tiles = ceil_div(j.m, BM);
+  j.n_tiles = ceil_div(j.n, BN);
+  if (j.splits <= 1) {
+    j.splits = 1;
+    j.k_split = j.k;
+  } else {
+    j.k_split = ceil_div(ceil_div(j.k, j.splits), BK) * BK;
+    j.splits = ceil_div(j.k, j.k_split);
+  }
+  // 8 x 4 tiles run on an XCD's 32 CUs at a time.
+  j.band = j.n_tiles < 8 ? j.n_tiles : 8;
+  const int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
+  product_kernel<T, TA, TB, BM, BN, WM, WN, S, USE, OCC>
+      <<<static_cast<uint32_t>(groups), 64 * WM * WN, 0, stream>>>(j, a);
+  return hipGetLastError();
+}
+
+// By the tile sizes of `size`: 0: 128 x 64, 1: 128 x 128, 2: 256 x 256.
+template <typename T, bool TA, bool TB, Use USE>
+hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
+  if (size == 2) return launch_product<T, TA, TB, 256, 256, 2, 4, 2, USE, 2>(j, a, stream);
+  if constexpr (!TB)
+    if (size == 0) return launch_product<T, TA, TB, 128, 64, 4, 1, 3, USE, 2>(j, a, stream);
+  return launch_product<T, TA, TB, 128, 128, 2, 2, 2, USE, 2>(j, a, stream);
+}
+
+template <typename T>
+hipError_t forward(const LinearArgs& a, const LinearWork& w, hipStream_t stream) {
+  for (int64_t r0 = 0; r0 < a.n_rows; r0 += w.rows) {
+    LinearArgs b = a;
+    b.n_rows = static_cast<int32_t>(a.n_rows - r0 < w.rows ? a.n_rows - r0 : w.rows);
+    b.first_row = static_cast<int32_t>(a.first_row + r0);
+    b.hidden = static_cast<const char*>(a.hidden) + r0 * a.ld * sizeof(T);
+    b.entropy = a.entropy + r0;
+    b.lse = a.lse + r0;
+    Job j{};
+    j.a = static_cast<const char*>(a.weight);
+    j.b = static_cast<const char*>(b.hidden);
+    j.lda = int64_t(a.width) * sizeof(T);
+    j.ldb = a.ld * sizeof(T);
+    j.m = a.vocab;
+    j.n = b.n_rows;
+    j.k = a.width;
+    j.c = a.inv_t * kLog2e;
+    j.part = reinterpret_cast<float4*>(a.ws);
+    hipError_t e = launch_sized<T, false, false, kStats>(w.size, j, b, stream);
+    if (e != hipSuccess) return e;
+    const int slots = ceil_div(a.vocab, w.size == 2 ? 256 : 128);
+    finish_kernel<T><<<ceil_div(b.n_rows, 4), 256, 0, stream>>>(b, j.part, slots);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// out (or acc) = add + the product, over splits where there are several.
+template <typename T, bool TB>
+hipError_t sum_product(int size, int splits, float* parts, Job j, float* acc, const float* add, void* out,
+                       const LinearArgs& a, hipStream_t stream) {
+  j.splits = splits;
+  if (splits <= 1) {
+    j.acc = acc;
+    j.add = add;
+    j.out = out;
+    return launch_sized<T, true, TB, kSum>(size, j, a, stream);
+  }
+  j.acc = parts;
+  j.acc_split = int64_t(j.m) * j.n;
+  hipError_t e = launch_sized<T, true, TB, kSum>(size, j, a, stream);
+  if (e != hipSuccess) return e;
+  constexpr int BK = product::kStep / int(sizeof(T));
+  const int k_split = ceil_div(ceil_div(j.k, splits), BK) * BK;
+  const int64_t quads = j.acc_split / 4;
+  const int64_t groups = (quads + 255) / 256;
+  split_sum_kernel<T><<<static_cast<uint32_t>(groups < 8192 ? groups : 8192), 256, 0, stream>>>(
+      parts, j.acc_split, ceil_div(j.k, k_split), add, acc, out, quads);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t backward(const LinearArgs& a, const LinearWork& w, hipStream_t stream) {
+  char* base = static_cast<char*>(a.ws);
+  float4* row = reinterpret_cast<float4*>(base);
+  int4* ids = reinterpret_cast<int4*>(base + w.ids);
+  float* dh = reinterpret_cast<float*>(base + w.dhidden);
+  float* dw = reinterpret_cast<float*>(base + w.dweight);
+  float* parts = reinterpret_cast<float*>(base + w.parts);
+  const int64_t es = sizeof(T);
+  for (int64_t r0 = 0; r0 < a.n_rows; r0 += w.rows) {
+    LinearArgs b = a;
+    b.n_rows = static_cast<int32_t>(a.n_rows - r0 < w.rows ? a.n_rows - r0 : w.rows);
+    b.first_row = static_cast<int32_t>(a.first_row + r0);
+    b.hidden = static_cast<const char*>(a.hidden) + r0 * a.ld * es;
+    b.lse_in = a.lse_in + r0;
+    b.entropy_in = a.entropy_in ? a.entropy_in + r0 : nullptr;
+    b.dentropy = a.dentropy ? a.dentropy + r0 : nullptr;
+    row_kernel<<<ceil_div(b.n_rows, 4), 256, 0, stream>>>(b, row, ids);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const bool first_rows = r0 == 0, last_rows = r0 + w.rows >= a.n_rows;
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += w.piece) {
+      const int32_t nv = static_cast<int32_t>(a.vocab - v0 < w.piece ? a.vocab - v0 : w.piece);
+      const bool first = v0 == 0, last = v0 + w.piece >= a.vocab;
+      const char* weight = static_cast<const char*>(a.weight) + v0 * a.width * es;
+      Job j{};  // D of this piece
+      j.a = weight;
+      j.b = static_cast<const char*>(b.hidden);
+      j.lda = a.width * es;
+      j.ldb = a.ld * es;
+      j.m = nv;
+      j.n = b.n_rows;
+      j.k = a.width;
+      j.row = row;
+      j.ids = ids;
+      j.inv_t = a.inv_t;
+      j.v0 = static_cast<int32_t>(v0);
+      j.d = base + w.d;
+      j.ldd = w.ldd;
+      e = launch_sized<T, false, false, kGrad>(w.size, j, b, stream);
+      if (e != hipSuccess) return e;
+      j = Job{};  // dhidden [rows, width] += D weight
+      j.a = weight;
+      j.b = base + w.d;
+      j.lda = a.width * es;
+      j.ldb = w.ldd * es;
+      j.m = a.width;
+      j.n = b.n_rows;
+      j.k = nv;
+      e = sum_product<T, false>(w.size_h, w.splits_h, parts, j, dh, first ? nullptr : dh,
+                                last ? static_cast<char*>(a.dhidden) + r0 * a.width * es : nullptr, b, stream);
+      if (e != hipSuccess) return e;
+      j.a = static_cast<const char*>(b.hidden);  // dweight [nv, width] += D^T hidden
+      j.lda = a.ld * es;
+      j.n = nv;
+      j.k = b.n_rows;
+      float* acc = dw + v0 * a.width;
+      e = sum_product<T, true>(w.size_w, w.splits_w, parts, j, acc, first_rows ? nullptr : acc,
+                               last_rows ? static_cast<char*>(a.dweight) + v0 * a.width * es : nullptr, b, stream);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinearArgs& a, const LinearWork& w, int dtype, hipStream_t stream) {
+  return dtype == TREE_DTYPE_BF16 ? forward<uint16_t>(a, w, stream) : forward<float>(a, w, stream);
+}
+
+hipError_t launch_linear_backward(const LinearArgs& a, const LinearWork& w, int dtype, hipStream_t stream) {
+  return dtype == TREE_DTYPE_BF16 ? backward<uint16_t>(a, w, stream) : backward<float>(a, w, stream);
+}
+
+}  // namespace tg

@@ -25,6 +25,7 @@
 #include "../../include/tree_gdn.h"
 #include "chunk_mfma.hpp"
 #include "launch.hpp"
+#include "trie_rows.hpp"
 
 namespace tg {
 
@@ -92,44 +93,6 @@ struct Slice {
   __device__ __forceinline__ int ends() const { return head + n - tail; }
   __device__ __forceinline__ int end_col(int i) const { return i < head ? i : tail + i - head; }
 };
-
-// The segment of packed row r: a 64-way search by the whole wave.
-__device__ __forceinline__ int seg_of(const int32_t* seg_off, int n_seg, int r, int lane) {
-  int lo = 0, hi = n_seg;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) >> 6, at = lo + lane * step;
-    const bool le = at < hi && seg_off[at] <= r;
-    lo += (__popcll(__ballot(le)) - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
-// The tokens behind packed row r.
-struct Behind {
-  int n, row;         // how many; the only one's row (middle of a segment)
-  const int32_t *kid, *seg_off;
-  bool root_start;    // r is a root's first token (it has no row in front)
-  __device__ __forceinline__ Behind(const LogprobArgs& a, int r, int lane) : seg_off(a.seg_off) {
-    const int s = seg_of(a.seg_off, a.n_seg, r, lane);
-    const bool last = r + 1 == a.seg_off[s + 1];
-    kid = last ? a.kid + a.kid_off[s] : nullptr;
-    n = last ? a.kid_off[s + 1] - a.kid_off[s] : 1;
-    row = r + 1;
-    root_start = a.parent[s] < 0 && r == a.seg_off[s];
-  }
-  __device__ __forceinline__ int at(int j) const { return kid ? seg_off[kid[j]] : row; }
-};
-
-// Token id of row t, or -1 where it is outside the vocabulary.
-__device__ __forceinline__ int token(const LogprobArgs& a, int t) {
-  if (a.token64) {
-    const int64_t x = static_cast<const int64_t*>(a.tokens)[t];
-    return x >= 0 && x < a.vocab ? static_cast<int>(x) : -1;
-  }
-  const int32_t x = static_cast<const int32_t*>(a.tokens)[t];
-  return x >= 0 && x < a.vocab ? x : -1;
-}
 
 // Thread j's token behind the row, if there is one, and its logit: half a dozen
 // dependent loads.
