@@ -249,7 +249,29 @@ struct Tile {
   static constexpr int LOADS = OpA::NI + OpB::NI;
 };
 
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// The fragments of 16 k of a wave's blocks.
+template <typename C>
+struct Frags {
+  uint4 a[C::MB], b[C::NB];
+  static constexpr int N = C::MB + C::NB;
+  // Loads the i-th of them, in the order in which the products use them.
+  __device__ __forceinline__ void load(int i, const typename C::RdA& ra, const typename C::RdB& rb, const char* ta,
+                                       const char* tb, int ks) {
+    if (i == 0) a[0] = ra.bf16(ta, 0, ks);
+    else if (i <= C::NB) b[i - 1] = rb.bf16(tb, i - 1, ks);
+    else a[i - C::NB] = ra.bf16(ta, i - C::NB, ks);
+  }
+};
+
 // acc = the tile's products over the k (>= 1) elements from where A and B stand.
+//
+// bf16: while the matrix units work on one fragment step, the next one's reads are
+// issued between its MFMAs, across the barrier into the next k-step too; fences
+// keep that order.  The barrier stands before the last fragment step of a k-step:
+// by then its last fragments have been read, so its place in the ring can be
+// staged anew, and the next k-step has had S - 1 steps' time to land.
 template <typename C>
 __device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA& A, typename C::OpB& B,
                                     const typename C::RdA& ra, const typename C::RdB& rb, int k, char* lds) {
@@ -267,32 +289,60 @@ __device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA
     A.stage(at + buf * C::STEP, k - t * C::BK);
     B.stage(at + buf * C::STEP + C::OpA::BYTES, C::B_PADDED ? C::BK : k - t * C::BK);
   };
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int t = 0; t < S - 1; ++t)
-    if (t < steps) stage(t, t);
-  int cur = 0, into = S - 1;
-  for (int t = 0; t < steps; ++t) {
-    // Step t has landed for every wave, and step t - 1 has been read by every wave.
-    if (t + S - 1 <= steps) wait_step<C::LOADS * (S - 2)>();
+    for (int t = 0; t < S; ++t)
+      if (t < steps) stage(t, t);
+    if (steps >= S) wait_step<C::LOADS * (S - 1)>();
     else wait_step<0>();
     barrier();
-    if (t + S - 1 < steps) stage(t + S - 1, into);
-    const char* ta = lds + cur * C::STEP;
-    const char* tb = ta + C::OpA::BYTES;
-    if constexpr (sizeof(T) == 2) {
+    Frags<C> f[2];
+#pragma unroll
+    for (int i = 0; i < Frags<C>::N; ++i) f[0].load(i, ra, rb, lds, lds + C::OpA::BYTES, 0);
+    int cur = 0;
+    for (int t = 0; t < steps; ++t) {
+      const int next = cur + 1 == S ? 0 : cur + 1;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        uint4 a[MB], b[NB];
+        const bool turn = ks == KS - 1;
+        if (turn) {
+          // Step t + 1 has landed for every wave, and step t has been read by every wave.
+          if (t + S <= steps) wait_step<C::LOADS * (S - 2)>();
+          else wait_step<0>();
+          barrier();
+        }
+        const char* ta = lds + (turn ? next : cur) * C::STEP;
+        const char* tb = ta + C::OpA::BYTES;
+        Frags<C>& x = f[ks & 1];
+        Frags<C>& y = f[(ks + 1) & 1];
+        constexpr int PER = (Frags<C>::N + MB * NB - 1) / (MB * NB);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) b[n] = rb.bf16(tb, n, ks);
+        for (int i = 0; i < MB * NB; ++i) {
+          acc[i / NB][i % NB] = mma(x.a[i / NB], x.b[i % NB], acc[i / NB][i % NB]);
 #pragma unroll
-        for (int m = 0; m < MB; ++m) a[m] = ra.bf16(ta, m, ks);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-          for (int n = 0; n < NB; ++n) acc[m][n] = mma(a[m], b[n], acc[m][n]);
+          for (int j = 0; j < PER; ++j)
+            if (i * PER + j < Frags<C>::N) y.load(i * PER + j, ra, rb, ta, tb, (ks + 1) % KS);
+          fence();
+        }
+        if (turn && t + S < steps) stage(t + S, cur);
       }
-    } else {
+      cur = next;
+    }
+    return;
+  }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int t = 0; t < S - 1; ++t)
+      if (t < steps) stage(t, t);
+    int cur = 0, into = S - 1;
+    for (int t = 0; t < steps; ++t) {
+      // Step t has landed for every wave, and step t - 1 has been read by every wave.
+      if (t + S - 1 <= steps) wait_step<C::LOADS * (S - 2)>();
+      else wait_step<0>();
+      barrier();
+      if (t + S - 1 < steps) stage(t + S - 1, into);
+      const char* ta = lds + cur * C::STEP;
+      const char* tb = ta + C::OpA::BYTES;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         Split b[NB];
@@ -311,9 +361,9 @@ __device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA
           for (int n = 0; n < NB; ++n) acc[m][n] = mma(a, b[n], acc[m][n]);
         }
       }
+      cur = cur + 1 == S ? 0 : cur + 1;
+      into = into + 1 == S ? 0 : into + 1;
     }
-    cur = cur + 1 == S ? 0 : cur + 1;
-    into = into + 1 == S ? 0 : into + 1;
   }
 }
 
