@@ -310,6 +310,7 @@ __device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA
           if (t + S <= steps) wait_step<C::LOADS * (S - 2)>();
           else wait_step<0>();
           barrier();
+          if (t + S < steps) stage(t + S, cur);
         }
         const char* ta = lds + (turn ? next : cur) * C::STEP;
         const char* tb = ta + C::OpA::BYTES;
@@ -324,7 +325,6 @@ __device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA
             if (i * PER + j < Frags<C>::N) y.load(i * PER + j, ra, rb, ta, tb, (ks + 1) % KS);
           fence();
         }
-        if (turn && t + S < steps) stage(t + S, cur);
       }
       cur = next;
     }
