@@ -5,12 +5,12 @@
 // contiguous (rows k), so that one kernel serves a product and both of its
 // gradients without a transposed copy of anything.  A k-step of 128 bytes (64
 // bf16, 32 fp32) of both goes to LDS by DMA, S steps in a ring; waves read
-// their 32x32x16 MFMA fragments from there, rows by 16-byte reads, TR tiles by
+// their 16x16x32 MFMA fragments from there, rows by 16-byte reads, TR tiles by
 // the transposing read (bf16) or by words (fp32).
 //
-// A wave owns MB x NB blocks of 32 x 32.  Lane l of a block holds column n = l %
-// 32 and rows m = 8 (i / 4) + 4 (l / 32) + i % 4 of register i: four neighbouring
-// m of one n, which is 8 or 16 bytes of a row of `out`.
+// A wave owns MB x NB blocks of 16 x 16.  Lane l of a block holds column n = l %
+// 16 and rows m = 4 (l / 16) + i of register i: four neighbouring m of one n,
+// which is 8 or 16 bytes of a row of `out`.
 //
 // fp32: a value is the sum of three bf16 (rounded, the rest rounded, the rest of
 // that: exact to 2^-26 of it), and a product of two the six largest of the nine
@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
+#include <utility>
 
 #include "chunk_mfma.hpp"
 
@@ -31,7 +33,7 @@ namespace product {
 using chunk::bf16x8;
 using chunk::pk2;
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+using chunk::f32x4;
 typedef __attribute__((address_space(3))) const chunk::u32x4 lds_u4;
 typedef __attribute__((address_space(3))) const uint32_t lds_u1;
 
@@ -45,23 +47,22 @@ __device__ __forceinline__ uint4 lds16(const char* p) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 bytes a lane to LDS at lds + 16 lane, from src + off (src the same for all
-// lanes) or from a lane's own address.  In inline asm, because the compiler
+// 16 bytes a lane to LDS at lds + IMM + 16 lane, from src + off (src the same for
+// all lanes) or from a lane's own address.  In inline asm, because the compiler
 // would otherwise wait for all DMA in flight before any read of LDS; it has no
 // output registers, and wait_step() is the wait.
+template <int IMM>
 __device__ __forceinline__ void dma16(uint64_t src, uint32_t off, uint32_t lds) {
-  int m0;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
-               : "=&s"(m0)
-               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(src)
-               : "memory");
+  asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "i"(IMM), "v"(off), "s"(src)
+               : "memory", "m0", "scc");
 }
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
-  int m0;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
-               : "=&s"(m0)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_at(const char* lds) {
   return __builtin_amdgcn_readfirstlane(
@@ -85,12 +86,12 @@ struct Operand {
   uint32_t off[NI];  // this lane's pieces
   int wave, lane;
 
-  // The 16-byte piece c of row r sits at slot c ^ swz(r): operand reads (32 rows,
-  // one piece each) and transposing reads (4 rows x 64 bytes) then spread
-  // evenly over the banks.
+  // The 16-byte piece c of row r sits at slot c ^ swz(r): operand reads (16 rows,
+  // one piece each), transposing reads (4 rows x 64 bytes) and reads by words (4
+  // rows 8 apart x 64 bytes) then touch every bank once.
   static __device__ __forceinline__ int swz(int r) {
     if (!TR) return 4 * ((r >> 1) & 1) + ((r >> 2) & 3);
-    return ES == 2 ? 4 * (r & 3) + ((r >> 2) & 3) : 8 * ((r >> 3) & 1);
+    return ES == 2 ? 4 * (r & 3) + ((r >> 2) & 3) : 4 * ((r >> 3) & 3);
   }
   __device__ __forceinline__ static int slot_row(int q, int lane) { return (q * 1024 + lane * 16) / RB; }
   __device__ __forceinline__ static int slot_chunk(int q, int lane) {
@@ -113,11 +114,24 @@ struct Operand {
       else off[i] = static_cast<uint32_t>(min(r, most - 1) * ld) + 16u * c;
     }
   }
-  // Starts the DMA of a step of `k` (<= BK) valid k, and moves on.
+  // The I-th DMA instruction of a whole step.  `lds` is where this wave's first one
+  // goes.
+  template <int I>
+  __device__ __forceinline__ void issue(uint32_t lds) {
+    if constexpr (I < NI) dma16<I * W * 1024>(src, off[I], lds);
+  }
+  template <int I = 0>
+  __device__ __forceinline__ void issue_all(uint32_t lds) {
+    if constexpr (I < NI) {
+      issue<I>(lds);
+      issue_all<I + 1>(lds);
+    }
+  }
+  __device__ __forceinline__ void advance() { src += TR ? BK * ld : kStep; }
+  // Starts the DMA of a step of `k` valid k, and moves on.
   __device__ __forceinline__ void stage(uint32_t lds, int k) {
     if (k >= BK) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) dma16(src, off[i], lds + (wave + W * i) * 1024);
+      issue_all(lds);
     } else {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -126,45 +140,46 @@ struct Operand {
         // Rows k past the end repeat the last (the other operand is zero there).
         if (TR) p -= r >= k ? static_cast<int64_t>(r - (k - 1)) * ld : 0;
         else if (c * E16 >= k) p = reinterpret_cast<const char*>(&kZeros);
-        dma16(p, lds + q * 1024);
+        dma16(p, lds + W * i * 1024);
       }
     }
-    src += TR ? BK * ld : kStep;
+    advance();
   }
 };
 
-// Fragment reads of `NBLK` blocks of 32 rows from block `blk0` on.
+// Fragment reads of blocks of 16 rows (m or n) from block `blk0` on, 32 k each: lane l
+// has row l % 16 and k = 8 (l / 16) .. + 7.
 template <typename T, bool TR, int R>
 struct Reader {
   static constexpr int ES = sizeof(T);
   static constexpr int RB = TR ? R * ES : kStep;
   int base;
   __device__ __forceinline__ Reader(int blk0, int lane) {
-    const int r = lane & 31, h = lane >> 5, i = lane & 15;
+    const int i = lane & 15, g = lane >> 4;
     if (!TR) {
-      const int sw = 4 * ((r >> 1) & 1) + ((r >> 2) & 3);
-      base = (32 * blk0 + r) * RB + 16 * ((ES == 2 ? h : 2 * h) ^ sw);
+      const int sw = 4 * ((i >> 1) & 1) + ((i >> 2) & 3);
+      base = (16 * blk0 + i) * RB + 16 * ((ES == 2 ? g : 2 * g) ^ sw);
     } else if (ES == 2) {
-      const int sw = 4 * (i >> 2) + 2 * h;
-      base = (8 * h + (i >> 2)) * RB + 16 * ((4 * blk0 + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) ^ sw) + 8 * (i & 1);
+      const int sw = 4 * (i >> 2) + ((2 * g) & 3);
+      base = (8 * g + (i >> 2)) * RB + 16 * ((2 * blk0 + ((i & 3) >> 1)) ^ sw) + 8 * (i & 1);
     } else {
-      base = 8 * h * RB + 16 * ((8 * blk0 + (r >> 2)) ^ (8 * h)) + 4 * (r & 3);
+      base = 8 * g * RB + 16 * ((4 * blk0 + (i >> 2)) ^ (4 * g)) + 4 * (i & 3);
     }
   }
-  // bf16: fragment of 16 k from 16 ks on, block b.
+  // bf16: the fragment of block b (a multiple of its count below blk0), k from 32 ks on.
   __device__ __forceinline__ uint4 bf16(const char* t, int b, int ks) const {
     if constexpr (!TR) {
-      return lds16(t + ((base ^ (32 * ks)) + b * 32 * RB));
+      return lds16(t + ((base ^ (64 * ks)) + b * 16 * RB));
     } else {
-      const int o = (base ^ (64 * b)) + 16 * ks * RB;
-      const int o4 = (base ^ (64 * b) ^ 16) + (16 * ks + 4) * RB;
+      const int o = (base ^ (32 * b)) + 32 * ks * RB;
+      const int o4 = (base ^ (32 * b) ^ 16) + (32 * ks + 4) * RB;
       return chunk::cat(chunk::tile_tr(t, o), chunk::tile_tr(t, o4));
     }
   }
   // fp32: its 8 values.
-  __device__ __forceinline__ void f32(const char* t, int b, int ks, float (&x)[8]) const {
+  __device__ __forceinline__ void f32(const char* t, int b, float (&x)[8]) const {
     if constexpr (!TR) {
-      const int o = (base ^ (64 * ks)) + b * 32 * RB;
+      const int o = base + b * 16 * RB;
       const uint4 lo = lds16(t + o), hi = lds16(t + (o ^ 16));
       x[0] = __uint_as_float(lo.x), x[1] = __uint_as_float(lo.y), x[2] = __uint_as_float(lo.z),
       x[3] = __uint_as_float(lo.w);
@@ -172,8 +187,7 @@ struct Reader {
       x[7] = __uint_as_float(hi.w);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = __uint_as_float(*(lds_u1*)(t + ((base ^ (128 * b)) + (16 * ks + e) * RB)));
+      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(*(lds_u1*)(t + ((base ^ (64 * b)) + e * RB)));
     }
   }
 };
@@ -200,12 +214,12 @@ __device__ __forceinline__ Split split3(const float (&x)[8]) {
   return s;
 }
 
-__device__ __forceinline__ f32x16 mma(const uint4 a, const uint4 b, const f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+__device__ __forceinline__ f32x4 mma(const uint4 a, const uint4 b, const f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
 }
 // The six largest partial products, the smallest first.
-__device__ __forceinline__ f32x16 mma(const Split& a, const Split& b, f32x16 c) {
+__device__ __forceinline__ f32x4 mma(const Split& a, const Split& b, f32x4 c) {
   c = mma(a.p[1], b.p[1], c);
   c = mma(a.p[2], b.p[0], c);
   c = mma(a.p[0], b.p[2], c);
@@ -233,10 +247,10 @@ template <typename T_, bool TA, bool TB, int BM_, int BN_, int WM_, int WN_, int
 struct Tile {
   using T = T_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, W = WM * WN;
-  static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;
+  static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
   static constexpr int THREADS = 64 * W;
   static constexpr int BK = kStep / int(sizeof(T));
-  static constexpr int KS = BK / 16;  // fragments along a step
+  static constexpr int KS = BK / 32;  // fragments along a step
   // B stored by k: rows of zeros follow its last, up to a whole step (A's repeat
   // its last there).
   static constexpr bool B_PADDED = TB;
@@ -249,88 +263,120 @@ struct Tile {
   static constexpr int LOADS = OpA::NI + OpB::NI;
 };
 
+// f(std::integral_constant<int, 0>) .. f(.. N - 1).
+template <typename F, int... I>
+__device__ __forceinline__ void unrolled_(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  unrolled_(f, std::make_integer_sequence<int, N>{});
+}
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// The fragments of 16 k of a wave's blocks.
-template <typename C>
-struct Frags {
-  uint4 a[C::MB], b[C::NB];
-  static constexpr int N = C::MB + C::NB;
-  // Loads the i-th of them, in the order in which the products use them.
-  __device__ __forceinline__ void load(int i, const typename C::RdA& ra, const typename C::RdB& rb, const char* ta,
-                                       const char* tb, int ks) {
-    if (i == 0) a[0] = ra.bf16(ta, 0, ks);
-    else if (i <= C::NB) b[i - 1] = rb.bf16(tb, i - 1, ks);
-    else a[i - C::NB] = ra.bf16(ta, i - C::NB, ks);
+// When the next fragments are read: the MFMA (of MB x NB, all n of an m one after
+// another) behind which the i-th is, and which it is: b[n] as n, a[m] as NB + m.
+// b[0], a[0], the other b, the other a; a[m] is read over the one in use, so not before
+// its last MFMA; and none before `START`.
+template <int MB, int NB>
+struct Order {
+  static constexpr int N = MB + NB, START = MB * NB / 4;
+  int at[N] = {}, what[N] = {};
+  constexpr Order() {
+    int s = START - 1;
+    for (int i = 0; i < N; ++i) {
+      what[i] = i == 0 ? 0 : i == 1 ? NB : i <= NB ? i - 1 : i;
+      const int m = what[i] - NB, free = m < 0 ? 0 : NB * (m + 1) - 1;
+      s = s + 1 > free ? s + 1 : free;
+      if (s > MB * NB - 1) s = MB * NB - 1;
+      at[i] = s;
+    }
   }
 };
 
 // acc = the tile's products over the k (>= 1) elements from where A and B stand.
 //
-// bf16: while the matrix units work on one fragment step, the next one's reads are
-// issued between its MFMAs, across the barrier into the next k-step too; fences
-// keep that order.  The barrier stands before the last fragment step of a k-step:
-// by then its last fragments have been read, so its place in the ring can be
+// bf16: while the matrix units work on the fragments of 32 k, the next ones' reads
+// are issued between the MFMAs, across the barrier into the next k-step too; fences
+// keep that order.  The barrier stands a quarter into the last fragments of a
+// k-step: by then those have been read, so the step's place in the ring can be
 // staged anew, and the next k-step has had S - 1 steps' time to land.
 template <typename C>
-__device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA& A, typename C::OpB& B,
+__device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA& A, typename C::OpB& B,
                                     const typename C::RdA& ra, const typename C::RdB& rb, int k, char* lds) {
   using T = typename C::T;
   constexpr int MB = C::MB, NB = C::NB, KS = C::KS, S = C::S;
-  const uint32_t at = lds_at(lds);
+  const uint32_t at = lds_at(lds) + A.wave * 1024;
   const int steps = (k + C::BK - 1) / C::BK;
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
+    for (int n = 0; n < NB; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   const auto stage = [&](int t, int buf) {
     A.stage(at + buf * C::STEP, k - t * C::BK);
     B.stage(at + buf * C::STEP + C::OpA::BYTES, C::B_PADDED ? C::BK : k - t * C::BK);
   };
   if constexpr (sizeof(T) == 2) {
+    constexpr Order<MB, NB> order;
+    static_assert(KS % 2 == 0, "b alternates");
 #pragma unroll
     for (int t = 0; t < S; ++t)
       if (t < steps) stage(t, t);
     if (steps >= S) wait_step<C::LOADS * (S - 1)>();
     else wait_step<0>();
     barrier();
-    Frags<C> f[2];
+    uint4 a[MB], b[2][NB];
 #pragma unroll
-    for (int i = 0; i < Frags<C>::N; ++i) f[0].load(i, ra, rb, lds, lds + C::OpA::BYTES, 0);
+    for (int n = 0; n < NB; ++n) b[0][n] = rb.bf16(lds + C::OpA::BYTES, n, 0);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) a[m] = ra.bf16(lds, m, 0);
     int cur = 0;
     for (int t = 0; t < steps; ++t) {
       const int next = cur + 1 == S ? 0 : cur + 1;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const bool turn = ks == KS - 1;
-        if (turn) {
-          // Step t + 1 has landed for every wave, and step t has been read by every wave.
-          if (t + S <= steps) wait_step<C::LOADS * (S - 2)>();
-          else wait_step<0>();
-          barrier();
-          if (t + S < steps) stage(t + S, cur);
-        }
+      const uint32_t into = at + cur * C::STEP;
+      unrolled<KS>([&](auto ks_) {
+        constexpr int ks = decltype(ks_)::value;
+        constexpr bool turn = ks == KS - 1;
         const char* ta = lds + (turn ? next : cur) * C::STEP;
         const char* tb = ta + C::OpA::BYTES;
-        Frags<C>& x = f[ks & 1];
-        Frags<C>& y = f[(ks + 1) & 1];
-        constexpr int PER = (Frags<C>::N + MB * NB - 1) / (MB * NB);
+        bool whole = false;
+        unrolled<MB * NB>([&](auto slot) {
+          constexpr int i = decltype(slot)::value;
+          acc[i / NB][i % NB] = mma(a[i / NB], b[ks & 1][i % NB], acc[i / NB][i % NB]);
+          if constexpr (turn && i == order.START - 1) {
+            // Step t + 1 has landed for every wave, and step t has been read by every wave.
+            if (t + S <= steps) wait_step<C::LOADS * (S - 2)>();
+            else wait_step<0>();
+            barrier();
+            whole = k - (t + S) * C::BK >= C::BK;
+            if (!whole && t + S < steps) stage(t + S, cur);
+          }
 #pragma unroll
-        for (int i = 0; i < MB * NB; ++i) {
-          acc[i / NB][i % NB] = mma(x.a[i / NB], x.b[i % NB], acc[i / NB][i % NB]);
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (i * PER + j < Frags<C>::N) y.load(i * PER + j, ra, rb, ta, tb, (ks + 1) % KS);
+          for (int j = 0; j < order.N; ++j)
+            if (order.at[j] == i) {
+              const int w = order.what[j];
+              if (w < NB) b[(ks + 1) & 1][w] = rb.bf16(tb, w, (ks + 1) % KS);
+              else a[w - NB] = ra.bf16(ta, w - NB, (ks + 1) % KS);
+            }
+          if constexpr (turn && i >= order.START) {
+            constexpr int SLOTS = MB * NB - order.START, D = (C::LOADS + SLOTS - 1) / SLOTS;
+            if (whole)
+              unrolled<D>([&](auto d) {
+                constexpr int q = (i - order.START) * D + decltype(d)::value;
+                if constexpr (q < C::OpA::NI) A.template issue<q>(into);
+                else if constexpr (q < C::LOADS) B.template issue<q - C::OpA::NI>(into + C::OpA::BYTES);
+              });
+          }
           fence();
+        });
+        if (turn && whole) {
+          A.advance();
+          B.advance();
         }
-      }
+      });
       cur = next;
     }
-    return;
-  }
-  if constexpr (sizeof(T) == 4) {
+  } else {
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
       if (t < steps) stage(t, t);
@@ -343,23 +389,20 @@ __device__ __forceinline__ void run(f32x16 (&acc)[C::MB][C::NB], typename C::OpA
       if (t + S - 1 < steps) stage(t + S - 1, into);
       const char* ta = lds + cur * C::STEP;
       const char* tb = ta + C::OpA::BYTES;
+      Split b[NB];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        Split b[NB];
+      for (int n = 0; n < NB; ++n) {
+        float x[8];
+        rb.f32(tb, n, x);
+        b[n] = split3(x);
+      }
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          float x[8];
-          rb.f32(tb, n, ks, x);
-          b[n] = split3(x);
-        }
+      for (int m = 0; m < MB; ++m) {
+        float x[8];
+        ra.f32(ta, m, x);
+        const Split a = split3(x);
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          float x[8];
-          ra.f32(ta, m, ks, x);
-          const Split a = split3(x);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) acc[m][n] = mma(a, b[n], acc[m][n]);
-        }
+        for (int n = 0; n < NB; ++n) acc[m][n] = mma(a, b[n], acc[m][n]);
       }
       cur = cur + 1 == S ? 0 : cur + 1;
       into = into + 1 == S ? 0 : into + 1;

@@ -30,7 +30,7 @@ namespace {
 
 using chunk::ex2;
 using chunk::kLog2e;
-using product::f32x16;
+using chunk::f32x4;
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -119,12 +119,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
   B.init(j.b, j.ldb, n0, j.n - n0, k0, wave, lane);
   const typename C::RdA ra(wm * C::MB, lane);
   const typename C::RdB rb(wn * C::NB, lane);
-  f32x16 acc[C::MB][C::NB];
+  f32x4 acc[C::MB][C::NB];
   product::run<C>(acc, A, B, ra, rb, k, lds);
 
-  const int l32 = lane & 31, h = lane >> 5;
-  const int mw = m0 + wm * C::MB * 32 + 4 * h;  // this lane's first m
-  const int nw = n0 + wn * C::NB * 32 + l32;    // and n
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int mw = m0 + wm * C::MB * 16 + 4 * g4;  // this lane's first m
+  const int nw = n0 + wn * C::NB * 16 + l16;     // and n
   if constexpr (USE == kStats) {
     float* red = reinterpret_cast<float*>(lds);  // [3][WM][BN]
     product::barrier();                          // the last step has been read
@@ -134,25 +134,28 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (mw + 32 * mb + 8 * (i >> 2) + (i & 3) >= j.m) acc[mb][nb][i] = kNegInf;
+        for (int i = 0; i < 4; ++i) {
+          if (mw + 16 * mb + i >= j.m) acc[mb][nb][i] = kNegInf;
           top = fmaxf(top, acc[mb][nb][i]);
         }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = top == kNegInf ? 0.f : top * j.c;
       float s = 0.f, t = 0.f;
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const float y = fmaf(acc[mb][nb][i], j.c, -m), e = ex2(y);
           s += e;
           t = fmaf(e, fmaxf(y, -3.4e38f), t);  // e = 0 where y = -inf
         }
+      s += __shfl_xor(s, 16, 64);
+      t += __shfl_xor(t, 16, 64);
       s += __shfl_xor(s, 32, 64);
       t += __shfl_xor(t, 32, 64);
-      if (h == 0) {
-        const int o = wm * BN + (wn * C::NB + nb) * 32 + l32;
+      if (g4 == 0) {
+        const int o = wm * BN + (wn * C::NB + nb) * 16 + l16;
         red[o] = top == kNegInf ? kNegInf : m;
         red[o + WM * BN] = s;
         red[o + 2 * WM * BN] = t;
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
   } else if constexpr (USE == kGrad) {
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb) {
-      const int n = nw + 32 * nb;
+      const int n = nw + 16 * nb;
       const bool valid = n < j.n;
       const float4 rc = j.row[valid ? n : 0];
       const int4 who = j.ids[valid ? n : 0];
@@ -177,8 +180,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int m = mw + 32 * mb + 8 * (i >> 2) + (i & 3);
+        for (int i = 0; i < 4; ++i) {
+          const int m = mw + 16 * mb + i;
           const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x);
           const float d = ex2(lp * kLog2e) * fmaf(rc.z, fmaxf(lp, -1e4f), rc.y);  // exp is 0 below -104
           acc[mb][nb][i] = live && m < j.m ? d : 0.f;
@@ -199,41 +202,36 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
           }
         }
         const int o = v < 0 ? -1 : v - j.v0 - mw;  // from this lane's first m
-        if (!__any(v >= 0 && o >= 0 && o < 32 * C::MB)) continue;
+        if (!__any(v >= 0 && o >= 0 && o < 16 * C::MB)) continue;
 #pragma unroll
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (v >= 0 && o == 32 * mb + 8 * (i >> 2) + (i & 3)) acc[mb][nb][i] += g;
+          for (int i = 0; i < 4; ++i)
+            if (v >= 0 && o == 16 * mb + i) acc[mb][nb][i] += g;
       }
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          put4<T>(j.d, int64_t(n) * j.ldd + mw + 32 * mb + 8 * i, acc[mb][nb][4 * i], acc[mb][nb][4 * i + 1],
-                  acc[mb][nb][4 * i + 2], acc[mb][nb][4 * i + 3]);
+        put4<T>(j.d, int64_t(n) * j.ldd + mw + 16 * mb, acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2],
+                acc[mb][nb][3]);
     }
   } else {
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb) {
-      const int n = nw + 32 * nb;
+      const int n = nw + 16 * nb;
       if (n >= j.n) continue;
 #pragma unroll
-      for (int mb = 0; mb < C::MB; ++mb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = mw + 32 * mb + 8 * i;
-          if (m >= j.m) continue;
-          const int64_t o = int64_t(n) * j.m + m;
-          float4 x = make_float4(acc[mb][nb][4 * i], acc[mb][nb][4 * i + 1], acc[mb][nb][4 * i + 2],
-                                 acc[mb][nb][4 * i + 3]);
-          if (j.add) {
-            const float4 y = *reinterpret_cast<const float4*>(j.add + o);
-            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-          }
-          if (j.out) put4<T>(j.out, o, x.x, x.y, x.z, x.w);
-          else *reinterpret_cast<float4*>(j.acc + split * j.acc_split + o) = x;
+      for (int mb = 0; mb < C::MB; ++mb) {
+        const int m = mw + 16 * mb;
+        if (m >= j.m) continue;
+        const int64_t o = int64_t(n) * j.m + m;
+        float4 x = make_float4(acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2], acc[mb][nb][3]);
+        if (j.add) {
+          const float4 y = *reinterpret_cast<const float4*>(j.add + o);
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
+        if (j.out) put4<T>(j.out, o, x.x, x.y, x.z, x.w);
+        else *reinterpret_cast<float4*>(j.acc + split * j.acc_split + o) = x;
+      }
     }
   }
 }
@@ -351,7 +349,7 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
     j.splits = ceil_div(j.k, j.k_split);
   }
   // 8 x 4 tiles run on an XCD's 32 CUs at a time.
-  j.band = j.n_tiles < 8 ? j.n_tiles : 8;
+  j.band = j.n_tiles < 4 ? j.n_tiles : 4;
   const int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
   product_kernel<T, TA, TB, BM, BN, WM, WN, S, USE, OCC>
       <<<static_cast<uint32_t>(groups), 64 * WM * WN, 0, stream>>>(j, a);
