@@ -410,6 +410,118 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
   }
 }
 
+// A 256 x 256 tile of bf16 by 8 waves (2 along m, 4 along n), staged as four 128-row
+// halves A0, A1, B0, B1 of a 128-byte k-step, two steps in LDS.  A wave has 64 rows of each
+// A half and 32 of each B half, and takes the halves' products one after another: A0 B0,
+// A0 B1, A1 B1, A1 B0.  So each half is read in one go (over the fragments just used), and
+// its place in LDS is staged anew, two steps on, as soon as all waves have read it:
+// a DMA has one and a half steps' time to land, and DMA is spread over the step,
+// where staging whole steps (run()) gives one and a burst.
+template <bool TA, bool TB>
+struct Big {
+  using T = uint16_t;
+  static constexpr bool TRA = TA, TRB = TB;
+  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, W = 8, MB = 8, NB = 4;
+  static constexpr int THREADS = 64 * W, BK = 64;
+  using OpA = Operand<T, TA, 128, W>;
+  using OpB = Operand<T, TB, 128, W>;
+  using RdA = Reader<T, TA, 128>;
+  using RdB = Reader<T, TB, 128>;
+  static constexpr int HALF = OpA::BYTES, STEP = 4 * HALF, LDS = 2 * STEP;
+  static_assert(OpA::NI == 2 && OpB::NI == 2, "what is counted as in flight");
+};
+
+template <bool TA, bool TB>
+__device__ __forceinline__ void run_big(f32x4 (&acc)[8][4], typename Big<TA, TB>::OpA (&A)[2],
+                                        typename Big<TA, TB>::OpB (&B)[2], const typename Big<TA, TB>::RdA& ra,
+                                        const typename Big<TA, TB>::RdB& rb, int k, char* lds) {
+  using C = Big<TA, TB>;
+  constexpr int HALF = C::HALF, BK = C::BK;
+  const uint32_t at = lds_at(lds) + A[0].wave * 1024;
+  const int steps = (k + BK - 1) / BK;
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // Groups of halves of step t: A0, B0, B1; and A1.
+  const auto stage0 = [&](int t) {
+    const uint32_t to = at + (t & 1) * C::STEP;
+    const int left = k - t * BK, left_b = TB ? BK : left;
+    A[0].stage(to, left);
+    B[0].stage(to + 2 * HALF, left_b);
+    B[1].stage(to + 3 * HALF, left_b);
+  };
+  const auto stage1 = [&](int t) { A[1].stage(at + (t & 1) * C::STEP + HALF, k - t * BK); };
+  stage0(0);
+  stage1(0);
+  if (steps > 1) {
+    stage0(1);
+    stage1(1);
+    wait_step<10>();
+  } else {
+    wait_step<2>();
+  }
+  barrier();
+  uint4 a[2][4], b[2][2][2];  // [ks][m], [half][ks][n]
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) a[ks][m] = ra.bf16(lds, m, ks);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) b[0][ks][n] = rb.bf16(lds + 2 * HALF, n, ks);
+  }
+  for (int t = 0; t < steps; ++t) {
+    const char* now = lds + (t & 1) * C::STEP;
+    const char* next = lds + ((t + 1) & 1) * C::STEP;
+    const uint32_t to = at + (t & 1) * C::STEP;
+    const bool whole = k - (t + 2) * BK >= BK;  // step t + 2 is there, and whole
+    unrolled<64>([&](auto slot) {
+      constexpr int s = decltype(slot)::value;
+      constexpr int p = s / 16, ks = s / 8 % 2, m = s / 2 % 4, n = s % 2;
+      constexpr int ah = p >= 2, bh = p == 1 || p == 2;
+      acc[4 * ah + m][2 * bh + n] = mma(a[ks][m], b[bh][ks][n], acc[4 * ah + m][2 * bh + n]);
+      // Reads, each behind the last use of what it overwrites.
+      if constexpr (s >= 2 && s < 6) b[1][(s - 2) / 2][s % 2] = rb.bf16(now + 3 * HALF, s % 2, (s - 2) / 2);
+      if constexpr (p == 1 && n == 1) a[ks][m] = ra.bf16(now + HALF, m, ks);
+      if constexpr (p == 3 && n == 1) a[ks][m] = ra.bf16(next, m, ks);
+      if constexpr (s == 55 || s == 56) b[0][0][s - 55] = rb.bf16(next + 2 * HALF, s - 55, 0);
+      if constexpr (s == 62 || s == 63) b[0][1][s - 62] = rb.bf16(next + 2 * HALF, s - 62, 1);
+      if constexpr (s == 14) {
+        // A1 of this step has landed for every wave; every wave has read A0, B0 and B1.
+        if (t + 1 < steps) wait_step<8>();
+        else wait_step<0>();
+        barrier();
+        if (!whole && t + 2 < steps) stage0(t + 2);
+      }
+      if constexpr (s == 44) {
+        // A0, B0 and B1 of the next step have landed; every wave has read A1.
+        if (t + 2 < steps) wait_step<8>();
+        else wait_step<0>();
+        barrier();
+        if (!whole && t + 2 < steps) stage1(t + 2);
+      }
+      if constexpr (s >= 15 && s <= 25 && s % 2 == 1) {
+        constexpr int q = (s - 15) / 2;
+        if (whole) {
+          if constexpr (q < 2) A[0].template issue<q>(to);
+          else if constexpr (q < 4) B[0].template issue<q - 2>(to + 2 * HALF);
+          else B[1].template issue<q - 4>(to + 3 * HALF);
+        }
+      }
+      if constexpr (s == 46 || s == 48) {
+        if (whole) A[1].template issue<(s - 46) / 2>(to + HALF);
+      }
+      fence();
+    });
+    if (whole) {
+      A[0].advance();
+      A[1].advance();
+      B[0].advance();
+      B[1].advance();
+    }
+  }
+}
+
 // The tile that work-group `id` of `total` computes: neighbouring ids go to the 8
 // XCDs in turn, and each XCD is given a contiguous share of the tiles, so that
 // what its work-groups read together comes from its own L2.

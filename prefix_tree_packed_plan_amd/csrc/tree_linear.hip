@@ -96,9 +96,9 @@ struct Job {
 // T at the entries that stand behind it.
 //   row: (lse, ca, cb, g of the first token)
 //   ids: (the first token's entry or -1, tokens behind, first of them in kid or -1, 0)
-template <typename T, bool TA, bool TB, int BM, int BN, int WM, int WN, int S, Use USE, int OCC>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, LinearArgs la) {
-  using C = product::Tile<T, TA, TB, BM, BN, WM, WN, S>;
+template <typename T, typename C, bool BIG, Use USE>
+__global__ __launch_bounds__(C::THREADS, 2) void product_kernel(Job j, LinearArgs la) {
+  constexpr int BM = C::BM, BN = C::BN, WM = C::WM;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -113,18 +113,35 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
   const int m0 = mt * BM, n0 = nt * BN;
   const int k0 = split * j.k_split, k = min(j.k - k0, j.k_split);
 
-  typename C::OpA A;
-  typename C::OpB B;
-  A.init(j.a, j.lda, m0, j.m - m0, k0, wave, lane);
-  B.init(j.b, j.ldb, n0, j.n - n0, k0, wave, lane);
-  const typename C::RdA ra(wm * C::MB, lane);
-  const typename C::RdB rb(wn * C::NB, lane);
   f32x4 acc[C::MB][C::NB];
-  product::run<C>(acc, A, B, ra, rb, k, lds);
+  if constexpr (BIG) {
+    typename C::OpA A[2];
+    typename C::OpB B[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // A second half past the end repeats the first (its results are not used).
+      const int ma = m0 + 128 * i < j.m ? m0 + 128 * i : m0, nb = n0 + 128 * i < j.n ? n0 + 128 * i : n0;
+      A[i].init(j.a, j.lda, ma, j.m - ma, k0, wave, lane);
+      B[i].init(j.b, j.ldb, nb, j.n - nb, k0, wave, lane);
+    }
+    const typename C::RdA ra(4 * wm, lane);
+    const typename C::RdB rb(2 * wn, lane);
+    product::run_big<C::TRA, C::TRB>(acc, A, B, ra, rb, k, lds);
+  } else {
+    typename C::OpA A;
+    typename C::OpB B;
+    A.init(j.a, j.lda, m0, j.m - m0, k0, wave, lane);
+    B.init(j.b, j.ldb, n0, j.n - n0, k0, wave, lane);
+    const typename C::RdA ra(wm * C::MB, lane);
+    const typename C::RdB rb(wn * C::NB, lane);
+    product::run<C>(acc, A, B, ra, rb, k, lds);
+  }
+  // Blocks mb, nb begin at m0 + am(mb), n0 + an(nb).
+  const auto am = [&](int mb) { return BIG ? 128 * (mb / 4) + 64 * wm + 16 * (mb % 4) : 16 * (wm * C::MB + mb); };
+  const auto an = [&](int nb) { return BIG ? 128 * (nb / 2) + 32 * wn + 16 * (nb % 2) : 16 * (wn * C::NB + nb); };
 
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int mw = m0 + wm * C::MB * 16 + 4 * g4;  // this lane's first m
-  const int nw = n0 + wn * C::NB * 16 + l16;     // and n
+  const int mw = m0 + 4 * g4, nw = n0 + l16;  // this lane's first m of block 0, and its n
   if constexpr (USE == kStats) {
     float* red = reinterpret_cast<float*>(lds);  // [3][WM][BN]
     product::barrier();                          // the last step has been read
@@ -135,7 +152,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (mw + 16 * mb + i >= j.m) acc[mb][nb][i] = kNegInf;
+          if (mw + am(mb) + i >= j.m) acc[mb][nb][i] = kNegInf;
           top = fmaxf(top, acc[mb][nb][i]);
         }
       top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -155,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
       s += __shfl_xor(s, 32, 64);
       t += __shfl_xor(t, 32, 64);
       if (g4 == 0) {
-        const int o = wm * BN + (wn * C::NB + nb) * 16 + l16;
+        const int o = wm * BN + an(nb) + l16;
         red[o] = top == kNegInf ? kNegInf : m;
         red[o + WM * BN] = s;
         red[o + 2 * WM * BN] = t;
@@ -172,7 +189,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
   } else if constexpr (USE == kGrad) {
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb) {
-      const int n = nw + 16 * nb;
+      const int n = nw + an(nb);
       const bool valid = n < j.n;
       const float4 rc = j.row[valid ? n : 0];
       const int4 who = j.ids[valid ? n : 0];
@@ -181,7 +198,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int m = mw + 16 * mb + i;
+          const int m = mw + am(mb) + i;
           const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x);
           const float d = ex2(lp * kLog2e) * fmaf(rc.z, fmaxf(lp, -1e4f), rc.y);  // exp is 0 below -104
           acc[mb][nb][i] = live && m < j.m ? d : 0.f;
@@ -202,26 +219,26 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void product_kernel(Job j, Linea
           }
         }
         const int o = v < 0 ? -1 : v - j.v0 - mw;  // from this lane's first m
-        if (!__any(v >= 0 && o >= 0 && o < 16 * C::MB)) continue;
+        if (!__any(v >= 0 && o >= 0 && o < BM)) continue;
 #pragma unroll
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (v >= 0 && o == 16 * mb + i) acc[mb][nb][i] += g;
+            if (v >= 0 && o == am(mb) + i) acc[mb][nb][i] += g;
       }
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
-        put4<T>(j.d, int64_t(n) * j.ldd + mw + 16 * mb, acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2],
+        put4<T>(j.d, int64_t(n) * j.ldd + mw + am(mb), acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2],
                 acc[mb][nb][3]);
     }
   } else {
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb) {
-      const int n = nw + 16 * nb;
+      const int n = nw + an(nb);
       if (n >= j.n) continue;
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb) {
-        const int m = mw + 16 * mb;
+        const int m = mw + am(mb);
         if (m >= j.m) continue;
         const int64_t o = int64_t(n) * j.m + m;
         float4 x = make_float4(acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2], acc[mb][nb][3]);
@@ -336,11 +353,11 @@ __global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int
 // ---- launches -----------------------------------------------------------------------
 int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
 
-template <typename T, bool TA, bool TB, int BM, int BN, int WM, int WN, int S, Use USE, int OCC>
+template <typename T, typename C, bool BIG, Use USE>
 hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   constexpr int BK = product::kStep / int(sizeof(T));
-  j.m_tiles = ceil_div(j.m, BM);
-  j.n_tiles = ceil_div(j.n, BN);
+  j.m_tiles = ceil_div(j.m, C::BM);
+  j.n_tiles = ceil_div(j.n, C::BN);
   if (j.splits <= 1) {
     j.splits = 1;
     j.k_split = j.k;
@@ -351,18 +368,21 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   // 8 x 4 tiles run on an XCD's 32 CUs at a time.
   j.band = j.n_tiles < 4 ? j.n_tiles : 4;
   const int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
-  product_kernel<T, TA, TB, BM, BN, WM, WN, S, USE, OCC>
-      <<<static_cast<uint32_t>(groups), 64 * WM * WN, 0, stream>>>(j, a);
+  product_kernel<T, C, BIG, USE><<<static_cast<uint32_t>(groups), C::THREADS, 0, stream>>>(j, a);
   return hipGetLastError();
 }
 
 // By the tile sizes of `size`: 0: 128 x 64, 1: 128 x 128, 2: 256 x 256.
 template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
-  if (size == 2) return launch_product<T, TA, TB, 256, 256, 2, 4, 2, USE, 2>(j, a, stream);
+  using product::Tile;
+  if (size == 2) {
+    if constexpr (sizeof(T) == 2) return launch_product<T, product::Big<TA, TB>, true, USE>(j, a, stream);
+    else return launch_product<T, Tile<T, TA, TB, 256, 256, 2, 4, 2>, false, USE>(j, a, stream);
+  }
   if constexpr (!TB)
-    if (size == 0) return launch_product<T, TA, TB, 128, 64, 4, 1, 3, USE, 2>(j, a, stream);
-  return launch_product<T, TA, TB, 128, 128, 2, 2, 2, USE, 2>(j, a, stream);
+    if (size == 0) return launch_product<T, Tile<T, TA, TB, 128, 64, 4, 1, 3>, false, USE>(j, a, stream);
+  return launch_product<T, Tile<T, TA, TB, 128, 128, 2, 2, 2>, false, USE>(j, a, stream);
 }
 
 template <typename T>
