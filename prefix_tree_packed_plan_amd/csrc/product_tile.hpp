@@ -248,7 +248,7 @@ struct Tile {
   using T = T_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, W = WM * WN;
   static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
-  static constexpr int THREADS = 64 * W;
+  static constexpr int THREADS = 64 * W, OCC = 2;
   static constexpr int BK = kStep / int(sizeof(T));
   static constexpr int KS = BK / 32;  // fragments along a step
   // B stored by k: rows of zeros follow its last, up to a whole step (A's repeat
@@ -410,39 +410,39 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
   }
 }
 
-// A 256 x 256 tile of bf16 by 8 waves (2 along m, 4 along n), staged as four 128-row
-// halves A0, A1, B0, B1 of a 128-byte k-step, two steps in LDS.  A wave has 64 rows of each
-// A half and 32 of each B half, and takes the halves' products one after another: A0 B0,
-// A0 B1, A1 B1, A1 B0.  So each half is read in one go (over the fragments just used), and
+// A 256 x 256 tile of bf16 by W waves (2 along m), staged as four 128-row halves A0, A1,
+// B0, B1 of a 128-byte k-step, two steps in LDS.  A wave has 64 rows of each A half and
+// 16 NH of each B half, and takes the halves' products one after another: A0 B0, A0 B1,
+// A1 B1, A1 B0.  So each half is read in one go (over the fragments just used), and
 // its place in LDS is staged anew, two steps on, as soon as all waves have read it:
 // a DMA has one and a half steps' time to land, and DMA is spread over the step,
 // where staging whole steps (run()) gives one and a burst.
-template <bool TA, bool TB>
+template <bool TA, bool TB, int W_>
 struct Big {
   using T = uint16_t;
   static constexpr bool TRA = TA, TRB = TB;
-  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, W = 8, MB = 8, NB = 4;
-  static constexpr int THREADS = 64 * W, BK = 64;
+  static constexpr int W = W_, BM = 256, BN = 256, WM = 2, WN = W / 2, MB = 8, NB = 16 / WN, NH = NB / 2;
+  static constexpr int THREADS = 64 * W, OCC = W / 4, BK = 64;
   using OpA = Operand<T, TA, 128, W>;
   using OpB = Operand<T, TB, 128, W>;
   using RdA = Reader<T, TA, 128>;
   using RdB = Reader<T, TB, 128>;
   static constexpr int HALF = OpA::BYTES, STEP = 4 * HALF, LDS = 2 * STEP;
-  static_assert(OpA::NI == 2 && OpB::NI == 2, "what is counted as in flight");
+  static constexpr int NI = OpA::NI;
+  static_assert(NI == OpB::NI, "what is counted as in flight");
 };
 
-template <bool TA, bool TB>
-__device__ __forceinline__ void run_big(f32x4 (&acc)[8][4], typename Big<TA, TB>::OpA (&A)[2],
-                                        typename Big<TA, TB>::OpB (&B)[2], const typename Big<TA, TB>::RdA& ra,
-                                        const typename Big<TA, TB>::RdB& rb, int k, char* lds) {
-  using C = Big<TA, TB>;
-  constexpr int HALF = C::HALF, BK = C::BK;
+template <typename C>
+__device__ __forceinline__ void run_big(f32x4 (&acc)[C::MB][C::NB], typename C::OpA (&A)[2], typename C::OpB (&B)[2],
+                                        const typename C::RdA& ra, const typename C::RdB& rb, int k, char* lds) {
+  constexpr int HALF = C::HALF, BK = C::BK, NI = C::NI, NH = C::NH;
+  constexpr bool TB = C::TRB;
   const uint32_t at = lds_at(lds) + A[0].wave * 1024;
   const int steps = (k + BK - 1) / BK;
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < C::MB; ++m)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < C::NB; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   // Groups of halves of step t: A0, B0, B1; and A1.
   const auto stage0 = [&](int t) {
     const uint32_t to = at + (t & 1) * C::STEP;
@@ -457,65 +457,78 @@ __device__ __forceinline__ void run_big(f32x4 (&acc)[8][4], typename Big<TA, TB>
   if (steps > 1) {
     stage0(1);
     stage1(1);
-    wait_step<10>();
+    wait_step<5 * NI>();
   } else {
-    wait_step<2>();
+    wait_step<NI>();
   }
   barrier();
-  uint4 a[2][4], b[2][2][2];  // [ks][m], [half][ks][n]
+  uint4 a[2][4], b[2][2][NH];  // [ks][m], [half][ks][n]
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) a[ks][m] = ra.bf16(lds, m, ks);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) b[0][ks][n] = rb.bf16(lds + 2 * HALF, n, ks);
+    for (int n = 0; n < NH; ++n) b[0][ks][n] = rb.bf16(lds + 2 * HALF, n, ks);
   }
+  constexpr int P = 8 * NH;                        // MFMA of a product of halves
+  constexpr int Y = 2 * NH + 10, X = 2 * P + 12;   // behind which the barriers stand
+  // The q-th DMA instruction of a step is behind MFMA D0 + EVERY q, the last ones in the
+  // next turn of the loop: evenly spread, since a burst of them fills the queue to the
+  // address units and then holds up the waves' MFMA too.
+  constexpr int D0 = Y + 2, EVERY = P / NI, BEFORE_X = (X - D0 + EVERY - 1) / EVERY;
+  static_assert(D0 + EVERY * (4 * NI - 1) - 4 * P < Y && D0 + EVERY * 3 * NI > X, "halves are staged once read");
+  const auto issue = [&](auto index, uint32_t to) {
+    constexpr int q = decltype(index)::value;
+    if constexpr (q < NI) A[0].template issue<q>(to);
+    else if constexpr (q < 2 * NI) B[0].template issue<q - NI>(to + 2 * HALF);
+    else if constexpr (q < 3 * NI) B[1].template issue<q - 2 * NI>(to + 3 * HALF);
+    else A[1].template issue<q - 3 * NI>(to + HALF);
+  };
+  bool whole = false, was_whole = false;
   for (int t = 0; t < steps; ++t) {
     const char* now = lds + (t & 1) * C::STEP;
     const char* next = lds + ((t + 1) & 1) * C::STEP;
-    const uint32_t to = at + (t & 1) * C::STEP;
-    const bool whole = k - (t + 2) * BK >= BK;  // step t + 2 is there, and whole
-    unrolled<64>([&](auto slot) {
+    const uint32_t to = at + (t & 1) * C::STEP, was_to = at + ((t + 1) & 1) * C::STEP;
+    was_whole = whole;
+    whole = k - (t + 2) * BK >= BK;  // step t + 2 is there, and whole
+    unrolled<4 * P>([&](auto slot) {
       constexpr int s = decltype(slot)::value;
-      constexpr int p = s / 16, ks = s / 8 % 2, m = s / 2 % 4, n = s % 2;
+      constexpr int p = s / P, ks = s % P / (4 * NH), m = s / NH % 4, n = s % NH;
       constexpr int ah = p >= 2, bh = p == 1 || p == 2;
-      acc[4 * ah + m][2 * bh + n] = mma(a[ks][m], b[bh][ks][n], acc[4 * ah + m][2 * bh + n]);
+      acc[4 * ah + m][NH * bh + n] = mma(a[ks][m], b[bh][ks][n], acc[4 * ah + m][NH * bh + n]);
       // Reads, each behind the last use of what it overwrites.
-      if constexpr (s >= 2 && s < 6) b[1][(s - 2) / 2][s % 2] = rb.bf16(now + 3 * HALF, s % 2, (s - 2) / 2);
-      if constexpr (p == 1 && n == 1) a[ks][m] = ra.bf16(now + HALF, m, ks);
-      if constexpr (p == 3 && n == 1) a[ks][m] = ra.bf16(next, m, ks);
-      if constexpr (s == 55 || s == 56) b[0][0][s - 55] = rb.bf16(next + 2 * HALF, s - 55, 0);
-      if constexpr (s == 62 || s == 63) b[0][1][s - 62] = rb.bf16(next + 2 * HALF, s - 62, 1);
-      if constexpr (s == 14) {
+      if constexpr (s >= 2 && s < 2 + 2 * NH)
+        b[1][(s - 2) / NH][(s - 2) % NH] = rb.bf16(now + 3 * HALF, (s - 2) % NH, (s - 2) / NH);
+      if constexpr (p == 1 && n == NH - 1) a[ks][m] = ra.bf16(now + HALF, m, ks);
+      if constexpr (p == 3 && n == NH - 1) a[ks][m] = ra.bf16(next, m, ks);
+      if constexpr (p == 3 && m == 3) b[0][ks][n] = rb.bf16(next + 2 * HALF, n, ks);
+      if constexpr (s == Y) {
         // A1 of this step has landed for every wave; every wave has read A0, B0 and B1.
-        if (t + 1 < steps) wait_step<8>();
+        if (t + 1 < steps) wait_step<4 * NI>();
         else wait_step<0>();
         barrier();
         if (!whole && t + 2 < steps) stage0(t + 2);
       }
-      if constexpr (s == 44) {
+      if constexpr (s == X) {
         // A0, B0 and B1 of the next step have landed; every wave has read A1.
-        if (t + 2 < steps) wait_step<8>();
+        if (t + 2 < steps) wait_step<NI + BEFORE_X>();
         else wait_step<0>();
         barrier();
         if (!whole && t + 2 < steps) stage1(t + 2);
       }
-      if constexpr (s >= 15 && s <= 25 && s % 2 == 1) {
-        constexpr int q = (s - 15) / 2;
-        if (whole) {
-          if constexpr (q < 2) A[0].template issue<q>(to);
-          else if constexpr (q < 4) B[0].template issue<q - 2>(to + 2 * HALF);
-          else B[1].template issue<q - 4>(to + 3 * HALF);
+      constexpr int q = (s - D0) / EVERY, last = (s + 4 * P - D0) / EVERY;
+      if constexpr (s >= D0 && (s - D0) % EVERY == 0 && q < 4 * NI) {
+        if (whole) issue(std::integral_constant<int, q>{}, to);
+      } else if constexpr (s < D0 && (s + 4 * P - D0) % EVERY == 0 && last < 4 * NI) {
+        if (was_whole) {
+          issue(std::integral_constant<int, last>{}, was_to);
+          if constexpr (last == 4 * NI - 1) A[1].advance();
         }
-      }
-      if constexpr (s == 46 || s == 48) {
-        if (whole) A[1].template issue<(s - 46) / 2>(to + HALF);
       }
       fence();
     });
     if (whole) {
       A[0].advance();
-      A[1].advance();
       B[0].advance();
       B[1].advance();
     }

@@ -97,7 +97,7 @@ struct Job {
 //   row: (lse, ca, cb, g of the first token)
 //   ids: (the first token's entry or -1, tokens behind, first of them in kid or -1, 0)
 template <typename T, typename C, bool BIG, Use USE>
-__global__ __launch_bounds__(C::THREADS, 2) void product_kernel(Job j, LinearArgs la) {
+__global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, LinearArgs la) {
   constexpr int BM = C::BM, BN = C::BN, WM = C::WM;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -125,8 +125,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(Job j, LinearArg
       B[i].init(j.b, j.ldb, nb, j.n - nb, k0, wave, lane);
     }
     const typename C::RdA ra(4 * wm, lane);
-    const typename C::RdB rb(2 * wn, lane);
-    product::run_big<C::TRA, C::TRB>(acc, A, B, ra, rb, k, lds);
+    const typename C::RdB rb(C::NH * wn, lane);
+    product::run_big<C>(acc, A, B, ra, rb, k, lds);
   } else {
     typename C::OpA A;
     typename C::OpB B;
@@ -138,7 +138,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(Job j, LinearArg
   }
   // Blocks mb, nb begin at m0 + am(mb), n0 + an(nb).
   const auto am = [&](int mb) { return BIG ? 128 * (mb / 4) + 64 * wm + 16 * (mb % 4) : 16 * (wm * C::MB + mb); };
-  const auto an = [&](int nb) { return BIG ? 128 * (nb / 2) + 32 * wn + 16 * (nb % 2) : 16 * (wn * C::NB + nb); };
+  constexpr int NH = C::NB / 2;
+  const auto an = [&](int nb) { return BIG ? 128 * (nb / NH) + 16 * (NH * wn + nb % NH) : 16 * (wn * C::NB + nb); };
 
   const int l16 = lane & 15, g4 = lane >> 4;
   const int mw = m0 + 4 * g4, nw = n0 + l16;  // this lane's first m of block 0, and its n
@@ -377,7 +378,7 @@ template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
   using product::Tile;
   if (size == 2) {
-    if constexpr (sizeof(T) == 2) return launch_product<T, product::Big<TA, TB>, true, USE>(j, a, stream);
+    if constexpr (sizeof(T) == 2) return launch_product<T, product::Big<TA, TB, 8>, true, USE>(j, a, stream);
     else return launch_product<T, Tile<T, TA, TB, 256, 256, 2, 4, 2>, false, USE>(j, a, stream);
   }
   if constexpr (!TB)
