@@ -137,13 +137,25 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
     product::run<C>(acc, A, B, ra, rb, k, lds);
   }
   // Blocks mb, nb begin at m0 + am(mb), n0 + an(nb).
-  const auto am = [&](int mb) { return BIG ? 128 * (mb / 4) + 64 * wm + 16 * (mb % 4) : 16 * (wm * C::MB + mb); };
+  const auto am = [&](int mb) {
+    if (C::PAIR) return 128 * (mb / 4) + 64 * wm + 32 * (mb % 4 / 2) + 4 * (mb % 2);
+    return BIG ? 128 * (mb / 4) + 64 * wm + 16 * (mb % 4) : 16 * (wm * C::MB + mb);
+  };
   constexpr int NH = C::NB / 2;
   const auto an = [&](int nb) { return BIG ? 128 * (nb / NH) + 16 * (NH * wn + nb % NH) : 16 * (wn * C::NB + nb); };
 
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int mw = m0 + 4 * g4, nw = n0 + l16;  // this lane's first m of block 0, and its n
+  const int mw = m0 + (C::PAIR ? 8 : 4) * g4, nw = n0 + l16;  // this lane's first m of block 0, and its n
   if constexpr (USE == kStats) {
+    if (m0 + BM > j.m) {  // past the vocabulary
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (mw + am(mb) + i >= j.m)
+#pragma unroll
+            for (int nb = 0; nb < C::NB; ++nb) acc[mb][nb][i] = kNegInf;
+    }
     float* red = reinterpret_cast<float*>(lds);  // [3][WM][BN]
     product::barrier();                          // the last step has been read
 #pragma unroll
@@ -152,10 +164,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (mw + am(mb) + i >= j.m) acc[mb][nb][i] = kNegInf;
-          top = fmaxf(top, acc[mb][nb][i]);
-        }
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, acc[mb][nb][i]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = top == kNegInf ? 0.f : top * j.c;
@@ -199,11 +208,16 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int m = mw + am(mb) + i;
           const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x);
-          const float d = ex2(lp * kLog2e) * fmaf(rc.z, fmaxf(lp, -1e4f), rc.y);  // exp is 0 below -104
-          acc[mb][nb][i] = live && m < j.m ? d : 0.f;
+          acc[mb][nb][i] = ex2(lp * kLog2e) * fmaf(rc.z, fmaxf(lp, -1e4f), rc.y);  // exp is 0 below -104
         }
+      if (!__all(live) || m0 + BM > j.m) {
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!live || mw + am(mb) + i >= j.m) acc[mb][nb][i] = 0.f;
+      }
       // The tokens behind the row: the first, and where there are more the others.
       const int mine = live ? who.y : 0;
       for (int t = 0; __any(t < mine); ++t) {
@@ -228,9 +242,17 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
             if (v >= 0 && o == am(mb) + i) acc[mb][nb][i] += g;
       }
 #pragma unroll
-      for (int mb = 0; mb < C::MB; ++mb)
-        put4<T>(j.d, int64_t(n) * j.ldd + mw + am(mb), acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2],
-                acc[mb][nb][3]);
+      for (int mb = 0; mb < C::MB; mb += C::PAIR ? 2 : 1) {
+        const int64_t o = int64_t(n) * j.ldd + mw + am(mb);
+        const f32x4 x = acc[mb][nb];
+        if constexpr (C::PAIR) {
+          const f32x4 y = acc[mb + 1][nb];
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.d) + o) =
+              make_uint4(chunk::pk2(x[0], x[1]), chunk::pk2(x[2], x[3]), chunk::pk2(y[0], y[1]), chunk::pk2(y[2], y[3]));
+        } else {
+          put4<T>(j.d, o, x[0], x[1], x[2], x[3]);
+        }
+      }
     }
   } else {
 #pragma unroll
@@ -378,7 +400,7 @@ template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
   using product::Tile;
   if (size == 2) {
-    if constexpr (sizeof(T) == 2) return launch_product<T, product::Big<TA, TB, 8>, true, USE>(j, a, stream);
+    if constexpr (sizeof(T) == 2) return launch_product<T, product::Big<TA, TB, USE == kGrad>, true, USE>(j, a, stream);
     else return launch_product<T, Tile<T, TA, TB, 256, 256, 2, 4, 2>, false, USE>(j, a, stream);
   }
   if constexpr (!TB)
