@@ -257,12 +257,14 @@ constexpr int32_t kLinearVocab = 1 << 22, kLinearWidth = 1 << 16;
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile sizes and splits of a sum product of m x n over k.  256 x 256 tiles, one
-// work-group a CU, reach the highest rate; smaller ones where those would leave CUs
-// idle.
-int32_t product_size(int64_t m, int64_t n, bool rows_only) {
+// Tile sizes and splits of a product of m x n over k.  256 x 256 tiles, one work-group a
+// CU, reach the highest rate in bf16; smaller ones where those would leave CUs idle.
+// fp32 takes 128 x 128: two work-groups a CU, one of which splits values while the
+// other's products run (1685 rows x 50001 x 1000 forward as fast as with 256 x 256, the
+// gradients of 1117 x 20001 x 1000 1290 -> 1030 us).
+int32_t product_size(int64_t m, int64_t n, int32_t dtype, bool rows_only) {
   if (!rows_only && n <= 64) return 0;
-  return ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 2 : 1;
+  return dtype == TREE_DTYPE_BF16 && ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 2 : 1;
 }
 void product_splits(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t size, int32_t* splits) {
   const int64_t bm = size == 2 ? 256 : 128, bn = size == 2 ? 256 : size == 1 ? 128 : 64;
@@ -275,10 +277,10 @@ bool linear_sizes_ok(int64_t n_rows, int32_t vocab, int32_t width, int32_t dtype
          width <= kLinearWidth && dtype_ok(dtype) && width % (dtype == TREE_DTYPE_F32 ? 4 : 8) == 0;
 }
 // The forward's: the tiles' sums of up to 32768 rows, 1 GiB of them at most.
-tg::LinearWork linear_work(int64_t n_rows, int32_t vocab) {
+tg::LinearWork linear_work(int64_t n_rows, int32_t vocab, int32_t dtype) {
   tg::LinearWork w{};
   w.rows = std::min<int64_t>(n_rows, 32768);
-  w.size = product_size(vocab, w.rows, false);
+  w.size = product_size(vocab, w.rows, dtype, false);
   const int64_t slots = ceil_div(vocab, w.size == 2 ? 256 : 128);
   w.rows = std::min(w.rows, std::max<int64_t>(256, (int64_t(1) << 26) / slots / 256 * 256));
   w.bytes = static_cast<size_t>(w.rows) * slots * 16;
@@ -293,10 +295,10 @@ tg::LinearWork linear_backward_work(int64_t n_rows, int32_t vocab, int32_t width
   const int64_t rows_up = ceil_div(w.rows, 256) * 256;
   w.piece = std::min<int64_t>(vocab, (int64_t(1) << 28) / rows_up / 256 * 256);
   w.ldd = ceil_div(w.piece, 256) * 256;
-  w.size = product_size(w.piece, w.rows, false);
-  w.size_h = product_size(width, w.rows, false);
+  w.size = product_size(w.piece, w.rows, dtype, false);
+  w.size_h = product_size(width, w.rows, dtype, false);
   product_splits(width, w.rows, w.piece, dtype, w.size_h, &w.splits_h);
-  w.size_w = product_size(width, w.piece, true);
+  w.size_w = product_size(width, w.piece, dtype, true);
   product_splits(width, w.piece, w.rows, dtype, w.size_w, &w.splits_w);
   const size_t fw = static_cast<size_t>(width) * sizeof(float);
   w.ids = up256(w.rows * 16);
@@ -1189,7 +1191,7 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
 }
 
 size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
-  return linear_sizes_ok(n_rows, vocab, width, dtype) ? linear_work(n_rows, vocab).bytes : 0;
+  return linear_sizes_ok(n_rows, vocab, width, dtype) ? linear_work(n_rows, vocab, dtype).bytes : 0;
 }
 
 int tree_linear_logprobs(const void* hidden, const void* weight, const void* tokens, float* logp, float* entropy,
@@ -1203,7 +1205,7 @@ int tree_linear_logprobs(const void* hidden, const void* weight, const void* tok
   if (const int rc = check_linear(p, hidden, ld, weight, n_tokens, first_row, n_rows, vocab, width, token_bytes,
                                   temperature, dtype, fn))
     return rc;
-  const tg::LinearWork w = linear_work(n_rows, vocab);
+  const tg::LinearWork w = linear_work(n_rows, vocab, dtype);
   if (!ws || ws_bytes < w.bytes)
     return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, w.bytes);
   if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;

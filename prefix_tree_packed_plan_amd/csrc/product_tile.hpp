@@ -197,25 +197,23 @@ struct Reader {
   }
 };
 
-// Three bf16 whose sum is x, of 8 values.
+// Three bf16 whose sum is x, of 8 values; pair j of them.
 struct Split {
-  uint4 p[3];
+  uint32_t w[3][4];
+  __device__ __forceinline__ uint4 part(int q) const { return make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]); }
 };
+__device__ __forceinline__ void split_pair(Split& s, int j, float a, float b) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    s.w[q][j] = pk2(a, b);
+    a -= chunk::lo_f(s.w[q][j]);
+    b -= chunk::hi_f(s.w[q][j]);
+  }
+}
 __device__ __forceinline__ Split split3(const float (&x)[8]) {
   Split s;
-  uint32_t w[3][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float a = x[2 * j], b = x[2 * j + 1];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      w[q][j] = pk2(a, b);
-      a -= chunk::lo_f(w[q][j]);
-      b -= chunk::hi_f(w[q][j]);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 3; ++q) s.p[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+  for (int j = 0; j < 4; ++j) split_pair(s, j, x[2 * j], x[2 * j + 1]);
   return s;
 }
 
@@ -225,12 +223,12 @@ __device__ __forceinline__ f32x4 mma(const uint4 a, const uint4 b, const f32x4 c
 }
 // The six largest partial products, the smallest first.
 __device__ __forceinline__ f32x4 mma(const Split& a, const Split& b, f32x4 c) {
-  c = mma(a.p[1], b.p[1], c);
-  c = mma(a.p[2], b.p[0], c);
-  c = mma(a.p[0], b.p[2], c);
-  c = mma(a.p[1], b.p[0], c);
-  c = mma(a.p[0], b.p[1], c);
-  return mma(a.p[0], b.p[0], c);
+  c = mma(a.part(1), b.part(1), c);
+  c = mma(a.part(2), b.part(0), c);
+  c = mma(a.part(0), b.part(2), c);
+  c = mma(a.part(1), b.part(0), c);
+  c = mma(a.part(0), b.part(1), c);
+  return mma(a.part(0), b.part(0), c);
 }
 
 // Waits until all but the youngest N of this wave's loads have landed, and its
@@ -395,20 +393,28 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
       if (t + S - 1 < steps) stage(t + S - 1, into);
       const char* ta = lds + cur * C::STEP;
       const char* tb = ta + C::OpA::BYTES;
-      Split b[NB];
+      // All of the step's values are read first; those of the next a are split between the
+      // MFMAs of the one before.
+      float xa[MB][8], xb[NB][8];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        float x[8];
-        rb.f32(tb, n, x);
-        b[n] = split3(x);
-      }
+      for (int n = 0; n < NB; ++n) rb.f32(tb, n, xb[n]);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) ra.f32(ta, m, xa[m]);
+      Split b[NB], a[2];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) b[n] = split3(xb[n]);
+      a[0] = split3(xa[0]);
+      fence();
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        float x[8];
-        ra.f32(ta, m, x);
-        const Split a = split3(x);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) acc[m][n] = mma(a, b[n], acc[m][n]);
+        for (int n = 0; n < NB; ++n) {
+          acc[m][n] = mma(a[m & 1], b[n], acc[m][n]);
+          if (m + 1 < MB)
+#pragma unroll
+            for (int j = n * 4 / NB; j < (n + 1) * 4 / NB; ++j) split_pair(a[(m + 1) & 1], j, xa[m + 1][2 * j], xa[m + 1][2 * j + 1]);
+          fence();
+        }
       }
       cur = cur + 1 == S ? 0 : cur + 1;
       into = into + 1 == S ? 0 : into + 1;

@@ -395,14 +395,12 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// By the tile sizes of `size`: 0: 128 x 64, 1: 128 x 128, 2: 256 x 256.
+// By the tile sizes of `size`: 0: 128 x 64, 1: 128 x 128, 2 (bf16): 256 x 256.
 template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
   using product::Tile;
-  if (size == 2) {
-    if constexpr (sizeof(T) == 2) return launch_product<T, product::Big<TA, TB, USE == kGrad>, true, USE>(j, a, stream);
-    else return launch_product<T, Tile<T, TA, TB, 256, 256, 2, 4, 2>, false, USE>(j, a, stream);
-  }
+  if constexpr (sizeof(T) == 2)
+    if (size == 2) return launch_product<T, product::Big<TA, TB, USE == kGrad>, true, USE>(j, a, stream);
   if constexpr (!TB)
     if (size == 0) return launch_product<T, Tile<T, TA, TB, 128, 64, 4, 1, 3>, false, USE>(j, a, stream);
   return launch_product<T, Tile<T, TA, TB, 128, 128, 2, 2, 2>, false, USE>(j, a, stream);
