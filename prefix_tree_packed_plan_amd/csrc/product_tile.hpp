@@ -10,7 +10,7 @@
 //
 // A wave owns MB x NB blocks of 16 x 16.  Lane l of a block holds column n = l %
 // 16 and rows m = 4 (l / 16) + i of register i: four neighbouring m of one n,
-// which is 8 or 16 bytes of a row of `out` (paired blocks: 16 bytes of bf16).
+// which is 8 or 16 bytes of a row of `out`; pair_up() makes it 16 for bf16.
 //
 // fp32: a value is the sum of three bf16 (rounded, the rest rounded, the rest of
 // that: exact to 2^-26 of it), and a product of two the six largest of the nine
@@ -69,13 +69,8 @@ __device__ __forceinline__ uint32_t lds_at(const char* lds) {
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)lds)));
 }
 
-// Which row of 32 is row i of the first (odd: the second) of two blocks of 16 whose
-// accumulators hold 8 neighbouring rows: 16 bytes of bf16 a lane for a row of `out`.
-__device__ __forceinline__ int paired(int i) { return 8 * (i >> 2) + (i & 3); }
-
-// An operand of R rows (m or n) a tile, staged by W waves.  PAIRED: its blocks are read
-// two at a time, by paired().
-template <typename T, bool TR, int R, int W, bool PAIRED = false>
+// An operand of R rows (m or n) a tile, staged by W waves.
+template <typename T, bool TR, int R, int W>
 struct Operand {
   static constexpr int ES = sizeof(T);
   static constexpr int BK = kStep / ES;          // k of a step
@@ -95,7 +90,7 @@ struct Operand {
   // one piece each), transposing reads (4 rows x 64 bytes) and reads by words (4
   // rows 8 apart x 64 bytes) then touch every bank once.
   static __device__ __forceinline__ int swz(int r) {
-    if (!TR) return 4 * ((r >> 1) & 1) + ((r >> (PAIRED ? 3 : 2)) & 3);
+    if (!TR) return 4 * ((r >> 1) & 1) + ((r >> 2) & 3);
     return ES == 2 ? 4 * (r & 3) + ((r >> 2) & 3) : 4 * ((r >> 3) & 3);
   }
   __device__ __forceinline__ static int slot_row(int q, int lane) { return (q * 1024 + lane * 16) / RB; }
@@ -154,7 +149,7 @@ struct Operand {
 
 // Fragment reads of blocks of 16 rows (m or n) from block `blk0` on, 32 k each: lane l
 // has row l % 16 and k = 8 (l / 16) .. + 7.
-template <typename T, bool TR, int R, bool PAIRED = false>
+template <typename T, bool TR, int R>
 struct Reader {
   static constexpr int ES = sizeof(T);
   static constexpr int RB = TR ? R * ES : kStep;
@@ -163,7 +158,7 @@ struct Reader {
     const int i = lane & 15, g = lane >> 4;
     if (!TR) {
       const int sw = 4 * ((i >> 1) & 1) + ((i >> 2) & 3);
-      base = (16 * blk0 + (PAIRED ? paired(i) : i)) * RB + 16 * ((ES == 2 ? g : 2 * g) ^ sw);
+      base = (16 * blk0 + i) * RB + 16 * ((ES == 2 ? g : 2 * g) ^ sw);
     } else if (ES == 2) {
       const int sw = 4 * (i >> 2) + ((2 * g) & 3);
       base = (8 * g + (i >> 2)) * RB + 16 * ((2 * blk0 + ((i & 3) >> 1)) ^ sw) + 8 * (i & 1);
@@ -174,7 +169,7 @@ struct Reader {
   // bf16: the fragment of block b (a multiple of its count below blk0), k from 32 ks on.
   __device__ __forceinline__ uint4 bf16(const char* t, int b, int ks) const {
     if constexpr (!TR) {
-      return lds16(t + ((base ^ (64 * ks)) + (PAIRED ? (b / 2) * 32 + (b % 2) * 4 : b * 16) * RB));
+      return lds16(t + ((base ^ (64 * ks)) + b * 16 * RB));
     } else {
       const int o = (base ^ (32 * b)) + 32 * ks * RB;
       const int o4 = (base ^ (32 * b) ^ 16) + (32 * ks + 4) * RB;
@@ -231,6 +226,15 @@ __device__ __forceinline__ f32x4 mma(const Split& a, const Split& b, f32x4 c) {
   return mma(a.part(0), b.part(0), c);
 }
 
+// Blocks x and y, y behind x along m, as 8 neighbouring bf16 a lane: of block x (lanes of
+// even l / 16) or y, from its row 8 (l / 32) on.
+__device__ __forceinline__ uint4 pair_up(const f32x4 x, const f32x4 y) {
+  // Swaps the odd 16 lanes of the first with the even ones of the second.
+  const auto lo = __builtin_amdgcn_permlane16_swap(pk2(x[0], x[1]), pk2(y[0], y[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pk2(x[2], x[3]), pk2(y[2], y[3]), false, false);
+  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
+}
+
 // Waits until all but the youngest N of this wave's loads have landed, and its
 // reads of LDS have ended.
 template <int N>
@@ -252,7 +256,6 @@ struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, W = WM * WN;
   static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
   static constexpr int THREADS = 64 * W, OCC = 2;
-  static constexpr bool PAIR = false;
   static constexpr int BK = kStep / int(sizeof(T));
   static constexpr int KS = BK / 32;  // fragments along a step
   // B stored by k: rows of zeros follow its last, up to a whole step (A's repeat
@@ -429,16 +432,15 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
 // its place in LDS is staged anew, two steps on, as soon as all waves have read it:
 // a DMA has one and a half steps' time to land, and DMA is spread over the step,
 // where staging whole steps (run()) gives one and a burst.
-template <bool TA, bool TB, bool PAIRED>
+template <bool TA, bool TB>
 struct Big {
   using T = uint16_t;
-  static constexpr bool TRA = TA, TRB = TB, PAIR = PAIRED;
-  static_assert(!(TA && PAIRED), "transposing reads of paired blocks would meet in the banks");
+  static constexpr bool TRA = TA, TRB = TB;
   static constexpr int W = 8, BM = 256, BN = 256, WM = 2, WN = 4, MB = 8, NB = 4, NH = NB / 2;
   static constexpr int THREADS = 64 * W, OCC = 2, BK = 64;
-  using OpA = Operand<T, TA, 128, W, PAIRED>;
+  using OpA = Operand<T, TA, 128, W>;
   using OpB = Operand<T, TB, 128, W>;
-  using RdA = Reader<T, TA, 128, PAIRED>;
+  using RdA = Reader<T, TA, 128>;
   using RdB = Reader<T, TB, 128>;
   static constexpr int HALF = OpA::BYTES, STEP = 4 * HALF, LDS = 2 * STEP;
   static constexpr int NI = OpA::NI;

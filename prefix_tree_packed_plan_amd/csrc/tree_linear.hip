@@ -66,6 +66,20 @@ __device__ __forceinline__ void put4<float>(void* p, int64_t i, float a, float b
   *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
 }
 
+// Neighbouring blocks x and y, from m on, to a row of T; the row ends at `end`.
+template <typename T>
+__device__ __forceinline__ void put_blocks(T* row, int m, int g4, int end, const f32x4 x, const f32x4 y) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 w = product::pair_up(x, y);
+    m += 16 * (g4 & 1) + 8 * (g4 >> 1);
+    if (m < end) *reinterpret_cast<uint4*>(row + m) = w;
+  } else {
+    m += 4 * g4;
+    if (m < end) *reinterpret_cast<f32x4*>(row + m) = x;
+    if (m + 16 < end) *reinterpret_cast<f32x4*>(row + m + 16) = y;
+  }
+}
+
 enum Use { kStats, kGrad, kSum };
 
 // A product's operands and where its tiles stand.
@@ -138,14 +152,13 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
   }
   // Blocks mb, nb begin at m0 + am(mb), n0 + an(nb).
   const auto am = [&](int mb) {
-    if (C::PAIR) return 128 * (mb / 4) + 64 * wm + 32 * (mb % 4 / 2) + 4 * (mb % 2);
     return BIG ? 128 * (mb / 4) + 64 * wm + 16 * (mb % 4) : 16 * (wm * C::MB + mb);
   };
   constexpr int NH = C::NB / 2;
   const auto an = [&](int nb) { return BIG ? 128 * (nb / NH) + 16 * (NH * wn + nb % NH) : 16 * (wn * C::NB + nb); };
 
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int mw = m0 + (C::PAIR ? 8 : 4) * g4, nw = n0 + l16;  // this lane's first m of block 0, and its n
+  const int mw = m0 + 4 * g4, nw = n0 + l16;  // this lane's first m of block 0, and its n
   if constexpr (USE == kStats) {
     if (m0 + BM > j.m) {  // past the vocabulary
 #pragma unroll
@@ -242,17 +255,8 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
             if (v >= 0 && o == am(mb) + i) acc[mb][nb][i] += g;
       }
 #pragma unroll
-      for (int mb = 0; mb < C::MB; mb += C::PAIR ? 2 : 1) {
-        const int64_t o = int64_t(n) * j.ldd + mw + am(mb);
-        const f32x4 x = acc[mb][nb];
-        if constexpr (C::PAIR) {
-          const f32x4 y = acc[mb + 1][nb];
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.d) + o) =
-              make_uint4(chunk::pk2(x[0], x[1]), chunk::pk2(x[2], x[3]), chunk::pk2(y[0], y[1]), chunk::pk2(y[2], y[3]));
-        } else {
-          put4<T>(j.d, o, x[0], x[1], x[2], x[3]);
-        }
-      }
+      for (int mb = 0; mb < C::MB; mb += 2)
+        put_blocks<T>(static_cast<T*>(j.d) + int64_t(n) * j.ldd, m0 + am(mb), g4, j.m_tiles * BM, acc[mb][nb], acc[mb + 1][nb]);
     }
   } else {
 #pragma unroll
@@ -260,17 +264,17 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
       const int n = nw + an(nb);
       if (n >= j.n) continue;
 #pragma unroll
-      for (int mb = 0; mb < C::MB; ++mb) {
-        const int m = mw + am(mb);
-        if (m >= j.m) continue;
-        const int64_t o = int64_t(n) * j.m + m;
-        float4 x = make_float4(acc[mb][nb][0], acc[mb][nb][1], acc[mb][nb][2], acc[mb][nb][3]);
-        if (j.add) {
-          const float4 y = *reinterpret_cast<const float4*>(j.add + o);
-          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-        }
-        if (j.out) put4<T>(j.out, o, x.x, x.y, x.z, x.w);
-        else *reinterpret_cast<float4*>(j.acc + split * j.acc_split + o) = x;
+      for (int mb = 0; mb < C::MB; mb += 2) {
+        f32x4 x[2] = {acc[mb][nb], acc[mb + 1][nb]};
+        const int64_t row = int64_t(n) * j.m;
+        if (j.add)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int m = mw + am(mb + i);
+            if (m < j.m) x[i] += *reinterpret_cast<const f32x4*>(j.add + row + m);
+          }
+        if (j.out) put_blocks<T>(static_cast<T*>(j.out) + row, m0 + am(mb), g4, j.m, x[0], x[1]);
+        else put_blocks<float>(j.acc + split * j.acc_split + row, m0 + am(mb), g4, j.m, x[0], x[1]);
       }
     }
   }
@@ -400,7 +404,7 @@ template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
   using product::Tile;
   if constexpr (sizeof(T) == 2)
-    if (size == 2) return launch_product<T, product::Big<TA, TB, USE == kGrad>, true, USE>(j, a, stream);
+    if (size == 2) return launch_product<T, product::Big<TA, TB>, true, USE>(j, a, stream);
   if constexpr (!TB)
     if (size == 0) return launch_product<T, Tile<T, TA, TB, 128, 64, 4, 1, 3>, false, USE>(j, a, stream);
   return launch_product<T, Tile<T, TA, TB, 128, 128, 2, 2, 2>, false, USE>(j, a, stream);
