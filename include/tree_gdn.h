@@ -640,7 +640,7 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
 
 /*
  * tree_linear_logprobs_workspace_bytes -- device workspace of
- * tree_linear_logprobs: for every row and 128 or 256 entries of the vocabulary
+ * tree_linear_logprobs: for every row and 64 to 256 entries of the vocabulary
  * 16 bytes, 1 GiB at most (more rows go one part after another).  0 for sizes
  * that the call refuses.
  */

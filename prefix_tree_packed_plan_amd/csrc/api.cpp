@@ -281,9 +281,10 @@ tg::LinearWork linear_work(int64_t n_rows, int32_t vocab, int32_t dtype) {
   tg::LinearWork w{};
   w.rows = std::min<int64_t>(n_rows, 32768);
   w.size = product_size(vocab, w.rows, dtype, false);
-  const int64_t slots = ceil_div(vocab, w.size == 2 ? 256 : 128);
+  const int64_t slots = ceil_div(vocab, w.size == 2 ? 256 : w.size == 1 ? 128 : 64);
   w.rows = std::min(w.rows, std::max<int64_t>(256, (int64_t(1) << 26) / slots / 256 * 256));
-  w.bytes = static_cast<size_t>(w.rows) * slots * 16;
+  w.ids = static_cast<size_t>(w.rows) * slots * 16;
+  w.bytes = w.ids + static_cast<size_t>(w.rows) * 16;
   return w;
 }
 // The backward's: D of up to 16384 rows and a piece of the vocabulary, 256 Mi elements

@@ -82,6 +82,56 @@ __device__ __forceinline__ void put_blocks(T* row, int m, int g4, int end, const
 
 enum Use { kStats, kGrad, kSum };
 
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+// A row's tokens and their logits, by work-groups beside those of the product, which
+// they take no longer than: a wave a row.  found: (logit of the first token, that token,
+// the row's segment, flags); the logits of further ones go to their logp.
+constexpr int kAny = 1, kOutside = 2, kMore = 4, kRootStart = 8;
+template <typename T>
+__device__ __forceinline__ void find_row(const LinearArgs& a, int lr, int4* found) {
+  constexpr int N = 16 / sizeof(T);
+  const int lane = threadIdx.x & 63;
+  const Behind b(a, a.first_row + lr, lane);
+  const uint4* hrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.hidden) + int64_t(lr) * a.ld);
+  float first = 0.f;
+  int t0 = 0, flags = (b.n > 0 ? kAny : 0) | (b.n > 1 ? kMore : 0) | (b.root_start ? kRootStart : 0);
+  for (int j = 0; j < b.n; ++j) {
+    const int t = b.at(j), id = token(a, t);
+    float x = 0.f;
+    if (id >= 0) {
+      const uint4* wrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.weight) + int64_t(id) * a.width);
+#pragma unroll 4
+      for (int i = lane; i < a.width / N; i += 64) {
+        const uint4 u = hrow[i], w = wrow[i];
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (sizeof(T) == 4) {
+            x = fmaf(__uint_as_float(uu[q]), __uint_as_float(ww[q]), x);
+          } else {
+            x = fmaf(chunk::lo_f(uu[q]), chunk::lo_f(ww[q]), x);
+            x = fmaf(chunk::hi_f(uu[q]), chunk::hi_f(ww[q]), x);
+          }
+        }
+      }
+      x = wave_sum(x);
+    }
+    if (j == 0) {
+      first = x;
+      t0 = t;
+      if (id < 0) flags |= kOutside;
+    } else if (lane == 0) {
+      a.logp[t] = x;
+    }
+  }
+  if (lane == 0) found[lr] = make_int4(__float_as_int(first), t0, b.seg, flags);
+}
+
 // A product's operands and where its tiles stand.
 struct Job {
   const char *a, *b;
@@ -92,6 +142,7 @@ struct Job {
   // kStats: z of entry m, row n, times c
   float c;
   float4* part;             // [n, m_tiles]: largest z c, sum, weighted sum
+  int4* found;              // [n]: find_row
   // kGrad: entry v0 + m
   const float4* row;        // RowGrad of each row
   const int4* ids;
@@ -118,7 +169,15 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int tiles = j.m_tiles * j.n_tiles;
-  const int id = product::of_xcd(blockIdx.x, gridDim.x);
+  if constexpr (USE == kStats) {
+    // The work-groups behind the tiles'.
+    if (static_cast<int>(blockIdx.x) >= tiles) {
+      const int lr = (blockIdx.x - tiles) * (C::THREADS / 64) + wave;
+      if (lr < la.n_rows) find_row<T>(la, lr, j.found);
+      return;
+    }
+  }
+  const int id = product::of_xcd(blockIdx.x, tiles * j.splits);
   const int split = id / tiles, tile = id % tiles;
   // Bands of `band` n tiles; within one, all n of an m.
   const int in_band = j.band * j.m_tiles, band = tile / in_band, at = tile % in_band;
@@ -297,21 +356,14 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* part, int64
   }
 }
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o, 64);
-  return x;
-}
-
 // A wave a row: joins the tiles' sums; log probabilities of the tokens behind it.
-template <typename T>
-__global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4* part, int slots) {
-  constexpr int N = 16 / sizeof(T);
+__global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4* part, int slots, const int4* found) {
   const int lane = threadIdx.x & 63;
   const int lr = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   if (lr >= a.n_rows) return;
-  const Behind b(a, a.first_row + lr, lane);
+  const int4 f = found[lr];
   LinearSums z{kNegInf, 0.f, 0.f};
+#pragma unroll 4
   for (int i = lane; i < slots; i += 64) {
     const float4 y = part[int64_t(lr) * slots + i];
     z = join(z, LinearSums{y.x, y.y, y.z});
@@ -320,36 +372,20 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4*
   for (int o = 32; o; o >>= 1)
     z = join(z, LinearSums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)});
   const bool empty = z.m == kNegInf && z.s == 0.f;  // every logit is -inf
-  const float ls = __log2f(z.s);
+  const float ls = __log2f(z.s), c = a.inv_t * kLog2e;
   if (lane == 0) {
     a.lse[lr] = empty ? kNegInf : (z.m + ls) * kLn2;
     a.entropy[lr] = empty ? 0.f : (ls - z.t / z.s) * kLn2;
-    if (b.root_start) a.logp[a.first_row + lr] = 0.f;
+    if (f.w & kRootStart) a.logp[a.first_row + lr] = 0.f;
   }
-  const float c = a.inv_t * kLog2e;
-  const char* hrow = static_cast<const char*>(a.hidden) + int64_t(lr) * a.ld * sizeof(T);
-  for (int j = 0; j < b.n; ++j) {
-    const int t = b.at(j), id = token(a, t);
-    float x = 0.f;
-    if (id >= 0) {
-      const char* wrow = static_cast<const char*>(a.weight) + int64_t(id) * a.width * sizeof(T);
-      for (int i = lane; i < a.width / N; i += 64) {
-        const uint4 u = reinterpret_cast<const uint4*>(hrow)[i], w = reinterpret_cast<const uint4*>(wrow)[i];
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (sizeof(T) == 4) {
-            x = fmaf(__uint_as_float(uu[q]), __uint_as_float(ww[q]), x);
-          } else {
-            x = fmaf(chunk::lo_f(uu[q]), chunk::lo_f(ww[q]), x);
-            x = fmaf(chunk::hi_f(uu[q]), chunk::hi_f(ww[q]), x);
-          }
-        }
-      }
-      x = wave_sum(x);
+  const auto logp = [&](float x) { return empty ? kNegInf : (fmaf(x, c, -z.m) - ls) * kLn2; };
+  if (lane == 0 && f.w & kAny) a.logp[f.y] = f.w & kOutside ? 0.f : logp(__int_as_float(f.x));
+  // The other children's first tokens: their logits wait in logp.
+  if (f.w & kMore)
+    for (int j = 1 + lane; j < a.kid_off[f.z + 1] - a.kid_off[f.z]; j += 64) {
+      const int t = a.seg_off[a.kid[a.kid_off[f.z] + j]];
+      a.logp[t] = token(a, t) < 0 ? 0.f : logp(a.logp[t]);
     }
-    if (lane == 0) a.logp[t] = id < 0 ? 0.f : empty ? kNegInf : (fmaf(x, c, -z.m) - ls) * kLn2;
-  }
 }
 
 // A wave a row: the coefficients of its gradient.
@@ -394,19 +430,24 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   }
   // 8 x 4 tiles run on an XCD's 32 CUs at a time.
   j.band = j.n_tiles < 4 ? j.n_tiles : 4;
-  const int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
+  int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
+  if (USE == kStats) groups += ceil_div(j.n, C::THREADS / 64);
   product_kernel<T, C, BIG, USE><<<static_cast<uint32_t>(groups), C::THREADS, 0, stream>>>(j, a);
   return hipGetLastError();
 }
 
-// By the tile sizes of `size`: 0: 128 x 64, 1: 128 x 128, 2 (bf16): 256 x 256.
+// By the tile sizes of `size`: 0: 64 rows (64 x 64, of a sum product 128 x 64), 1: 128 x
+// 128, 2 (bf16): 256 x 256.
 template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
   using product::Tile;
   if constexpr (sizeof(T) == 2)
     if (size == 2) return launch_product<T, product::Big<TA, TB>, true, USE>(j, a, stream);
-  if constexpr (!TB)
+  if constexpr (!TA) {
+    if (size == 0) return launch_product<T, Tile<T, TA, TB, 64, 64, 2, 2, 5>, false, USE>(j, a, stream);
+  } else if constexpr (!TB) {
     if (size == 0) return launch_product<T, Tile<T, TA, TB, 128, 64, 4, 1, 3>, false, USE>(j, a, stream);
+  }
   return launch_product<T, Tile<T, TA, TB, 128, 128, 2, 2, 2>, false, USE>(j, a, stream);
 }
 
@@ -428,11 +469,12 @@ hipError_t forward(const LinearArgs& a, const LinearWork& w, hipStream_t stream)
     j.n = b.n_rows;
     j.k = a.width;
     j.c = a.inv_t * kLog2e;
-    j.part = reinterpret_cast<float4*>(a.ws);
+    j.part = static_cast<float4*>(a.ws);
+    j.found = reinterpret_cast<int4*>(static_cast<char*>(a.ws) + w.ids);
     hipError_t e = launch_sized<T, false, false, kStats>(w.size, j, b, stream);
     if (e != hipSuccess) return e;
-    const int slots = ceil_div(a.vocab, w.size == 2 ? 256 : 128);
-    finish_kernel<T><<<ceil_div(b.n_rows, 4), 256, 0, stream>>>(b, j.part, slots);
+    const int slots = ceil_div(a.vocab, w.size == 2 ? 256 : w.size == 1 ? 128 : 64);
+    finish_kernel<<<ceil_div(b.n_rows, 4), 256, 0, stream>>>(b, j.part, slots, j.found);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -25,11 +25,12 @@ __device__ __forceinline__ int seg_of(const int32_t* seg_off, int n_seg, int r, 
 // parent, kid_off, kid) and its tokens (tokens, token64, vocab).
 struct Behind {
   int n, row;         // how many; the only one's row (middle of a segment)
+  int seg;            // r's segment
   const int32_t *kid, *seg_off;
   bool root_start;    // r is a root's first token (it has no row in front)
   template <typename A>
   __device__ __forceinline__ Behind(const A& a, int r, int lane) : seg_off(a.seg_off) {
-    const int s = seg_of(a.seg_off, a.n_seg, r, lane);
+    const int s = seg = seg_of(a.seg_off, a.n_seg, r, lane);
     const bool last = r + 1 == a.seg_off[s + 1];
     kid = last ? a.kid + a.kid_off[s] : nullptr;
     n = last ? a.kid_off[s + 1] - a.kid_off[s] : 1;
