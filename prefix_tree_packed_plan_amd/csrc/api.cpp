@@ -245,7 +245,7 @@ EmbedWork embed_work(int64_t n_tokens, int32_t vocab, int32_t width) {
   EmbedWork w{};
   w.n_parts = n_tokens > tg::kEmbedPart ? static_cast<int32_t>((n_tokens + tg::kEmbedPart - 1) / tg::kEmbedPart) : 0;
   w.order = up((static_cast<size_t>(vocab) + 1) * sizeof(int32_t));
-  w.part = w.order + up(static_cast<size_t>(n_tokens) * sizeof(int32_t));
+  w.part = w.order + up(static_cast<size_t>(n_tokens) * sizeof(int2));
   w.bytes = w.part + static_cast<size_t>(w.n_parts) * 2 * width * sizeof(float);
   // 512 work-groups (two on each CU) share the table, as long as their rows fit.
   w.span = std::min<int32_t>((vocab + 511) / 512, tg::kEmbedSpan);
@@ -1279,7 +1279,7 @@ int tree_embedding(const void* tokens, const void* table, void* out, int64_t n_t
   a.vocab = vocab;
   a.width = width;
   a.scale = scale;
-  a.lanes_log2 = tg::embed_lanes_log2(width, dtype);
+  a.lanes_log2 = tg::embed_lanes_log2(width, dtype, 0);
   const hipError_t e = tg::launch_embed(a, dtype, token_bytes == 8, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("tree_embedding: launch", e);
   return TREE_OK;
@@ -1311,11 +1311,11 @@ int tree_embedding_backward(const void* tokens, const void* dout, void* dtable, 
   a.vocab = vocab;
   a.width = width;
   a.scale = scale;
-  a.lanes_log2 = tg::embed_lanes_log2(width, dtype);
+  a.lanes_log2 = tg::embed_lanes_log2(width, dtype, 6);  // whole waves
   a.span = w.span;
   a.n_parts = w.n_parts;
   a.start = reinterpret_cast<int32_t*>(base);
-  a.order = reinterpret_cast<int32_t*>(base + w.order);
+  a.order = reinterpret_cast<int2*>(base + w.order);
   a.part = reinterpret_cast<float*>(base + w.part);
   const hipError_t e = tg::launch_embed_backward(a, dtype, token_bytes == 8, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("tree_embedding_backward: launch", e);

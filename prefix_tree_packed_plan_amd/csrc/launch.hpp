@@ -344,15 +344,15 @@ struct EmbedArgs {
   int32_t span;         // rows of the table a work-group sorts the tokens of
   int32_t n_parts;      // parts of kEmbedPart tokens, 0 if no row can have more
   int32_t* start;       // workspace [vocab + 1]: where each row's tokens begin in `order`
-  int32_t* order;       // workspace [n_tokens]: the tokens by row, ascending
+  int2* order;          // workspace [n_tokens]: the tokens by row, ascending, each with its row
   float* part;          // workspace [n_parts, 2, width]
 };
 
-constexpr int kEmbedSpanLog2 = 10;
+constexpr int kEmbedSpanLog2 = 9;
 constexpr int kEmbedSpan = 1 << kEmbedSpanLog2;  // most rows of a sorting work-group
 constexpr int kEmbedPart = 64;
 
-int embed_lanes_log2(int32_t width, int dtype);
+int embed_lanes_log2(int32_t width, int dtype, int least);
 hipError_t launch_embed(const EmbedArgs& a, int dtype, bool token64, hipStream_t stream);
 hipError_t launch_embed_backward(const EmbedArgs& a, int dtype, bool token64, hipStream_t stream);
 

@@ -7,18 +7,18 @@
 // pieces at any address).
 //
 // The gradient takes the tokens sorted by their row of the table.  sort_kernel
-// makes that order: every work-group owns `span` rows and looks through all
-// tokens twice (they come from L2: 512 work-groups read 10240 tokens of 8 bytes
-// in 3 us), first to count, then to place.  It needs no pass over global
+// makes that order: every work-group owns `span` rows and looks through all tokens,
+// which come from L2, counts its own and places them.  It needs no pass over global
 // memory and no atomic whose order shows: each wave keeps counters of its own
 // for its share of the tokens, and within 64 tokens a lane's place among its
 // equals comes from comparing the ids bit by bit.  A row's list is therefore
-// in ascending order of the tokens, and the sums are the same in every run.
+// in ascending order of the tokens, and the sums are the same in every run.  Rows
+// without a token, most of a large table, are cleared on the way.
 //
-// sum_kernel then writes every row of the gradient, also those without a
-// token.  Rows of more than kPart tokens would keep one work-group busy long
-// after the others (a token that is a fifth of all of them); their lists are cut
-// into parts at multiples of kPart, and join_kernel adds the parts in order.
+// sum_kernel then writes the rows that have tokens, one for every position of the order at
+// which a row begins.  Rows of more than kPart tokens would keep one work-group busy
+// long after the others (a token that is a fifth of all of them); their lists are
+// cut into parts at multiples of kPart, and join_kernel adds the parts in order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -39,6 +39,8 @@ constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kPart = kEmbedPart;
+static_assert(kPart == 64, "a part's tokens are held by the lanes of a wave");
+constexpr int kKept = 256;  // tokens in range a sorting wave keeps at hand
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // 16 bytes at any address.
 typedef u32x4 any_u32x4 __attribute__((aligned(2)));
@@ -119,42 +121,67 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(EmbedArgs a) {
 }
 
 // ---- the tokens in order of their rows ----------------------------------------------
-// This work-group's rows: lo .. lo + span - 1.  cnt[w][r]: tokens of row lo + r in
-// wave w's share; then where its next one goes.
+// Token n as an unsigned row of the table; one without a row is above all of them.
 template <typename I>
+__device__ __forceinline__ uint32_t row_of(const EmbedArgs& a, int n);
+template <>
+__device__ __forceinline__ uint32_t row_of<int32_t>(const EmbedArgs& a, int n) {
+  const uint32_t x = static_cast<const uint32_t*>(a.tokens)[n];
+  return x < static_cast<uint32_t>(a.vocab) ? x : ~0u;
+}
+template <>
+__device__ __forceinline__ uint32_t row_of<int64_t>(const EmbedArgs& a, int n) {
+  const uint2 x = static_cast<const uint2*>(a.tokens)[n];
+  return x.y == 0 && x.x < static_cast<uint32_t>(a.vocab) ? x.x : ~0u;
+}
+
+// This work-group's rows: lo .. lo + span - 1.  cnt[w][r]: tokens of row lo + r in
+// wave w's share; then where its next one goes.  Rows without a token are cleared.
+template <typename T, typename I>
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
   constexpr int U = 8;
   __shared__ int cnt[kSortWaves * kEmbedSpan];
+  __shared__ int2 kept[kSortWaves * kKept];
   __shared__ int wave_total[kSortWaves];
   __shared__ int wave_less[kSortWaves];
+  __shared__ uint64_t empty[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lo = blockIdx.x * a.span, span = min(a.span, a.vocab - lo);
   const int n = static_cast<int>(a.n_tokens);
   const int share = ((n + kSortThreads - 1) / kSortThreads) * 64;
   const int t0 = min(n, wave * share), t1 = min(n, t0 + share);
+  const uint64_t lower = (uint64_t(1) << lane) - 1;
   int* mine = cnt + wave * kEmbedSpan;
   for (int i = tid; i < kSortWaves * kEmbedSpan; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  // Calls f(token's row minus lo, n) for 64 tokens at a time, in order; -1 past
-  // the end or without a row.
+  // Calls f(row minus lo, token) for 64 tokens of this wave's share at a time, in order,
+  // where one of them is in range; `less` counts those below lo.
+  int less = 0;
   const auto each = [&](auto f) {
     for (int t = t0; t < t1; t += 64 * U) {
-      int id[U];
+      uint32_t id[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = t + 64 * u + lane;
-        id[u] = at < t1 ? token<I>(a, at) : -1;
+        id[u] = at < t1 ? row_of<I>(a, at) : ~0u;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) f(id[u], t + 64 * u + lane);
+      for (int u = 0; u < U; ++u) {
+        less += id[u] < static_cast<uint32_t>(lo);
+        const uint32_t r = id[u] - lo;
+        if (__any(r < static_cast<uint32_t>(span))) f(r, t + 64 * u + lane);
+      }
     }
   };
-  int less = 0;
-  each([&](int id, int) {
-    less += id >= 0 && id < lo;
-    const int r = id - lo;
-    if (id >= lo && r < span) atomicAdd(&mine[r], 1);
+  int held = 0;  // tokens in range so far: the first kKept are kept in LDS
+  each([&](uint32_t r, int t) {
+    const bool in = r < static_cast<uint32_t>(span);
+    const uint64_t who = __ballot(in);
+    const int at = held + __popcll(who & lower);
+    if (in) atomicAdd(&mine[r], 1);
+    if (in && at < kKept) kept[wave * kKept + at] = make_int2(r, t);
+    held += __popcll(who);
   });
 #pragma unroll
   for (int o = 32; o; o >>= 1) less += __shfl_xor(less, o, 64);
@@ -168,6 +195,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
   if (tid < span)
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) total += cnt[w * kEmbedSpan + tid];
+  const uint64_t none = __ballot(total == 0);
+  if (lane == 0) empty[wave] = none;
   int sum = total;  // of this lane and those below
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -190,52 +219,78 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
     }
   }
   __syncthreads();
-  each([&](int id, int t) {
-    const int r = id - lo;
-    const bool in = id >= lo && r < span;
+  const auto place = [&](uint32_t r, int t) {
+    const bool in = r < static_cast<uint32_t>(span);
     uint64_t same = __ballot(in);
-    if (same == 0) return;
 #pragma unroll
     for (int b = 0; b < kEmbedSpanLog2; ++b) {
       const uint64_t ones = __ballot((r >> b) & 1);
       same &= (r >> b) & 1 ? ones : ~ones;
     }
-    const uint64_t below = same & ((uint64_t(1) << lane) - 1);
+    const uint64_t below = same & lower;
     int first = 0;
     // The first of its equals moves their counter on; waves share none.
     if (in && below == 0) first = atomicAdd(&mine[r], static_cast<int>(__popcll(same)));
     const int leader = in ? __builtin_ctzll(same) : lane;
     first = __shfl(first, leader, 64);
-    if (in) a.order[first + __popcll(below)] = t;
-  });
+    if (in) a.order[first + __popcll(below)] = make_int2(t, lo + static_cast<int>(r));
+  };
+  if (held <= kKept) {
+    for (int i = 0; i < held; i += 64) {
+      const int2 x = i + lane < held ? kept[wave * kKept + i + lane] : make_int2(-1, 0);
+      place(x.x, x.y);
+    }
+  } else {
+    each(place);
+  }
+  // A wave a row: zeros where there is no token.
+  constexpr int N = Vec<T>::N;
+  const int vecs = a.width / N;
+  for (int r = wave; r < span; r += kSortWaves) {
+    if (!((empty[r >> 6] >> (r & 63)) & 1)) continue;
+    T* out = static_cast<T*>(a.out) + int64_t(lo + r) * a.width;
+#pragma unroll 4
+    for (int j = lane; j < vecs; j += 64) *reinterpret_cast<any_u32x4*>(out + j * N) = u32x4{0, 0, 0, 0};
+    for (int c = vecs * N + lane; c < a.width; c += 64) Vec<T>::put(out + c, 0.f);
+  }
 }
 
 // ---- sums ----------------------------------------------------------------------------
-// Positions p0 .. p1 - 1 of the order, this lane's piece j (or, TAIL, column j),
-// added in ascending order with U rows' loads in flight.
+// Calls f(whether it is a single column, column) for this thread's pieces of a row.
+template <typename T, typename F>
+__device__ __forceinline__ void columns(const EmbedArgs& a, int j0, int lanes, F f) {
+  constexpr int N = Vec<T>::N;
+  const int vecs = a.width / N;
+  for (int j = j0; j < vecs; j += lanes) f(std::false_type{}, j * N);
+  for (int c = vecs * N + j0; c < a.width; c += lanes) f(std::true_type{}, c);
+}
+
+// The tokens that lanes i0 .. i1 - 1 hold: their gradients at a column (TAIL) or piece
+// from `col` on, added in order with U rows' loads in flight.
 template <typename T, bool TAIL>
-__device__ __forceinline__ void add_rows(const EmbedArgs& a, int p0, int p1, int64_t col, float* x) {
+__device__ __forceinline__ void add_rows(const EmbedArgs& a, int held, int i0, int i1, int col, float* x) {
   constexpr int N = TAIL ? 1 : Vec<T>::N, U = 8;
   const T* d = static_cast<const T*>(a.dout) + col;
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = 0.f;
-  for (int p = p0; p < p1; p += U) {
-    int64_t row[U];
+  for (int p = i0; p < i1; p += U) {
+    const T* row[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) row[u] = a.order[min(p + u, p1 - 1)];
+    for (int u = 0; u < U; ++u)
+      row[u] = d + int64_t(__builtin_amdgcn_readlane(held, min(p + u, i1 - 1))) * a.width;
     if constexpr (TAIL) {
       float w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = Vec<T>::one(d + row[u] * a.width);
+      for (int u = 0; u < U; ++u) w[u] = Vec<T>::one(row[u]);
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[0] += p + u < p1 ? w[u] : 0.f;
+      for (int u = 0; u < U; ++u) x[0] += p + u < i1 ? w[u] : 0.f;
     } else {
       u32x4 w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const any_u32x4*>(d + row[u] * a.width);
+      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const any_u32x4*>(row[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (p + u >= p1) break;
+        if (p + u >= i1) break;
         float y[N];
         Vec<T>::unpack(w[u], y);
 #pragma unroll
@@ -243,15 +298,6 @@ __device__ __forceinline__ void add_rows(const EmbedArgs& a, int p0, int p1, int
       }
     }
   }
-}
-
-// Calls f(whether it is a single column, column) for this thread's pieces of a row.
-template <typename T, typename F>
-__device__ __forceinline__ void columns(const EmbedArgs& a, const Item& it, F f) {
-  constexpr int N = Vec<T>::N;
-  const int vecs = a.width / N;
-  for (int j = it.j0; j < vecs; j += it.lanes) f(std::false_type{}, j * N);
-  for (int c = vecs * N + it.j0; c < a.width; c += it.lanes) f(std::true_type{}, c);
 }
 
 template <typename T, bool TAIL>
@@ -264,15 +310,31 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, int64_t v, int col, 
   else *reinterpret_cast<any_u32x4*>(o) = Vec<T>::pack(x);
 }
 
-// Items 0 .. vocab - 1: rows of the table; then the parts of long lists.  Part q
-// is positions kPart q .. kPart (q + 1) - 1; at most its first and its last row have
+// Position p of the order: the row that begins there, if one does and it has at most
+// kPart tokens.  Every wave of the item reads the whole list, an entry a lane.
+template <typename T>
+__device__ __forceinline__ void sum_row(const EmbedArgs& a, int p, int n, const Item& it, int lane) {
+  const int2 e = p + lane < n ? a.order[p + lane] : make_int2(0, -1);
+  const int before = p > 0 ? a.order[p - 1].y : -1, after = p + kPart < n ? a.order[p + kPart].y : -1;
+  const int v = __builtin_amdgcn_readfirstlane(e.y);
+  if (v == before || v == after) return;
+  const int count = __popcll(__ballot(e.y == v));
+  columns<T>(a, it.j0, it.lanes, [&](auto tail, int col) {
+    constexpr bool TAIL = decltype(tail)::value;
+    float x[Vec<T>::N];
+    add_rows<T, TAIL>(a, e.x, 0, count, col, x);
+    put_row<T, TAIL>(a, v, col, x);
+  });
+}
+
+// Part q, positions kPart q .. kPart (q + 1) - 1: at most its first and its last row have
 // more than kPart tokens, and their sums are part[q][0] and part[q][1].
-template <typename T, typename I>
-__device__ __forceinline__ void sum_part(const EmbedArgs& a, const Item& it) {
-  const int q = static_cast<int>(it.i - a.vocab);
-  const int p0 = q * kPart, p1 = min(a.start[a.vocab], p0 + kPart);
+template <typename T>
+__device__ __forceinline__ void sum_part(const EmbedArgs& a, int q, int n, const Item& it, int lane) {
+  const int p0 = q * kPart, p1 = min(n, p0 + kPart);
   if (p0 >= p1) return;
-  const int first = token<I>(a, a.order[p0]), last = token<I>(a, a.order[p1 - 1]);
+  const int2 e = a.order[min(p0 + lane, p1 - 1)];
+  const int first = __builtin_amdgcn_readfirstlane(e.y), last = __builtin_amdgcn_readlane(e.y, p1 - 1 - p0);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int v = s ? last : first;
@@ -280,66 +342,81 @@ __device__ __forceinline__ void sum_part(const EmbedArgs& a, const Item& it) {
     const int r0 = a.start[v], r1 = a.start[v + 1];
     if (r1 - r0 <= kPart) continue;
     float* out = a.part + (int64_t(q) * 2 + s) * a.width;
-    columns<T>(a, it, [&](auto tail, int col) {
+    columns<T>(a, it.j0, it.lanes, [&](auto tail, int col) {
       constexpr bool TAIL = decltype(tail)::value;
       float x[Vec<T>::N];
-      add_rows<T, TAIL>(a, max(p0, r0), min(p1, r1), col, x);
+      add_rows<T, TAIL>(a, e.x, max(p0, r0) - p0, min(p1, r1) - p0, col, x);
 #pragma unroll
       for (int i = 0; i < (TAIL ? 1 : Vec<T>::N); ++i) out[col + i] = x[i];
     });
   }
 }
 
-template <typename T, typename I>
+// Items: the parts of long lists, which take longest, then the positions.
+template <typename T>
 __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedArgs a) {
-  Item it(a);
-  for (; it.i < a.vocab; it.next()) {
-    const int p0 = a.start[it.i], p1 = a.start[it.i + 1];
-    if (p1 - p0 > kPart) continue;
-    columns<T>(a, it, [&](auto tail, int col) {
-      constexpr bool TAIL = decltype(tail)::value;
-      float x[Vec<T>::N];
-      add_rows<T, TAIL>(a, p0, p1, col, x);
-      put_row<T, TAIL>(a, it.i, col, x);
-    });
+  const int lane = threadIdx.x & 63, n = a.start[a.vocab];
+  const Item all(a);
+  for (Item it = all; it.i < a.n_parts + a.n_tokens; it.next()) {
+    const int i = __builtin_amdgcn_readfirstlane(static_cast<int>(it.i));
+    if (i < a.n_parts) sum_part<T>(a, i, n, it, lane);
+    else if (i - a.n_parts < n) sum_row<T>(a, i - a.n_parts, n, it, lane);
   }
-  for (; it.i < int64_t(a.vocab) + a.n_parts; it.next()) sum_part<T, I>(a, it);
 }
 
 // Item q: the row of more than kPart tokens whose list begins in part q, if there is
-// one (it reaches past the part's end, so there is at most one).
-template <typename T, typename I>
+// one (it reaches past the part's end, so there is at most one).  A work-group takes
+// kJoinColumns columns of it; each wave adds a quarter of the parts, and the
+// quarters are added in order.
+constexpr int kJoinColumns = 256;
+template <typename T>
 __global__ __launch_bounds__(kThreads) void join_kernel(EmbedArgs a) {
-  constexpr int U = 16;
-  for (Item it(a); it.i < a.n_parts; it.next()) {
-    const int q = static_cast<int>(it.i), end = (q + 1) * kPart;
-    if (end > a.start[a.vocab]) continue;
-    const int v = token<I>(a, a.order[end - 1]);
+  constexpr int U = 8, W = kThreads / 64;
+  __shared__ float4 sums[W][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int q = blockIdx.x; q < a.n_parts; q += gridDim.x) {
+    const int end = (q + 1) * kPart;
+    if (end > a.start[a.vocab]) return;
+    const int v = a.order[end - 1].y;
     const int r0 = a.start[v], r1 = a.start[v + 1];
     if (r1 - r0 <= kPart || r0 < q * kPart) continue;
-    const int q1 = (r1 - 1) / kPart;
+    const int q1 = (r1 - 1) / kPart + 1, each = (q1 - q + W - 1) / W;
     const int s0 = r0 == q * kPart ? 0 : 1;  // other parts begin with this row
-    columns<T>(a, it, [&](auto tail, int col) {
-      constexpr bool TAIL = decltype(tail)::value;
-      constexpr int N = TAIL ? 1 : Vec<T>::N;
-      float x[Vec<T>::N] = {};
-      for (int p = q; p <= q1; p += U) {
-        float y[U][N];
+    const int b = q + wave * each, e = min(q1, b + each);
+    for (int c0 = blockIdx.y * kJoinColumns; c0 < a.width; c0 += gridDim.y * kJoinColumns) {
+      const int col = c0 + 4 * lane, left = a.width - col;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int p = b; p < e; p += U) {
+        float y[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int pu = min(p + u, q1);
+          const int pu = min(p + u, e - 1);
           const float* src = a.part + (int64_t(pu) * 2 + (pu == q ? s0 : 0)) * a.width + col;
 #pragma unroll
-          for (int i = 0; i < N; ++i) y[u][i] = src[i];
+          for (int i = 0; i < 4; ++i) y[u][i] = i < left ? src[i] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (p + u <= q1)
+          if (p + u < e)
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] += y[u][i];
+            for (int i = 0; i < 4; ++i) x[i] += y[u][i];
       }
-      put_row<T, TAIL>(a, v, col, x);
-    });
+      sums[wave][lane] = make_float4(x[0], x[1], x[2], x[3]);
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+          const float4 y = sums[w][lane];
+          x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
+        }
+        T* o = static_cast<T*>(a.out) + int64_t(v) * a.width + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < left) Vec<T>::put(o + i, x[i] * a.scale);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -358,10 +435,10 @@ uint32_t groups(int64_t items, int lanes_log2) {
 
 }  // namespace
 
-// Threads of one row: a power of two that covers it, 256 at most.
-int embed_lanes_log2(int32_t width, int dtype) {
+// Threads of one row: a power of two that covers it, `least` at least and 256 at most.
+int embed_lanes_log2(int32_t width, int dtype, int least) {
   const int n = dtype == TREE_DTYPE_BF16 ? 8 : 4;
-  int l = 0;
+  int l = least;
   while (l < 8 && (int64_t(n) << l) < width) ++l;
   return l;
 }
@@ -376,14 +453,15 @@ hipError_t launch_embed(const EmbedArgs& a, int dtype, bool token64, hipStream_t
 hipError_t launch_embed_backward(const EmbedArgs& a, int dtype, bool token64, hipStream_t stream) {
   return by_type(dtype, token64, [&](auto t, auto i) {
     using T = decltype(t);
-    using I = decltype(i);
-    sort_kernel<I><<<(a.vocab + a.span - 1) / a.span, kSortThreads, 0, stream>>>(a);
+    sort_kernel<T, decltype(i)><<<(a.vocab + a.span - 1) / a.span, kSortThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    sum_kernel<T, I><<<groups(int64_t(a.vocab) + a.n_parts, a.lanes_log2), kThreads, 0, stream>>>(a);
+    if (e != hipSuccess || a.n_tokens == 0) return e;
+    sum_kernel<T><<<groups(a.n_tokens + a.n_parts, a.lanes_log2), kThreads, 0, stream>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess || a.n_parts == 0) return e;
-    join_kernel<T, I><<<groups(a.n_parts, a.lanes_log2), kThreads, 0, stream>>>(a);
+    const int columns = (a.width + kJoinColumns - 1) / kJoinColumns;
+    const dim3 grid(std::min(a.n_parts, 65536), std::min(columns, 64));
+    join_kernel<T><<<grid, kThreads, 0, stream>>>(a);
     return hipGetLastError();
   });
 }

@@ -96,9 +96,9 @@ def test_lengths(n):
         check_backward(tok, dout, 37, 2.5)
 
 
-@pytest.mark.parametrize("vocab", [1, 2, 511, 512, 513, 1003, 1025, 524288, 524289, 600001])
+@pytest.mark.parametrize("vocab", [1, 2, 511, 512, 513, 1003, 1025, 262144, 262145, 524288, 524289, 600001])
 def test_vocabularies(vocab):
-    """524288 rows are what 512 sorting work-groups cover; beyond that there are more."""
+    """262144 rows are what 512 sorting work-groups cover; beyond that there are more."""
     say(f"embedding vocab={vocab}")
     tok, table, dout = inputs(3000, vocab, 16, torch.bfloat16, seed=vocab)
     tok[:3] = vocab - 1
@@ -169,6 +169,20 @@ def test_repeats_give_the_same_bits_in_token_order():
     a = check_backward(tok, dout, 300, 1.0)
     for _ in range(3):
         assert torch.equal(a, ptp.tree_embedding_backward(tok, dout, 300))
+
+
+@pytest.mark.parametrize("n", [5000, 70000])
+def test_sorting_waves_with_more_tokens_than_they_keep(n):
+    """A wave keeps 256 tokens of its rows at hand and looks for the others again; some
+    waves do and some do not."""
+    g = torch.Generator().manual_seed(n)
+    tok = torch.randint(0, 40000, (n,), generator=g)
+    tok[:n // 2] = torch.randint(0, 30, (n // 2,), generator=g)
+    tok[n // 2 + 7] = 39999
+    dout = torch.randn((n, 20), generator=g).to(DEV)
+    say(f"embedding kept n={n}")
+    check_backward(tok.to(DEV), dout, 40000, 1.0)
+    check_backward(tok.int().to(DEV), dout.bfloat16(), 40000, 2.0)
 
 
 def test_unaligned_tensors():
