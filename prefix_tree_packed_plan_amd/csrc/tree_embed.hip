@@ -265,39 +265,47 @@ __device__ __forceinline__ void columns(const EmbedArgs& a, int j0, int lanes, F
   for (int c = vecs * N + j0; c < a.width; c += lanes) f(std::true_type{}, c);
 }
 
-// The tokens that lanes i0 .. i1 - 1 hold: their gradients at a column (TAIL) or piece
-// from `col` on, added in order with U rows' loads in flight.
-template <typename T, bool TAIL>
-__device__ __forceinline__ void add_rows(const EmbedArgs& a, int held, int i0, int i1, int col, float* x) {
-  constexpr int N = TAIL ? 1 : Vec<T>::N, U = 8;
-  const T* d = static_cast<const T*>(a.dout) + col;
+// x += the gradients, at a column (TAIL) or piece from `col` on, of the tokens that lanes
+// p .. p + U - 1 hold (REST: of those below i1), in order and with all loads in flight.
+template <typename T, bool TAIL, int U, bool REST>
+__device__ __forceinline__ void add_some(const EmbedArgs& a, int held, int p, int i1, int col, float* x) {
+  constexpr int N = TAIL ? 1 : Vec<T>::N;
+  const T* row[U];
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = 0.f;
-  for (int p = i0; p < i1; p += U) {
-    const T* row[U];
+  for (int u = 0; u < U; ++u)
+    row[u] = static_cast<const T*>(a.dout) + col +
+             int64_t(__builtin_amdgcn_readlane(held, REST ? min(p + u, i1 - 1) : p + u)) * a.width;
+  if constexpr (TAIL) {
+    float y[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      row[u] = d + int64_t(__builtin_amdgcn_readlane(held, min(p + u, i1 - 1))) * a.width;
-    if constexpr (TAIL) {
-      float w[U];
+    for (int u = 0; u < U; ++u) y[u] = Vec<T>::one(row[u]);
 #pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = Vec<T>::one(row[u]);
+    for (int u = 0; u < U; ++u) x[0] += !REST || p + u < i1 ? y[u] : 0.f;
+  } else {
+    u32x4 w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[0] += p + u < i1 ? w[u] : 0.f;
-    } else {
-      u32x4 w[U];
+    for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const any_u32x4*>(row[u]);
+    __builtin_amdgcn_sched_barrier(0);  // all loads, then one row's values at a time
 #pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const any_u32x4*>(row[u]);
+    for (int u = 0; u < U; ++u) {
+      float y[N];
+      Vec<T>::unpack(w[u], y);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (p + u >= i1) break;
-        float y[N];
-        Vec<T>::unpack(w[u], y);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] += y[i];
-      }
+      for (int i = 0; i < N; ++i) x[i] += !REST || p + u < i1 ? y[i] : 0.f;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+}
+// The same of lanes i0 .. i1 - 1, from 0 on.
+template <typename T, bool TAIL>
+__device__ __forceinline__ void add_rows(const EmbedArgs& a, int held, int i0, int i1, int col, float* x) {
+  constexpr int U = 8;
+#pragma unroll
+  for (int i = 0; i < (TAIL ? 1 : Vec<T>::N); ++i) x[i] = 0.f;
+  int p = i0;
+  for (; p + U <= i1; p += U) add_some<T, TAIL, U, false>(a, held, p, i1, col, x);
+  if (i1 - p > 4) add_some<T, TAIL, U, true>(a, held, p, i1, col, x);
+  else if (i1 > p) add_some<T, TAIL, 4, true>(a, held, p, i1, col, x);
 }
 
 template <typename T, bool TAIL>
