@@ -348,8 +348,7 @@ struct EmbedArgs {
   float* part;          // workspace [n_parts, 2, width]
 };
 
-constexpr int kEmbedSpanLog2 = 9;
-constexpr int kEmbedSpan = 1 << kEmbedSpanLog2;  // most rows of a sorting work-group
+constexpr int kEmbedSpan = 512;  // most rows of a sorting work-group
 constexpr int kEmbedPart = 64;
 
 int embed_lanes_log2(int32_t width, int dtype, int least);

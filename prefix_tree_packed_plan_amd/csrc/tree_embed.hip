@@ -155,33 +155,41 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
   int* mine = cnt + wave * kEmbedSpan;
   for (int i = tid; i < kSortWaves * kEmbedSpan; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  // Calls f(row minus lo, token) for 64 tokens of this wave's share at a time, in order,
-  // where one of them is in range; `less` counts those below lo.
-  int less = 0;
+  // Calls f(rows, t) for U times 64 tokens from t on of this wave's share, in order; the
+  // next ones are on their way meanwhile.
   const auto each = [&](auto f) {
-    for (int t = t0; t < t1; t += 64 * U) {
-      uint32_t id[U];
+    uint32_t id[U];
+    const auto load = [&](int t) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = t + 64 * u + lane;
         id[u] = at < t1 ? row_of<I>(a, at) : ~0u;
       }
+    };
+    load(t0);
+    for (int t = t0; t < t1; t += 64 * U) {
+      uint32_t now[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        less += id[u] < static_cast<uint32_t>(lo);
-        const uint32_t r = id[u] - lo;
-        if (__any(r < static_cast<uint32_t>(span))) f(r, t + 64 * u + lane);
-      }
+      for (int u = 0; u < U; ++u) now[u] = id[u];
+      load(t + 64 * U);
+      f(now, t);
     }
   };
+  int less = 0;  // tokens of rows below lo
   int held = 0;  // tokens in range so far: the first kKept are kept in LDS
-  each([&](uint32_t r, int t) {
-    const bool in = r < static_cast<uint32_t>(span);
-    const uint64_t who = __ballot(in);
-    const int at = held + __popcll(who & lower);
-    if (in) atomicAdd(&mine[r], 1);
-    if (in && at < kKept) kept[wave * kKept + at] = make_int2(r, t);
-    held += __popcll(who);
+  each([&](const uint32_t (&id)[U], int t) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      less += id[u] < static_cast<uint32_t>(lo);
+      const uint32_t r = id[u] - lo;
+      const bool in = r < static_cast<uint32_t>(span);
+      const uint64_t who = __ballot(in);
+      if (who == 0) continue;
+      const int at = held + __popcll(who & lower);
+      if (in) atomicAdd(&mine[r], 1);
+      if (in && at < kKept) kept[wave * kKept + at] = make_int2(r, t + 64 * u + lane);
+      held += __popcll(who);
+    }
   });
 #pragma unroll
   for (int o = 32; o; o >>= 1) less += __shfl_xor(less, o, 64);
@@ -219,29 +227,54 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
     }
   }
   __syncthreads();
-  const auto place = [&](uint32_t r, int t) {
-    const bool in = r < static_cast<uint32_t>(span);
-    uint64_t same = __ballot(in);
+  // K times 64 tokens: all of one kind of step, then all of the next, so that LDS is
+  // waited for once.
+  const auto place = [&](auto count, const uint32_t* r, const int* t) {
+    constexpr int K = decltype(count)::value;
+    uint64_t same[K];
+    int first[K];
 #pragma unroll
-    for (int b = 0; b < kEmbedSpanLog2; ++b) {
-      const uint64_t ones = __ballot((r >> b) & 1);
-      same &= (r >> b) & 1 ? ones : ~ones;
+    for (int u = 0; u < K; ++u) {
+      same[u] = __ballot(r[u] < static_cast<uint32_t>(span));
+      for (uint32_t bit = 1; bit < static_cast<uint32_t>(span); bit += bit) {
+        const bool set = r[u] & bit;
+        const uint64_t ones = __ballot(set);
+        same[u] &= set ? ones : ~ones;
+      }
+      // The first of its equals moves their counter on; waves share none.
+      first[u] = 0;
+      if (r[u] < static_cast<uint32_t>(span) && (same[u] & lower) == 0)
+        first[u] = atomicAdd(&mine[r[u]], static_cast<int>(__popcll(same[u])));
     }
-    const uint64_t below = same & lower;
-    int first = 0;
-    // The first of its equals moves their counter on; waves share none.
-    if (in && below == 0) first = atomicAdd(&mine[r], static_cast<int>(__popcll(same)));
-    const int leader = in ? __builtin_ctzll(same) : lane;
-    first = __shfl(first, leader, 64);
-    if (in) a.order[first + __popcll(below)] = make_int2(t, lo + static_cast<int>(r));
+#pragma unroll
+    for (int u = 0; u < K; ++u)
+      first[u] = __shfl(first[u], r[u] < static_cast<uint32_t>(span) ? __builtin_ctzll(same[u]) : lane, 64);
+#pragma unroll
+    for (int u = 0; u < K; ++u)
+      if (r[u] < static_cast<uint32_t>(span))
+        a.order[first[u] + __popcll(same[u] & lower)] = make_int2(t[u], lo + static_cast<int>(r[u]));
   };
   if (held <= kKept) {
     for (int i = 0; i < held; i += 64) {
       const int2 x = i + lane < held ? kept[wave * kKept + i + lane] : make_int2(-1, 0);
-      place(x.x, x.y);
+      const uint32_t r = x.x;
+      place(std::integral_constant<int, 1>{}, &r, &x.y);
     }
   } else {
-    each(place);
+    constexpr int K = 4;
+    each([&](const uint32_t (&id)[U], int t) {
+#pragma unroll
+      for (int h = 0; h < U; h += K) {
+        uint32_t r[K];
+        int at[K];
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+          r[u] = id[h + u] - lo;  // without a row: 2^32 - 1 - lo, out of range
+          at[u] = t + 64 * (h + u) + lane;
+        }
+        place(std::integral_constant<int, K>{}, r, at);
+      }
+    });
   }
   // A wave a row: zeros where there is no token.
   constexpr int N = Vec<T>::N;
@@ -379,14 +412,17 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedArgs a) {
 constexpr int kJoinColumns = 256;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void join_kernel(EmbedArgs a) {
-  constexpr int U = 8, W = kThreads / 64;
+  constexpr int U = 16, W = kThreads / 64;
   __shared__ float4 sums[W][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int q = blockIdx.x; q < a.n_parts; q += gridDim.x) {
     const int end = (q + 1) * kPart;
-    if (end > a.start[a.vocab]) return;
-    const int v = a.order[end - 1].y;
+    // The row goes on behind the part.
+    if (end >= a.n_tokens) return;
+    const int n = a.start[a.vocab], v = a.order[end - 1].y, next = a.order[end].y;
+    if (end >= n) return;
+    if (next != v) continue;
     const int r0 = a.start[v], r1 = a.start[v + 1];
     if (r1 - r0 <= kPart || r0 < q * kPart) continue;
     const int q1 = (r1 - 1) / kPart + 1, each = (q1 - q + W - 1) / W;
@@ -395,20 +431,23 @@ __global__ __launch_bounds__(kThreads) void join_kernel(EmbedArgs a) {
     for (int c0 = blockIdx.y * kJoinColumns; c0 < a.width; c0 += gridDim.y * kJoinColumns) {
       const int col = c0 + 4 * lane, left = a.width - col;
       float x[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int p = b; p < e; p += U) {
-        float y[U][4];
+      if (left >= 4) {
+        for (int p = b; p < e; p += U) {
+          u32x4 y[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int pu = min(p + u, e - 1);
-          const float* src = a.part + (int64_t(pu) * 2 + (pu == q ? s0 : 0)) * a.width + col;
+          for (int u = 0; u < U; ++u) {
+            const int pu = min(p + u, e - 1);
+            y[u] = *reinterpret_cast<const any_u32x4*>(a.part + (int64_t(pu) * 2 + (pu == q ? s0 : 0)) * a.width + col);
+          }
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[u][i] = i < left ? src[i] : 0.f;
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += p + u < e ? __uint_as_float(y[u][i]) : 0.f;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (p + u < e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += y[u][i];
+      } else if (left > 0) {
+        for (int p = b; p < e; ++p)
+          for (int i = 0; i < left; ++i) x[i] += a.part[(int64_t(p) * 2 + (p == q ? s0 : 0)) * a.width + col + i];
       }
       sums[wave][lane] = make_float4(x[0], x[1], x[2], x[3]);
       __syncthreads();
