@@ -216,14 +216,13 @@ __device__ __forceinline__ f32x4 mma(const uint4 a, const uint4 b, const f32x4 c
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
 }
-// The six largest partial products, the smallest first.
-__device__ __forceinline__ f32x4 mma(const Split& a, const Split& b, f32x4 c) {
+// The five smaller ones of the six largest partial products, the smallest first.
+__device__ __forceinline__ f32x4 mma_rest(const Split& a, const Split& b, f32x4 c) {
   c = mma(a.part(1), b.part(1), c);
   c = mma(a.part(2), b.part(0), c);
   c = mma(a.part(0), b.part(2), c);
   c = mma(a.part(1), b.part(0), c);
-  c = mma(a.part(0), b.part(1), c);
-  return mma(a.part(0), b.part(0), c);
+  return mma(a.part(0), b.part(1), c);
 }
 
 // Blocks x and y, y behind x along m, as 8 neighbouring bf16 a lane: of block x (lanes of
@@ -260,7 +259,7 @@ struct Tile {
   static constexpr int KS = BK / 32;  // fragments along a step
   // B stored by k: rows of zeros follow its last, up to a whole step (A's repeat
   // its last there).
-  static constexpr bool B_PADDED = TB;
+  static constexpr bool B_PADDED = TB, A_BY_K = TA;
   using OpA = Operand<T, TA, BM, W>;
   using OpB = Operand<T, TB, BN, W>;
   using RdA = Reader<T, TA, BM>;
@@ -387,6 +386,11 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
       if (t < steps) stage(t, t);
+    // Logits: the five smaller partial products are added up by themselves, below 2^-8 of
+    // the sum, so that it is rounded once for 32 k instead of six times (the largest
+    // error of an fp32 gradient is that of a probability near 1).
+    constexpr bool APART = !C::B_PADDED && !C::A_BY_K;
+    f32x4 rest[APART ? MB : 1][APART ? NB : 1] = {};
     int cur = 0, into = S - 1;
     for (int t = 0; t < steps; ++t) {
       // Step t has landed for every wave, and step t - 1 has been read by every wave.
@@ -412,7 +416,9 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
       for (int m = 0; m < MB; ++m) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          acc[m][n] = mma(a[m & 1], b[n], acc[m][n]);
+          if constexpr (APART) rest[m][n] = mma_rest(a[m & 1], b[n], rest[m][n]);
+          else acc[m][n] = mma_rest(a[m & 1], b[n], acc[m][n]);
+          acc[m][n] = mma(a[m & 1].part(0), b[n].part(0), acc[m][n]);
           if (m + 1 < MB)
 #pragma unroll
             for (int j = n * 4 / NB; j < (n + 1) * 4 / NB; ++j) split_pair(a[(m + 1) & 1], j, xa[m + 1][2 * j], xa[m + 1][2 * j + 1]);
@@ -422,6 +428,11 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
       cur = cur + 1 == S ? 0 : cur + 1;
       into = into + 1 == S ? 0 : into + 1;
     }
+    if constexpr (APART)
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[m][n] += rest[m][n];
   }
 }
 

@@ -280,8 +280,11 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x);
-          acc[mb][nb][i] = ex2(lp * kLog2e) * fmaf(rc.z, fmaxf(lp, -1e4f), rc.y);  // exp is 0 below -104
+          const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x), held = fmaxf(lp, -1e4f);  // exp is 0 below -104
+          float e = ex2(lp * kLog2e);
+          // That product's rounding, 2^-24 of up to 20 or more, is too much for fp32.
+          if (sizeof(T) == 4) e = fmaf(e, fmaf(held, kLog2e, -(held * kLog2e)) * kLn2, e);
+          acc[mb][nb][i] = e * fmaf(rc.z, held, rc.y);
         }
       if (!__all(live) || m0 + BM > j.m) {
 #pragma unroll
