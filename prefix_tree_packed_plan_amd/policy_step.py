@@ -1,21 +1,40 @@
 """A policy update on a packed trie of rollouts, end to end on the library's
 operators.
 
-    python -m prefix_tree_packed_plan_amd.policy_step
+    python -m prefix_tree_packed_plan_amd.policy_step [--no-logits]
 
 A small language model -- one recurrent mixer (tree conv + tree gated delta
 rule) and one attention layer -- over a prompt with several sampled
 completions, each shared token computed once.  Its loss weights every token's
 log probability with an advantage and adds an entropy bonus; gradients come
 from the library's backward entry points, and the update is plain SGD.  The
-program prints the loss of each step.
+program prints the loss of each step.  With --no-logits the log probabilities
+and their gradients come straight from the hidden states and the output weight,
+no [N, vocab] tensor is kept, and every gradient is bitwise repeatable.
 """
 from __future__ import annotations
+
+import argparse
+import sys
 
 import torch
 from torch.autograd.function import once_differentiable
 
 import prefix_tree_packed_plan_amd as ptp
+
+
+class Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, table):
+        ctx.vocab = table.shape[0]
+        ctx.save_for_backward(tokens)
+        return ptp.tree_embedding(tokens, table)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dx):
+        (tokens,) = ctx.saved_tensors
+        return None, ptp.tree_embedding_backward(tokens, dx.contiguous(), ctx.vocab)
 
 
 class Conv(torch.autograd.Function):
@@ -82,6 +101,25 @@ class Logprobs(torch.autograd.Function):
         return d, None, None, None
 
 
+class LinearLogprobs(torch.autograd.Function):
+    """Logprobs of the logits hidden @ weight.T, which are not kept."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, tokens, plan, temperature):
+        r = ptp.tree_linear_logprobs(hidden, weight, tokens, plan, temperature=temperature)
+        ctx.plan, ctx.temperature = plan, temperature
+        ctx.save_for_backward(hidden, weight, tokens, r.lse, r.entropy)
+        return r.logp, r.entropy
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp, dentropy):
+        hidden, weight, tokens, lse, entropy = ctx.saved_tensors
+        return (*ptp.tree_linear_logprobs_backward(hidden, weight, tokens, lse, entropy, dlogp.contiguous(), ctx.plan,
+                                                   dentropy=dentropy.contiguous(), temperature=ctx.temperature),
+                None, None, None)
+
+
 class Model:
     """Embedding, recurrent mixer, attention, tied output; `heads` query heads
     over half as many key/value heads of d."""
@@ -101,9 +139,9 @@ class Model:
         self.qkv = weight(c, (heads + 2 * self.kv) * d, std=c ** -0.5)
         self.weights = [self.embed, self.conv, self.mix, self.gate, self.qkv]
 
-    def logits(self, tokens, plan):
-        n, h, d = tokens.shape[0], self.heads, self.d
-        x = self.embed[tokens]
+    def hidden(self, x, plan):
+        """The last layer's output for embedded tokens x [N, heads * d]."""
+        n, h, d = x.shape[0], self.heads, self.d
         y = Conv.apply(x, self.conv, plan)
         q, k, v = (y @ self.mix).view(n, 3, h, d).unbind(1)
         q, k = (torch.nn.functional.normalize(t.float(), dim=-1).to(x.dtype) for t in (q, k))
@@ -111,14 +149,24 @@ class Model:
         x = x + Scan.apply(q.contiguous(), k.contiguous(), v.contiguous(), -torch.nn.functional.softplus(g),
                            torch.sigmoid(beta), plan).reshape(n, h * d)
         qkv = (x @ self.qkv).view(n, h + 2 * self.kv, d)
-        x = x + Attention.apply(qkv[:, :h], qkv[:, h:h + self.kv], qkv[:, h + self.kv:], plan).reshape(n, h * d)
-        return (x @ self.embed.t()) * (h * d) ** -0.5
+        return x + Attention.apply(qkv[:, :h], qkv[:, h:h + self.kv], qkv[:, h + self.kv:], plan).reshape(n, h * d)
+
+    def logits(self, tokens, plan):
+        return (self.hidden(self.embed[tokens], plan) @ self.embed.t()) * (self.heads * self.d) ** -0.5
+
+    def logprobs(self, tokens, plan, temperature):
+        """(logp, entropy) without logits: their scale goes into the temperature."""
+        x = self.hidden(Embedding.apply(tokens, self.embed), plan)
+        return LinearLogprobs.apply(x, self.embed, tokens, plan, temperature * (self.heads * self.d) ** 0.5)
 
 
-def policy_loss(model, tokens, advantage, plan, temperature=1.0, entropy_bonus=0.01):
+def policy_loss(model, tokens, advantage, plan, temperature=1.0, entropy_bonus=0.01, keep_logits=True):
     """-(sum over tokens of advantage x log probability + bonus x entropy) / N,
     each token under its own root-to-token path."""
-    logp, entropy = Logprobs.apply(model.logits(tokens, plan), tokens, plan, temperature)
+    if keep_logits:
+        logp, entropy = Logprobs.apply(model.logits(tokens, plan), tokens, plan, temperature)
+    else:
+        logp, entropy = model.logprobs(tokens, plan, temperature)
     return -((advantage * logp).sum() + entropy_bonus * entropy.sum()) / tokens.shape[0]
 
 
@@ -144,14 +192,18 @@ def rollouts(vocab, device, prompt=160, completions=6, length=90, seed=0):
     return tokens, advantage, ptp.tree_plan(parents, lens, 4)
 
 
-def main():
+def main(argv=()):
+    ap = argparse.ArgumentParser(description="A policy update on a packed trie of rollouts.")
+    ap.add_argument("--no-logits", action="store_true", help="log probabilities without an [N, vocab] tensor")
+    keep = not ap.parse_args(argv).no_logits
     device = "cuda:0"
     model = Model(vocab=1003, heads=4, d=64, dtype=torch.bfloat16, device=device)
     tokens, advantage, plan = rollouts(1003, device)
     print(f"{plan.n_tokens} tokens for {plan.stats['path_tokens']} on the paths")
     for i in range(8):
-        print(f"step {i}: loss {policy_step(model, tokens, advantage, plan).item():.4f}", flush=True)
+        print(f"step {i}: loss {policy_step(model, tokens, advantage, plan, keep_logits=keep).item():.4f}",
+              flush=True)
 
 
 if __name__ == "__main__":
-    main()
+    main(sys.argv[1:])
