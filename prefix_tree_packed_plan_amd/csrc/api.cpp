@@ -261,7 +261,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // CU, reach the highest rate in bf16; smaller ones where those would leave CUs idle.
 // fp32 takes 128 x 128: two work-groups a CU, one of which splits values while the
 // other's products run (1685 rows x 50001 x 1000 forward as fast as with 256 x 256, the
-// gradients of 1117 x 20001 x 1000 1290 -> 1030 us).
+// gradients of 1526 x 20001 x 1000 1290 -> 1030 us).
 int32_t product_size(int64_t m, int64_t n, int32_t dtype, bool rows_only) {
   if (!rows_only && n <= 64) return 0;
   return dtype == TREE_DTYPE_BF16 && ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 2 : 1;

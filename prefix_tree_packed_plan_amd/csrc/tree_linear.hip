@@ -88,48 +88,56 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-// A row's tokens and their logits, by work-groups beside those of the product, which
-// they take no longer than: a wave a row.  found: (logit of the first token, that token,
-// the row's segment, flags); the logits of further ones go to their logp.
+// hidden row lr x weight row id, to all lanes of a wave.
+template <typename T>
+__device__ __forceinline__ float dot(const LinearArgs& a, int lr, int id) {
+  constexpr int N = 16 / sizeof(T);
+  const uint4* hrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.hidden) + int64_t(lr) * a.ld);
+  const uint4* wrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.weight) + int64_t(id) * a.width);
+  float x = 0.f;
+#pragma unroll 4
+  for (int i = threadIdx.x & 63; i < a.width / N; i += 64) {
+    const uint4 u = hrow[i], w = wrow[i];
+    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (sizeof(T) == 4) {
+        x = fmaf(__uint_as_float(uu[q]), __uint_as_float(ww[q]), x);
+      } else {
+        x = fmaf(chunk::lo_f(uu[q]), chunk::lo_f(ww[q]), x);
+        x = fmaf(chunk::hi_f(uu[q]), chunk::hi_f(ww[q]), x);
+      }
+    }
+  }
+  return wave_sum(x);
+}
+
+// Tokens and their logits, by work-groups beside those of the product, which they take
+// no longer than: a wave a row, for the first token behind it, and a wave a segment
+// that is not its parent's first child, for its first token (a row with 1024 children
+// would keep one wave longer than the product takes).
+//   found: (logit of the first token, that token, the row's segment, flags)
+// The logits of further tokens go to their logp.
 constexpr int kAny = 1, kOutside = 2, kMore = 4, kRootStart = 8;
 template <typename T>
 __device__ __forceinline__ void find_row(const LinearArgs& a, int lr, int4* found) {
-  constexpr int N = 16 / sizeof(T);
   const int lane = threadIdx.x & 63;
   const Behind b(a, a.first_row + lr, lane);
-  const uint4* hrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.hidden) + int64_t(lr) * a.ld);
-  float first = 0.f;
-  int t0 = 0, flags = (b.n > 0 ? kAny : 0) | (b.n > 1 ? kMore : 0) | (b.root_start ? kRootStart : 0);
-  for (int j = 0; j < b.n; ++j) {
-    const int t = b.at(j), id = token(a, t);
-    float x = 0.f;
-    if (id >= 0) {
-      const uint4* wrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.weight) + int64_t(id) * a.width);
-#pragma unroll 4
-      for (int i = lane; i < a.width / N; i += 64) {
-        const uint4 u = hrow[i], w = wrow[i];
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (sizeof(T) == 4) {
-            x = fmaf(__uint_as_float(uu[q]), __uint_as_float(ww[q]), x);
-          } else {
-            x = fmaf(chunk::lo_f(uu[q]), chunk::lo_f(ww[q]), x);
-            x = fmaf(chunk::hi_f(uu[q]), chunk::hi_f(ww[q]), x);
-          }
-        }
-      }
-      x = wave_sum(x);
-    }
-    if (j == 0) {
-      first = x;
-      t0 = t;
-      if (id < 0) flags |= kOutside;
-    } else if (lane == 0) {
-      a.logp[t] = x;
-    }
-  }
-  if (lane == 0) found[lr] = make_int4(__float_as_int(first), t0, b.seg, flags);
+  int flags = (b.n > 0 ? kAny : 0) | (b.n > 1 ? kMore : 0) | (b.root_start ? kRootStart : 0);
+  const int t = b.n > 0 ? b.at(0) : 0, id = b.n > 0 ? token(a, t) : -1;
+  if (id < 0) flags |= kOutside;
+  const float x = id >= 0 ? dot<T>(a, lr, id) : 0.f;
+  if (lane == 0) found[lr] = make_int4(__float_as_int(x), t, b.seg, flags);
+}
+template <typename T>
+__device__ __forceinline__ void find_segment(const LinearArgs& a, int s) {
+  const int p = a.parent[s];
+  if (p < 0 || a.kid[a.kid_off[p]] == s) return;
+  const int lr = a.seg_off[p + 1] - 1 - a.first_row, t = a.seg_off[s];
+  if (lr < 0 || lr >= a.n_rows) return;
+  const int id = token(a, t);
+  const float x = id >= 0 ? dot<T>(a, lr, id) : 0.f;
+  if ((threadIdx.x & 63) == 0) a.logp[t] = x;
 }
 
 // A product's operands and where its tiles stand.
@@ -172,8 +180,9 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
   if constexpr (USE == kStats) {
     // The work-groups behind the tiles'.
     if (static_cast<int>(blockIdx.x) >= tiles) {
-      const int lr = (blockIdx.x - tiles) * (C::THREADS / 64) + wave;
-      if (lr < la.n_rows) find_row<T>(la, lr, j.found);
+      const int i = (blockIdx.x - tiles) * (C::THREADS / 64) + wave;
+      if (i < la.n_rows) find_row<T>(la, i, j.found);
+      else if (i - la.n_rows < la.n_seg) find_segment<T>(la, i - la.n_rows);
       return;
     }
   }
@@ -293,28 +302,43 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
           for (int i = 0; i < 4; ++i)
             if (!live || mw + am(mb) + i >= j.m) acc[mb][nb][i] = 0.f;
       }
-      // The tokens behind the row: the first, and where there are more the others.
-      const int mine = live ? who.y : 0;
-      for (int t = 0; __any(t < mine); ++t) {
-        int v = -1;
-        float g = 0.f;
-        if (t < mine) {
-          if (t == 0) {
-            v = who.x;
-            g = rc.w;
-          } else {
-            const int at = la.seg_off[la.kid[who.z + t]];
-            v = token(la, at);
-            g = v >= 0 ? la.dlogp[at] * j.inv_t : 0.f;
-          }
-        }
-        const int o = v < 0 ? -1 : v - j.v0 - mw;  // from this lane's first m
-        if (!__any(v >= 0 && o >= 0 && o < BM)) continue;
+      // The tokens behind the row: the first here, further ones (a branch point's) below.
+      const int o = live && who.y > 0 && who.x >= 0 ? who.x - j.v0 - mw : -1;
+      if (__any(o >= 0 && o < BM)) {
 #pragma unroll
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (v >= 0 && o == am(mb) + i) acc[mb][nb][i] += g;
+            if (o >= 0 && o == am(mb) + i) acc[mb][nb][i] += rc.w;
+      }
+      // A lane a token, and those in this tile one after another.
+      uint64_t branch = __ballot(live && who.y > 1 && g4 == 0);
+      while (branch) {
+        const int c = __builtin_ctzll(branch), kids = __builtin_amdgcn_readlane(who.y, c);
+        const int32_t* kid = la.kid + __builtin_amdgcn_readlane(who.z, c);
+        branch &= branch - 1;
+        for (int t = 1; t < kids; t += 64) {
+          int v = -1;
+          float g = 0.f;
+          if (t + lane < kids) {
+            const int at = la.seg_off[kid[t + lane]];
+            v = token(la, at);
+            g = v >= 0 ? la.dlogp[at] * j.inv_t : 0.f;
+          }
+          const int from = v < 0 ? -1 : v - j.v0 - m0;
+          uint64_t hit = __ballot(from >= 0 && from < BM);
+          while (hit) {
+            const int l = __builtin_ctzll(hit);
+            hit &= hit - 1;
+            const int at = __builtin_amdgcn_readlane(from, l) - 4 * g4;
+            const float add = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), l));
+#pragma unroll
+            for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (l16 == c && at == am(mb) + i) acc[mb][nb][i] += add;
+          }
+        }
       }
 #pragma unroll
       for (int mb = 0; mb < C::MB; mb += 2)
@@ -434,7 +458,7 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   // 8 x 4 tiles run on an XCD's 32 CUs at a time.
   j.band = j.n_tiles < 4 ? j.n_tiles : 4;
   int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
-  if (USE == kStats) groups += ceil_div(j.n, C::THREADS / 64);
+  if (USE == kStats) groups += ceil_div(int64_t(j.n) + a.n_seg, C::THREADS / 64);
   product_kernel<T, C, BIG, USE><<<static_cast<uint32_t>(groups), C::THREADS, 0, stream>>>(j, a);
   return hipGetLastError();
 }

@@ -238,6 +238,40 @@ def test_tokens_outside_and_many_children():
         assert torch.equal(r.logp, r2.logp) and all(torch.equal(a, b) for a, b in zip(d, d2))
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("vocab", [41, 700])
+def test_hundreds_of_children(vocab, dtype):
+    """More children than lanes, at two branch points of one tile of rows and one of
+    another, many with the same token and some outside the vocabulary; and the rows in
+    two calls, which must write the tokens behind their own rows alone."""
+    parents = [-1] + [0] * 150 + [3] * 70 + [150] * 130 + [-1]
+    lens = [4] + [1 + i % 2 for i in range(350)] + [3]
+    n = sum(lens)
+    say(f"linear logprobs n={n} children={350} vocab={vocab} {dtype}")
+    h, w, tok, dlogp, dent = inputs(n, vocab, 40, DT[dtype], seed=vocab)
+    tok[10:300:17] = -1
+    tok[40:90] = 7
+    plan, r, (_, dw) = run_case(parents, lens, h, w, tok, dlogp, dent)
+    logp = torch.full((n,), 5.0, device=DEV)
+    for a, b in ((130, n), (0, 130)):
+        before = logp.clone()
+        ptp.tree_linear_logprobs(h[a:b], w, tok, plan, first_row=a, logp=logp)
+        front = _front(parents, lens)
+        mine = torch.tensor([a <= f < b for f in front], device=DEV)
+        start = torch.tensor([f < 0 and a <= t < b for t, f in enumerate(front)], device=DEV)
+        assert torch.equal(logp[~mine & ~start], before[~mine & ~start])
+    # The two calls' tiles are cut elsewhere: sums differ in their order.
+    assert (logp - r.logp).abs().max() <= 2.0 ** -17
+
+
+def _front(parents, lens):
+    first = np.concatenate([[0], np.cumsum(lens)])
+    out = []
+    for s, p in enumerate(parents):
+        out += [int(first[p + 1]) - 1 if p >= 0 else -1] + list(range(int(first[s]), int(first[s + 1]) - 1))
+    return out
+
+
 def test_values_that_are_not_finite():
     for dtype in DT.values():
         say(f"linear logprobs not finite {dtype}")
