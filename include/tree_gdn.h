@@ -1,7 +1,8 @@
 /*
  * tree_gdn.h -- C ABI of the tree conv + tree Gated DeltaNet library (forward and
  * backward), with a tree Mamba2 (SSD) forward, tree attention and token log
- * probabilities (each forward and backward) beside it,
+ * probabilities (each forward and backward) beside it, from logits or from hidden
+ * states and the output weight, and the token embedding (forward and backward),
  * for AMD Instinct MI355X (gfx950).
  *
  * The library runs the forward pass of a recurrent mixer over a prefix trie
@@ -670,7 +671,8 @@ size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32
  *          bytes.
  * dtype    TREE_DTYPE_BF16 (bf16 MFMA, sums and all that follows in fp32) or
  *          TREE_DTYPE_F32 (each value as three bf16, the six largest partial
- *          products: fp32 accuracy; values above 3.38e38 are taken as infinite).
+ *          products: fp32 accuracy; values above 3.38e38 are taken as infinite, and what is
+ *          infinite makes its logits NaN).
  * A row whose logits are all -inf has lse -inf, entropy 0 and log probabilities
  * -inf; a logit of NaN or +inf (of hidden or weight not finite, or products too
  * large) makes its row's results NaN.
@@ -708,8 +710,9 @@ size_t tree_linear_logprobs_backward_workspace_bytes(int32_t n_rows, int32_t voc
  * dhidden    device, [n_rows, width], dtype, contiguous   (written; no alias)
  * dweight    device, [vocab, width], dtype, contiguous: of these rows alone
  *                                                         (written; no alias)
- * A row whose logits are all -inf adds nothing; one whose results are NaN makes
- * all of dweight NaN.  p is recomputed from the fp32 lse, to a relative error of
+ * D is zero in a row whose logits are all -inf (zero times what is infinite in
+ * hidden or weight is NaN) and NaN in one whose results are NaN, which makes all of
+ * dweight NaN.  p is recomputed from the fp32 lse, to a relative error of
  * about 2^-24 (|lse| + |log p|): a percent where |lse| is 2^17.
  * ws         device workspace, ws_bytes >=
  *            tree_linear_logprobs_backward_workspace_bytes.
@@ -759,7 +762,7 @@ size_t tree_embedding_backward_workspace_bytes(int64_t n_tokens, int32_t vocab, 
  * dtable  device, [vocab, width], dtype                     (written; no alias)
  * ws      device workspace, ws_bytes >= tree_embedding_backward_workspace_bytes,
  *         aligned to 16 bytes.
- * Everything else as for tree_embedding.
+ * vocab   in 1 .. 2^22; everything else as for tree_embedding.
  * Errors: INVALID_ARG, WORKSPACE, HIP.
  */
 int tree_embedding_backward(const void* tokens, const void* dout, void* dtable, int64_t n_tokens, int32_t vocab,

@@ -220,15 +220,18 @@ int check_logprobs(const tg::Plan& p, int64_t ld, int64_t n_tokens, int32_t firs
 
 // Sizes of an embedding call.  Up to 2^30 tokens and rows of the table: positions
 // and rows are counted in 32 bits, with room for what a wave reads past the end.
-bool embed_sizes_ok(int64_t n_tokens, int32_t vocab, int32_t width) {
-  return n_tokens >= 0 && n_tokens <= (int64_t(1) << 30) && vocab > 0 && vocab <= (1 << 30) && width > 0 &&
+constexpr int32_t kEmbedVocab = 1 << 30;
+// The gradient's: every kEmbedSpan rows of the table look through all tokens.
+constexpr int32_t kSortVocab = 1 << 22;
+bool embed_sizes_ok(int64_t n_tokens, int32_t vocab, int32_t width, int32_t most) {
+  return n_tokens >= 0 && n_tokens <= (int64_t(1) << 30) && vocab > 0 && vocab <= most && width > 0 &&
          width <= (1 << 24);
 }
-int check_embed(int64_t n_tokens, int32_t vocab, int32_t width, int32_t token_bytes, float scale, int32_t dtype,
-                const char* fn) {
-  if (!embed_sizes_ok(n_tokens, vocab, width))
-    return fail(TREE_ERR_INVALID_ARG, "%s: n_tokens %lld must be in 0..2^30, vocab %d in 1..2^30, width %d in 1..2^24", fn,
-                static_cast<long long>(n_tokens), vocab, width);
+int check_embed(int64_t n_tokens, int32_t vocab, int32_t width, int32_t most, int32_t token_bytes, float scale,
+                int32_t dtype, const char* fn) {
+  if (!embed_sizes_ok(n_tokens, vocab, width, most))
+    return fail(TREE_ERR_INVALID_ARG, "%s: n_tokens %lld must be in 0..2^30, vocab %d in 1..%d, width %d in 1..2^24", fn,
+                static_cast<long long>(n_tokens), vocab, most, width);
   if (token_bytes != 4 && token_bytes != 8)
     return fail(TREE_ERR_INVALID_ARG, "%s: token_bytes must be 4 or 8 (got %d)", fn, token_bytes);
   if (!dtype_ok(dtype)) return fail(TREE_ERR_INVALID_ARG, "%s: bad dtype %d", fn, dtype);
@@ -1265,7 +1268,7 @@ int tree_linear_logprobs_backward(const void* hidden, const void* weight, const 
 int tree_embedding(const void* tokens, const void* table, void* out, int64_t n_tokens, int32_t vocab, int32_t width,
                    int32_t token_bytes, float scale, int32_t dtype, void* stream) {
   const char* fn = "tree_embedding";
-  if (const int rc = check_embed(n_tokens, vocab, width, token_bytes, scale, dtype, fn)) return rc;
+  if (const int rc = check_embed(n_tokens, vocab, width, kEmbedVocab, token_bytes, scale, dtype, fn)) return rc;
   if (!table || (n_tokens > 0 && (!tokens || !out))) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
   if (out == table) return fail(TREE_ERR_INVALID_ARG, "%s: out must not alias the table", fn);
   if (const int rc = check_element_aligned(table, dtype, "table", fn)) return rc;
@@ -1286,14 +1289,14 @@ int tree_embedding(const void* tokens, const void* table, void* out, int64_t n_t
 }
 
 size_t tree_embedding_backward_workspace_bytes(int64_t n_tokens, int32_t vocab, int32_t width) {
-  return embed_sizes_ok(n_tokens, vocab, width) ? embed_work(n_tokens, vocab, width).bytes : 0;
+  return embed_sizes_ok(n_tokens, vocab, width, kSortVocab) ? embed_work(n_tokens, vocab, width).bytes : 0;
 }
 
 int tree_embedding_backward(const void* tokens, const void* dout, void* dtable, int64_t n_tokens, int32_t vocab,
                             int32_t width, int32_t token_bytes, float scale, int32_t dtype, void* ws, size_t ws_bytes,
                             void* stream) {
   const char* fn = "tree_embedding_backward";
-  if (const int rc = check_embed(n_tokens, vocab, width, token_bytes, scale, dtype, fn)) return rc;
+  if (const int rc = check_embed(n_tokens, vocab, width, kSortVocab, token_bytes, scale, dtype, fn)) return rc;
   if (!dtable || (n_tokens > 0 && (!tokens || !dout))) return fail(TREE_ERR_INVALID_ARG, "%s: null argument", fn);
   if (dtable == dout) return fail(TREE_ERR_INVALID_ARG, "%s: dtable must not alias dout", fn);
   if (const int rc = check_element_aligned(dout, dtype, "dout", fn)) return rc;

@@ -50,7 +50,8 @@ __device__ __forceinline__ uint4 lds16(const char* p) {
 // 16 bytes a lane to LDS at lds + IMM + 16 lane, from src + off (src the same for
 // all lanes) or from a lane's own address.  In inline asm, because the compiler
 // would otherwise wait for all DMA in flight before any read of LDS; it has no
-// output registers, and wait_step() is the wait.
+// output registers, and wait_step() is the wait.  Nothing else here needs m0 (LDS
+// instructions of gfx9 on do not), so it is not put back.
 template <int IMM>
 __device__ __forceinline__ void dma16(uint64_t src, uint32_t off, uint32_t lds) {
   asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"

@@ -40,7 +40,8 @@ def test_embedding_backward_refusals_need_no_device():
     assert size(-1, 10, 8) == 0 and size(5, 0, 8) == 0 and size(5, 10, 0) == 0 and size(MOST + 1, 10, 8) == 0
     # Lists of more than 64 tokens are cut: two fp32 rows for every 64 tokens.
     assert size(1000, 10, 8) - size(64, 10, 8) >= 16 * 2 * 8 * 4
-    assert size(MOST, MOST, 1 << 24) > (1 << 50)  # no overflow
+    assert size(MOST, 1 << 22, 1 << 24) > (1 << 50)  # no overflow
+    assert size(5, (1 << 22) + 1, 8) == 0  # all tokens are looked through for every 512 rows
     good = dict(tok=P, dout=P2, dtable=P3, n=5, vocab=10, width=8, tb=8, scale=1.0, dtype=1, ws=P, bytes=need,
                 stream=None)
 
@@ -49,7 +50,8 @@ def test_embedding_backward_refusals_need_no_device():
 
     for name in ("tok", "dout", "dtable"):
         assert call(**{name: None}) == -1 and b"null" in lib.tree_last_error()
-    for bad in (dict(n=-1), dict(n=MOST + 1), dict(vocab=0), dict(width=0), dict(tb=1), dict(dtype=7)):
+    for bad in (dict(n=-1), dict(n=MOST + 1), dict(vocab=0), dict(vocab=(1 << 22) + 1), dict(width=0), dict(tb=1),
+                dict(dtype=7)):
         assert call(**bad) == -1, bad
     for scale in (0.0, -2.0, NAN, INF, 1e-31, 1e31):
         assert call(scale=scale) == -1
