@@ -260,30 +260,51 @@ constexpr int32_t kLinearVocab = 1 << 22, kLinearWidth = 1 << 16;
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile sizes and splits of a product of m x n over k.  256 x 256 tiles, one work-group a
-// CU, reach the highest rate in bf16; smaller ones where those would leave CUs idle.
-// fp32 takes 128 x 128: two work-groups a CU, one of which splits values while the
-// other's products run (1685 rows x 50001 x 1000 forward as fast as with 256 x 256, the
-// gradients of 1526 x 20001 x 1000 1290 -> 1030 us).
-int32_t product_size(int64_t m, int64_t n, int32_t dtype, bool rows_only) {
-  if (!rows_only && n <= 64) return 0;
-  return dtype == TREE_DTYPE_BF16 && ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 2 : 1;
-}
-void product_splits(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t size, int32_t* splits) {
-  const int64_t bm = size == 2 ? 256 : 128, bn = size == 2 ? 256 : size == 1 ? 128 : 64;
-  const int64_t tiles = ceil_div(m, bm) * ceil_div(n, bn), steps = ceil_div(k, dtype == TREE_DTYPE_F32 ? 32 : 64);
-  const int64_t want = size == 2 ? 256 : 512;
-  *splits = static_cast<int32_t>(std::max<int64_t>(1, std::min(want / tiles, steps / 8)));
+// Tile sizes and splits of a product of m x n over k.  Up to 64 rows n take 64 of them a
+// tile, and a sum as many splits as fill the CUs.  Otherwise the least of: rounds of
+// work-groups (256 tiles of 256 x 256, one a CU; 512 of 128 x 128, two) times a round's
+// time, in us as measured for a k-step of it, and the parts' way through memory.  Large
+// bf16 products so take 256 x 256 (8192 x 131072 x 4096 forward 6480 us, with 128 x 128
+// 8350); where those leave CUs idle, 128 x 128 (100 rows x 50000 x 2048: 40.5 us, 61 with
+// 256 x 256) or, for sums, splits (gradients of 1100 x 50000 x 4096: 1311 us with 256 x
+// 256 in 3 splits, 1815 with 128 x 128).  fp32 takes 128 x 128: one work-group splits
+// values while the other's products run (1685 rows x 50001 x 1000 forward as fast as
+// with 256 x 256, the gradients of 1526 x 20001 x 1000 1290 -> 1030 us).
+struct ProductChoice {
+  int32_t size, splits;
+};
+ProductChoice product_choice(int64_t m, int64_t n, int64_t k, int32_t dtype, bool sum, bool few) {
+  const bool f32 = dtype == TREE_DTYPE_F32;
+  const int64_t steps = ceil_div(k, f32 ? 32 : 64), most = sum ? std::max<int64_t>(1, steps / 8) : 1;
+  if (few && n <= 64)
+    return {0, static_cast<int32_t>(std::max<int64_t>(1, std::min(512 / (ceil_div(m, 128) * ceil_div(n, 64)), most)))};
+  ProductChoice best{};
+  double least = 0;
+  for (int size = f32 ? 1 : 2; size >= 1; --size) {
+    const int64_t b = size == 2 ? 256 : 128, at_once = size == 2 ? 256 : 512;
+    const double step_us = f32 ? 2.7 : size == 2 ? 1.57 : 1.0;
+    const int64_t tiles = ceil_div(m, b) * ceil_div(n, b);
+    for (int64_t s = 1; s <= std::min<int64_t>(most, 64); ++s) {
+      const double rounds = static_cast<double>(ceil_div(tiles * s, at_once));
+      double us = rounds * (static_cast<double>(ceil_div(steps, s)) * step_us + 1.0);
+      if (s > 1) us += 5.0 + static_cast<double>(s) * m * n * 8 / 5e6;
+      if (best.size == 0 || us < least) {
+        best = {size, static_cast<int32_t>(s)};
+        least = us;
+      }
+    }
+  }
+  return best;
 }
 bool linear_sizes_ok(int64_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
   return n_rows > 0 && n_rows < (int64_t(1) << 31) && vocab > 0 && vocab <= kLinearVocab && width > 0 &&
          width <= kLinearWidth && dtype_ok(dtype) && width % (dtype == TREE_DTYPE_F32 ? 4 : 8) == 0;
 }
 // The forward's: the tiles' sums of up to 32768 rows, 1 GiB of them at most.
-tg::LinearWork linear_work(int64_t n_rows, int32_t vocab, int32_t dtype) {
+tg::LinearWork linear_work(int64_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
   tg::LinearWork w{};
   w.rows = std::min<int64_t>(n_rows, 32768);
-  w.size = product_size(vocab, w.rows, dtype, false);
+  w.size = product_choice(vocab, w.rows, width, dtype, false, true).size;
   const int64_t slots = ceil_div(vocab, w.size == 2 ? 256 : w.size == 1 ? 128 : 64);
   w.rows = std::min(w.rows, std::max<int64_t>(256, (int64_t(1) << 26) / slots / 256 * 256));
   w.ids = static_cast<size_t>(w.rows) * slots * 16;
@@ -299,11 +320,13 @@ tg::LinearWork linear_backward_work(int64_t n_rows, int32_t vocab, int32_t width
   const int64_t rows_up = ceil_div(w.rows, 256) * 256;
   w.piece = std::min<int64_t>(vocab, (int64_t(1) << 28) / rows_up / 256 * 256);
   w.ldd = ceil_div(w.piece, 256) * 256;
-  w.size = product_size(w.piece, w.rows, dtype, false);
-  w.size_h = product_size(width, w.rows, dtype, false);
-  product_splits(width, w.rows, w.piece, dtype, w.size_h, &w.splits_h);
-  w.size_w = product_size(width, w.piece, dtype, true);
-  product_splits(width, w.piece, w.rows, dtype, w.size_w, &w.splits_w);
+  w.size = product_choice(w.piece, w.rows, width, dtype, false, true).size;
+  const ProductChoice h = product_choice(width, w.rows, w.piece, dtype, true, true);
+  const ProductChoice d = product_choice(width, w.piece, w.rows, dtype, true, false);
+  w.size_h = h.size;
+  w.splits_h = h.splits;
+  w.size_w = d.size;
+  w.splits_w = d.splits;
   const size_t fw = static_cast<size_t>(width) * sizeof(float);
   w.ids = up256(w.rows * 16);
   w.d = w.ids + up256(w.rows * 16);
@@ -1195,7 +1218,7 @@ int tree_logprobs_backward(const void* logits, const void* tokens, const float* 
 }
 
 size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32_t width, int32_t dtype) {
-  return linear_sizes_ok(n_rows, vocab, width, dtype) ? linear_work(n_rows, vocab, dtype).bytes : 0;
+  return linear_sizes_ok(n_rows, vocab, width, dtype) ? linear_work(n_rows, vocab, width, dtype).bytes : 0;
 }
 
 int tree_linear_logprobs(const void* hidden, const void* weight, const void* tokens, float* logp, float* entropy,
@@ -1209,7 +1232,7 @@ int tree_linear_logprobs(const void* hidden, const void* weight, const void* tok
   if (const int rc = check_linear(p, hidden, ld, weight, n_tokens, first_row, n_rows, vocab, width, token_bytes,
                                   temperature, dtype, fn))
     return rc;
-  const tg::LinearWork w = linear_work(n_rows, vocab, dtype);
+  const tg::LinearWork w = linear_work(n_rows, vocab, width, dtype);
   if (!ws || ws_bytes < w.bytes)
     return fail(TREE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, ws ? ws_bytes : 0, w.bytes);
   if (const int rc = check_aligned(ws, "the workspace", fn)) return rc;

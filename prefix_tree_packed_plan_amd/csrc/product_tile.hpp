@@ -443,7 +443,9 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
 // A1 B1, A1 B0.  So each half is read in one go (over the fragments just used), and
 // its place in LDS is staged anew, two steps on, as soon as all waves have read it:
 // a DMA has one and a half steps' time to land, and DMA is spread over the step,
-// where staging whole steps (run()) gives one and a burst.
+// where staging whole steps (run()) gives one and a burst: 8192 x 131072 x 4096, 1350
+// TFLOP/s against 1190 with whole steps of 256 x 256 tiles.  128 x 128 tiles, two a CU,
+// read twice the bytes for a product: 1080.
 template <bool TA, bool TB>
 struct Big {
   using T = uint16_t;

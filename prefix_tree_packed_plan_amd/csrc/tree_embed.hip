@@ -19,6 +19,12 @@
 // which a row begins.  Rows of more than kPart tokens would keep one work-group busy
 // long after the others (a token that is a fifth of all of them); their lists are
 // cut into parts at multiples of kPart, and join_kernel adds the parts in order.
+//
+// Measured (us; a copy reaches 4.9 TB/s here, a fill 6.9): 10240 tokens of 131072 x 4096
+// bf16, forward 24.5 (5.1 TB/s of rows read and written); gradient 243: the sort with
+// its clearing 173 (5.8 TB/s of zeros), the sums 49, the join, without work, 5.  65536
+// tokens, a fifth of them equal, of 32000 x 2048: 173: the sort 80 (one work-group's
+// long row: vector issue), the sums 79 (3.4 TB/s of dout), the join 12.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -136,7 +142,10 @@ __device__ __forceinline__ uint32_t row_of<int64_t>(const EmbedArgs& a, int n) {
 }
 
 // This work-group's rows: lo .. lo + span - 1.  cnt[w][r]: tokens of row lo + r in
-// wave w's share; then where its next one goes.  Rows without a token are cleared.
+// wave w's share; then where its next one goes.  Rows without a token are cleared here,
+// where their number is known early and clearing overlaps others' sorting (in
+// sum_kernel, one item a row of the table, 131072 x 4096 took 354 us instead of 291).
+// 16 waves, so that a share is short: the longest row's work-group sets the time.
 template <typename T, typename I>
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
   constexpr int U = 8;
@@ -228,7 +237,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(EmbedArgs a) {
   }
   __syncthreads();
   // K times 64 tokens: all of one kind of step, then all of the next, so that LDS is
-  // waited for once.
+  // waited for once; as many bits are compared as the rows need (65536 tokens of 32000
+  // rows, a fifth equal: 173 us, 184 with 9 bits).
   const auto place = [&](auto count, const uint32_t* r, const int* t) {
     constexpr int K = decltype(count)::value;
     uint64_t same[K];
@@ -299,7 +309,8 @@ __device__ __forceinline__ void columns(const EmbedArgs& a, int j0, int lanes, F
 }
 
 // x += the gradients, at a column (TAIL) or piece from `col` on, of the tokens that lanes
-// p .. p + U - 1 hold (REST: of those below i1), in order and with all loads in flight.
+// p .. p + U - 1 hold (REST: of those below i1), in order and with all loads in flight
+// (one after another: 291 us instead of 249 for 10240 tokens of 131072 x 4096).
 template <typename T, bool TAIL, int U, bool REST>
 __device__ __forceinline__ void add_some(const EmbedArgs& a, int held, int p, int i1, int col, float* x) {
   constexpr int N = TAIL ? 1 : Vec<T>::N;
@@ -408,7 +419,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(EmbedArgs a) {
 // Item q: the row of more than kPart tokens whose list begins in part q, if there is
 // one (it reaches past the part's end, so there is at most one).  A work-group takes
 // kJoinColumns columns of it; each wave adds a quarter of the parts, and the
-// quarters are added in order.
+// quarters are added in order (13 us for 205 parts of 2048 columns).
 constexpr int kJoinColumns = 256;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void join_kernel(EmbedArgs a) {

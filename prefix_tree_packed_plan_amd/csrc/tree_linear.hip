@@ -15,6 +15,13 @@
 // pieces: a piece's D is computed from the same products, stored (rounded to the
 // inputs' type, as the operand of the two products that follow), and multiplied
 // into dhidden, in fp32 over the pieces, and the piece's dweight.
+//
+// Measured (us): 8192 rows x 131072 x 4096 bf16 6530 (1350 TFLOP/s; a library product
+// of that shape alone reaches 1496), gradients of 8192 x 131072 x 2048 10400 (1270), fp32
+// 1685 x 50001 x 1000 935 (180), gradients of 1526 x 20001 x 1000 1000 (183; a library
+// fp32 product 155); 33 rows x 32000 x 2048 39 (the product 22: 131 MB of weight at 5.9
+// TB/s) and 112.  Large ones are bound by the matrix units at two thirds of their
+// cycles, with DMA and LDS reads between, and by the clock under load.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -455,7 +462,7 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
     j.k_split = ceil_div(ceil_div(j.k, j.splits), BK) * BK;
     j.splits = ceil_div(j.k, j.k_split);
   }
-  // 8 x 4 tiles run on an XCD's 32 CUs at a time.
+  // 8 x 4 tiles run on an XCD's 32 CUs at a time: operands of 12 tiles for 32 products.
   j.band = j.n_tiles < 4 ? j.n_tiles : 4;
   int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
   if (USE == kStats) groups += ceil_div(int64_t(j.n) + a.n_seg, C::THREADS / 64);

@@ -120,7 +120,7 @@ def test_rows(n, dtype):
 @pytest.mark.parametrize("dtype", sorted(DT))
 @pytest.mark.parametrize("n,vocab,width", [(300, 25000, 64), (1100, 10300, 72), (600, 6500, 1032), (129, 24700, 264)])
 def test_large_tiles_and_splits(n, vocab, width, dtype):
-    """256 x 256 tiles from 192 of them on; few tiles over a long contraction are split."""
+    """256 x 256 tiles where they fill the chip; few tiles over a long contraction are split."""
     say(f"linear logprobs n={n} vocab={vocab} width={width} {dtype}")
     run_case(*chain(n), *inputs(n, vocab, width, DT[dtype], seed=n))
 
@@ -176,6 +176,32 @@ def test_parts_of_rows_and_pieces_of_the_vocabulary(n, vocab, dtype):
     # A rounding of D and one of the result, u / sqrt(3) each at most in the mean;
     # fp32 sums of a few thousand terms, by the square root of their number.
     most = 2.0 ** -8 * (2 / 3) ** 0.5 if dtype == "bf16" else 3e-6
+    for name, x, y in zip(("dhidden", "dweight"), d, want[3:]):
+        rel = ((x.double() - y).norm() / y.norm()).item()
+        worst = ((x.double() - y).norm(dim=1) / (y.norm(dim=1) + 1e-3 * y.norm(dim=1).mean())).max().item()
+        say(f"  {name}: {rel:.2e} of the norm, worst row {worst:.2e}")
+        assert rel <= most and worst <= 4 * most
+
+
+@pytest.mark.parametrize("n,vocab,width", [(1100, 30001, 2056), (4100, 1100, 2056)])
+def test_large_tiles_of_the_hidden_states_gradient(n, vocab, width):
+    """dhidden by 256 x 256 tiles, in several splits and in one; bf16."""
+    say(f"linear logprobs n={n} vocab={vocab} width={width} bf16")
+    parents, lens = chain(n)
+    h, w, tok, dlogp, dent = inputs(n, vocab, width, torch.bfloat16, seed=3)
+    plan = ptp.tree_plan(parents, lens, 4)
+    r = ptp.tree_linear_logprobs(h, w, tok, plan)
+    d = ptp.tree_linear_logprobs_backward(h, w, tok, r.lse, r.entropy, dlogp, plan, dentropy=dent)
+    torch.cuda.synchronize()
+    want = exact(parents, lens, h, w, tok, dlogp, dent, 1.0)
+    # 65 sums of 32 products, each rounded at a size of 16 at most (2^-21), and as many
+    # of the exponentials' sums, to whose logarithm each gives 2^-24.
+    for name, x, y in zip(("logp", "entropy", "lse"), (r.logp, r.entropy, r.lse), want):
+        err = (x.double() - y).abs().max().item()
+        say(f"  {name}: {err:.2e}")
+        assert err <= 65 * 2.0 ** -21 + 1e-5
+    # As above: two roundings.
+    most = 2.0 ** -8 * (2 / 3) ** 0.5
     for name, x, y in zip(("dhidden", "dweight"), d, want[3:]):
         rel = ((x.double() - y).norm() / y.norm()).item()
         worst = ((x.double() - y).norm(dim=1) / (y.norm(dim=1) + 1e-3 * y.norm(dim=1).mean())).max().item()
