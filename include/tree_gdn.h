@@ -700,7 +700,8 @@ size_t tree_linear_logprobs_backward_workspace_bytes(int32_t n_rows, int32_t voc
  * gradient (tree_logprobs_backward's formula):
  *   dhidden = D weight,   dweight = D^T hidden.
  * Sums run in fp32 and a fixed order (the result is deterministic); D is rounded
- * to dtype for its products, the gradients once at the end.
+ * to dtype for its products (to two bf16 for up to 64 rows), the gradients once at
+ * the end.
  *
  * hidden, weight, tokens, ld, first_row, n_rows ..  as for tree_linear_logprobs.
  * lse, entropy  device, [n_rows] fp32: tree_linear_logprobs' results (read)

@@ -321,8 +321,12 @@ tg::LinearWork linear_backward_work(int64_t n_rows, int32_t vocab, int32_t width
   w.piece = std::min<int64_t>(vocab, (int64_t(1) << 28) / rows_up / 256 * 256);
   w.ldd = ceil_div(w.piece, 256) * 256;
   w.size = product_choice(w.piece, w.rows, width, dtype, false, true).size;
-  const ProductChoice h = product_choice(width, w.rows, w.piece, dtype, true, true);
-  const ProductChoice d = product_choice(width, w.piece, w.rows, dtype, true, false);
+  // Up to 64 rows in bf16, where memory is the bound, D is two bf16 (its rounding would
+  // be as large as the result's): 2 stack rows.
+  w.stack = dtype == TREE_DTYPE_BF16 && n_rows <= 64 ? (n_rows <= 32 ? 32 : 64) : 0;
+  const int64_t d_rows = w.stack ? 2 * w.stack : w.rows;
+  const ProductChoice h = product_choice(width, d_rows, w.piece, dtype, true, true);
+  const ProductChoice d = product_choice(width, w.piece, d_rows, dtype, true, false);
   w.size_h = h.size;
   w.splits_h = h.splits;
   w.size_w = d.size;
@@ -332,8 +336,9 @@ tg::LinearWork linear_backward_work(int64_t n_rows, int32_t vocab, int32_t width
   w.d = w.ids + up256(w.rows * 16);
   w.dhidden = w.d + static_cast<size_t>(rows_up) * w.ldd * es;
   w.dweight = w.dhidden + (w.piece < vocab ? up256(w.rows * fw) : 0);
-  w.parts = w.dweight + (w.rows < n_rows ? up256(vocab * fw) : 0);
-  const size_t ph = w.splits_h > 1 ? w.splits_h * w.rows * fw : 0, pw = w.splits_w > 1 ? w.splits_w * w.piece * fw : 0;
+  w.hidden2 = w.dweight + (w.rows < n_rows ? up256(vocab * fw) : 0);
+  w.parts = w.hidden2 + up256(2 * w.stack * width * es);
+  const size_t ph = w.splits_h > 1 || w.stack ? w.splits_h * d_rows * fw : 0, pw = w.splits_w > 1 ? w.splits_w * w.piece * fw : 0;
   w.bytes = w.parts + std::max(ph, pw);
   return w;
 }

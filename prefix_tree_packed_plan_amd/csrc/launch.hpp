@@ -324,7 +324,8 @@ struct LinearWork {
   int32_t size_h, splits_h;    // dhidden
   int32_t size_w, splits_w;    // dweight
   int64_t ldd;                 // elements between rows of D
-  size_t ids, d, dhidden, dweight, parts, bytes;
+  int32_t stack;               // 0, or rows of each of D's two parts (bf16, few rows)
+  size_t ids, d, dhidden, dweight, hidden2, parts, bytes;
 };
 
 hipError_t launch_linear(const LinearArgs& a, const LinearWork& w, int dtype, hipStream_t stream);

@@ -13,7 +13,8 @@
 // sum of exponentials times exponent; a wave a row joins these and takes the dot
 // products of the tokens behind it.  The backward goes through the vocabulary in
 // pieces: a piece's D is computed from the same products, stored (rounded to the
-// inputs' type, as the operand of the two products that follow), and multiplied
+// inputs' type, as the operand of the two products that follow; for few rows in bf16 as
+// two bf16, a row of the largest parts and one of what they leave), and multiplied
 // into dhidden, in fp32 over the pieces, and the piece's dweight.
 //
 // Measured (us): 8192 rows x 131072 x 4096 bf16 6530 (1350 TFLOP/s; a library product
@@ -165,6 +166,7 @@ struct Job {
   int32_t v0;
   void* d;                  // [padded n, ldd]
   int64_t ldd;
+  int32_t stack;            // LinearWork's: rows `stack` .. have what rounding row 0 .. left
   // kSum: out[n][m], or fp32 sums (of a split) in acc
   void* out;
   float* acc;
@@ -347,6 +349,23 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
           }
         }
       }
+      if constexpr (sizeof(T) == 2 && C::BN == 64)
+        if (j.stack) {
+          if (n0 + an(nb) >= j.stack) continue;
+          f32x4 rest[C::MB];
+#pragma unroll
+          for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const uint32_t w = chunk::pk2(acc[mb][nb][i], acc[mb][nb][i + 1]);
+              rest[mb][i] = acc[mb][nb][i] - chunk::lo_f(w);
+              rest[mb][i + 1] = acc[mb][nb][i + 1] - chunk::hi_f(w);
+            }
+#pragma unroll
+          for (int mb = 0; mb < C::MB; mb += 2)
+            put_blocks<T>(static_cast<T*>(j.d) + int64_t(n + j.stack) * j.ldd, m0 + am(mb), g4, j.m_tiles * BM, rest[mb],
+                          rest[mb + 1]);
+        }
 #pragma unroll
       for (int mb = 0; mb < C::MB; mb += 2)
         put_blocks<T>(static_cast<T*>(j.d) + int64_t(n) * j.ldd, m0 + am(mb), g4, j.m_tiles * BM, acc[mb][nb], acc[mb + 1][nb]);
@@ -422,10 +441,21 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4*
     }
 }
 
-// A wave a row: the coefficients of its gradient.
-__global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int4* ids) {
+// A wave a row: the coefficients of its gradient; and, with `stack`, the row's hidden
+// states (bf16; zeros past the last row) at rows lr and stack + lr of hidden2.
+__global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int4* ids, int stack, uint4* hidden2) {
   const int lane = threadIdx.x & 63;
   const int lr = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (lr < stack) {
+    const int n = a.width / 8;
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + int64_t(lr) * a.ld);
+#pragma unroll 4
+    for (int i = lane; i < n; i += 64) {
+      const uint4 x = lr < a.n_rows ? from[i] : make_uint4(0, 0, 0, 0);
+      hidden2[lr * n + i] = x;
+      hidden2[(stack + lr) * n + i] = x;
+    }
+  }
   if (lr >= a.n_rows) return;
   const Behind b(a, a.first_row + lr, lane);
   float g = 0.f, g0 = 0.f;
@@ -515,12 +545,13 @@ hipError_t forward(const LinearArgs& a, const LinearWork& w, hipStream_t stream)
   return hipSuccess;
 }
 
-// out (or acc) = add + the product, over splits where there are several.
+// out (or acc) = add + the product, over splits where there are several; with `stack`,
+// rows n and stack + n of it are added up for the n_rows first.
 template <typename T, bool TB>
-hipError_t sum_product(int size, int splits, float* parts, Job j, float* acc, const float* add, void* out,
+hipError_t sum_product(int size, int splits, float* parts, int stack, Job j, float* acc, const float* add, void* out,
                        const LinearArgs& a, hipStream_t stream) {
   j.splits = splits;
-  if (splits <= 1) {
+  if (splits <= 1 && !stack) {
     j.acc = acc;
     j.add = add;
     j.out = out;
@@ -532,10 +563,11 @@ hipError_t sum_product(int size, int splits, float* parts, Job j, float* acc, co
   if (e != hipSuccess) return e;
   constexpr int BK = product::kStep / int(sizeof(T));
   const int k_split = ceil_div(ceil_div(j.k, splits), BK) * BK;
-  const int64_t quads = j.acc_split / 4;
+  const int64_t each = stack ? int64_t(stack) * j.m : j.acc_split;
+  const int64_t quads = (stack ? int64_t(a.n_rows) * j.m : each) / 4;
   const int64_t groups = (quads + 255) / 256;
   split_sum_kernel<T><<<static_cast<uint32_t>(groups < 8192 ? groups : 8192), 256, 0, stream>>>(
-      parts, j.acc_split, ceil_div(j.k, k_split), add, acc, out, quads);
+      parts, each, ceil_div(j.k, k_split) * static_cast<int>(j.acc_split / each), add, acc, out, quads);
   return hipGetLastError();
 }
 
@@ -546,6 +578,7 @@ hipError_t backward(const LinearArgs& a, const LinearWork& w, hipStream_t stream
   int4* ids = reinterpret_cast<int4*>(base + w.ids);
   float* dh = reinterpret_cast<float*>(base + w.dhidden);
   float* dw = reinterpret_cast<float*>(base + w.dweight);
+  uint4* hidden2 = reinterpret_cast<uint4*>(base + w.hidden2);
   float* parts = reinterpret_cast<float*>(base + w.parts);
   const int64_t es = sizeof(T);
   for (int64_t r0 = 0; r0 < a.n_rows; r0 += w.rows) {
@@ -556,7 +589,7 @@ hipError_t backward(const LinearArgs& a, const LinearWork& w, hipStream_t stream
     b.lse_in = a.lse_in + r0;
     b.entropy_in = a.entropy_in ? a.entropy_in + r0 : nullptr;
     b.dentropy = a.dentropy ? a.dentropy + r0 : nullptr;
-    row_kernel<<<ceil_div(b.n_rows, 4), 256, 0, stream>>>(b, row, ids);
+    row_kernel<<<ceil_div(w.stack ? w.stack : b.n_rows, 4), 256, 0, stream>>>(b, row, ids, w.stack, hidden2);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool first_rows = r0 == 0, last_rows = r0 + w.rows >= a.n_rows;
@@ -578,6 +611,7 @@ hipError_t backward(const LinearArgs& a, const LinearWork& w, hipStream_t stream
       j.v0 = static_cast<int32_t>(v0);
       j.d = base + w.d;
       j.ldd = w.ldd;
+      j.stack = w.stack;
       e = launch_sized<T, false, false, kGrad>(w.size, j, b, stream);
       if (e != hipSuccess) return e;
       j = Job{};  // dhidden [rows, width] += D weight
@@ -586,17 +620,17 @@ hipError_t backward(const LinearArgs& a, const LinearWork& w, hipStream_t stream
       j.lda = a.width * es;
       j.ldb = w.ldd * es;
       j.m = a.width;
-      j.n = b.n_rows;
+      j.n = w.stack ? 2 * w.stack : b.n_rows;
       j.k = nv;
-      e = sum_product<T, false>(w.size_h, w.splits_h, parts, j, dh, first ? nullptr : dh,
+      e = sum_product<T, false>(w.size_h, w.splits_h, parts, w.stack, j, dh, first ? nullptr : dh,
                                 last ? static_cast<char*>(a.dhidden) + r0 * a.width * es : nullptr, b, stream);
       if (e != hipSuccess) return e;
-      j.a = static_cast<const char*>(b.hidden);  // dweight [nv, width] += D^T hidden
-      j.lda = a.ld * es;
+      j.a = w.stack ? base + w.hidden2 : static_cast<const char*>(b.hidden);  // dweight [nv, width] += D^T hidden
+      j.lda = (w.stack ? a.width : a.ld) * es;
+      j.k = j.n;
       j.n = nv;
-      j.k = b.n_rows;
       float* acc = dw + v0 * a.width;
-      e = sum_product<T, true>(w.size_w, w.splits_w, parts, j, acc, first_rows ? nullptr : acc,
+      e = sum_product<T, true>(w.size_w, w.splits_w, parts, 0, j, acc, first_rows ? nullptr : acc,
                                last_rows ? static_cast<char*>(a.dweight) + v0 * a.width * es : nullptr, b, stream);
       if (e != hipSuccess) return e;
     }

@@ -209,6 +209,27 @@ def test_large_tiles_of_the_hidden_states_gradient(n, vocab, width):
         assert rel <= most and worst <= 4 * most
 
 
+@pytest.mark.parametrize("n,vocab,width", [(1, 300, 264), (5, 9001, 72), (32, 2000, 136), (33, 32000, 64),
+                                           (64, 5000, 264), (40, (1 << 20) + 300, 8), (65, 5000, 264)])
+def test_few_rows_round_once(n, vocab, width):
+    """Up to 64 rows of bf16 the logits' gradient is two bf16 numbers, so that the gradients
+    are off by their own rounding alone; 65 and more by both."""
+    say(f"linear logprobs n={n} vocab={vocab} width={width} bf16")
+    parents, lens = chain(n)
+    h, w, tok, dlogp, dent = inputs(n, vocab, width, torch.bfloat16, seed=n, pad=8)
+    plan = ptp.tree_plan(parents, lens, 4)
+    r = ptp.tree_linear_logprobs(h, w, tok, plan)
+    d = ptp.tree_linear_logprobs_backward(h, w, tok, r.lse, r.entropy, dlogp, plan, dentropy=dent)
+    torch.cuda.synchronize()
+    want = exact(parents, lens, h, w, tok, dlogp, dent, 1.0)
+    for name, x, y in zip(("dhidden", "dweight"), d, want[3:]):
+        rel = ((x.double() - y).norm() / y.norm()).item()
+        say(f"  {name}: {rel:.2e} of the norm")
+        # A rounding is 2^-8 / sqrt(3) at most in the mean, 0.74 of that over mantissas
+        # spread evenly, which leaves room for chance over 264 values and more.
+        assert rel <= 2.0 ** -8 * ((1 if n <= 64 else 2) / 3) ** 0.5
+
+
 @pytest.mark.parametrize("temperature", [0.3, 1.7])
 def test_temperature_and_strides(temperature):
     for dtype in DT.values():
