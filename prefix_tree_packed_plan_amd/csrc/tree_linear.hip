@@ -21,7 +21,7 @@
 // of that shape alone reaches 1496), gradients of 8192 x 131072 x 2048 10400 (1270), fp32
 // 1685 x 50001 x 1000 935 (180), gradients of 1526 x 20001 x 1000 1000 (183; a library
 // fp32 product 155); 33 rows x 32000 x 2048 39 (the product 22: 131 MB of weight at 5.9
-// TB/s) and 112.  Large ones are bound by the matrix units at two thirds of their
+// TB/s) and 125.  Large ones are bound by the matrix units at two thirds of their
 // cycles, with DMA and LDS reads between, and by the clock under load.
 #include <hip/hip_runtime.h>
 
