@@ -261,7 +261,10 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tile sizes and splits of a product of m x n over k.  Up to 64 rows n take 64 of them a
-// tile, and a sum as many splits as fill the CUs.  Otherwise the least of: rounds of
+// tile, and a sum as many splits as fill the CUs; so do logits, which cannot be split,
+// as long as the 64 x 64 tiles run at once (106 rows x 3135 x 4032 fp32 102 us, with 128 x
+// 128 195; 512 tiles, 256 rows x 8192 x 2048 bf16, 23 and 29; but 1024 tiles, 512 x 8192 x
+// 2048, 36 and 30).  Otherwise the least of: rounds of
 // work-groups (256 tiles of 256 x 256, one a CU; 512 of 128 x 128, two) times a round's
 // time, in us as measured for a k-step of it, and the parts' way through memory.  Large
 // bf16 products so take 256 x 256 (8192 x 131072 x 4096 forward 6480 us, with 128 x 128
@@ -276,6 +279,7 @@ struct ProductChoice {
 ProductChoice product_choice(int64_t m, int64_t n, int64_t k, int32_t dtype, bool sum, bool few) {
   const bool f32 = dtype == TREE_DTYPE_F32;
   const int64_t steps = ceil_div(k, f32 ? 32 : 64), most = sum ? std::max<int64_t>(1, steps / 8) : 1;
+  if (!sum && ceil_div(m, 64) * ceil_div(n, 64) <= 512) return {0, 1};
   if (few && n <= 64)
     return {0, static_cast<int32_t>(std::max<int64_t>(1, std::min(512 / (ceil_div(m, 128) * ceil_div(n, 64)), most)))};
   ProductChoice best{};

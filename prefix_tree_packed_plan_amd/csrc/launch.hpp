@@ -316,7 +316,7 @@ struct LinearArgs {
 };
 
 // How a call is cut: `rows` rows at a time and, in the backward, `piece` entries of
-// the vocabulary; the tile sizes (0: 64 rows, 1: 128 x 128, 2: 256 x 256, bf16) and splits
+// the vocabulary; the tile sizes (0: 64 x 64, of sums 128 x 64, 1: 128 x 128, 2: 256 x 256, bf16) and splits
 // of the contraction of its products; and its workspace.
 struct LinearWork {
   int64_t rows, piece;

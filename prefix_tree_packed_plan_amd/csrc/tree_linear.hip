@@ -500,7 +500,7 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// By the tile sizes of `size`: 0: 64 rows (64 x 64, of a sum product 128 x 64), 1: 128 x
+// By the tile sizes of `size`: 0: 64 x 64, of a sum product 128 x 64, 1: 128 x
 // 128, 2 (bf16): 256 x 256.
 template <typename T, bool TA, bool TB, Use USE>
 hipError_t launch_sized(int size, const Job& j, const LinearArgs& a, hipStream_t stream) {
