@@ -43,19 +43,21 @@ using chunk::f32x4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// Of some values z / T, in powers of 2: m (largest z log2(e) / T; -inf: nothing
-// yet), sum of e = exp2(y) with y = z log2(e) / T - m, sum of e y.
+// Of some products x, whose logits are x / T: m (the largest; -inf: nothing yet), sum of e =
+// exp2(y) with y = (x - m) c, c = log2(e) / T, and sum of e y.  The difference comes
+// before the scale, so that m c may be too large for fp32 (entries masked by the
+// lowest number) and y is off by roundings of its own size alone.
 struct LinearSums {
   float m, s, t;
 };
-__device__ __forceinline__ LinearSums join(const LinearSums a, const LinearSums b) {
+__device__ __forceinline__ LinearSums join(const LinearSums a, const LinearSums b, float c) {
   const float m = fmaxf(a.m, b.m);
   if (m == kNegInf) return LinearSums{m, a.s + b.s, a.t + b.t};
   LinearSums r;
   r.m = m;
   // A factor of 0 (that side is empty, or far below) drops t, whose shift may
   // overflow; a NaN stays in s.
-  const float da = a.m - m, db = b.m - m;
+  const float da = (a.m - m) * c, db = (b.m - m) * c;
   const float fa = ex2(da), fb = ex2(db);
   r.s = a.s * fa + b.s * fb;
   r.t = (fa == 0.f ? 0.f : fmaf(da, a.s, a.t) * fa) + (fb == 0.f ? 0.f : fmaf(db, b.s, b.t) * fb);
@@ -155,9 +157,9 @@ struct Job {
   int32_t m, n, k;
   int32_t m_tiles, n_tiles, band;  // tiles run through `band` n for each m
   int32_t splits, k_split;  // k is cut into `splits` of k_split (a multiple of a step)
-  // kStats: z of entry m, row n, times c
-  float c;
-  float4* part;             // [n, m_tiles]: largest z c, sum, weighted sum
+  // kStats
+  float c;                  // log2(e) / T
+  float4* part;             // [n, m_tiles]: LinearSums of a tile's entries
   int4* found;              // [n]: find_row
   // kGrad: entry v0 + m
   const float4* row;        // RowGrad of each row
@@ -257,13 +259,13 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
         for (int i = 0; i < 4; ++i) top = fmaxf(top, acc[mb][nb][i]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float m = top == kNegInf ? 0.f : top * j.c;
+      const float m = top == kNegInf ? 0.f : top;
       float s = 0.f, t = 0.f;
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float y = fmaf(acc[mb][nb][i], j.c, -m), e = ex2(y);
+          const float y = (acc[mb][nb][i] - m) * j.c, e = ex2(y);
           s += e;
           t = fmaf(e, fmaxf(y, -3.4e38f), t);  // e = 0 where y = -inf
         }
@@ -273,7 +275,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
       t += __shfl_xor(t, 32, 64);
       if (g4 == 0) {
         const int o = wm * BN + an(nb) + l16;
-        red[o] = top == kNegInf ? kNegInf : m;
+        red[o] = top;
         red[o + WM * BN] = s;
         red[o + 2 * WM * BN] = t;
       }
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
       LinearSums z{red[n], red[n + WM * BN], red[n + 2 * WM * BN]};
 #pragma unroll
       for (int w = 1; w < WM; ++w)
-        z = join(z, LinearSums{red[n + w * BN], red[n + (WM + w) * BN], red[n + (2 * WM + w) * BN]});
+        z = join(z, LinearSums{red[n + w * BN], red[n + (WM + w) * BN], red[n + (2 * WM + w) * BN]}, j.c);
       j.part[int64_t(n0 + n) * j.m_tiles + mt] = make_float4(z.m, z.s, z.t, 0.f);
     }
   } else if constexpr (USE == kGrad) {
@@ -415,23 +417,28 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4*
   const int lr = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   if (lr >= a.n_rows) return;
   const int4 f = found[lr];
+  const float c = a.inv_t * kLog2e;
   LinearSums z{kNegInf, 0.f, 0.f};
 #pragma unroll 4
   for (int i = lane; i < slots; i += 64) {
     const float4 y = part[int64_t(lr) * slots + i];
-    z = join(z, LinearSums{y.x, y.y, y.z});
+    z = join(z, LinearSums{y.x, y.y, y.z}, c);
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1)
-    z = join(z, LinearSums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)});
-  const bool empty = z.m == kNegInf && z.s == 0.f;  // every logit is -inf
-  const float ls = __log2f(z.s), c = a.inv_t * kLog2e;
+    z = join(z, LinearSums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)}, c);
+  // The largest logit: of +inf the results are NaN; of -inf, so are all others.
+  const float largest = z.m * a.inv_t;
+  if (largest == -kNegInf) z.s = __builtin_nanf("");
+  const bool empty = largest == kNegInf && z.s == z.s;
+  const float ls = __log2f(z.s);
   if (lane == 0) {
-    a.lse[lr] = empty ? kNegInf : (z.m + ls) * kLn2;
+    a.lse[lr] = empty ? kNegInf : fmaf(z.m, a.inv_t, ls * kLn2);
     a.entropy[lr] = empty ? 0.f : (ls - z.t / z.s) * kLn2;
     if (f.w & kRootStart) a.logp[a.first_row + lr] = 0.f;
   }
-  const auto logp = [&](float x) { return empty ? kNegInf : (fmaf(x, c, -z.m) - ls) * kLn2; };
+  // Halves, whose difference is in range.
+  const auto logp = [&](float x) { return empty ? kNegInf : fmaf(0.5f * x - 0.5f * z.m, 2.f * a.inv_t, -(ls * kLn2)); };
   if (lane == 0 && f.w & kAny) a.logp[f.y] = f.w & kOutside ? 0.f : logp(__int_as_float(f.x));
   // The other children's first tokens: their logits wait in logp.
   if (f.w & kMore)
