@@ -654,7 +654,8 @@ size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32
  *   lse = log sum_i exp(z_i),  entropy = -sum_i p_i log p_i, p_i = exp(z_i - lse),
  *   logp[t] = z_{tokens[t]} - lse   for every token t behind the row,
  * the next token of its segment or the first token of every child ("Tree
- * Training" section 3.1 Eq. 6), 0 for a root's first token.
+ * Training" section 3.1 Eq. 6), 0 for a root's first token.  A token's logit is bitwise
+ * one of those that lse is made of: no log probability is above 0.
  *
  * hidden   device, [n_rows, width], dtype, ld elements between rows: those of
  *          packed rows first_row .. first_row + n_rows - 1 (a part of the trie

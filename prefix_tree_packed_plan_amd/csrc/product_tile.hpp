@@ -213,6 +213,12 @@ __device__ __forceinline__ Split split3(const float (&x)[8]) {
   return s;
 }
 
+__device__ __forceinline__ Split split3(const uint4 (&w)[2]) {
+  const float x[8] = {__uint_as_float(w[0].x), __uint_as_float(w[0].y), __uint_as_float(w[0].z), __uint_as_float(w[0].w),
+                      __uint_as_float(w[1].x), __uint_as_float(w[1].y), __uint_as_float(w[1].z), __uint_as_float(w[1].w)};
+  return split3(x);
+}
+
 __device__ __forceinline__ f32x4 mma(const uint4 a, const uint4 b, const f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);

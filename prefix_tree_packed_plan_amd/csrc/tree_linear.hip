@@ -98,28 +98,53 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-// hidden row lr x weight row id, to all lanes of a wave.
+// hidden row lr x weight row id, to all lanes of a wave: by the matrix instructions of a
+// tile in the tile's order, so that it is bitwise what the row's maximum and sum are made of
+// (summed otherwise, a log probability near 0 came out as up to 4e-5, width 4096).
+// Lane 16 g + i loads piece g of the i-th 32 k; of an instruction's 256 sums the i-th on
+// the diagonal is the one wanted, and all start from the last one.
 template <typename T>
-__device__ __forceinline__ float dot(const LinearArgs& a, int lr, int id) {
-  constexpr int N = 16 / sizeof(T);
-  const uint4* hrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.hidden) + int64_t(lr) * a.ld);
-  const uint4* wrow = reinterpret_cast<const uint4*>(static_cast<const T*>(a.weight) + int64_t(id) * a.width);
-  float x = 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x & 63; i < a.width / N; i += 64) {
-    const uint4 u = hrow[i], w = wrow[i];
-    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float logit(const LinearArgs& a, int lr, int id) {
+  constexpr int E16 = 16 / sizeof(T), P = 8 / E16;  // pieces of 16 bytes a lane has of 32 k
+  constexpr int U = sizeof(T) == 2 ? 4 : 1;         // 512 k, loaded at once
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const char* hrow = reinterpret_cast<const char*>(static_cast<const T*>(a.hidden) + int64_t(lr) * a.ld);
+  const char* wrow = reinterpret_cast<const char*>(static_cast<const T*>(a.weight) + int64_t(id) * a.width);
+  float x = 0.f, rest = 0.f;
+  for (int k0 = 0; k0 < a.width; k0 += 512 * U) {
+    uint4 w[U][P], h[U][P];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (sizeof(T) == 4) {
-        x = fmaf(__uint_as_float(uu[q]), __uint_as_float(ww[q]), x);
-      } else {
-        x = fmaf(chunk::lo_f(uu[q]), chunk::lo_f(ww[q]), x);
-        x = fmaf(chunk::hi_f(uu[q]), chunk::hi_f(ww[q]), x);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int k = k0 + 512 * u + 32 * i + 8 * g + E16 * p;
+        const bool in = k < a.width;  // zeros past the end
+        w[u][p] = in ? *reinterpret_cast<const uint4*>(wrow + k * sizeof(T)) : make_uint4(0, 0, 0, 0);
+        h[u][p] = in ? *reinterpret_cast<const uint4*>(hrow + k * sizeof(T)) : make_uint4(0, 0, 0, 0);
       }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      product::Split ws, hs;
+      if constexpr (sizeof(T) == 4) {
+        ws = product::split3(w[u]);
+        hs = product::split3(h[u]);
+      }
+      product::unrolled<16>([&](auto step) {
+        constexpr int j = decltype(step)::value, from = 16 * (j / 4) + j;
+        if (k0 + 512 * u + 32 * j >= a.width) return;
+        const auto diagonal = [&](const f32x4 c) {
+          return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(c[j % 4]), from));
+        };
+        if constexpr (sizeof(T) == 2) {
+          x = diagonal(product::mma(w[u][0], h[u][0], f32x4{x, x, x, x}));
+        } else {
+          rest = diagonal(product::mma_rest(ws, hs, f32x4{rest, rest, rest, rest}));
+          x = diagonal(product::mma(ws.part(0), hs.part(0), f32x4{x, x, x, x}));
+        }
+      });
     }
   }
-  return wave_sum(x);
+  return x + rest;
 }
 
 // Tokens and their logits, by work-groups beside those of the product, which they take
@@ -136,7 +161,7 @@ __device__ __forceinline__ void find_row(const LinearArgs& a, int lr, int4* foun
   int flags = (b.n > 0 ? kAny : 0) | (b.n > 1 ? kMore : 0) | (b.root_start ? kRootStart : 0);
   const int t = b.n > 0 ? b.at(0) : 0, id = b.n > 0 ? token(a, t) : -1;
   if (id < 0) flags |= kOutside;
-  const float x = id >= 0 ? dot<T>(a, lr, id) : 0.f;
+  const float x = id >= 0 ? logit<T>(a, lr, id) : 0.f;
   if (lane == 0) found[lr] = make_int4(__float_as_int(x), t, b.seg, flags);
 }
 template <typename T>
@@ -146,7 +171,7 @@ __device__ __forceinline__ void find_segment(const LinearArgs& a, int s) {
   const int lr = a.seg_off[p + 1] - 1 - a.first_row, t = a.seg_off[s];
   if (lr < 0 || lr >= a.n_rows) return;
   const int id = token(a, t);
-  const float x = id >= 0 ? dot<T>(a, lr, id) : 0.f;
+  const float x = id >= 0 ? logit<T>(a, lr, id) : 0.f;
   if ((threadIdx.x & 63) == 0) a.logp[t] = x;
 }
 
