@@ -41,6 +41,7 @@ using chunk::kLog2e;
 using chunk::f32x4;
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2eRest = 1.92596299e-8f;  // log2(e) - kLog2e
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Of some products x, whose logits are x / T: m (the largest; -inf: nothing yet), sum of e =
@@ -327,8 +328,10 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
         for (int i = 0; i < 4; ++i) {
           const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x), held = fmaxf(lp, -1e4f);  // exp is 0 below -104
           float e = ex2(lp * kLog2e);
-          // That product's rounding, 2^-24 of up to 20 or more, is too much for fp32.
-          if (sizeof(T) == 4) e = fmaf(e, fmaf(held, kLog2e, -(held * kLog2e)) * kLn2, e);
+          // That product's rounding, 2^-24 of up to 20 or more, is too much for fp32, and so
+          // is its constant's, 2^-26 of as much and the same way in all entries.
+          if (sizeof(T) == 4)
+            e = fmaf(e, fmaf(held, kLog2eRest, fmaf(held, kLog2e, -(held * kLog2e))) * kLn2, e);
           acc[mb][nb][i] = e * fmaf(rc.z, held, rc.y);
         }
       if (!__all(live) || m0 + BM > j.m) {
