@@ -1,11 +1,13 @@
 """fp32 gradients of log probabilities from hidden states and the output weight,
-held to fp32's accuracy: the exponentials of far entries."""
+held to fp32's accuracy: the exponentials of far entries, and each of the six
+partial products that stand for a product of two fp32 numbers."""
 import sys
 
 import pytest
 import torch
 
 import prefix_tree_packed_plan_amd as ptp
+from oracle.split import SPLIT_CASES, SPLIT_REL, SPLIT_RMS, split_exact, split_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +32,23 @@ def test_exponentials_of_far_entries(n, vocab):
     # coefficient, three of the sum of its parts.  (The constant's alone would be 2^-26 x 70.)
     worst = (dw[:-1, :-1].double() / want[:-1] - 1).abs().max().item()
     assert worst <= 7 * 2.0 ** -24, worst
+
+
+@pytest.mark.parametrize("n,vocab,width", SPLIT_CASES)
+def test_six_partial_products(n, vocab, width):
+    """The errors' size over the whole result, which no worst case's bound holds to a
+    partial product: leaving one out of the products makes it one and a half times the limit or more
+    (the oracle's test plants that)."""
+    print(f"six products n={n} vocab={vocab} width={width}", file=sys.stderr, flush=True)
+    parents, lens, h, w, tok, dlogp = (x.to(DEV) if isinstance(x, torch.Tensor) else x
+                                       for x in split_inputs(n, vocab, width))
+    plan = ptp.tree_plan(parents, lens, 4)
+    r = ptp.tree_linear_logprobs(h, w, tok, plan)
+    dh, dw = ptp.tree_linear_logprobs_backward(h, w, tok, r.lse, None, dlogp, plan)
+    torch.cuda.synchronize()
+    logp, want_dh, want_dw = split_exact(parents, lens, h, w, tok, dlogp)
+    for name, got, want, most in (("logp", r.logp, logp, SPLIT_RMS), ("dhidden", dh, want_dh, SPLIT_REL),
+                                  ("dweight", dw, want_dw, SPLIT_REL)):
+        err = (got.double() - want).norm().item() / (len(want) ** 0.5 if name == "logp" else want.norm().item())
+        print(f"  {name}: {err:.2e}, limit {most:.2e}", file=sys.stderr, flush=True)
+        assert err <= most, name
