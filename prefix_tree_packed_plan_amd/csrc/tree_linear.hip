@@ -217,9 +217,12 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
   if constexpr (USE == kStats) {
     // The work-groups behind the tiles'.
     if (static_cast<int>(blockIdx.x) >= tiles) {
-      const int i = (blockIdx.x - tiles) * (C::THREADS / 64) + wave;
-      if (i < la.n_rows) find_row<T>(la, i, j.found);
-      else if (i - la.n_rows < la.n_seg) find_segment<T>(la, i - la.n_rows);
+      constexpr int W = C::THREADS / 64;
+      const int64_t step = int64_t(gridDim.x - tiles) * W, end = int64_t(la.n_rows) + la.n_seg;
+      for (int64_t i = int64_t(blockIdx.x - tiles) * W + wave; i < end; i += step) {
+        if (i < la.n_rows) find_row<T>(la, static_cast<int>(i), j.found);
+        else find_segment<T>(la, static_cast<int>(i - la.n_rows));
+      }
       return;
     }
   }
@@ -515,6 +518,13 @@ __global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int
 // ---- launches -----------------------------------------------------------------------
 int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
 
+// Work-groups of `waves` that look for tokens, a wave a row or segment.  A launch's
+// work items are counted in 32 bits: past 2^16 work-groups a wave takes several.
+int32_t find_groups(int32_t n_rows, int32_t n_seg, int32_t waves) {
+  const int64_t groups = ceil_div(int64_t(n_rows) + n_seg, waves), most = 1 << 16;
+  return static_cast<int32_t>(groups < most ? groups : most);
+}
+
 template <typename T, typename C, bool BIG, Use USE>
 hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   constexpr int BK = product::kStep / int(sizeof(T));
@@ -530,7 +540,7 @@ hipError_t launch_product(Job j, const LinearArgs& a, hipStream_t stream) {
   // 8 x 4 tiles run on an XCD's 32 CUs at a time: operands of 12 tiles for 32 products.
   j.band = j.n_tiles < 4 ? j.n_tiles : 4;
   int64_t groups = int64_t(j.m_tiles) * j.n_tiles * j.splits;
-  if (USE == kStats) groups += ceil_div(int64_t(j.n) + a.n_seg, C::THREADS / 64);
+  if (USE == kStats) groups += find_groups(j.n, a.n_seg, C::THREADS / 64);
   product_kernel<T, C, BIG, USE><<<static_cast<uint32_t>(groups), C::THREADS, 0, stream>>>(j, a);
   return hipGetLastError();
 }
