@@ -674,10 +674,11 @@ size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32
  *          TREE_DTYPE_F32 (each value as three bf16, the six largest partial
  *          products: fp32 accuracy; values above 3.38e38 are taken as infinite, and what is
  *          infinite makes its logits NaN).
- * Logits may be of any finite size (entries masked by the lowest bf16, say).  A row whose
- * logits are all -inf, or below fp32's range, has lse -inf, entropy 0 and log
- * probabilities -inf; a logit of NaN or +inf (of hidden or weight not finite, or
- * products too large) makes its row's results NaN.
+ * Logits are taken relative to their row's largest, so that they may be of any size as
+ * long as the product of hidden and weight is finite (entries masked by the lowest
+ * bf16, say); lse is held at the largest fp32 value.  A row whose products are all
+ * -inf has lse -inf, entropy 0 and log probabilities -inf; one of NaN or +inf (of
+ * hidden or weight not finite, or products too large) makes its row's results NaN.
  * dplan, dplan_bytes  device copy of `plan`, as for tree_conv.
  * ws       device workspace, ws_bytes >= tree_linear_logprobs_workspace_bytes.
  * Errors: INVALID_ARG, SIZE, UNSUPPORTED (width, vocab), WORKSPACE, HIP.

@@ -43,6 +43,7 @@ using chunk::f32x4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2eRest = 1.92596299e-8f;  // log2(e) - kLog2e
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kFltMax = 3.402823466e38f;
 
 // Of some products x, whose logits are x / T: m (the largest; -inf: nothing yet), sum of e =
 // exp2(y) with y = (x - m) c, c = log2(e) / T, and sum of e y.  The difference comes
@@ -458,13 +459,12 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4*
 #pragma unroll
   for (int o = 32; o; o >>= 1)
     z = join(z, LinearSums{__shfl_xor(z.m, o, 64), __shfl_xor(z.s, o, 64), __shfl_xor(z.t, o, 64)}, c);
-  // The largest logit: of +inf the results are NaN; of -inf, so are all others.
-  const float largest = z.m * a.inv_t;
-  if (largest == -kNegInf) z.s = __builtin_nanf("");
-  const bool empty = largest == kNegInf && z.s == z.s;
+  const bool empty = z.m == kNegInf && z.s == 0.f;  // every logit is -inf
   const float ls = __log2f(z.s);
   if (lane == 0) {
-    a.lse[lr] = empty ? kNegInf : fmaf(z.m, a.inv_t, ls * kLn2);
+    float lse = fmaf(z.m, a.inv_t, ls * kLn2);  // held at the largest fp32 value; a NaN stays one
+    lse = lse < -kFltMax ? -kFltMax : lse > kFltMax ? kFltMax : lse;
+    a.lse[lr] = empty ? kNegInf : lse;
     a.entropy[lr] = empty ? 0.f : (ls - z.t / z.s) * kLn2;
     if (f.w & kRootStart) a.logp[a.first_row + lr] = 0.f;
   }

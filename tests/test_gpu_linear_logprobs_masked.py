@@ -87,7 +87,7 @@ def test_masked_entries_count_for_nothing(n, first, keep, vocab, temperature, dt
 @pytest.mark.parametrize("x", [1.0e38, 2.0e38, 2.5e38, 3.2e38, -1.0e38, -2.0e38, -2.5e38, -3.2e38])
 def test_logits_at_the_ends_of_the_range(x, n, vocab, dtype):
     """All logits of a row equal and large: the entropy is log V and every log probability
-    its negative.  Past fp32's range, up: NaN; down: as for logits of -inf."""
+    its negative, also where a temperature of 1/4 takes the logits out of fp32's range."""
     print(f"large {x} n={n} vocab={vocab} {dtype}", file=sys.stderr, flush=True)
     h = torch.zeros((n, 8), dtype=DT[dtype], device=DEV)
     h[:, 0] = 1
@@ -106,14 +106,9 @@ def test_logits_at_the_ends_of_the_range(x, n, vocab, dtype):
     assert (r.lse.double() / value - 1).abs().max() <= 2.0 ** -23
     r = ptp.tree_linear_logprobs(h, w, tok, plan, temperature=0.25)
     torch.cuda.synchronize()
-    if x > 0:
-        assert all(torch.isnan(y).all() for y in (r.lse, r.entropy, r.logp[1:]))
-    else:
-        assert (r.lse == float("-inf")).all() and not r.entropy.any() and (r.logp[1:] == float("-inf")).all()
-        dh, dw = ptp.tree_linear_logprobs_backward(h, w, tok, r.lse, r.entropy, torch.ones(n, device=DEV), plan,
-                                                   temperature=0.25)
-        torch.cuda.synchronize()
-        assert not dh.any() and not dw.any()
+    assert (r.entropy.double() - log_v).abs().max() <= 4 * 2.0 ** -24 * log_v
+    assert (r.logp[1:].double() + log_v).abs().max() <= 4 * 2.0 ** -24 * log_v + 1e-12
+    assert (r.lse == torch.finfo(torch.float32).max * (1 if x > 0 else -1)).all()
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))
