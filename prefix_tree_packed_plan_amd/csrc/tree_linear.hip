@@ -206,7 +206,8 @@ struct Job {
 // The gradient's coefficients of a row: D = exp(z - lse) (cb log p + ca), plus g /
 // T at the entries that stand behind it.
 //   row: (lse, ca, cb, g of the first token)
-//   ids: (the first token's entry or -1, tokens behind, first of them in kid or -1, 0)
+//   ids: (the first token's entry or -1, tokens behind, first of them in kid or -1, a
+//        product x0; lse is then that of the products less x0: 0 but for far rows)
 template <typename T, typename C, bool BIG, Use USE>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, LinearArgs la) {
   constexpr int BM = C::BM, BN = C::BN, WM = C::WM;
@@ -326,11 +327,12 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void product_kernel(Job j, Line
       const float4 rc = j.row[valid ? n : 0];
       const int4 who = j.ids[valid ? n : 0];
       const bool live = valid && rc.x != kNegInf;
+      const float x0 = __int_as_float(who.w);
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float lp = fmaf(acc[mb][nb][i], j.inv_t, -rc.x), held = fmaxf(lp, -1e4f);  // exp is 0 below -104
+          const float lp = fmaf(acc[mb][nb][i] - x0, j.inv_t, -rc.x), held = fmaxf(lp, -1e4f);  // exp is 0 below -104
           float e = ex2(lp * kLog2e);
           // That product's rounding, 2^-24 of up to 20 or more, is too much for fp32, and so
           // is its constant's, 2^-26 of as much and the same way in all entries.
@@ -479,11 +481,62 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4*
     }
 }
 
+// Products of 16 rows of the weight (this lane's: wrow) and 16 of hidden (hrow), as a
+// tile's, bitwise.
+template <typename T>
+__device__ __forceinline__ f32x4 products16(const T* wrow, const T* hrow, int width) {
+  constexpr int E16 = 16 / sizeof(T), P = 8 / E16;  // pieces of 16 bytes a lane has of 32 k
+  constexpr int U = 8 / P;                          // 32 k each, loaded at once
+  const int g8 = 8 * ((threadIdx.x & 63) >> 4);
+  f32x4 x = {0.f, 0.f, 0.f, 0.f}, rest = x;
+  for (int k0 = 0; k0 < width; k0 += 32 * U) {
+    uint4 w[U][P], h[U][P];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int k = k0 + 32 * u + g8 + E16 * p;
+        const bool in = k < width;  // zeros past the end
+        w[u][p] = in ? *reinterpret_cast<const uint4*>(wrow + k) : make_uint4(0, 0, 0, 0);
+        h[u][p] = in ? *reinterpret_cast<const uint4*>(hrow + k) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + 32 * u >= width) break;
+      if constexpr (sizeof(T) == 2) {
+        x = product::mma(w[u][0], h[u][0], x);
+      } else {
+        const product::Split ws = product::split3(w[u]), hs = product::split3(h[u]);
+        rest = product::mma_rest(ws, hs, rest);
+        x = product::mma(ws.part(0), hs.part(0), x);
+      }
+    }
+  }
+  return x + rest;
+}
+
+// The largest of some products, and the sum of exp2((x - m) c).
+__device__ __forceinline__ float2 join(const float2 a, const float2 b, float c) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == kNegInf) return make_float2(m, 0.f);
+  return make_float2(m, a.y * ex2((a.x - m) * c) + b.y * ex2((b.x - m) * c));
+}
+
 // A wave a row: the coefficients of its gradient; and, with `stack`, the row's hidden
 // states (bf16; zeros past the last row) at rows lr and stack + lr of hidden2.
-__global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int4* ids, int stack, uint4* hidden2) {
+//
+// Where |lse| is kFarLse or more, its rounding would show in the probabilities, up to
+// infinity (rows whose logits are masked throughout by large finite numbers).  A
+// work-group with such a row finds the largest product and the sum of its 16 rows
+// again, a wave 16 entries at a time: one work-group's pass over the weight.
+constexpr int kRowWaves = 16;
+constexpr float kFarLse = 16384.f;
+template <typename T>
+__global__ __launch_bounds__(64 * kRowWaves) void row_kernel(LinearArgs a, float4* row, int4* ids, int stack,
+                                                             uint4* hidden2) {
   const int lane = threadIdx.x & 63;
-  const int lr = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = blockIdx.x * kRowWaves + wave;
   if (lr < stack) {
     const int n = a.width / 8;
     const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + int64_t(lr) * a.ld);
@@ -494,25 +547,56 @@ __global__ __launch_bounds__(256) void row_kernel(LinearArgs a, float4* row, int
       hidden2[(stack + lr) * n + i] = x;
     }
   }
-  if (lr >= a.n_rows) return;
-  const Behind b(a, a.first_row + lr, lane);
-  float g = 0.f, g0 = 0.f;
-  int id0 = -1;
-  for (int j = lane; j < b.n; j += 64) {
-    const int t = b.at(j), id = token(a, t);
-    const float gj = id < 0 ? 0.f : a.dlogp[t];
-    g += gj;
-    if (j == 0) {
-      g0 = gj;
-      id0 = id;
+  const float lse = lr < a.n_rows ? a.lse_in[lr] : 0.f;
+  const bool far = fabsf(lse) >= kFarLse && fabsf(lse) <= kFltMax;
+  if (lr < a.n_rows) {
+    const Behind b(a, a.first_row + lr, lane);
+    float g = 0.f, g0 = 0.f;
+    int id0 = -1;
+    for (int j = lane; j < b.n; j += 64) {
+      const int t = b.at(j), id = token(a, t);
+      const float gj = id < 0 ? 0.f : a.dlogp[t];
+      g += gj;
+      if (j == 0) {
+        g0 = gj;
+        id0 = id;
+      }
+    }
+    g = wave_sum(g);
+    if (lane == 0) {
+      const float dh = a.dentropy ? a.dentropy[lr] : 0.f;
+      row[lr] = make_float4(lse, -(g + (a.dentropy ? dh * a.entropy_in[lr] : 0.f)) * a.inv_t, -dh * a.inv_t,
+                            g0 * a.inv_t);
+      ids[lr] = make_int4(id0, b.n, b.kid ? static_cast<int>(b.kid - a.kid) : -1, 0);
     }
   }
-  g = wave_sum(g);
-  if (lane != 0) return;
-  const float dh = a.dentropy ? a.dentropy[lr] : 0.f;
-  row[lr] = make_float4(a.lse_in[lr], -(g + (a.dentropy ? dh * a.entropy_in[lr] : 0.f)) * a.inv_t, -dh * a.inv_t,
-                        g0 * a.inv_t);
-  ids[lr] = make_int4(id0, b.n, b.kid ? static_cast<int>(b.kid - a.kid) : -1, 0);
+  if (!__syncthreads_or(far)) return;
+
+  __shared__ float2 sums[kRowWaves][16];
+  const int i = lane & 15, g4 = lane >> 4;
+  const float c = a.inv_t * kLog2e;
+  const T* hrow = static_cast<const T*>(a.hidden) +
+                  int64_t(min(static_cast<int>(blockIdx.x) * kRowWaves + i, a.n_rows - 1)) * a.ld;
+  float2 z = make_float2(kNegInf, 0.f);
+  for (int v0 = 16 * wave; v0 < a.vocab; v0 += 16 * kRowWaves) {
+    const T* wrow = static_cast<const T*>(a.weight) + int64_t(min(v0 + i, a.vocab - 1)) * a.width;
+    const f32x4 x = products16<T>(wrow, hrow, a.width);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v0 + 4 * g4 + e < a.vocab) z = join(z, make_float2(x[e], 1.f), c);
+  }
+#pragma unroll
+  for (int o = 16; o < 64; o += o) z = join(z, make_float2(__shfl_xor(z.x, o, 64), __shfl_xor(z.y, o, 64)), c);
+  if (g4 == 0) sums[wave][i] = z;
+  __syncthreads();
+  if (!far) return;
+  z = sums[i][wave];
+#pragma unroll
+  for (int o = 1; o < 16; o += o) z = join(z, make_float2(__shfl_xor(z.x, o, 64), __shfl_xor(z.y, o, 64)), c);
+  if (lane == 0) {
+    row[lr].x = __log2f(z.y) * kLn2;
+    ids[lr].w = __float_as_int(z.x);
+  }
 }
 
 // ---- launches -----------------------------------------------------------------------
@@ -634,7 +718,8 @@ hipError_t backward(const LinearArgs& a, const LinearWork& w, hipStream_t stream
     b.lse_in = a.lse_in + r0;
     b.entropy_in = a.entropy_in ? a.entropy_in + r0 : nullptr;
     b.dentropy = a.dentropy ? a.dentropy + r0 : nullptr;
-    row_kernel<<<ceil_div(w.stack ? w.stack : b.n_rows, 4), 256, 0, stream>>>(b, row, ids, w.stack, hidden2);
+    row_kernel<T><<<ceil_div(w.stack ? w.stack : b.n_rows, kRowWaves), 64 * kRowWaves, 0, stream>>>(b, row, ids, w.stack,
+                                                                                                  hidden2);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool first_rows = r0 == 0, last_rows = r0 + w.rows >= a.n_rows;
