@@ -486,7 +486,7 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a, const float4*
 template <typename T>
 __device__ __forceinline__ f32x4 products16(const T* wrow, const T* hrow, int width) {
   constexpr int E16 = 16 / sizeof(T), P = 8 / E16;  // pieces of 16 bytes a lane has of 32 k
-  constexpr int U = 8 / P;                          // 32 k each, loaded at once
+  constexpr int U = 4 / P;                          // 32 k each, loaded at once
   const int g8 = 8 * ((threadIdx.x & 63) >> 4);
   f32x4 x = {0.f, 0.f, 0.f, 0.f}, rest = x;
   for (int k0 = 0; k0 < width; k0 += 32 * U) {
@@ -527,12 +527,14 @@ __device__ __forceinline__ float2 join(const float2 a, const float2 b, float c) 
 //
 // Where |lse| is kFarLse or more, its rounding would show in the probabilities, up to
 // infinity (rows whose logits are masked throughout by large finite numbers).  A
-// work-group with such a row finds the largest product and the sum of its 16 rows
-// again, a wave 16 entries at a time: one work-group's pass over the weight.
-constexpr int kRowWaves = 16;
+// work-group with such a row finds the largest product and the sum of its 8 rows
+// again, a wave 16 entries at a time: one work-group's pass over the weight (32000 x
+// 2048 bf16 7 ms, 131072 x 2048 30, and 115 for 8192 such rows; 58 by 16 waves, but then
+// calls without such a row, nearly all, take 1.5 us more; so registers are kept few too).
+constexpr int kRowWaves = 8;
 constexpr float kFarLse = 16384.f;
 template <typename T>
-__global__ __launch_bounds__(64 * kRowWaves) void row_kernel(LinearArgs a, float4* row, int4* ids, int stack,
+__global__ __launch_bounds__(64 * kRowWaves, sizeof(T) == 2 ? 8 : 4) void row_kernel(LinearArgs a, float4* row, int4* ids, int stack,
                                                              uint4* hidden2) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -590,7 +592,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void row_kernel(LinearArgs a, float
   if (g4 == 0) sums[wave][i] = z;
   __syncthreads();
   if (!far) return;
-  z = sums[i][wave];
+  z = i < kRowWaves ? sums[i][wave] : make_float2(kNegInf, 0.f);
 #pragma unroll
   for (int o = 1; o < 16; o += o) z = join(z, make_float2(__shfl_xor(z.x, o, 64), __shfl_xor(z.y, o, 64)), c);
   if (lane == 0) {
