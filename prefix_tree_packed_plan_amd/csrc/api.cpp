@@ -262,9 +262,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tile sizes and splits of a product of m x n over k.  Up to 64 rows n take 64 of them a
 // tile, and a sum as many splits as fill the CUs; so do logits, which cannot be split,
-// as long as the 64 x 64 tiles run at once (106 rows x 3135 x 4032 fp32 102 us, with 128 x
-// 128 195; 512 tiles, 256 rows x 8192 x 2048 bf16, 23 and 29; but 1024 tiles, 512 x 8192 x
-// 2048, 36 and 30).  Otherwise the least of: rounds of
+// as long as the 64 x 64 tiles run at once (106 rows x 3135 x 4032 fp32 100 us, with 128 x
+// 128 195, bf16 23 and 48; 512 tiles, 256 rows x 8192 x 2048, fp32 80 and 104, bf16 23 and
+// 29; but 1024 tiles, 512 x 8192 x 2048, fp32 147 and 105, bf16 39 and 30).  Otherwise the least of: rounds of
 // work-groups (256 tiles of 256 x 256, one a CU; 512 of 128 x 128, two) times a round's
 // time, in us as measured for a k-step of it, and the parts' way through memory.  Large
 // bf16 products so take 256 x 256 (8192 x 131072 x 4096 forward 6480 us, with 128 x 128

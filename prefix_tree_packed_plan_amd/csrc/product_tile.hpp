@@ -13,8 +13,9 @@
 // which is 8 or 16 bytes of a row of `out`; pair_up() makes it 16 for bf16.
 //
 // fp32: a value is the sum of three bf16 (rounded, the rest rounded, the rest of
-// that: exact to 2^-26 of it), and a product of two the six largest of the nine
-// partial products; those left out are below 2^-26 of it.  Six bf16 MFMA do 2.7
+// that: exact to 2^-26 of it; the second is up to 2^-8 of it, the third 2^-17), and a
+// product of two the six largest of the nine partial products; those left out are up to
+// 2^-24 of it, 2^-27 in the mean.  Six bf16 MFMA do 2.7
 // times the work of fp32 MFMA in the same time.  Values within a factor of 2^-8
 // of the largest fp32 may round to infinity.
 #pragma once
@@ -393,9 +394,9 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
       if (t < steps) stage(t, t);
-    // Logits: the five smaller partial products are added up by themselves, below 2^-8 of
-    // the sum, so that it is rounded once for 32 k instead of six times (the largest
-    // error of an fp32 gradient is that of a probability near 1).
+    // Logits: the five smaller partial products, up to 2^-7 of the terms' sizes, are added
+    // up by themselves, so that the sum is rounded once for 32 k instead of six times (the
+    // largest error of an fp32 gradient is that of a probability near 1).
     constexpr bool APART = !C::B_PADDED && !C::A_BY_K;
     f32x4 rest[APART ? MB : 1][APART ? NB : 1] = {};
     int cur = 0, into = S - 1;

@@ -20,8 +20,9 @@
 // long after the others (a token that is a fifth of all of them); their lists are
 // cut into parts at multiples of kPart, and join_kernel adds the parts in order.
 //
-// Measured (us; a copy reaches 4.9 TB/s here, a fill 6.9): 10240 tokens of 131072 x 4096
-// bf16, forward 24.5 (5.1 TB/s of distinct rows read and all written); gradient 243: the sort with
+// Measured (us; inputs that change from call to call; a copy reaches 4.9 TB/s here, a fill
+// 6.9): 10240 tokens of 131072 x 4096 bf16, forward 25 (5.1 TB/s of distinct rows read and
+// all written; 22 where those rows stay in the last-level cache); gradient 245: the sort with
 // its clearing 173 (5.8 TB/s of zeros), the sums 49, the join, without work, 5.  65536
 // tokens, a fifth of them equal, of 32000 x 2048: 173: the sort 80 (one work-group's
 // long row: vector issue), the sums 79 (3.4 TB/s of dout), the join 12.

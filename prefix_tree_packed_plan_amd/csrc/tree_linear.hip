@@ -17,11 +17,12 @@
 // two bf16, a row of the largest parts and one of what they leave), and multiplied
 // into dhidden, in fp32 over the pieces, and the piece's dweight.
 //
-// Measured (us): 8192 rows x 131072 x 4096 bf16 6530 (1350 TFLOP/s; a library product
-// of that shape alone reaches 1496), gradients of 8192 x 131072 x 2048 10400 (1270), fp32
-// 1685 x 50001 x 1000 935 (180), gradients of 1526 x 20001 x 1000 1000 (183; a library
-// fp32 product 155); 33 rows x 32000 x 2048 39 (the product 22: 131 MB of weight at 5.9
-// TB/s) and 125.  Large ones are bound by the matrix units at two thirds of their
+// Measured (us; inputs that change from call to call): 8192 rows x 131072 x 4096 bf16 6460
+// (1360 TFLOP/s; a library product of that shape alone reaches 1496), gradients of 8192 x
+// 131072 x 2048 10340 (1280), fp32 1685 x 50001 x 1000 920 (183), gradients of 1526 x
+// 20001 x 1000 1000 (183; a library fp32 product 155); 33 rows x 32000 x 2048 39 (the
+// product 30: 131 MB of weight at 4.4 TB/s) and 126.  Where those 131 MB stay in the
+// last-level cache these take 30 (22: 5.9 TB/s) and 105.  Large ones are bound by the matrix units at two thirds of their
 // cycles, with DMA and LDS reads between, and by the clock under load.
 #include <hip/hip_runtime.h>
 
