@@ -672,11 +672,10 @@ size_t tree_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t vocab, int32
  *          bytes.
  * dtype    TREE_DTYPE_BF16 (bf16 MFMA, sums and all that follows in fp32) or
  *          TREE_DTYPE_F32 (each value as three bf16, the six largest partial
- *          products: fp32 accuracy; values above 3.38e38 are taken as infinite, and what is
- *          infinite makes its logits NaN).
+ *          products: fp32 accuracy; what is infinite makes its logits NaN).
  * Logits are taken relative to their row's largest, so that they may be of any size as
- * long as the product of hidden and weight is finite (entries masked by the lowest
- * bf16, say); lse is held at the largest fp32 value.  A row whose products are all
+ * long as the product of hidden and weight is finite (entries masked by the
+ * type's lowest, say); lse is held at the largest fp32 value.  A row whose products are all
  * -inf has lse -inf, entropy 0 and log probabilities -inf; one of NaN or +inf (of
  * hidden or weight not finite, or products too large) makes its row's results NaN.
  * dplan, dplan_bytes  device copy of `plan`, as for tree_conv.

@@ -13,7 +13,7 @@ PRODUCTS = ((0, 0), (0, 1), (1, 0), (0, 2), (2, 0), (1, 1))
 SPLIT_CASES = ((64, 700, 136), (40, 9000, 72), (300, 900, 256), (600, 6500, 520))
 # An error relative to a gradient's norm.  Sums round by 2^-24 / sqrt(3) of a running sum in
 # the mean, in 6 steps or more for 32 terms; over a few hundred steps that is a few
-# 1e-7, while a partial product of parts whose exponents differ by 16 is 2.5e-6 of its terms.
+# 1e-7, while a partial product of parts whose exponents differ by 16 is 4e-6 of its terms.
 SPLIT_REL = 1e-6
 # A log probability's, in the mean: the same of logits of spread 2, and the log-sum-exp's
 # rounding, 2^-22 / sqrt(3).
@@ -53,9 +53,9 @@ def split_exact(parents, lens, hidden, weight, tokens, dlogp, products=None):
 
 
 def parts(x):
-    """Three bf16 (as fp32) whose sum is x to 2^-26 or so."""
-    out = []
-    for _ in range(3):
-        out.append(x.to(torch.bfloat16).float())
+    """Three bf16 (as fp32) whose sum is x: its first 8 bits, the rest rounded, and so on."""
+    out = [(x.contiguous().view(torch.int32) & -65536).view(torch.float32)]
+    for _ in range(2):
         x = x - out[-1]
+        out.append(x.to(torch.bfloat16).float())
     return out

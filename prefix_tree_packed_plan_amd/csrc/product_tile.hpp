@@ -12,12 +12,13 @@
 // 16 and rows m = 4 (l / 16) + i of register i: four neighbouring m of one n,
 // which is 8 or 16 bytes of a row of `out`; pair_up() makes it 16 for bf16.
 //
-// fp32: a value is the sum of three bf16 (rounded, the rest rounded, the rest of
-// that: exact to 2^-26 of it; the second is up to 2^-8 of it, the third 2^-17), and a
+// fp32: a value is the sum of three bf16 (its first 8 bits, the rest rounded, the rest of
+// that, which is exact; the second is below 2^-7 of it, the third up to 2^-16), and a
 // product of two the six largest of the nine partial products; those left out are up to
-// 2^-24 of it, 2^-27 in the mean.  Six bf16 MFMA do 2.7
-// times the work of fp32 MFMA in the same time.  Values within a factor of 2^-8
-// of the largest fp32 may round to infinity.
+// 2^-22 of it, 2^-24 in the mean.  Six bf16 MFMA do 2.7 times the work of fp32 MFMA in
+// the same time.  (First parts rounded to the nearest leave out a quarter of that, which
+// does not show in a gradient's error, but round the largest fp32 numbers, the usual
+// masks, to infinity; held in range they cost 5% of the time.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -202,7 +203,7 @@ struct Split {
 __device__ __forceinline__ void split_pair(Split& s, int j, float a, float b) {
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    s.w[q][j] = pk2(a, b);
+    s.w[q][j] = q ? pk2(a, b) : __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
     a -= chunk::lo_f(s.w[q][j]);
     b -= chunk::hi_f(s.w[q][j]);
   }
@@ -394,7 +395,7 @@ __device__ __forceinline__ void run(f32x4 (&acc)[C::MB][C::NB], typename C::OpA&
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
       if (t < steps) stage(t, t);
-    // Logits: the five smaller partial products, up to 2^-7 of the terms' sizes, are added
+    // Logits: the five smaller partial products, up to 2^-6 of the terms' sizes, are added
     // up by themselves, so that the sum is rounded once for 32 k instead of six times (the
     // largest error of an fp32 gradient is that of a probability near 1).
     constexpr bool APART = !C::B_PADDED && !C::A_BY_K;

@@ -37,7 +37,7 @@ def test_exponentials_of_far_entries(n, vocab):
 @pytest.mark.parametrize("n,vocab,width", SPLIT_CASES)
 def test_six_partial_products(n, vocab, width):
     """The errors' size over the whole result, which no worst case's bound holds to a
-    partial product: leaving one out of the products makes it one and a half times the limit or more
+    partial product: leaving one out of the products makes it three times the limit or more
     (the oracle's test plants that)."""
     print(f"six products n={n} vocab={vocab} width={width}", file=sys.stderr, flush=True)
     parents, lens, h, w, tok, dlogp = (x.to(DEV) if isinstance(x, torch.Tensor) else x

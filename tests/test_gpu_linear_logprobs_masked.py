@@ -1,6 +1,6 @@
 """Log probabilities from hidden states and the output weight where logits reach
-the ends of fp32: entries masked by the lowest bf16, which fill tiles or parts of
-them, and rows whose logits are all that large."""
+the ends of fp32: entries masked by the lowest number of a type, which fill tiles or
+parts of them, and rows whose logits are all that large."""
 import sys
 
 import numpy as np
@@ -31,13 +31,13 @@ def near(name, got, want, bound):
     assert np.all(err <= bound), (name, float((err / bound).max()))
 
 
-@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("dtype,low", [("bf16", LOW), ("f32", LOW), ("f32", torch.finfo(torch.float32).min)])
 @pytest.mark.parametrize("temperature", [0.5, 1.0, 2.0])
 @pytest.mark.parametrize("n,first,keep,vocab", [(22, 0, 100, 300), (22, 200, 300, 300), (22, 70, 71, 140),
                                                 (300, 0, 1000, 9000), (300, 8000, 9000, 9000),
                                                 (1100, 10000, 10300, 10300)])
-def test_masked_entries_count_for_nothing(n, first, keep, vocab, temperature, dtype):
-    """A first column of 1 in hidden adds the lowest bf16 to the logits of all entries but
+def test_masked_entries_count_for_nothing(n, first, keep, vocab, temperature, dtype, low):
+    """A first column of 1 in hidden adds the lowest number to the logits of all entries but
     first .. keep - 1: the results are those of these entries alone, and the gradients
     of the others are zero."""
     print(f"masked n={n} {first}..{keep} of {vocab} T={temperature} {dtype}", file=sys.stderr, flush=True)
@@ -51,7 +51,7 @@ def test_masked_entries_count_for_nothing(n, first, keep, vocab, temperature, dt
     masked = torch.ones(vocab, dtype=torch.bool)
     masked[first:keep] = False
     w[masked] = 0
-    w[masked, 0] = LOW
+    w[masked, 0] = low
     tok = torch.randint(first, keep, (n,), generator=g)
     dlogp, dent = torch.randn(n, generator=g), torch.randn(n, generator=g) * 0.1
     if masked[0]:
@@ -70,7 +70,7 @@ def test_masked_entries_count_for_nothing(n, first, keep, vocab, temperature, dt
     ref = tree_linear_logprobs_reference(parents, lens, np64(h), few, t, temperature, TERMS[dtype])
     if masked[0]:
         # z / T - lse, where lse is far below a rounding of z; past fp32 -inf.
-        z = LOW / temperature
+        z = low / temperature
         assert r.logp[3].item() == float("-inf") if z < -3.41e38 else abs(r.logp[3].item() / z - 1) <= 2.0 ** -22
         r.logp[3] = 0
     for name in ("logp", "entropy", "lse"):
